@@ -1,0 +1,496 @@
+"""Workloads of the layer operators around the chunked delta rule: the short causal
+convolution, the selective state space scan and the single-token delta rule step.
+
+Each case is one pass through one operator.  With ``own`` false, ``run`` evaluates the
+operator's plain form in fp32 torch arithmetic; with ``own`` true it makes the library's
+calls.  ``exact`` evaluates the definitions in fp64, token by token.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+_IO = {"bf16": torch.bfloat16, "fp32": torch.float32}
+_DEV = "cuda"
+
+
+# ----------------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # serving: several prompts of different lengths packed into one row, q and k of a
+        # 16-head layer side by side, each prompt with the rows its cache kept
+        dict(name="conv prompts packed", op="conv", io="bf16", B=1, T=8192, seqs=7, C=2048, W=4, act=True, bias=True, state=True),
+        # one short fp32 prompt, width 3, no activation: a call whose latency counts
+        dict(name="conv prompt short", op="conv", io="fp32", B=1, T=37, seqs=0, C=512, W=3, act=False, bias=False, state=False),
+        # training step at the repository's training shape (4 x 4096 tokens, 2 x 8 heads of 128)
+        dict(name="conv train", op="conv_train", io="bf16", B=4, T=4096, seqs=0, C=2048, W=4, act=True, bias=True, state=False),
+        # decoding: one token of each of 256 sequences
+        dict(name="conv step", op="conv_step", io="bf16", B=256, C=4096, W=4, act=True, bias=True),
+        # prompts of a batch, gated output, 16 states a channel
+        dict(name="scan prompt", op="scan", io="bf16", B=2, T=2048, seqs=0, D=4096, N=16, G=1, z=True, state=False),
+        # one long prompt of one user: little parallelism but for the time axis
+        dict(name="scan prompt long", op="scan", io="bf16", B=1, T=16384, seqs=0, D=2048, N=16, G=1, z=True, state=False),
+        # continued prompts of odd lengths packed, wide states in four groups
+        dict(name="scan prompts packed", op="scan", io="bf16", B=1, T=3001, seqs=6, D=1024, N=64, G=4, z=False, state=True),
+        # training step, forward that keeps its states and the backward from them
+        dict(name="scan train", op="scan_train", io="bf16", B=4, T=2048, seqs=0, D=2048, N=16, G=1, z=True, state=False),
+        # fp32 training over short odd sequences, two groups, states in and out
+        dict(name="scan train ragged fp32", op="scan_train", io="fp32", B=1, T=777, seqs=4, D=320, N=32, G=2, z=True, state=True),
+        # decoding: one token of each of 64 sequences
+        dict(name="scan step", op="scan_step", io="bf16", B=64, D=4096, N=16, G=1, z=True),
+        # decoding for one user: latency
+        dict(name="delta step one", op="step", io="bf16", B=1, H=8, Dk=128, Dv=128, channel=False),
+        # decoding for a large batch, one decay per key channel: the state's bytes count
+        dict(name="delta step batch", op="step", io="bf16", B=128, H=16, Dk=128, Dv=128, channel=True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["conv", "conv_train", "conv_step", "scan", "scan", "scan_train", "scan_train", "scan_step", "step", "step"])
+    io = rng.choice(["bf16", "bf16", "fp32"])
+    flag = lambda: rng.random() < 0.5  # noqa: E731
+    if op == "conv_step":
+        return dict(op=op, io=io, B=_log(rng, 1, 512), C=8 * _log(rng, 8, 512), W=rng.choice([2, 3, 4]), act=flag(), bias=flag())
+    if op == "scan_step":
+        G = rng.choice([1, 1, 2, 4])
+        return dict(op=op, io=io, B=_log(rng, 1, 128), D=8 * G * _log(rng, 8, 512 // G), N=rng.choice([8, 16, 16, 32, 64]), G=G, z=flag())
+    if op == "step":
+        return dict(op=op, io=io, B=_log(rng, 1, 128), H=_log(rng, 1, 16), Dk=rng.choice([64, 128]),
+                    Dv=16 * rng.randint(1, 8), channel=flag())
+    packed = rng.random() < 0.4
+    T = _log(rng, 1 if not packed else 64, 8192)
+    B = 1 if packed else _log(rng, 1, 4)
+    seqs = rng.randint(2, 9) if packed else 0
+    if op in ("conv", "conv_train"):
+        C = 8 * _log(rng, 8, 256)
+        return dict(op=op, io=io, B=B, T=min(T, 4096) if B > 1 else T, seqs=seqs, C=C, W=rng.choice([2, 3, 4]), act=flag(), bias=flag(),
+                    state=flag())
+    N, G = rng.choice([8, 16, 16, 32, 64]), rng.choice([1, 1, 2, 4])
+    D = 8 * G * _log(rng, 8, 256 // G)
+    most = (1 << 28) if op == "scan" else (1 << 27)  # B T D N
+    T = max(1, min(T, most // (B * D * N)))
+    if packed:
+        T = max(T, 16)
+    return dict(op=op, io=io, B=B, T=T, seqs=seqs, D=D, N=N, G=G, z=flag(), state=flag())
+
+
+def _offsets(case):
+    """Offsets of the packed sequences of a case: ragged, with an empty one among four or more."""
+    T, n = case["T"], case["seqs"]
+    r = random.Random(1000 * T + n)
+    cuts = sorted(r.randint(0, T) for _ in range(n - 1))
+    if n >= 4:
+        cuts[1] = cuts[0]
+    return [0] + cuts + [T]
+
+
+# ----------------------------------------------------------------------------- inputs
+
+def _inputs(case, seed):
+    g = torch.Generator(device=_DEV)
+    g.manual_seed(seed)
+    io = _IO[case["io"]]
+    B, op = case["B"], case["op"]
+
+    def normal(*shape, std=1.0, dtype=io):
+        return (torch.randn(*shape, generator=g, device=_DEV) * std).to(dtype)
+
+    def uniform(lo, hi, *shape):
+        return torch.rand(*shape, generator=g, device=_DEV) * (hi - lo) + lo
+
+    s = dict(case=case, cu=None)
+    seqs = case.get("seqs", 0)
+    if seqs:
+        s["offsets"] = _offsets(case)
+        s["cu"] = torch.tensor(s["offsets"], dtype=torch.int64, device=_DEV)
+    n = seqs or B
+    if op in ("conv", "conv_train", "conv_step"):
+        T, C, W = case.get("T", 1), case["C"], case["W"]
+        s["x"] = normal(B, T, C)
+        s["weight"] = uniform(-W ** -0.5, W ** -0.5, C, W)
+        s["bias"] = uniform(-W ** -0.5, W ** -0.5, C) if case["bias"] else None
+        s["state"] = normal(n, W - 1, C) if case.get("state", True) else None
+        if op == "conv_train":
+            s["dy"] = normal(B, T, C)
+            s["dstate"] = normal(n, W - 1, C) if case["state"] else None
+    elif op in ("scan", "scan_train", "scan_step"):
+        T, D, N, G = case.get("T", 1), case["D"], case["N"], case["G"]
+        s["u"], s["dt"] = normal(B, T, D), normal(B, T, D, std=0.5)
+        # rates 1 .. N a channel, steps of 0.001 .. 0.1 behind the softplus
+        s["A"] = -torch.arange(1, N + 1, device=_DEV, dtype=torch.float32) * uniform(0.8, 1.2, D, N)
+        step = torch.exp(uniform(math.log(1e-3), math.log(1e-1), D))
+        s["dt_bias"] = step + torch.log(-torch.expm1(-step))
+        s["Bm"], s["Cm"] = normal(B, T, G, N), normal(B, T, G, N)
+        s["D"] = uniform(0.5, 1.5, D)
+        s["z"] = normal(B, T, D) if case["z"] else None
+        s["state"] = normal(n, D, N, std=0.5, dtype=torch.float32) if case.get("state", True) else None
+        if op == "scan_train":
+            s["dy"] = normal(B, T, D)
+            s["dstate"] = normal(n, D, N, std=0.5, dtype=torch.float32) if case["state"] else None
+    else:
+        H, Dk, Dv = case["H"], case["Dk"], case["Dv"]
+        unit = lambda t: (t / t.norm(dim=-1, keepdim=True)).to(io)  # noqa: E731
+        s["q"] = unit(normal(B, 1, H, Dk, dtype=torch.float32))
+        s["k"] = unit(normal(B, 1, H, Dk, dtype=torch.float32))
+        s["v"] = normal(B, 1, H, Dv)
+        gate = normal(B, 1, H, Dk, dtype=torch.float32) if case["channel"] else normal(B, 1, H, dtype=torch.float32)
+        s["g"] = -0.5 * torch.log1p(torch.exp(gate))
+        s["beta"] = torch.sigmoid(normal(B, 1, H, dtype=torch.float32))
+        s["state"] = normal(B, H, Dk, Dv, std=0.1, dtype=torch.float32)
+        s["scale"] = Dk ** -0.5
+    return s
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    if own:
+        import gated_deltanet_chunked_gdn_amd as gdn
+
+        s["gdn"] = gdn
+        # the packed offsets as a serving loop holds them: built once for a batch
+        s["seqs"] = gdn.SeqLens(s["offsets"], _DEV) if s["cu"] is not None else None
+    return s
+
+
+def run(s):
+    return (_run_own if own else _run_plain)(s)
+
+
+def _run_own(s):
+    gdn, case, seqs = s["gdn"], s["case"], s["seqs"]
+    op = case["op"]
+    act = "silu" if case.get("act") else None
+    if op == "conv":
+        y, last = gdn.conv_fwd(s["x"], s["weight"], bias=s["bias"], state0=s["state"], cu_seqlens=seqs, activation=act)
+        return {"y": y, "state": last}
+    if op == "conv_train":
+        y, _ = gdn.conv_fwd(s["x"], s["weight"], bias=s["bias"], state0=s["state"], cu_seqlens=seqs, activation=act, output_final_state=False)
+        return {"y": y, **gdn.conv_bwd(s["x"], s["weight"], s["dy"], bias=s["bias"], state0=s["state"], dstate_final=s["dstate"],
+                                       cu_seqlens=seqs, activation=act)}
+    if op == "conv_step":
+        y = gdn.conv_step(s["x"], s["weight"], s["state"], bias=s["bias"], activation=act)
+        return {"y": y, "state": s["state"]}
+    if op == "scan":
+        y, h = gdn.scan_fwd(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"], h0=s["state"],
+                            cu_seqlens=seqs)
+        return {"y": y, "state": h}
+    if op == "scan_train":
+        y, h, saved = gdn.scan_fwd_save(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"],
+                                        h0=s["state"], cu_seqlens=seqs)
+        return {"y": y, "state": h, **gdn.scan_bwd_saved(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], s["dy"], saved, D=s["D"], z=s["z"],
+                                                         dt_bias=s["dt_bias"], dh_final=s["dstate"], cu_seqlens=seqs)}
+    if op == "scan_step":
+        y = gdn.scan_step(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], s["state"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"])
+        return {"y": y, "state": s["state"]}
+    step = gdn.kda_step if case["channel"] else gdn.step
+    o = step(s["q"], s["k"], s["v"], s["g"], s["beta"], s["state"], scale=s["scale"])
+    return {"o": o, "state": s["state"]}
+
+
+# ----------------------------------------------------------------------------- plain forms, fp32
+
+def _run_plain(s):
+    op = s["case"]["op"]
+    if op in ("conv", "conv_train", "conv_step"):
+        return _plain_conv(s)
+    return _plain_scan(s) if op in ("scan", "scan_train", "scan_step") else _plain_step(s)
+
+
+def _sequences(s, B, T):
+    """Per row of the flattened (B, T) tokens: its sequence, and the offsets of all sequences."""
+    cu = s["cu"] if s["cu"] is not None else torch.arange(B + 1, device=_DEV) * T
+    rows = torch.arange(B * T, device=_DEV)
+    return torch.searchsorted(cu, rows, right=True) - 1, cu
+
+
+def _plain_conv(s):
+    case, x = s["case"], s["x"]
+    B, T, C = x.shape
+    W, io = case["W"], x.dtype
+    w = s["weight"]
+    seq, cu = _sequences(s, B, T)
+    n = cu.numel() - 1
+    # every sequence's kept rows in front of its own: row r of sequence q sits at r + (q + 1) (W - 1)
+    at = torch.arange(B * T, device=_DEV) + (seq + 1) * (W - 1)
+    head = (cu[:-1] + torch.arange(n, device=_DEV) * (W - 1)).unsqueeze(1) + torch.arange(W - 1, device=_DEV)
+    tail = (cu[1:] + torch.arange(n, device=_DEV) * (W - 1)).unsqueeze(1) + torch.arange(W - 1, device=_DEV)
+    line = torch.zeros(B * T + n * (W - 1), C, device=_DEV)
+    line[at] = x.reshape(B * T, C).float()
+    if s["state"] is not None:
+        line[head] = s["state"].float()
+    windows = line.unfold(0, W, 1)[at - (W - 1)]  # (B T, C, W)
+    p = (windows * w).sum(-1)
+    if s["bias"] is not None:
+        p = p + s["bias"]
+    sig = torch.sigmoid(p)
+    y = (p * sig if case["act"] else p).to(io).reshape(B, T, C)
+    last = line[tail].to(io)
+    if case["op"] == "conv_step":
+        s["state"].copy_(last)
+        return {"y": y, "state": s["state"]}
+    if case["op"] == "conv":
+        return {"y": y, "state": last}
+    dp = s["dy"].reshape(B * T, C).float()
+    if case["act"]:
+        dp = dp * sig * (1 + p * (1 - sig))
+    # the gradient of a line's row: the W places whose windows hold it
+    wide = torch.zeros(line.shape[0] + W - 1, C, device=_DEV)
+    wide[at] = dp
+    dline = (wide.unfold(0, W, 1) * w.flip(-1)).sum(-1)
+    if s["dstate"] is not None:
+        dline.index_put_((tail,), s["dstate"].float(), accumulate=True)
+    return {"y": y, "dx": dline[at].to(io).reshape(B, T, C), "dweight": (windows * dp.unsqueeze(-1)).sum(0),
+            "dbias": dp.sum(0) if s["bias"] is not None else None,
+            "dstate0": dline[head].to(io) if s["state"] is not None else None}
+
+
+def _running(a, b):
+    """h_t = a_t h_{t-1} + b_t along dim 0, by doubling."""
+    span = 1
+    while span < a.shape[0]:
+        b = torch.cat([b[:span], b[span:] + a[span:] * b[:-span]])
+        a = torch.cat([a[:span], a[span:] * a[:-span]])
+        span *= 2
+    return b
+
+
+def _plain_scan(s):
+    case, u = s["case"], s["u"]
+    B, T, D = u.shape
+    N, G, io = case["N"], case["G"], u.dtype
+    rows = B * T
+    seq, cu = _sequences(s, B, T)
+    first, some = cu[:-1], cu[1:] > cu[:-1]
+    uf, x = u.reshape(rows, D).float(), s["dt"].reshape(rows, D).float() + s["dt_bias"]
+    delta = torch.clamp(x, min=0) + torch.log1p(torch.exp(-x.abs()))
+    Bf = s["Bm"].reshape(rows, G, 1, N).float()
+    Cf = s["Cm"].reshape(rows, G, 1, N).float()
+    groups = lambda t: t.reshape(rows, G, D // G, -1)  # noqa: E731
+    flat = lambda t: t.reshape(rows, D, N)  # noqa: E731
+    a = torch.exp(delta.unsqueeze(-1) * s["A"])
+    b = flat(groups(delta * uf) * Bf)
+    h0 = s["state"] if s["state"] is not None else torch.zeros(cu.numel() - 1, D, N, device=_DEV)
+    starts = first[some]
+    b[starts] += a[starts] * h0[some]
+    cut = a.clone()
+    cut[starts] = 0
+    h = _running(cut, b)
+    sums = flat(groups(h) * Cf).sum(-1) + s["D"] * uf
+    sig = zf = None
+    y = sums
+    if s["z"] is not None:
+        zf = s["z"].reshape(rows, D).float()
+        sig = torch.sigmoid(zf)
+        y = sums * zf * sig
+    y = y.to(io).reshape(B, T, D)
+    last = h0.clone()
+    last[some] = h[cu[1:][some] - 1]
+    if case["op"] == "scan_step":
+        s["state"].copy_(last)
+        return {"y": y, "state": s["state"]}
+    if case["op"] == "scan":
+        return {"y": y, "state": last}
+    dy = s["dy"].reshape(rows, D).float()
+    ds = dy if zf is None else dy * zf * sig
+    db = flat(groups(ds) * Cf)
+    dlast = s["dstate"] if s["dstate"] is not None else torch.zeros_like(h0)
+    db[cu[1:][some] - 1] += dlast[some]
+    # reverse: g_t = db_t + a_{t+1} g_{t+1}, cut where the next row starts a sequence
+    after = torch.cat([cut[1:], torch.zeros_like(cut[:1])])
+    grad = _running(after.flip(0), db.flip(0)).flip(0)
+    before = torch.cat([torch.zeros_like(h[:1]), h[:-1]])
+    before[starts] = h0[some]
+    q = grad * a * before
+    du_b = flat(groups(grad) * Bf).sum(-1)
+    ddelta = uf * du_b + (q * s["A"]).sum(-1)
+    ddt = ddelta * torch.sigmoid(x)
+    dh0 = dlast.clone()
+    dh0[some] = a[starts] * grad[starts]
+    out = {"y": y, "state": last, "du": s["D"] * ds + delta * du_b, "ddt": ddt,
+           "dB": groups(flat(grad * (delta * uf).unsqueeze(-1))).reshape(rows, G, D // G, N).sum(2),
+           "dC": groups(flat(h * ds.unsqueeze(-1))).reshape(rows, G, D // G, N).sum(2),
+           "dz": dy * sums * sig * (1 + zf * (1 - sig)) if zf is not None else None}
+    shapes = {"du": (B, T, D), "ddt": (B, T, D), "dz": (B, T, D), "dB": (B, T, G, N), "dC": (B, T, G, N)}
+    out.update({k: out[k].to(io).reshape(v) for k, v in shapes.items() if out[k] is not None})
+    out.update(dA=(q * delta.unsqueeze(-1)).sum(0), dD=(ds * uf).sum(0), ddt_bias=ddt.sum(0),
+               dh0=dh0 if s["state"] is not None else None)
+    return out
+
+
+def _plain_step(s):
+    q, k, v = (s[name].float().squeeze(1) for name in ("q", "k", "v"))
+    g, beta, S = s["g"].squeeze(1), s["beta"].squeeze(1), s["state"]
+    decay = torch.exp(g).unsqueeze(-1) if s["case"]["channel"] else torch.exp(g).unsqueeze(-1).unsqueeze(-1)
+    S1 = S * decay
+    e = beta.unsqueeze(-1) * (v - (S1 * k.unsqueeze(-1)).sum(-2))
+    S1 = S1 + k.unsqueeze(-1) * e.unsqueeze(-2)
+    o = s["scale"] * (S1 * q.unsqueeze(-1)).sum(-2)
+    s["state"].copy_(S1)
+    return {"o": o.to(s["q"].dtype).unsqueeze(1), "state": s["state"]}
+
+
+# ----------------------------------------------------------------------------- what a pass cannot do without
+
+def work(case):
+    op, io = case["op"], 2 if case["io"] == "bf16" else 4
+    B = case["B"]
+    if op in ("conv", "conv_train", "conv_step"):
+        C, W = case["C"], case["W"]
+        n = case.get("seqs", 0) or B
+        values = B * case.get("T", 1) * C
+        kept = n * (W - 1) * C * io if case.get("state", True) else 0
+        out_state = 0 if op == "conv_train" else n * (W - 1) * C * io
+        params = C * W * 4 + (C * 4 if case["bias"] else 0)
+        act = 4 if case["act"] else 0
+        if op == "conv_train":  # x, dy in; y, dx out
+            return {"bytes": 4 * values * io + 3 * kept + 2 * params, "flops": values * (6 * W + 3 * act)}
+        return {"bytes": 2 * values * io + kept + out_state + params, "flops": values * (2 * W + act)}
+    if op in ("scan", "scan_train", "scan_step"):
+        D, N, G = case["D"], case["N"], case["G"]
+        n = case.get("seqs", 0) or B
+        rows = B * case.get("T", 1)
+        wide = 4 if case["z"] else 3  # u, dt, y and z
+        state = n * D * N * 4
+        params = D * N * 4 + 2 * D * 4
+        some = state if case.get("state", True) else 0
+        if op == "scan_train":  # those, dy, du, ddt and dz; B, C and their gradients
+            more = 4 if case["z"] else 3
+            return {"bytes": (wide + more) * rows * D * io + 4 * rows * G * N * io + 3 * some + state + 2 * params,
+                    "flops": rows * D * (N * 24 + 30)}
+        return {"bytes": wide * rows * D * io + 2 * rows * G * N * io + some + state + params, "flops": rows * D * (N * 7 + 10)}
+    H, Dk, Dv = case["H"], case["Dk"], case["Dv"]
+    gates = B * H * 4 * (Dk + 1 if case["channel"] else 2)
+    return {"bytes": 2 * B * H * Dk * Dv * 4 + B * H * (2 * Dk + 2 * Dv) * io + gates, "flops": 7 * B * H * Dk * Dv}
+
+
+# ----------------------------------------------------------------------------- definitions, fp64, token by token
+
+def exact(case, seed):
+    s = _inputs(case, seed)
+    s = {k: v.double() if isinstance(v, torch.Tensor) and v.is_floating_point() else v for k, v in s.items()}
+    op = case["op"]
+    if op in ("conv", "conv_train", "conv_step"):
+        return _exact_conv(case, s)
+    return _exact_scan(case, s) if op in ("scan", "scan_train", "scan_step") else _exact_step(case, s)
+
+
+def _spans(case, s):
+    """(batch row, first token, last token + 1) of every sequence."""
+    if s["cu"] is not None:
+        return [(0, a, b) for a, b in zip(s["offsets"], s["offsets"][1:])]
+    return [(i, 0, case.get("T", 1)) for i in range(case["B"])]
+
+
+def _exact_conv(case, s):
+    W, x, w = case["W"], s["x"], s["weight"]
+    C = x.shape[-1]
+    y, dx = torch.empty_like(x), torch.zeros_like(x)
+    last, dfirst = x.new_zeros(len(_spans(case, s)), W - 1, C), x.new_zeros(len(_spans(case, s)), W - 1, C)
+    dw, db = torch.zeros_like(w), x.new_zeros(C)
+    for n, (i, t0, t1) in enumerate(_spans(case, s)):
+        before = s["state"][n] if s["state"] is not None else x.new_zeros(W - 1, C)
+        line = torch.cat([before, x[i, t0:t1]])
+        T = t1 - t0
+        p = x.new_zeros(T, C)
+        for j in range(W):
+            p += w[:, j] * line[j:j + T]
+        if s["bias"] is not None:
+            p += s["bias"]
+        e = 1 / (1 + torch.exp(-p))
+        y[i, t0:t1] = p * e if case["act"] else p
+        last[n] = line[T:]
+        if case["op"] == "conv_train":
+            dp = s["dy"][i, t0:t1]
+            if case["act"]:
+                dp = dp * (e + p * e * (1 - e))
+            dline = torch.zeros_like(line)
+            for j in range(W):
+                dline[j:j + T] += w[:, j] * dp
+                dw[:, j] += (line[j:j + T] * dp).sum(0)
+            db += dp.sum(0)
+            if s["dstate"] is not None:
+                dline[T:] += s["dstate"][n]
+            dfirst[n], dx[i, t0:t1] = dline[:W - 1], dline[W - 1:]
+    if case["op"] != "conv_train":
+        return {"y": y, "state": last}
+    return {"y": y, "dx": dx, "dweight": dw, "dbias": db if s["bias"] is not None else None,
+            "dstate0": dfirst if s["state"] is not None else None}
+
+
+def _exact_scan(case, s):
+    u, A, N, G = s["u"], s["A"], case["N"], case["G"]
+    B, T, D = u.shape
+    per = D // G
+    pre = s["dt"] + s["dt_bias"]
+    delta = torch.logaddexp(pre, torch.zeros_like(pre))
+    train = case["op"] == "scan_train"
+    spans = _spans(case, s)
+    sums = torch.empty_like(u)
+    h_last = u.new_zeros(len(spans), D, N)
+    if train:
+        keep = u.new_empty(B, T, D, N)  # the state before each token
+        out = {k: torch.zeros_like(s[v]) for k, v in dict(du="u", ddt="dt", dB="Bm", dC="Cm", dA="A").items()}
+        dh0 = u.new_zeros(len(spans), D, N)
+    dense = s["cu"] is None
+    # a dense batch advances together, packed sequences one after another
+    runs = [(slice(0, B), 0, T, slice(0, B))] if dense else [(slice(0, 1), a, b, slice(n, n + 1)) for n, (_, a, b) in enumerate(spans)]
+    ds = None
+    if train:
+        ds = s["dy"] if s["z"] is None else s["dy"] * s["z"] / (1 + torch.exp(-s["z"]))
+    for i, t0, t1, n in runs:
+        m = B if dense else 1
+        h = s["state"][n].clone() if s["state"] is not None else u.new_zeros(m, D, N)
+        for t in range(t0, t1):
+            if train:
+                keep[i, t] = h
+            d = delta[i, t].unsqueeze(-1)
+            Bt = s["Bm"][i, t].repeat_interleave(per, 1)
+            Ct = s["Cm"][i, t].repeat_interleave(per, 1)
+            h = torch.exp(d * A) * h + d * u[i, t].unsqueeze(-1) * Bt
+            sums[i, t] = (h * Ct).sum(-1) + s["D"] * u[i, t]
+        h_last[n] = h
+        if not train:
+            continue
+        back = s["dstate"][n].clone() if s["dstate"] is not None else torch.zeros_like(h)
+        for t in range(t1 - 1, t0 - 1, -1):
+            d, ut, gt = delta[i, t].unsqueeze(-1), u[i, t].unsqueeze(-1), ds[i, t].unsqueeze(-1)
+            Bt = s["Bm"][i, t].repeat_interleave(per, 1)
+            Ct = s["Cm"][i, t].repeat_interleave(per, 1)
+            decay = torch.exp(d * A)
+            out["dC"][i, t] = ((decay * keep[i, t] + d * ut * Bt) * gt).reshape(m, G, per, N).sum(2)
+            back = back + Ct * gt
+            out["dB"][i, t] = (back * d * ut).reshape(m, G, per, N).sum(2)
+            through = (back * Bt).sum(-1)
+            out["du"][i, t] = s["D"] * ds[i, t] + delta[i, t] * through
+            moved = back * decay * keep[i, t]
+            out["dA"] += (moved * d).sum(0)
+            out["ddt"][i, t] = u[i, t] * through + (moved * A).sum(-1)
+            back = back * decay
+        dh0[n] = back
+    gate = 1 / (1 + torch.exp(-s["z"])) if s["z"] is not None else None
+    y = sums * s["z"] * gate if gate is not None else sums
+    if not train:
+        return {"y": y, "state": h_last}
+    out["ddt"] = out["ddt"] / (1 + torch.exp(-pre))
+    out.update(y=y, state=h_last, dD=(ds * u).sum((0, 1)), ddt_bias=out["ddt"].sum((0, 1)), dh0=dh0 if s["state"] is not None else None,
+               dz=s["dy"] * sums * (gate + s["z"] * gate * (1 - gate)) if gate is not None else None)
+    return out
+
+
+def _exact_step(case, s):
+    o = torch.empty_like(s["v"])
+    S = s["state"].clone()
+    a = torch.exp(s["g"][:, 0])
+    S = a.unsqueeze(-1) * S if case["channel"] else a[..., None, None] * S
+    held = torch.matmul(s["k"][:, 0].unsqueeze(-2), S).squeeze(-2)
+    e = s["beta"][:, 0].unsqueeze(-1) * (s["v"][:, 0] - held)
+    S = S + torch.matmul(s["k"][:, 0].unsqueeze(-1), e.unsqueeze(-2))
+    o[:, 0] = s["scale"] * torch.matmul(s["q"][:, 0].unsqueeze(-2), S).squeeze(-2)
+    return {"o": o, "state": S}
