@@ -185,7 +185,8 @@ def _run_own(s):
         y, h, saved = gdn.scan_fwd_save(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"],
                                         h0=s["state"], cu_seqlens=seqs)
         return {"y": y, "state": h, **gdn.scan_bwd_saved(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], s["dy"], saved, D=s["D"], z=s["z"],
-                                                         dt_bias=s["dt_bias"], dh_final=s["dstate"], cu_seqlens=seqs)}
+                                                         dt_bias=s["dt_bias"], dh_final=s["dstate"], cu_seqlens=seqs,
+                                                         want_dh0=s["state"] is not None)}
     if op == "scan_step":
         y = gdn.scan_step(s["u"], s["dt"], s["A"], s["Bm"], s["Cm"], s["state"], D=s["D"], z=s["z"], dt_bias=s["dt_bias"])
         return {"y": y, "state": s["state"]}
