@@ -46,12 +46,21 @@ GDN_PASS_KDA_FWD = 4
 GDN_PASS_CHUNK_SAVED = 5
 GDN_PASS_KDA_BWD = 6
 GDN_PASS_KDA_SAVED = 7
+# gdn_activation
+GDN_ACT_NONE = 0
+GDN_ACT_SILU = 1
+# gdn_scan_pass
+GDN_SCAN_FWD = 0
+GDN_SCAN_SAVED = 1
+GDN_SCAN_BWD = 2
 
 # Every symbol include/gdn.h declares.
 EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chunk_fwd",
             "gdn_chunk_bwd", "gdn_recurrent_ref", "gdn_prologue", "gdn_epilogue",
             "gdn_kda_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_device_copy", "gdn_chunk_fwd_save",
-            "gdn_chunk_bwd_saved", "gdn_kda_chunk_bwd", "gdn_kda_chunk_fwd_save", "gdn_kda_chunk_bwd_saved")
+            "gdn_chunk_bwd_saved", "gdn_kda_chunk_bwd", "gdn_kda_chunk_fwd_save", "gdn_kda_chunk_bwd_saved",
+            "gdn_step", "gdn_kda_step", "gdn_conv_fwd", "gdn_conv_workspace_size", "gdn_conv_bwd", "gdn_conv_step",
+            "gdn_scan_workspace_size", "gdn_scan_fwd", "gdn_scan_fwd_save", "gdn_scan_bwd_saved", "gdn_scan_step")
 
 
 class GdnLibraryMissing(RuntimeError):
@@ -76,6 +85,29 @@ class Problem(ctypes.Structure):
         ("chunk", ctypes.c_int32),
         ("num_segments", ctypes.c_int32),
         ("precision", ctypes.c_int32),
+    ]
+
+
+class ConvProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32), ("W", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("io_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+    ]
+
+
+class ScanProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("G", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("io_dtype", ctypes.c_int32),
+        ("dt_softplus", ctypes.c_int32),
     ]
 
 
@@ -127,6 +159,20 @@ def load():
     lib.gdn_kda_chunk_fwd_save.restype = ctypes.c_int
     lib.gdn_kda_chunk_bwd_saved.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.gdn_kda_chunk_bwd_saved.restype = ctypes.c_int
+    PC, PS, Z = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.c_size_t
+    for name, args in (
+            ("gdn_step", [PP] + [P] * 8), ("gdn_kda_step", [PP] + [P] * 8),
+            ("gdn_conv_fwd", [PC] + [P] * 7), ("gdn_conv_step", [PC] + [P] * 6),
+            ("gdn_conv_workspace_size", [PC, ctypes.POINTER(Z)]),
+            ("gdn_conv_bwd", [PC] + [P] * 11 + [Z, P]),
+            ("gdn_scan_workspace_size", [PS, ctypes.c_int32, ctypes.POINTER(Z)]),
+            ("gdn_scan_fwd", [PS] + [P] * 12 + [Z, P]),
+            ("gdn_scan_fwd_save", [PS] + [P] * 12 + [Z, P, Z, P]),
+            ("gdn_scan_bwd_saved", [PS] + [P] * 11 + [Z] + [P] * 10 + [Z, P]),
+            ("gdn_scan_step", [PS] + [P] * 11)):
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
     _lib = lib
     return lib
 

@@ -1,0 +1,111 @@
+// Host-visible kernel parameter blocks and launchers of the layer operators: the
+// single-token step of the delta rule, the short causal convolution, the selective
+// scan (internal).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gdn.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+struct StepParams {
+  const void* q;      // [B][H][Dk]
+  const void* k;
+  const void* v;      // [B][H][Dv]
+  const float* g;     // [B][H], or [B][H][Dk] (channel)
+  const float* beta;  // [B][H]
+  float* S;           // [B][H][Dk][Dv], updated in place
+  void* o;            // [B][H][Dv]
+  int64_t heads;      // B * H
+  int32_t Dv;
+  float scale;
+};
+hipError_t launch_step(const StepParams& p, int Dk, bool bf16, bool channel, hipStream_t s);
+
+struct ConvParams {
+  const void* x;
+  const float* weight;  // [C][W]
+  const float* bias;    // [C] or nullptr
+  const void* state0;   // [N][W-1][C] or nullptr
+  void* y;
+  void* state_final;    // [N][W-1][C] or nullptr
+  const void* dy;
+  const void* dstate_final;  // or nullptr
+  void* dx;
+  float* dweight;
+  float* dbias;         // or nullptr
+  void* dstate0;        // or nullptr
+  float* ws;            // backward: [token block][W + 1][C] partial sums
+  SeqInfo seq;
+  int64_t rows;         // B * T
+  int32_t N, C;
+  int32_t silu;
+};
+// Token blocks of the backward's partial sums.
+constexpr int kConvBwdRows = 512;
+inline int64_t conv_bwd_blocks(int64_t rows) { return (rows + kConvBwdRows - 1) / kConvBwdRows; }
+hipError_t launch_conv_fwd(const ConvParams& p, int W, bool bf16, hipStream_t s);
+hipError_t launch_conv_bwd(const ConvParams& p, int W, bool bf16, hipStream_t s);
+// state in p.state_final, updated in place
+hipError_t launch_conv_step(const ConvParams& p, int W, bool bf16, hipStream_t s);
+
+struct ScanParams {
+  const void* u;
+  const void* dt;
+  const float* A;
+  const void* Bm;
+  const void* Cm;
+  const float* Dskip;
+  const void* z;
+  const float* dt_bias;
+  const float* h0;
+  void* y;
+  float* h_final;
+  float* saved;         // [block slot][D][N] states before every block, or nullptr
+  // segments over the time axis: `segs` runs of `seg_len` tokens (a multiple of the
+  // block length) of every sequence
+  float* seg_end;       // [seg][sequence][D][N]
+  float* seg_sum;       // [seg][sequence][D]: sums of delta
+  SeqInfo seq;
+  int32_t nseq, D, G;
+  int32_t softplus;
+  int32_t segs;
+  int64_t seg_len;
+  // backward
+  const void* dy;
+  const float* dh_final;
+  void* du;
+  void* ddt;
+  float* dA;
+  void* dBm;
+  void* dCm;
+  float* dDskip;
+  void* dz;
+  float* ddt_bias;
+  float* dh0;
+  float* part_bc;       // [channel tile][row][2][N] partial dB, dC
+  float* part_a;        // [sequence, segment][D][N + 2] partial dA, dDskip, ddt_bias
+  int64_t rows;         // B * T
+};
+
+constexpr int kScanTile = 64;     // channels per workgroup
+constexpr int kScanBlock = 16;    // tokens between two kept states
+// Kept-state slots: block c of a sequence that starts at row bos uses slot
+// bos / block + n + c (distinct, as chunk_slots).
+inline int64_t scan_slots(int64_t rows, int64_t nseq) { return rows / kScanBlock + nseq + 1; }
+inline int scan_tiles(int D, int G) { return G * ((D / G + kScanTile - 1) / kScanTile); }
+// Segments of the longest sequence of max_len tokens, and their length.
+struct ScanSplit {
+  int32_t segs;
+  int64_t len;
+};
+ScanSplit scan_split(int64_t max_len, int64_t nseq, int D, int G, int N);
+hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
+hipError_t launch_scan_bwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
+// state in p.h_final, updated in place
+hipError_t launch_scan_step(const ScanParams& p, int N, bool bf16, hipStream_t s);
+
+}  // namespace gdn

@@ -1,0 +1,171 @@
+// Device parts shared by the selective scan's forward and backward kernels: the
+// channel tile of a workgroup, the staging of a tile of tokens in LDS, and the lane
+// reductions.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_layer.h"
+#include "gdn_layer_device.h"
+
+namespace gdn {
+namespace scan {
+
+using namespace layer;
+
+constexpr int kTile = 32;     // tokens staged at a time
+constexpr int kYStride = 80;  // row stride of output tiles: the four token rows a wave writes fall in other banks
+
+// A workgroup's channels d0 .. d0 + count - 1, all of group g.
+struct ChannelTile {
+  int g, tile, d0, count;  // tile: its number in the group
+  __device__ __forceinline__ ChannelTile(const ScanParams& p, int block) {
+    const int per = p.D / p.G, tiles = (per + kScanTile - 1) / kScanTile;
+    g = block / tiles;
+    tile = block - g * tiles;
+    const int at = tile * kScanTile;
+    d0 = g * per + at;
+    count = min(kScanTile, per - at);
+  }
+};
+
+// Slot of the state kept before token t (a multiple of kScanBlock) of sequence n.
+__device__ __forceinline__ int64_t saved_slot(int64_t bos, int n, int64_t t) {
+  return bos / kScanBlock + n + t / kScanBlock;
+}
+
+template <int S>
+__device__ __forceinline__ void load_states(const float* p, bool ok, float (&f)[S]) {
+#pragma unroll
+  for (int s = 0; s < S; ++s) f[s] = 0.f;
+  if (!ok) return;
+  if constexpr (S == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x; f[1] = v.y;
+  } else {
+#pragma unroll
+    for (int s = 0; s < S; s += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p + s);
+      f[s] = v.x; f[s + 1] = v.y; f[s + 2] = v.z; f[s + 3] = v.w;
+    }
+  }
+}
+template <int S>
+__device__ __forceinline__ void read_states(const float* p, float (&f)[S]) {
+  load_states<S>(p, true, f);
+}
+template <int S>
+__device__ __forceinline__ void store_states(float* p, const float (&f)[S]) {
+  if constexpr (S == 2) {
+    *reinterpret_cast<float2*>(p) = float2{f[0], f[1]};
+  } else {
+#pragma unroll
+    for (int s = 0; s < S; s += 4) *reinterpret_cast<float4*>(p + s) = float4{f[s], f[s + 1], f[s + 2], f[s + 3]};
+  }
+}
+
+typedef uint32_t u32pair_t __attribute__((ext_vector_type(2)));
+// a: lanes 0-31 of a, then lanes 0-31 of b; b: lanes 32-63 of a, then of b.
+__device__ __forceinline__ void swap32(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+// The same between the odd row of 16 lanes of a and the even one of b, in each half.
+__device__ __forceinline__ void swap16(float& a, float& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+// Lane 16 q + c gets x_q summed over the four rows of lanes (0..3) at c.
+__device__ __forceinline__ float reduce_rows4(float x0, float x1, float x2, float x3) {
+  swap32(x0, x2);
+  swap32(x1, x3);
+  float a = x0 + x2, b = x1 + x3;
+  swap16(a, b);
+  return a + b;
+}
+
+// A tile of TT tokens in LDS: (delta, delta u) of every channel, B and C rows in
+// fp32.  Tokens behind the end hold zeros, which leave the state as it is.
+template <int N, int TT>
+struct Stage {
+  float2 dd[TT][kScanTile];
+  float B[TT][N];
+  float C[TT][N];
+};
+
+// A thread's share of a tile of TT tokens: EL channels of one token (row, col), and
+// a piece of that token's B and C.
+template <typename E, int N, int TT>
+struct Loader {
+  static constexpr int EL = TT / 4;            // 64 channels over 256 / TT threads
+  static constexpr int kPer = 256 / TT;        // threads of a token
+  static constexpr int P = N > kPer ? N / kPer : 1;
+  const ScanParams& p;
+  int64_t bos;
+  int g, d, row, col, piece;
+  bool live, has_z;
+  Raw<E, EL> u, dt, z;
+  E b[P], c[P];
+  float bias[EL], skip[EL];
+
+  __device__ __forceinline__ Loader(const ScanParams& p_, const ChannelTile& ct, int64_t bos_, bool has_z_)
+      : p(p_), bos(bos_), g(ct.g), has_z(has_z_) {
+    row = threadIdx.x / kPer;
+    piece = threadIdx.x % kPer;
+    col = piece * EL;
+    live = col < ct.count;
+    d = ct.d0 + (live ? col : 0);
+    Raw<float, EL> rb, rs;
+    rb.zero();
+    rs.zero();
+    if (p.dt_bias) rb.load(p.dt_bias + d);
+    if (p.Dskip) rs.load(p.Dskip + d);
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+      bias[e] = rb.get(e);
+      skip[e] = rs.get(e);
+    }
+  }
+  __device__ __forceinline__ int64_t token(int64_t t0, int64_t end) const { return bos + min(t0 + row, end - 1); }
+  __device__ __forceinline__ void fetch(int64_t t0, int64_t end) {
+    const int64_t t = token(t0, end);
+    u.load(static_cast<const E*>(p.u) + t * p.D + d);
+    dt.load(static_cast<const E*>(p.dt) + t * p.D + d);
+    if (has_z) z.load(static_cast<const E*>(p.z) + t * p.D + d);
+    const int64_t bc = (t * p.G + g) * N + (piece * P < N ? piece * P : 0);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      b[i] = static_cast<const E*>(p.Bm)[bc + i];
+      c[i] = static_cast<const E*>(p.Cm)[bc + i];
+    }
+  }
+  // `delta` and its derivative `sig` by dt of this thread's channels (zero behind the end)
+  __device__ __forceinline__ void put(Stage<N, TT>& st, int64_t t0, int64_t end, float (&delta)[EL],
+                                      float (&sig)[EL]) const {
+    const bool ok = t0 + row < end, both = ok && live;
+    float2 v[EL];
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+      float x = dt.get(e) + bias[e];
+      sig[e] = 1.f;
+      if (p.softplus) x = softplus_(x, sig[e]);
+      delta[e] = both ? x : 0.f;
+      v[e] = both ? float2{x, x * u.get(e)} : float2{0.f, 0.f};
+    }
+#pragma unroll
+    for (int e = 0; e < EL; e += 2)
+      *reinterpret_cast<float4*>(&st.dd[row][col + e]) = float4{v[e].x, v[e].y, v[e + 1].x, v[e + 1].y};
+    if (piece * P < N) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        st.B[row][piece * P + i] = ok ? IoT<E>::ld(&b[i]) : 0.f;
+        st.C[row][piece * P + i] = ok ? IoT<E>::ld(&c[i]) : 0.f;
+      }
+    }
+  }
+};
+
+}  // namespace scan
+}  // namespace gdn

@@ -399,6 +399,150 @@ gdn_status gdn_epilogue(const gdn_problem* problem, const void* o, const void* z
  * asynchronous on `stream`. */
 gdn_status gdn_device_copy(void* dst, const void* src, size_t bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around and beside the chunked delta rule in a layer: its
+ * single-token step, the short causal convolution in front of it, and the
+ * selective state space scan.  The conventions above hold (ownership, streams,
+ * errors, packed sequences); what differs is said at each entry point.
+ * ------------------------------------------------------------------------- */
+
+/* One token of the gated delta rule for every sequence of a batch (decoding):
+ *     S <- exp(g) S;  e = beta (v - S^T k);  S <- S + k e^T;  o = scale S^T q
+ * with the state updated in place.  `problem` is dense with T == 1 (num_seqs ==
+ * B; GDN_ERR_SHAPE otherwise); chunk, num_segments and precision are checked as
+ * for gdn_recurrent_ref and not used.
+ *   in    : q, k [B,1,H,Dk], v [B,1,H,Dv] (io dtype); g, beta [B,1,H] fp32
+ *   in/out: S [B,H,Dk,Dv] fp32, 16-byte aligned
+ *   out   : o [B,1,H,Dv] (io dtype)
+ * All arithmetic is fp32 whatever the io dtype; o is rounded once.  B H < 2^24
+ * (GDN_ERR_UNSUPPORTED).  No output may
+ * overlap another tensor (GDN_ERR_ALIAS).  No workspace. */
+gdn_status gdn_step(const gdn_problem* problem, const void* q, const void* k, const void* v,
+                    const float* g, const float* beta, float* S, void* o, void* stream);
+
+/* gdn_step with one log-decay per key channel (the recurrence of
+ * gdn_kda_chunk_fwd): g [B,1,H,Dk] fp32, 4-byte aligned. */
+gdn_status gdn_kda_step(const gdn_problem* problem, const void* q, const void* k, const void* v,
+                        const float* g, const float* beta, float* S, void* o, void* stream);
+
+typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+
+/* Short causal depthwise convolution over the tokens of every sequence:
+ *     p_t[c] = bias[c] + sum_{j=0}^{W-1} weight[c][j] x_{t-(W-1)+j}[c]
+ *     y_t = p_t (GDN_ACT_NONE)  or  p_t sigmoid(p_t) (GDN_ACT_SILU)
+ * where the W - 1 rows before a sequence are its state (zero without one).
+ * Tensors: x, y, dy, dx [B,T,C]; state0, state_final, state, dstate_final, dstate0
+ * [N,W-1,C], oldest row first (io dtype; state rows are input rows, kept exactly);
+ * weight, dweight [C,W] and bias, dbias [C] fp32.  All of them 16-byte aligned.
+ * Supported: C a multiple of 8 up to 2^20, W in {2, 3, 4}, N <= 65535, B T < 2^31,
+ * else GDN_ERR_UNSUPPORTED.  Sums are fp32; io outputs are rounded once. */
+typedef struct gdn_conv_problem {
+  int32_t B, T, C, W;
+  int32_t num_seqs;                /* N: == B for dense input, else len(cu_seqlens) - 1     */
+  const int32_t* cu_seqlens_host;  /* host, N + 1 offsets, or NULL (dense)                  */
+  const int32_t* cu_seqlens_dev;   /* device copy of the same N + 1 values, or NULL         */
+  int32_t io_dtype;                /* gdn_dtype                                             */
+  int32_t activation;              /* gdn_activation; another value: GDN_ERR_UNSUPPORTED    */
+} gdn_conv_problem;
+
+/* Forward.  in: x, weight, bias (NULL: none), state0 (NULL: zero);
+ * out: y, state_final (NULL: not wanted; the last W - 1 rows of state0 followed by
+ * the sequence, so a sequence of no tokens keeps state0).  No workspace. */
+gdn_status gdn_conv_fwd(const gdn_conv_problem* problem, const void* x, const float* weight,
+                        const float* bias, const void* state0, void* y, void* state_final,
+                        void* stream);
+
+/* Bytes of workspace gdn_conv_bwd needs (partial sums of dweight and dbias). */
+gdn_status gdn_conv_workspace_size(const gdn_conv_problem* problem, size_t* bytes);
+
+/* Backward: gradients of L = <y, dy> + <state_final, dstate_final>.
+ *   in : x, weight, bias, state0 as gdn_conv_fwd; dy; dstate_final (NULL: zero)
+ *   out: dx, dweight; dbias and dstate0 (NULL: not wanted)
+ * The pre-activation is formed again from x.  dweight and dbias are summed in a
+ * fixed order (bit-identical from call to call). */
+gdn_status gdn_conv_bwd(const gdn_conv_problem* problem, const void* x, const float* weight,
+                        const float* bias, const void* state0, const void* dy,
+                        const void* dstate_final, void* dx, float* dweight, float* dbias,
+                        void* dstate0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (decoding; dense with T == 1): y from the state's
+ * rows and x, then the state shifted by one row in place.  y and state must not
+ * overlap another tensor.  No workspace. */
+gdn_status gdn_conv_step(const gdn_conv_problem* problem, const void* x, const float* weight,
+                         const float* bias, void* state, void* y, void* stream);
+
+/* Selective state space scan: per sequence, channel d and state n, with a state
+ * h[d][n] (initially h0, or zero) and for every token t in order
+ *     delta = softplus(dt_t[d] + dt_bias[d])   (dt_softplus; else dt_t[d] + dt_bias[d])
+ *     h[d][n] <- exp(delta A[d][n]) h[d][n] + delta u_t[d] Bm_t[grp(d)][n]
+ *     s = sum_n Cm_t[grp(d)][n] h[d][n] + Dskip[d] u_t[d]
+ *     y_t[d] = s   or, with z,   s z_t[d] sigmoid(z_t[d])
+ * where grp(d) = d / (D / G).  Tensors: u, dt, z, y [B,T,D], Bm, Cm [B,T,G,N] (io
+ * dtype); A [D,N], Dskip, dt_bias [D], h0, h_final [num_seqs,D,N] fp32.  All of them
+ * 16-byte aligned.  Supported: N in {8, 16, 32, 64}, D / G a multiple of 8, D up to
+ * 2^20, B T G < 2^31, up to 65535 sequences, else GDN_ERR_UNSUPPORTED.  A <= 0 and delta >= 0 are
+ * documented, not checked.  All arithmetic is fp32; io outputs are rounded once. */
+typedef struct gdn_scan_problem {
+  int32_t B, T, D, N, G;
+  int32_t num_seqs;                /* == B for dense input, else len(cu_seqlens) - 1        */
+  const int32_t* cu_seqlens_host;  /* host, num_seqs + 1 offsets, or NULL (dense)           */
+  const int32_t* cu_seqlens_dev;   /* device copy of the same values, or NULL               */
+  int32_t io_dtype;                /* gdn_dtype                                             */
+  int32_t dt_softplus;             /* nonzero: delta = softplus(dt + dt_bias)               */
+} gdn_scan_problem;
+
+typedef enum gdn_scan_pass {
+  GDN_SCAN_FWD = 0,   /* workspace of gdn_scan_fwd and gdn_scan_fwd_save */
+  GDN_SCAN_SAVED = 1, /* the `saved` buffer                              */
+  GDN_SCAN_BWD = 2    /* workspace of gdn_scan_bwd_saved                 */
+} gdn_scan_pass;
+
+/* Bytes of the device buffer `pass` needs (0 is possible; the pointer may then be
+ * NULL); GDN_ERR_UNSUPPORTED for another pass.  The sizes depend on the problem's
+ * sizes and offsets alone. */
+gdn_status gdn_scan_workspace_size(const gdn_scan_problem* problem, int32_t pass, size_t* bytes);
+
+/* Forward.  in: u, dt, A, Bm, Cm; Dskip, z, dt_bias, h0 (each may be NULL: no
+ * skip, no gate, no bias, zero); out: y, h_final (NULL: not wanted; a sequence of
+ * no tokens keeps h0).  Long sequences with few channels are split over the time
+ * axis: segment end states from a zero start are composed in fp32, so results are
+ * those of the serial order up to fp32 rounding. */
+gdn_status gdn_scan_fwd(const gdn_scan_problem* problem, const void* u, const void* dt, const float* A,
+                        const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                        const float* dt_bias, const float* h0, void* y, float* h_final,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Training: gdn_scan_fwd_save computes what gdn_scan_fwd computes (bit-identical)
+ * and keeps the state at regular tokens in `saved` (GDN_SCAN_SAVED bytes, 16-byte
+ * aligned); gdn_scan_bwd_saved forms from it the gradients of
+ *     L = <y, dy> + <h_final, dh_final>.
+ * The problem and the inputs must be those of the save call and `saved` unmodified
+ * (not checked).  `saved` is only read by the backward.
+ *   in : u, dt, A, Bm, Cm, Dskip, z, dt_bias as gdn_scan_fwd; dy; dh_final (NULL: zero)
+ *   out: du, ddt, dBm, dCm (io dtype), dA (fp32); dDskip, dz, ddt_bias, dh0 (NULL:
+ *        not wanted; dDskip may be asked for without Dskip and ddt_bias without dt_bias;
+ *        dz needs z, GDN_ERR_NULL otherwise)
+ * Sums over tokens and channels are fp32 in a fixed order (bit-identical from call
+ * to call). */
+gdn_status gdn_scan_fwd_save(const gdn_scan_problem* problem, const void* u, const void* dt, const float* A,
+                             const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                             const float* dt_bias, const float* h0, void* y, float* h_final,
+                             void* saved, size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                             void* stream);
+gdn_status gdn_scan_bwd_saved(const gdn_scan_problem* problem, const void* u, const void* dt, const float* A,
+                              const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                              const float* dt_bias, const void* dy, const float* dh_final,
+                              const void* saved, size_t saved_bytes, void* du, void* ddt, float* dA,
+                              void* dBm, void* dCm, float* dDskip, void* dz, float* ddt_bias, float* dh0,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (decoding; dense with T == 1): y, and the state h
+ * [B,D,N] fp32 updated in place.  y and h must not overlap another tensor.  No
+ * workspace. */
+gdn_status gdn_scan_step(const gdn_scan_problem* problem, const void* u, const void* dt, const float* A,
+                         const void* Bm, const void* Cm, const float* Dskip, const void* z,
+                         const float* dt_bias, float* h, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

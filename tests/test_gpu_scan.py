@@ -1,0 +1,147 @@
+"""Selective scan on the GPU against its float64 definition: forward (serial and split
+over the time axis), backward from the kept states, single-token step (marked gpu).
+
+Roundings counted per term of T tokens: three per token for the decays and the state
+(the exponential's two and the multiply-add), twice for the gradient's chain, the sums
+over N states and, for dB and dC, over the channels, and 64 for the softplus, the gate
+and the composed segment starts."""
+import pytest
+import torch
+
+import gated_deltanet_chunked_gdn_amd as gdn
+import _layer_oracle as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _inputs(B, T, D, N, G, io, z=True, skip=True, bias=True, state=True, cu=None, seed=0):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    n = B if cu is None else len(cu) - 1
+    a = dict(u=r(B, T, D).to(io), dt=r(B, T, D).to(io), A=-(0.1 + 3 * torch.rand(D, N, generator=gen, device=DEV)),
+             Bm=r(B, T, G, N).to(io), Cm=r(B, T, G, N).to(io), D=r(D) if skip else None, z=r(B, T, D).to(io) if z else None,
+             dt_bias=r(D) - 2 if bias else None)
+    return a, (r(n, D, N) if state else None), r(B, T, D).to(io), (r(n, D, N) if state else None)
+
+
+def _ref(a, h0, cu, softplus, dy=None, dlast=None, size=False):
+    return ref.scan(a["u"], a["dt"], a["A"], a["Bm"], a["Cm"], a["D"], a["z"], a["dt_bias"], h0, cu, softplus, dy, dlast, size)
+
+
+CASES = [  # B, T, D, N, G, cu, z, skip, bias, state
+    (2, 33, 64, 16, 1, None, True, True, True, True),
+    (1, 1, 8, 8, 1, None, True, True, True, True),
+    (2, 50, 72, 16, 1, None, False, True, False, False),
+    (1, 17, 80, 32, 2, None, True, False, True, True),
+    (1, 40, 144, 64, 2, None, True, True, True, True),
+    (3, 16, 24, 8, 3, None, False, False, True, False),
+    (1, 97, 64, 16, 1, [0, 0, 1, 16, 33, 33, 96, 97, 97], True, True, True, True),
+    (1, 60, 40, 64, 1, [0, 31, 60], True, True, True, True),
+    (1, 66, 136, 8, 1, [0, 2, 66], False, True, True, True),
+]
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("B,T,D,N,G,cu,z,skip,bias,state", CASES)
+def test_scan(B, T, D, N, G, cu, z, skip, bias, state, io):
+    a, h0, dy, dl = _inputs(B, T, D, N, G, io, z, skip, bias, state, cu)
+    want = _ref(a, h0, cu, True, dy, dl)
+    size = _ref(a, h0, cu, True, dy, dl, size=True)
+    room = torch.full((1, T + 2, D), 7.0, device=DEV, dtype=io) if B == 1 else None
+    y, h = gdn.scan_fwd(**a, h0=h0, cu_seqlens=cu, out=room[:, 1:T + 1] if room is not None else None)
+    y2, h2, saved = gdn.scan_fwd_save(**a, h0=h0, cu_seqlens=cu)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu)
+    again = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    if room is not None:
+        assert bool((room[:, 0] == 7).all()) and bool((room[:, T + 1] == 7).all())
+    assert torch.equal(y, y2) and torch.equal(h, h2)
+    ref.check("y", y, want["y"], size["y"], 3 * T + N + 64)
+    ref.check("state", h, want["state"], size["state"], 3 * T + 64)
+    for key in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"):
+        if got[key] is None:
+            assert key == "dD" and not skip or key == "dz" and not z or key == "ddt_bias" and not bias
+            continue
+        assert torch.equal(got[key], again[key]), key
+        ref.check(key, got[key], want[key], size[key], 6 * T + N + D + T + 128)
+
+
+@pytest.mark.parametrize("T,D,N,cu", [(1100, 8, 16, None), (2050, 64, 8, None), (1500, 16, 64, [0, 1000, 1003, 1003, 1500])])
+def test_split_over_time(T, D, N, cu):
+    """Few channels and many tokens: several segments, whose starts are composed."""
+    a, h0, dy, dl = _inputs(1, T, D, N, 1, F32, cu=cu)
+    sizes = gdn.scan_buffers(a["u"], a["A"], a["Bm"], cu_seqlens=cu)
+    assert sizes["forward"] > 0  # segment states: the split is taken
+    want = _ref(a, h0, cu, True, dy, dl)
+    size = _ref(a, h0, cu, True, dy, dl, size=True)
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0, cu_seqlens=cu)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    ref.check("y", y, want["y"], size["y"], 3 * T + N + 64)
+    ref.check("state", h, want["state"], size["state"], 3 * T + 64)
+    for key in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"):
+        ref.check(key, got[key], want[key], size[key], 6 * T + N + D + T + 128)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_raw_steps_and_extremes(io):
+    """No softplus; steps of zero (the state stays), large steps (it is forgotten), and
+    softplus arguments from -40 to 40."""
+    a, h0, dy, dl = _inputs(1, 24, 64, 16, 1, io, bias=False)
+    a["dt"] = a["dt"].abs()
+    a["dt"][:, 3] = 0
+    a["dt"][:, 9] = 300
+    for softplus in (False, True):
+        if softplus:
+            a["dt"] = torch.linspace(-40, 40, 24, device=DEV).reshape(1, 24, 1).expand(1, 24, 64).to(io).contiguous()
+        want = _ref(a, h0, None, softplus, dy, dl)
+        size = _ref(a, h0, None, softplus, dy, dl, size=True)
+        y, h, saved = gdn.scan_fwd_save(**a, h0=h0, dt_softplus=softplus)
+        got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, dt_softplus=softplus)
+        ref.check("y", y, want["y"], size["y"], 3 * 24 + 80)
+        ref.check("state", h, want["state"], size["state"], 3 * 24 + 64)
+        for key in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "dh0"):
+            ref.check(key, got[key], want[key], size[key], 7 * 24 + 16 + 64 + 128)
+
+
+def test_a_sequence_of_nan_stays_alone():
+    cu = [0, 10, 30, 41]
+    a, h0, dy, dl = _inputs(1, 41, 64, 16, 1, F32, cu=cu)
+    clean_y, clean_h, saved = gdn.scan_fwd_save(**a, h0=h0, cu_seqlens=cu)
+    clean = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu)
+    for key in ("u", "Bm", "z"):
+        a[key][:, 10:30] = float("nan")
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0, cu_seqlens=cu)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu)
+    for rows in (slice(0, 10), slice(30, 41)):
+        assert torch.equal(y[:, rows], clean_y[:, rows])
+        for key in ("du", "ddt", "dB", "dC", "dz"):
+            assert torch.equal(got[key][:, rows], clean[key][:, rows]), key
+    assert torch.equal(h[[0, 2]], clean_h[[0, 2]]) and torch.equal(got["dh0"][[0, 2]], clean["dh0"][[0, 2]])
+    assert bool(y[:, 10:30].isnan().all())
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("B,D,N,G,z", [(1, 8, 8, 1, True), (3, 72, 16, 1, True), (2, 144, 32, 2, False), (5, 64, 64, 4, True)])
+def test_step(B, D, N, G, z, io):
+    a, h0, _, _ = _inputs(B, 1, D, N, G, io, z)
+    want, size = _ref(a, h0, None, True), _ref(a, h0, None, True, size=True)
+    state = h0.clone()
+    y = gdn.scan_step(**a, state=state)
+    torch.cuda.synchronize()
+    ref.check("y", y, want["y"], size["y"], N + 80)
+    ref.check("state", state, want["state"], size["state"], 80)
+
+
+def test_no_tokens_and_no_sequences():
+    a, h0, dy, dl = _inputs(2, 0, 16, 16, 1, F32)
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl)
+    assert y.shape == (2, 0, 16) and torch.equal(h, h0) and torch.equal(got["dh0"], dl)
+    assert float(got["dA"].abs().max()) == 0 and float(got["ddt_bias"].abs().max()) == 0
+    a, h0, dy, dl = _inputs(0, 4, 16, 16, 1, F32)
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl)
+    assert y.shape == (0, 4, 16) and float(got["dA"].abs().max()) == 0
