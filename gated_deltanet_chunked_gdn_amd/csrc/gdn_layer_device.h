@@ -64,25 +64,17 @@ __device__ __forceinline__ float rcp_(float x) { return __builtin_amdgcn_rcpf(x)
 // 1 / (1 + exp(-x)); 0 and 1 at the infinities
 __device__ __forceinline__ float sigmoid_(float x) { return rcp_(1.f + exp2_(-kLog2e * x)); }
 
-// softplus(x) = max(x, 0) + log1p(exp(-|x|)).  With e = exp(-|x|) in (0, 1] and
-// s = e / (2 + e) <= 1/3, log1p(e) = 2 artanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...);
-// the terms left out (s^18/19 on) are below 2^-32 of the sum.  `sig` gets the
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  With w = 1 + e rounded,
+// log1p(e) = log(w) + (e - (w - 1)) / w up to the square of the second term, the
+// rounding of w; dividing it by w <= 2 is left out: it is at most 2^-24, next to a
+// logarithm that is above w - 1 >= 1/2 of e wherever it is not zero.  `sig` gets the
 // derivative, sigmoid(x).
 __device__ __forceinline__ float softplus_(float x, float& sig) {
-  const float e = exp2_(-kLog2e * fabsf(x));
-  const float s = e * rcp_(2.f + e), q = s * s;
-  float t = 1.f / 17.f;
-  t = fmaf(t, q, 1.f / 15.f);
-  t = fmaf(t, q, 1.f / 13.f);
-  t = fmaf(t, q, 1.f / 11.f);
-  t = fmaf(t, q, 1.f / 9.f);
-  t = fmaf(t, q, 1.f / 7.f);
-  t = fmaf(t, q, 1.f / 5.f);
-  t = fmaf(t, q, 1.f / 3.f);
-  t = fmaf(t, q, 1.f);
-  const float r = rcp_(1.f + e);
+  const float e = exp2_(-kLog2e * fabsf(x)), w = 1.f + e;
+  const float r = rcp_(w);
   sig = x >= 0.f ? r : e * r;
-  return fmaf(s + s, t, fmaxf(x, 0.f));
+  const float l = fmaf(__builtin_amdgcn_logf(w), 0.6931471805599453f, e - (w - 1.f));
+  return l + fmaxf(x, 0.f);
 }
 
 // The sequence that holds packed row t: the last n with cu[n] <= t.

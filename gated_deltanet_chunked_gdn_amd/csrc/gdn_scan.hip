@@ -37,6 +37,7 @@ template <typename E, int N, Mode M>
 __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
   constexpr int S = N / 4;
   constexpr bool FULL = M == kFull;
+  constexpr int EL = Loader<E, N, kTile>::EL;
   const int tid = threadIdx.x, lane = tid & 63, c = (tid >> 6) * 16 + (lane & 15), q = lane >> 4;
   const int n = blockIdx.z, seg = blockIdx.y;
   const ChannelTile ct(p, blockIdx.x);
@@ -47,8 +48,9 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
   const int64_t begin = seg * p.seg_len, end = min(len, begin + p.seg_len);
 
   __shared__ Stage<N, kTile> stage[2];
+  __shared__ ChannelParams cp;
   __shared__ float ybuf[FULL ? 2 : 1][FULL ? kTile : 1][kYStride];
-  __shared__ float sums[FULL ? 1 : 32][kScanTile];
+  __shared__ float sums[FULL ? 1 : 4][kScanTile];
 
   // this lane's states: channel ct.d0 + c, states q S .. q S + S - 1
   const bool chan = c < ct.count;
@@ -73,16 +75,18 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
   }
 
   Loader<E, N, kTile> ld(p, ct, bos, FULL && p.z);
-  float delta[8], sig[8];
+  float delta[EL], sig[EL];
+  cp.fill(p, ct);
+  __syncthreads();
   if (begin < end) {
     ld.fetch(begin, end);
-    ld.put(stage[0], begin, end, delta, sig);
+    ld.put(stage[0], cp, begin, end, delta, sig);
   }
   float dsum = 0.f;  // kSummary: delta of this thread's channel over a quarter of the tokens
   __syncthreads();
   int b = 0;
   for (int64_t t0 = begin; t0 < end; t0 += kTile, b ^= 1) {
-    const Raw<E, 8> ru = ld.u, rz = ld.z;
+    const Raw<E, EL> ru = ld.u, rz = ld.z;
     const bool more = t0 + kTile < end;
     if (more) ld.fetch(t0 + kTile, end);
     const Stage<N, kTile>& st = stage[b];
@@ -90,20 +94,34 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
     for (int t = 0; t < kTile; t += 4) {
       if (FULL && t % kScanBlock == 0 && p.saved && t0 + t < end && chan)
         store_states<S>(p.saved + saved_slot(bos, n, t0 + t) * p.D * N + hd, h);
-      float acc[4];
+      // four tokens' decays and writes first, then the chain through them: a wave
+      // has independent work while an exponential is on its way
+      float a[4][S], w[4][S], acc[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 dd = st.dd[t + j][c];
-        float Bv[S], Cv[S];
+        float Bv[S];
         read_states<S>(&st.B[t + j][q * S], Bv);
-        if (FULL) read_states<S>(&st.C[t + j][q * S], Cv);
-        float y = 0.f;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          h[s] = fmaf(exp2_(dd.x * A2[s]), h[s], dd.y * Bv[s]);
-          if (FULL) y = fmaf(h[s], Cv[s], y);
+          a[j][s] = dd.x * A2[s];
+          w[j][s] = dd.y * Bv[s];
         }
-        acc[j] = y;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int s = 0; s < S; ++s) a[j][s] = exp2_(a[j][s]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float Cv[S];
+        if (FULL) read_states<S>(&st.C[t + j][q * S], Cv);
+        acc[j] = 0.f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          h[s] = fmaf(a[j][s], h[s], w[j][s]);
+          if (FULL) acc[j] = fmaf(h[s], Cv[s], acc[j]);
+        }
       }
       if (FULL) ybuf[b][t + q][c] = reduce_rows4(acc[0], acc[1], acc[2], acc[3]);
     }
@@ -111,22 +129,22 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
 #pragma unroll
       for (int t = 0; t < kTile; t += 4) dsum += st.dd[t + q][c].x;
     }
-    if (more) ld.put(stage[b ^ 1], t0 + kTile, end, delta, sig);
+    if (more) ld.put(stage[b ^ 1], cp, t0 + kTile, end, delta, sig);
     __syncthreads();
     if (FULL) {
       const int64_t t = t0 + ld.row;
       if (t < end && ld.live) {
         const float* const yr = &ybuf[b][ld.row][ld.col];
-        float y[8];
+        float y[EL];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = fmaf(ld.skip[e], ru.get(e), yr[e]);
+        for (int e = 0; e < EL; ++e) {
+          y[e] = fmaf(cp.skip[ld.col + e], ru.get(e), yr[e]);
           if (p.z) {
             const float z = rz.get(e);
             y[e] *= z * sigmoid_(z);
           }
         }
-        store_vec<E, 8>(static_cast<E*>(p.y) + (bos + t) * p.D + ct.d0 + ld.col, y);
+        store_vec<E, EL>(static_cast<E*>(p.y) + (bos + t) * p.D + ct.d0 + ld.col, y);
       }
     }
   }
@@ -203,9 +221,13 @@ hipError_t step_t(const ScanParams& p, hipStream_t s) {
 // Serial needs the fewest instructions; the split runs the state's part of the work
 // twice.  It is taken where the channels alone leave SIMDs idle: segments of at least
 // 128 tokens, as many as give every SIMD two waves (512 workgroups of four).
+#ifndef SEGWG
+#define SEGWG 512
+#endif
+constexpr int64_t kSegGroups = SEGWG;
 ScanSplit scan_split(int64_t max_len, int64_t nseq, int D, int G, int N) {
   const int64_t groups = nseq * scan_tiles(D, G);
-  int64_t segs = std::min<int64_t>((512 + groups - 1) / groups, max_len / 128);
+  int64_t segs = std::min<int64_t>((kSegGroups + groups - 1) / groups, max_len / 128);
   if (segs < 3) return ScanSplit{1, std::max<int64_t>(max_len, 64)};
   const int64_t len = ((max_len + segs - 1) / segs + 63) / 64 * 64;
   return ScanSplit{static_cast<int32_t>((max_len + len - 1) / len), len};

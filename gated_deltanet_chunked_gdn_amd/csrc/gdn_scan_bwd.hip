@@ -27,22 +27,10 @@ using namespace layer;
 using namespace scan;
 
 constexpr int TT = kScanBlock;
-
-// Sum over the four lanes of a quad (channels c % 4), in all four.
-__device__ __forceinline__ float quad_sum(float x) {
-  x += dpp_f32<0xB1, 0xf>(x);  // quad_perm 1,0,3,2
-  x += dpp_f32<0x4E, 0xf>(x);  // quad_perm 2,3,0,1
-  return x;
-}
-// Sum over the lanes of a row that differ in bits 2 and 3 (a channel's four lanes).
-__device__ __forceinline__ float states_sum(float x) {
-  x += dpp_f32<0x128, 0xf>(x);  // row_ror:8
-  x += dpp_f32<0x124, 0xf>(x);  // row_ror:4
-  return x;
-}
-// v[i] summed over the wave's channels: afterwards r[i], i < 4, of a lane in row rr
-// holds v[4 rr + i] (of the lane's states).
-__device__ __forceinline__ void channels_sum16(float (&v)[16], float (&r)[4]) {
+// v[i], i < 16, summed over the wave's 16 channels: lane (cg, c3, q) gets value 4 cg + c3
+// of its quarter q of the states.  Two lane swaps halve the registers while they add the
+// rows of lanes (cg = c / 4), exchanges between the quads halve them over c % 4 = c3.
+__device__ __forceinline__ float channels_sum16(float (&v)[16], bool c_hi, bool c_lo) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     swap32(v[i], v[i + 8]);
@@ -51,17 +39,37 @@ __device__ __forceinline__ void channels_sum16(float (&v)[16], float (&r)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     swap16(v[i], v[i + 4]);
-    r[i] = quad_sum(v[i] + v[i + 4]);
+    v[i] += v[i + 4];
   }
+  const float x = (c_hi ? v[2] : v[0]) + dpp_f32<0x128, 0xf>(c_hi ? v[0] : v[2]);
+  const float y = (c_hi ? v[3] : v[1]) + dpp_f32<0x128, 0xf>(c_hi ? v[1] : v[3]);
+  // the neighbouring quad's: shl:4 into quads 0 and 2, shr:4 into 1 and 3
+  const int give = __float_as_int(c_lo ? x : y);
+  int got = __builtin_amdgcn_update_dpp(0, give, 0x104, 0xf, 0x5, false);
+  got = __builtin_amdgcn_update_dpp(got, give, 0x114, 0xf, 0xa, false);
+  return (c_lo ? y : x) + __int_as_float(got);
+}
+// x[i], i < 4, summed over the four lanes of a channel (a quad): lane q gets x[q].
+__device__ __forceinline__ float states_sum4(const float (&x)[4], bool q_hi, bool q_lo) {
+  const float a = (q_hi ? x[2] : x[0]) + dpp_f32<0x4E, 0xf>(q_hi ? x[0] : x[2]);
+  const float b = (q_hi ? x[3] : x[1]) + dpp_f32<0x4E, 0xf>(q_hi ? x[1] : x[3]);
+  return (q_lo ? b : a) + dpp_f32<0xB1, 0xf>(q_lo ? a : b);
 }
 
-// This lane's place: channel c of the tile's 64, quarter q of its states.
+// The first pass over a block's states sets a sum, the others add to it.
+template <int NG>
+__device__ __forceinline__ void add_sum(float* to, float x, int pass) {
+  *to = NG > 1 && pass > 0 ? *to + x : x;
+}
+
+// This lane's place: channel c of the tile's 64, quarter q of its states (the lanes of a
+// quad share a channel, the four quads of a row hold channels c % 4).
 struct Place {
   int c, q;
   __device__ __forceinline__ Place() {
     const int lane = threadIdx.x & 63;
-    c = (threadIdx.x >> 6) * 16 + (lane >> 4) * 4 + (lane & 3);
-    q = (lane >> 2) & 3;
+    c = (threadIdx.x >> 6) * 16 + (lane >> 2);
+    q = lane & 3;
   }
 };
 
@@ -107,6 +115,7 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
   if (begin >= end) return;
 
   __shared__ Stage<N, TT> st;
+  __shared__ ChannelParams cp;
   __shared__ float dsb[TT][kScanTile];
   __shared__ float sums[4][kScanTile];
   const bool chan = at.c < ct.count;
@@ -122,8 +131,10 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
   BwdLoader<E, N> ld(p, ct, bos);
   int64_t t0 = begin + (end - begin - 1) / TT * TT;
   ld.fetch(t0, end);
+  cp.fill(p, ct);
+  __syncthreads();
   for (; t0 >= begin; t0 -= TT) {
-    ld.put(st, t0, end, delta, sig);
+    ld.put(st, cp, t0, end, delta, sig);
     ld.put_ds(dsb, t0, end, ds);
     if (t0 > begin) ld.fetch(t0 - TT, end);
     __syncthreads();
@@ -146,11 +157,14 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
     p.seg_sum[part * p.D + ct.d0 + tid] = (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
 }
 
-template <typename E, int N>
-__global__ __launch_bounds__(256) void scan_bwd_kernel(ScanParams p) {
+// GATED: dz is wanted, and with it the outputs before the gate.
+template <typename E, int N, bool GATED>
+__global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   constexpr int S = N / 4;
   constexpr int SG = S < 4 ? S : 4;  // states of a lane taken at a time
+  constexpr int NG = S / SG;         // passes over a block
   constexpr int TG = 16 / SG;        // tokens whose dB, dC are summed together
+  constexpr int NW = 4 * SG;         // states of a pass
   constexpr int EL = BwdLoader<E, N>::EL;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const Place at;
@@ -163,162 +177,215 @@ __global__ __launch_bounds__(256) void scan_bwd_kernel(ScanParams p) {
   const int64_t part = static_cast<int64_t>(seg) * p.nseq + n;
 
   __shared__ Stage<N, TT> st;
+  __shared__ ChannelParams cp;
   __shared__ float dsb[TT][kScanTile];
-  __shared__ float gB[TT][kScanTile], Aq[TT][kScanTile], Ch[TT][kScanTile];  // sums over a channel's states
-  __shared__ float bc[4][TT][2][N];                                         // dB, dC of each wave's channels
+  __shared__ float sums[3][TT][kScanTile];              // over a channel's states: G B, A q, C h
+  __shared__ float bc[NG > 1 ? 2 : 1][4][TT][2][NW];    // dB, dC of each wave's channels, a pass
+  __shared__ f32x4_t carry[NG > 1 ? 2 * NG : 1][NG > 1 ? 256 : 1];  // G and dA between a lane's passes
 
+  const bool q_lo = lane & 1, q_hi = lane & 2, c_lo = lane & 4, c_hi = lane & 8;
+  const int v16 = lane >> 2;  // the value of a group of 16 this lane gets
   const bool chan = at.c < ct.count;
-  const int64_t hd = static_cast<int64_t>(ct.d0 + at.c) * N + at.q * S;
-  float A2[S], G[S], dA[S];
-  load_states<S>(p.A + hd, chan, A2);
-  load_states<S>(p.dh_final + static_cast<int64_t>(n) * p.D * N + hd, chan && p.dh_final, G);
+  // the lane's states of pass k: q SG + NW k .. + SG - 1
+  const int64_t hd = static_cast<int64_t>(ct.d0 + at.c) * N + at.q * SG;
+  float A2[SG], G[SG], dA[SG];
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    A2[s] *= kLog2e;
-    dA[s] = 0.f;
-  }
-  for (int g = last; g > seg; --g) {
-    const int64_t pt = static_cast<int64_t>(g) * p.nseq + n;
-    const float sum = chan ? p.seg_sum[pt * p.D + ct.d0 + at.c] : 0.f;
-    float e[S];
-    load_states<S>(p.seg_end + pt * p.D * N + hd, chan, e);
+  for (int k = NG - 1; k >= 0; --k) {
+    load_states<SG>(p.A + hd + k * NW, chan, A2);
+    load_states<SG>(p.dh_final + static_cast<int64_t>(n) * p.D * N + hd + k * NW, chan && p.dh_final, G);
 #pragma unroll
-    for (int s = 0; s < S; ++s) G[s] = fmaf(exp2_(A2[s] * sum), G[s], e[s]);
+    for (int s = 0; s < SG; ++s) {
+      A2[s] *= kLog2e;
+      dA[s] = 0.f;
+    }
+    for (int g = last; g > seg; --g) {
+      const int64_t pt = static_cast<int64_t>(g) * p.nseq + n;
+      const float sum = chan ? p.seg_sum[pt * p.D + ct.d0 + at.c] : 0.f;
+      float e[SG];
+      load_states<SG>(p.seg_end + pt * p.D * N + hd + k * NW, chan, e);
+#pragma unroll
+      for (int s = 0; s < SG; ++s) G[s] = fmaf(exp2_(A2[s] * sum), G[s], e[s]);
+    }
+    if constexpr (NG > 1) {
+      carry[2 * k][tid] = f32x4_t{G[0], G[1], G[2], G[3]};
+      carry[2 * k + 1][tid] = zero4();
+    }
   }
 
   float delta[EL], sig[EL], ds[EL], dD[EL], dbias[EL];
 #pragma unroll
   for (int e = 0; e < EL; ++e) dD[e] = dbias[e] = 0.f;
+  float* const part_bc = p.part_bc + ((static_cast<int64_t>(ct.tile) * p.rows + bos) * p.G + ct.g) * 2 * N;
   BwdLoader<E, N> ld(p, ct, bos);
   int64_t t0 = begin + (end - begin - 1) / TT * TT;
-  if (begin < end) ld.fetch(t0, end);
+  float hn[SG];  // the kept state of the next pass
+  const float* kept = p.saved + saved_slot(bos, n, t0) * p.D * N + hd;
+  if (begin < end) {
+    ld.fetch(t0, end);
+    load_states<SG>(kept, chan, hn);
+  }
+  cp.fill(p, ct);
+  __syncthreads();
   for (; begin < end && t0 >= begin; t0 -= TT) {
-    float h0[S];
-    load_states<S>(p.saved + saved_slot(bos, n, t0) * p.D * N + hd, chan, h0);
-    ld.put(st, t0, end, delta, sig);
+    ld.put(st, cp, t0, end, delta, sig);
     ld.put_ds(dsb, t0, end, ds);
     const Raw<E, EL> ru = ld.u, rz = ld.z, rdy = ld.dy;
     if (t0 > begin) ld.fetch(t0 - TT, end);
     __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < NG; ++k) {
+      float a[TT][SG], hb[TT + 1][SG];  // a token's decay, the state before it
 #pragma unroll
-    for (int s0 = 0; s0 < S; s0 += SG) {
-      float a[TT][SG], hb[TT + 1][SG];  // decay of a token, state before it
-#pragma unroll
-      for (int s = 0; s < SG; ++s) hb[0][s] = h0[s0 + s];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const float2 dd = st.dd[t][at.c];
-        float Bv[SG];
-        read_states<SG>(&st.B[t][at.q * S + s0], Bv);
+      for (int s = 0; s < SG; ++s) hb[0][s] = hn[s];
+      if (k + 1 < NG) {
+        load_states<SG>(kept + (k + 1) * NW, chan, hn);
+      } else if (t0 > begin) {
+        kept -= static_cast<int64_t>(p.D) * N;
+        load_states<SG>(kept, chan, hn);
+      }
+      if constexpr (NG > 1) {
+        const f32x4_t g4 = carry[2 * k][tid], a4 = carry[2 * k + 1][tid];
+        load_states<SG>(p.A + hd + k * NW, chan, A2);
 #pragma unroll
         for (int s = 0; s < SG; ++s) {
-          a[t][s] = exp2_(dd.x * A2[s0 + s]);
-          hb[t + 1][s] = fmaf(a[t][s], hb[t][s], dd.y * Bv[s]);
+          G[s] = g4[s];
+          dA[s] = a4[s];
+          A2[s] *= kLog2e;
         }
       }
+      // indexes the compiler cannot see through: on the way back the staged values are
+      // read again rather than kept in (96) registers
+      int ci = at.c, qi = at.q * SG + k * NW;
 #pragma unroll
-      for (int tg = TT - TG; tg >= 0; tg -= TG) {
-        float vB[16], vC[16];
+      for (int tg = 0; tg < TT; tg += TG) {
+        float v[16];
 #pragma unroll
-        for (int tt = TG - 1; tt >= 0; --tt) {
-          const int t = tg + tt;
-          const float2 dd = st.dd[t][at.c];
-          const float g = dsb[t][at.c];
-          float Bv[SG], Cv[SG];
-          read_states<SG>(&st.B[t][at.q * S + s0], Bv);
-          read_states<SG>(&st.C[t][at.q * S + s0], Cv);
-          float sB = 0.f, sA = 0.f, sC = 0.f;
+        for (int t4 = 0; t4 < TG; t4 += 4) {
+          float sC[4];
 #pragma unroll
-          for (int s = 0; s < SG; ++s) {
-            float& Gs = G[s0 + s];
-            Gs = fmaf(Cv[s], g, Gs);
-            vC[tt * SG + s] = hb[t + 1][s] * g;
-            vB[tt * SG + s] = Gs * dd.y;
-            sC = fmaf(hb[t + 1][s], Cv[s], sC);
-            sB = fmaf(Gs, Bv[s], sB);
-            Gs *= a[t][s];
-            const float qv = Gs * hb[t][s];
-            sA = fmaf(A2[s0 + s], qv, sA);
-            dA[s0 + s] = fmaf(dd.x, qv, dA[s0 + s]);
-          }
-          sB = states_sum(sB);
-          sA = states_sum(sA);
-          sC = states_sum(sC);
-          // the four lanes of a channel hold the same sums: each writes one (or none)
-          float* const to = at.q == 0 ? &gB[t][at.c] : at.q == 1 ? &Aq[t][at.c] : &Ch[t][at.c];
-          const float val = at.q == 0 ? sB : at.q == 1 ? sA : sC;
-          if (at.q < 3) *to = s0 == 0 ? val : *to + val;
-        }
-        float rB[4], rC[4];
-        channels_sum16(vB, rB);
-        channels_sum16(vC, rC);
-        if ((lane & 3) == 0) {
-          // value 4 rr + i of a group is state i % SG of token tg + (4 rr + i) / SG
-          const int rr = lane >> 4;
-          if constexpr (SG == 4) {
-            store_states<4>(&bc[wave][tg + rr][0][at.q * S + s0], rB);
-            store_states<4>(&bc[wave][tg + rr][1][at.q * S + s0], rC);
-          } else {
+          for (int j = 0; j < 4; ++j) {
+            const int t = tg + t4 + j;
+            const float2 dd = st.dd[t][ci];
+            const float g = dsb[t][ci];
+            float Bv[SG], Cv[SG];
+            read_states<SG>(&st.B[t][qi], Bv);
+            if (GATED) read_states<SG>(&st.C[t][qi], Cv);
+            sC[j] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              *reinterpret_cast<float2*>(&bc[wave][tg + 2 * rr + i / 2][0][at.q * S]) = float2{rB[i], rB[i + 1]};
-              *reinterpret_cast<float2*>(&bc[wave][tg + 2 * rr + i / 2][1][at.q * S]) = float2{rC[i], rC[i + 1]};
+            for (int s = 0; s < SG; ++s) {
+              a[t][s] = exp2_(dd.x * A2[s]);
+              hb[t + 1][s] = fmaf(a[t][s], hb[t][s], dd.y * Bv[s]);
+              v[(t4 + j) * SG + s] = hb[t + 1][s] * g;
+              if (GATED) sC[j] = fmaf(hb[t + 1][s], Cv[s], sC[j]);
             }
           }
+          if (GATED) add_sum<NG>(&sums[2][tg + t4 + at.q][at.c], states_sum4(sC, q_hi, q_lo), k);
         }
+        bc[k & (NG > 1)][wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      asm volatile("" : "+v"(ci), "+v"(qi));
+#pragma unroll
+      for (int tg = TT - TG; tg >= 0; tg -= TG) {
+        float v[16];
+#pragma unroll
+        for (int t4 = TG - 4; t4 >= 0; t4 -= 4) {
+          float sB[4], sA[4];
+#pragma unroll
+          for (int j = 3; j >= 0; --j) {
+            const int t = tg + t4 + j;
+            const float2 dd = st.dd[t][ci];
+            const float g = dsb[t][ci];
+            float Bv[SG], Cv[SG];
+            read_states<SG>(&st.B[t][qi], Bv);
+            read_states<SG>(&st.C[t][qi], Cv);
+            sB[j] = sA[j] = 0.f;
+#pragma unroll
+            for (int s = 0; s < SG; ++s) {
+              G[s] = fmaf(Cv[s], g, G[s]);
+              v[(t4 + j) * SG + s] = G[s] * dd.y;
+              sB[j] = fmaf(G[s], Bv[s], sB[j]);
+              G[s] *= a[t][s];
+              const float qv = G[s] * hb[t][s];
+              sA[j] = fmaf(A2[s], qv, sA[j]);
+              dA[s] = fmaf(dd.x, qv, dA[s]);
+            }
+          }
+          add_sum<NG>(&sums[0][tg + t4 + at.q][at.c], states_sum4(sB, q_hi, q_lo), k);
+          add_sum<NG>(&sums[1][tg + t4 + at.q][at.c], states_sum4(sA, q_hi, q_lo), k);
+        }
+        bc[k & (NG > 1)][wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (NG > 1) {
+        carry[2 * k][tid] = f32x4_t{G[0], G[1], G[2], G[3]};
+        carry[2 * k + 1][tid] = f32x4_t{dA[0], dA[1], dA[2], dA[3]};
+      }
+      __syncthreads();
+      // the waves' sums; the next pass writes the other buffer (or, after a barrier
+      // more, this one)
+      if (tid < TT * 2 * NW / 4) {
+        constexpr int kRow4 = 2 * NW / 4, kWave4 = TT * kRow4;
+        const int row = tid / kRow4, x = tid % kRow4;
+        const f32x4_t* const w = reinterpret_cast<const f32x4_t*>(&bc[k & (NG > 1)][0][0][0][0]) + tid;
+        if (t0 + row < end)
+          *reinterpret_cast<f32x4_t*>(part_bc + (t0 + row) * p.G * 2 * N + (x >= NW / 4 ? N : 0) + k * NW + x % (NW / 4) * 4) =
+              (w[0] + w[kWave4]) + (w[2 * kWave4] + w[3 * kWave4]);
       }
     }
-    __syncthreads();
     const int64_t t = t0 + ld.row;
     if (t < end && ld.live) {
       const int64_t off = (bos + t) * p.D + ct.d0 + ld.col;
       float du[EL], ddt[EL], dz[EL];
 #pragma unroll
       for (int e = 0; e < EL; ++e) {
-        const float u = ru.get(e), sB = gB[ld.row][ld.col + e], sA = Aq[ld.row][ld.col + e] * (1.f / kLog2e);
-        du[e] = fmaf(ld.skip[e], ds[e], delta[e] * sB);
+        const float u = ru.get(e), sB = sums[0][ld.row][ld.col + e], sA = sums[1][ld.row][ld.col + e] * (1.f / kLog2e);
+        du[e] = fmaf(cp.skip[ld.col + e], ds[e], delta[e] * sB);
         ddt[e] = fmaf(u, sB, sA) * sig[e];
         dD[e] = fmaf(ds[e], u, dD[e]);
         dbias[e] += ddt[e];
-        if (ld.has_z) {
+        if (GATED) {
           const float z = rz.get(e), sg = sigmoid_(z);
-          dz[e] = rdy.get(e) * fmaf(ld.skip[e], u, Ch[ld.row][ld.col + e]) * (sg * fmaf(z, 1.f - sg, 1.f));
+          dz[e] = rdy.get(e) * fmaf(cp.skip[ld.col + e], u, sums[2][ld.row][ld.col + e]) * (sg * fmaf(z, 1.f - sg, 1.f));
         }
       }
       store_vec<E, EL>(static_cast<E*>(p.du) + off, du);
       store_vec<E, EL>(static_cast<E*>(p.ddt) + off, ddt);
-      if (p.dz) store_vec<E, EL>(static_cast<E*>(p.dz) + off, dz);
-    }
-    for (int i = tid; i < TT * 2 * N; i += 256) {
-      const int row = i / (2 * N), k = i % (2 * N);
-      if (t0 + row < end) {
-        const float* const w = &bc[0][row][0][0] + k;
-        p.part_bc[((static_cast<int64_t>(ct.tile) * p.rows + bos + t0 + row) * p.G + ct.g) * 2 * N + k] =
-            (w[0] + w[TT * 2 * N]) + (w[2 * TT * 2 * N] + w[3 * TT * 2 * N]);
-      }
+      if (GATED) store_vec<E, EL>(static_cast<E*>(p.dz) + off, dz);
     }
   }
   // what goes over the tokens: dA of this lane's states, dD and ddt_bias of the tile's channels
   const int64_t pa = (part * p.D + ct.d0) * (N + 2);
-  if (chan) {
 #pragma unroll
-    for (int s = 0; s < S; ++s) p.part_a[pa + at.c * (N + 2) + at.q * S + s] = dA[s];
+  for (int k = 0; k < NG; ++k) {
+    if constexpr (NG > 1) {
+      const f32x4_t g4 = carry[2 * k][tid], a4 = carry[2 * k + 1][tid];
+#pragma unroll
+      for (int s = 0; s < SG; ++s) {
+        G[s] = g4[s];
+        dA[s] = a4[s];
+      }
+    }
+    if (chan) {
+#pragma unroll
+      for (int s = 0; s < SG; ++s) p.part_a[pa + at.c * (N + 2) + k * NW + at.q * SG + s] = dA[s];
+      if (seg == 0 && p.dh0) store_states<SG>(p.dh0 + static_cast<int64_t>(n) * p.D * N + hd + k * NW, G);
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < EL; ++e) {
-    gB[ld.row][ld.col + e] = dD[e];
-    Aq[ld.row][ld.col + e] = dbias[e];
+    sums[0][ld.row][ld.col + e] = dD[e];
+    sums[1][ld.row][ld.col + e] = dbias[e];
   }
   __syncthreads();
   if (tid < 2 * kScanTile) {
     const int c = tid % kScanTile, k = tid / kScanTile;
     float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < TT; ++r) sum += k ? Aq[r][c] : gB[r][c];
+    for (int r = 0; r < TT; ++r) sum += sums[k][r][c];
     if (c < ct.count) p.part_a[pa + c * (N + 2) + N + k] = sum;
   }
-  if (seg == 0 && p.dh0 && chan) store_states<S>(p.dh0 + static_cast<int64_t>(n) * p.D * N + hd, G);
 }
 
 // dB and dC: the channel tiles' sums in order.
@@ -360,7 +427,10 @@ hipError_t bwd_t(const ScanParams& p, hipStream_t s) {
   if (nseq > 0) {
     if (p.segs > 1)
       hipLaunchKernelGGL((scan_bwd_summary_kernel<E, N>), dim3(tiles, p.segs - 1, nseq), dim3(256), 0, s, p);
-    hipLaunchKernelGGL((scan_bwd_kernel<E, N>), dim3(tiles, p.segs, nseq), dim3(256), 0, s, p);
+    if (p.dz)
+      hipLaunchKernelGGL((scan_bwd_kernel<E, N, true>), dim3(tiles, p.segs, nseq), dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((scan_bwd_kernel<E, N, false>), dim3(tiles, p.segs, nseq), dim3(256), 0, s, p);
   }
   const int64_t items = p.rows * p.G * 2 * N;
   if (items > 0)

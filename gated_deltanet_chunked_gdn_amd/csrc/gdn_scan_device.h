@@ -13,7 +13,10 @@ namespace scan {
 
 using namespace layer;
 
-constexpr int kTile = 32;     // tokens staged at a time
+#ifndef KT
+#define KT 16
+#endif
+constexpr int kTile = KT;     // tokens staged at a time
 constexpr int kYStride = 80;  // row stride of output tiles: the four token rows a wave writes fall in other banks
 
 // A workgroup's channels d0 .. d0 + count - 1, all of group g.
@@ -95,6 +98,19 @@ struct Stage {
   float C[TT][N];
 };
 
+// dt_bias and D of the tile's channels (zero where there is none), in LDS: registers
+// are scarce across a tile.  Filled by one workgroup barrier before its use.
+struct ChannelParams {
+  float bias[kScanTile], skip[kScanTile];
+  __device__ __forceinline__ void fill(const ScanParams& p, const ChannelTile& ct) {
+    const int c = threadIdx.x;
+    if (c < kScanTile) {
+      bias[c] = p.dt_bias && c < ct.count ? p.dt_bias[ct.d0 + c] : 0.f;
+      skip[c] = p.Dskip && c < ct.count ? p.Dskip[ct.d0 + c] : 0.f;
+    }
+  }
+};
+
 // A thread's share of a tile of TT tokens: EL channels of one token (row, col), and
 // a piece of that token's B and C.
 template <typename E, int N, int TT>
@@ -108,7 +124,6 @@ struct Loader {
   bool live, has_z;
   Raw<E, EL> u, dt, z;
   E b[P], c[P];
-  float bias[EL], skip[EL];
 
   __device__ __forceinline__ Loader(const ScanParams& p_, const ChannelTile& ct, int64_t bos_, bool has_z_)
       : p(p_), bos(bos_), g(ct.g), has_z(has_z_) {
@@ -117,16 +132,6 @@ struct Loader {
     col = piece * EL;
     live = col < ct.count;
     d = ct.d0 + (live ? col : 0);
-    Raw<float, EL> rb, rs;
-    rb.zero();
-    rs.zero();
-    if (p.dt_bias) rb.load(p.dt_bias + d);
-    if (p.Dskip) rs.load(p.Dskip + d);
-#pragma unroll
-    for (int e = 0; e < EL; ++e) {
-      bias[e] = rb.get(e);
-      skip[e] = rs.get(e);
-    }
   }
   __device__ __forceinline__ int64_t token(int64_t t0, int64_t end) const { return bos + min(t0 + row, end - 1); }
   __device__ __forceinline__ void fetch(int64_t t0, int64_t end) {
@@ -142,17 +147,24 @@ struct Loader {
     }
   }
   // `delta` and its derivative `sig` by dt of this thread's channels (zero behind the end)
-  __device__ __forceinline__ void put(Stage<N, TT>& st, int64_t t0, int64_t end, float (&delta)[EL],
-                                      float (&sig)[EL]) const {
+  __device__ __forceinline__ void put(Stage<N, TT>& st, const ChannelParams& cp, int64_t t0, int64_t end,
+                                      float (&delta)[EL], float (&sig)[EL]) const {
     const bool ok = t0 + row < end, both = ok && live;
     float2 v[EL];
 #pragma unroll
     for (int e = 0; e < EL; ++e) {
-      float x = dt.get(e) + bias[e];
+      delta[e] = dt.get(e) + cp.bias[col + e];
       sig[e] = 1.f;
-      if (p.softplus) x = softplus_(x, sig[e]);
-      delta[e] = both ? x : 0.f;
-      v[e] = both ? float2{x, x * u.get(e)} : float2{0.f, 0.f};
+    }
+    if (p.softplus) {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) delta[e] = softplus_(delta[e], sig[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < EL; ++e) {
+      delta[e] = both ? delta[e] : 0.f;
+      const float du = delta[e] * u.get(e);
+      v[e] = float2{delta[e], both ? du : 0.f};
     }
 #pragma unroll
     for (int e = 0; e < EL; e += 2)
