@@ -102,7 +102,7 @@ struct ScanSplit {
   int32_t segs;
   int64_t len;
 };
-ScanSplit scan_split(int64_t max_len, int64_t nseq, int D, int G, int N);
+ScanSplit scan_split(int64_t max_len, int64_t nseq, int D, int G);
 hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
 // state in p.h_final, updated in place

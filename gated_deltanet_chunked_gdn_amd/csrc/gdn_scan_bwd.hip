@@ -179,8 +179,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   __shared__ Stage<N, TT> st;
   __shared__ ChannelParams cp;
   __shared__ float dsb[TT][kScanTile];
-  __shared__ float sums[3][TT][kScanTile];              // over a channel's states: G B, A q, C h
-  __shared__ float bc[NG > 1 ? 2 : 1][4][TT][2][NW];    // dB, dC of each wave's channels, a pass
+  __shared__ float sums[3][TT][kScanTile];   // over a channel's states: G B, A q, C h
+  __shared__ float bc[4][TT][2][NW];         // dB, dC of each wave's channels, a pass
   __shared__ f32x4_t carry[NG > 1 ? 2 * NG : 1][NG > 1 ? 256 : 1];  // G and dA between a lane's passes
 
   const bool q_lo = lane & 1, q_hi = lane & 2, c_lo = lane & 4, c_hi = lane & 8;
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
           }
           if (GATED) add_sum<NG>(&sums[2][tg + t4 + at.q][at.c], states_sum4(sC, q_hi, q_lo), k);
         }
-        bc[k & (NG > 1)][wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
+        bc[wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
         __builtin_amdgcn_sched_barrier(0);
       }
       asm volatile("" : "+v"(ci), "+v"(qi));
@@ -314,7 +314,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
           add_sum<NG>(&sums[0][tg + t4 + at.q][at.c], states_sum4(sB, q_hi, q_lo), k);
           add_sum<NG>(&sums[1][tg + t4 + at.q][at.c], states_sum4(sA, q_hi, q_lo), k);
         }
-        bc[k & (NG > 1)][wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
+        bc[wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (NG > 1) {
@@ -322,16 +322,16 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
         carry[2 * k + 1][tid] = f32x4_t{dA[0], dA[1], dA[2], dA[3]};
       }
       __syncthreads();
-      // the waves' sums; the next pass writes the other buffer (or, after a barrier
-      // more, this one)
+      // the waves' sums
       if (tid < TT * 2 * NW / 4) {
         constexpr int kRow4 = 2 * NW / 4, kWave4 = TT * kRow4;
         const int row = tid / kRow4, x = tid % kRow4;
-        const f32x4_t* const w = reinterpret_cast<const f32x4_t*>(&bc[k & (NG > 1)][0][0][0][0]) + tid;
+        const f32x4_t* const w = reinterpret_cast<const f32x4_t*>(&bc[0][0][0][0]) + tid;
         if (t0 + row < end)
           *reinterpret_cast<f32x4_t*>(part_bc + (t0 + row) * p.G * 2 * N + (x >= NW / 4 ? N : 0) + k * NW + x % (NW / 4) * 4) =
               (w[0] + w[kWave4]) + (w[2 * kWave4] + w[3 * kWave4]);
       }
+      if (k + 1 < NG) __syncthreads();
     }
     const int64_t t = t0 + ld.row;
     if (t < end && ld.live) {
@@ -443,13 +443,6 @@ hipError_t bwd_t(const ScanParams& p, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_scan_bwd(const ScanParams& p, int N, bool bf16, hipStream_t s) {
-  switch (N) {
-    case 8: return bf16 ? bwd_t<uint16_t, 8>(p, s) : bwd_t<float, 8>(p, s);
-    case 16: return bf16 ? bwd_t<uint16_t, 16>(p, s) : bwd_t<float, 16>(p, s);
-    case 32: return bf16 ? bwd_t<uint16_t, 32>(p, s) : bwd_t<float, 32>(p, s);
-    default: return bf16 ? bwd_t<uint16_t, 64>(p, s) : bwd_t<float, 64>(p, s);
-  }
-}
+hipError_t launch_scan_bwd(const ScanParams& p, int N, bool bf16, hipStream_t s) { GDN_SCAN_DISPATCH(bwd_t) }
 
 }  // namespace gdn

@@ -8,6 +8,15 @@
 #include "gdn_layer.h"
 #include "gdn_layer_device.h"
 
+// The instance for a state count (8, 16, 32, 64) and an io dtype.
+#define GDN_SCAN_DISPATCH(fn)                                                     \
+  switch (N) {                                                                    \
+    case 8: return bf16 ? fn<uint16_t, 8>(p, s) : fn<float, 8>(p, s);             \
+    case 16: return bf16 ? fn<uint16_t, 16>(p, s) : fn<float, 16>(p, s);          \
+    case 32: return bf16 ? fn<uint16_t, 32>(p, s) : fn<float, 32>(p, s);          \
+    default: return bf16 ? fn<uint16_t, 64>(p, s) : fn<float, 64>(p, s);          \
+  }
+
 namespace gdn {
 namespace scan {
 

@@ -28,6 +28,12 @@ import torch
 from . import _native as nat
 from .ops import _IO, SeqLens, _seqlens
 
+# the current device and the raw current stream, without building Python objects: a
+# single-token call is a few microseconds
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _ACT = {None: nat.GDN_ACT_NONE, "none": nat.GDN_ACT_NONE, "silu": nat.GDN_ACT_SILU}
 
 
@@ -45,19 +51,17 @@ def _want(t, shape, dtype, device, name, optional=False):
     """A contiguous tensor of this shape, dtype and device, as an address (None for an
     absent optional one).  A host pointer that reached a kernel would be a GPU memory
     fault, which the C ABI cannot detect."""
-    if t is None:
-        if optional:
-            return None
-        raise TypeError(f"{name} must be a torch.Tensor")
+    if t is None and optional:
+        return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
+        return t.data_ptr()
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} (got {tuple(t.shape)})")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} (got {tuple(t.shape)})")
 
 
 def _out(out, like, device, name):
@@ -70,12 +74,12 @@ def _out(out, like, device, name):
 def _call(device, name, *args):
     """The library call on the device's current stream, with that device current."""
     fn = getattr(nat.load(), name)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, stream)
+    index = device.index
+    if index == _current_device():
+        st = fn(*args, _current_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, stream)
+            st = fn(*args, _current_stream(index))
     if st:
         nat.check(st, name)
 
