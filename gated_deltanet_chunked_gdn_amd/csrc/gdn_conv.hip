@@ -1,8 +1,8 @@
 // Short causal depthwise convolution on gfx950: forward, backward and the
 // single-token step.
 //     p_t = bias + sum_j w_j x_{t-(W-1)+j},  y = p or p sigmoid(p)
-// A few multiply-adds a value, so every pass is HBM-bound: each thread owns one
-// 16-byte vector of channels and walks a run of tokens with the last W - 1 rows in
+// A few multiply-adds a value, so every pass is HBM-bound: each thread owns a
+// vector of channels and walks a run of tokens with the last W - 1 rows in
 // registers; the rows of the run are loaded together.  A run that crosses from one
 // packed sequence into the next starts again from the next one's state.
 #include <hip/hip_runtime.h>
@@ -17,11 +17,14 @@ using namespace layer;
 
 template <typename E>
 constexpr int kVec = 16 / static_cast<int>(sizeof(E));
+// Channels of a thread in the forward: eight-byte bf16 loads leave registers for more
+// waves (runs of eight rows of 4 x 4096 x 2048 bf16, 134 MB: 29 us, 4.6 TB/s; 33 us
+// with eight channels).
+constexpr int kWalkV = 4;
 
 // One thread's channels: weights, bias, and the reading of input and state rows.
-template <typename E, int W>
+template <typename E, int W, int V>
 struct Chan {
-  static constexpr int V = kVec<E>;
   float w[W][V], b[V];
   __device__ __forceinline__ void load(const ConvParams& p, int c0) {
     Raw<float, V * W> rw;
@@ -97,7 +100,7 @@ __device__ __forceinline__ void final_row(const ConvParams& p, int64_t item) {
 // kept rows.
 template <typename E, int W, int RT>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int64_t walkers, int64_t items) {
-  constexpr int V = kVec<E>;
+  constexpr int V = kWalkV;
   int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (id >= walkers) {
     id -= walkers;
@@ -111,7 +114,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvParams p, int64_t wal
   Raw<E, V> raw[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) raw[i].load(x + min(t0 + i, p.rows - 1) * p.C);
-  Chan<E, W> ch;
+  Chan<E, W, V> ch;
   ch.load(p, c0);
   int n = seq_of_row(p.seq, p.N, t0);
   int64_t bos, len;
@@ -153,7 +156,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvParams p, int64_t it
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j].load(state + static_cast<int64_t>(j) * p.C);
   rows[W - 1].load(static_cast<const E*>(p.x) + n * p.C + c0);
-  Chan<E, W> ch;
+  Chan<E, W, V> ch;
   ch.load(p, c0);
   float win[W - 1][V], xf[V], y[V];
 #pragma unroll
@@ -180,20 +183,25 @@ __device__ __forceinline__ float silu_grad(float p, float dy) {
 
 // Backward.  dx_s = sum_k w_{W-1-k} dp_{s+k} over the tokens s + k of s's sequence
 // (a row still open at token t is held in `open`), plus dstate_final on kept rows.
-// A workgroup covers 512 rows of 8 vectors: 32 runs of 16 rows, each followed by
-// W - 1 rows of the next run for their dp alone.  Its sums of dp x and dp are
-// reduced over the runs (lanes, then waves) and written once; a second kernel adds
+// A thread walks a run of 32 rows of four channels (and W - 1 rows of the next run for
+// their dp alone), two rows at a time with the next two in flight; four channels
+// rather than eight halve the registers of the weights and their gradients, for four
+// waves a SIMD (4 x 4096 x 2048 bf16, 201 MB: 51 us, 3.9 TB/s; with eight channels and two
+// waves 80 us, with four rows ahead and three waves 61 us).  A workgroup covers 512 rows of 64 channels: its sums of dp x and dp are
+// reduced over the runs (lanes, then waves) and written once, and a second kernel adds
 // the workgroups' sums in order.
+constexpr int kBwdV = 4, kBwdRun = 32, kBwdLanes = 16, kBwdAhead = 2;
+static_assert(256 / kBwdLanes * kBwdRun == kConvBwdRows, "rows of a workgroup");
+
 template <typename E, int W>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
-  constexpr int V = kVec<E>, RT = 16;
-  static_assert(RT * 32 == kConvBwdRows, "rows of a workgroup");
-  const int tid = threadIdx.x, lane = tid & 7, wave = tid >> 6;
+__global__ __launch_bounds__(256, sizeof(E) == 2 ? 4 : 3) void conv_bwd_kernel(ConvParams p) {
+  constexpr int V = kBwdV;
+  const int tid = threadIdx.x, lane = tid % kBwdLanes, wave = tid >> 6;
   const int nv = p.C / V;
-  const int vec = blockIdx.y * 8 + lane;
+  const int vec = blockIdx.y * kBwdLanes + lane;
   const int c0 = min(vec, nv - 1) * V;
   const bool live = vec < nv;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kConvBwdRows + (tid >> 3) * RT;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kConvBwdRows + tid / kBwdLanes * kBwdRun;
   float dw[W][V], db[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
@@ -202,19 +210,34 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
     db[e] = 0.f;
   }
   if (live && t0 < p.rows) {
-    Chan<E, W> ch;
+    const E* const x = static_cast<const E*>(p.x) + c0;
+    const E* const dy = static_cast<const E*>(p.dy) + c0;
+    E* const dx = static_cast<E*>(p.dx) + c0;
+    const int64_t own_end = min(t0 + kBwdRun, p.rows), last = min(t0 + kBwdRun + W - 1, p.rows);
+    Raw<E, V> rx[kBwdAhead], rd[kBwdAhead];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+      for (int i = 0; i < kBwdAhead; ++i) {
+        const int64_t at = min(t + i, last - 1) * p.C;
+        rx[i].load(x + at);
+        rd[i].load(dy + at);
+      }
+    };
+    fetch(t0);
+    Chan<E, W, V> ch;
     ch.load(p, c0);
     int n = seq_of_row(p.seq, p.N, t0);
     int64_t bos, len;
     chunk::seq_range(p.seq, n, bos, len);
     float win[W - 1][V], open[W - 1][V];  // open[k]: dx of row t - 1 - k so far
     ch.window(p, c0, n, bos, t0 - bos, win);
+    auto reset = [&] {
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k)
+      for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) open[k][e] = 0.f;
-    const int64_t own_end = min(t0 + RT, p.rows), last = min(t0 + RT + W - 1, p.rows);
-    E* const dx = static_cast<E*>(p.dx) + c0;
+        for (int e = 0; e < V; ++e) open[k][e] = 0.f;
+    };
+    reset();
     // rows end - 1 - k of a sequence that ends before row `end`
     auto flush = [&](int64_t end) {
 #pragma unroll
@@ -230,94 +253,89 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvParams p) {
         store_vec<E, V>(dx + s * p.C, open[k]);
       }
     };
-    int64_t t = t0;
-    for (; t < last; ++t) {
-      if (t == bos + len) {
-        flush(t);
-        if (t >= own_end) break;
-        do chunk::seq_range(p.seq, ++n, bos, len);
-        while (len == 0);
-        ch.window(p, c0, n, bos, 0, win);
+    bool done = false;
+#pragma unroll 1
+    for (int64_t tb = t0; tb < last && !done; tb += kBwdAhead) {
+      Raw<E, V> cx[kBwdAhead], cd[kBwdAhead];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-          for (int e = 0; e < V; ++e) open[k][e] = 0.f;
+      for (int i = 0; i < kBwdAhead; ++i) {
+        cx[i] = rx[i];
+        cd[i] = rd[i];
       }
-      Raw<E, V> rx, rd;
-      rx.load(static_cast<const E*>(p.x) + t * p.C + c0);
-      rd.load(static_cast<const E*>(p.dy) + t * p.C + c0);
-      float xf[V], pre[V], dp[V], done[V];
+      if (tb + kBwdAhead < last) fetch(tb + kBwdAhead);
 #pragma unroll
-      for (int e = 0; e < V; ++e) xf[e] = rx.get(e);
-      ch.pre(win, xf, pre);
+      for (int i = 0; i < kBwdAhead; ++i) {
+        const int64_t t = tb + i;
+        if (t >= last) break;
+        if (t == bos + len) {
+          flush(t);
+          if (t >= own_end) {
+            done = true;
+            break;
+          }
+          do chunk::seq_range(p.seq, ++n, bos, len);
+          while (len == 0);
+          ch.window(p, c0, n, bos, 0, win);
+          reset();
+        }
+        float xf[V], pre[V], dp[V], out[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        dp[e] = p.silu ? silu_grad(pre[e], rd.get(e)) : rd.get(e);
-        done[e] = fmaf(ch.w[0][e], dp[e], open[W - 2][e]);
-#pragma unroll
-        for (int k = W - 2; k > 0; --k) open[k][e] = fmaf(ch.w[W - 1 - k][e], dp[e], open[k - 1][e]);
-        open[0][e] = ch.w[W - 1][e] * dp[e];
-      }
-      const int64_t s = t - (W - 1);
-      if (s >= t0 && s >= bos) store_vec<E, V>(dx + s * p.C, done);
-      if (t < own_end) {
+        for (int e = 0; e < V; ++e) xf[e] = cx[i].get(e);
+        ch.pre(win, xf, pre);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+          dp[e] = p.silu ? silu_grad(pre[e], cd[i].get(e)) : cd[i].get(e);
+          out[e] = fmaf(ch.w[0][e], dp[e], open[W - 2][e]);
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(dp[e], win[j][e], dw[j][e]);
-          dw[W - 1][e] = fmaf(dp[e], xf[e], dw[W - 1][e]);
-          db[e] += dp[e];
+          for (int k = W - 2; k > 0; --k) open[k][e] = fmaf(ch.w[W - 1 - k][e], dp[e], open[k - 1][e]);
+          open[0][e] = ch.w[W - 1][e] * dp[e];
         }
+        const int64_t s = t - (W - 1);
+        if (s >= t0 && s >= bos) store_vec<E, V>(dx + s * p.C, out);
+        if (t < own_end) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) dw[j][e] = fmaf(dp[e], win[j][e], dw[j][e]);
+            dw[W - 1][e] = fmaf(dp[e], xf[e], dw[W - 1][e]);
+            db[e] += dp[e];
+          }
+        }
+        ch.shift(win, xf);
       }
-      ch.shift(win, xf);
     }
-    if (t == last && t == bos + len) flush(t);
+    if (!done && last == bos + len) flush(last);
   }
-  __shared__ float red[4][8][(W + 1) * V];
+  __shared__ float red[4][kBwdLanes][(W + 1) * V];
 #pragma unroll
   for (int j = 0; j <= W; ++j)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       float s = j < W ? dw[j < W ? j : 0][e] : db[e];
 #pragma unroll
-      for (int m = 8; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
-      if ((tid & 63) < 8) red[wave][lane][j * V + e] = s;
+      for (int m = kBwdLanes; m < 64; m <<= 1) s += __shfl_xor(s, m, 64);
+      if ((tid & 63) < kBwdLanes) red[wave][lane][j * V + e] = s;
     }
   __syncthreads();
-  for (int i = tid; i < 8 * (W + 1) * V; i += 256) {
-    const int l = i / ((W + 1) * V), je = i % ((W + 1) * V), j = je / V, e = je % V;
-    const int c = (blockIdx.y * 8 + l) * V + e;
+  for (int i = tid; i < kBwdLanes * (W + 1) * V; i += 256) {
+    const int l = i / V % kBwdLanes, e = i % V, j = i / (V * kBwdLanes), je = j * V + e;
+    const int c = (blockIdx.y * kBwdLanes + l) * V + e;
     if (c < p.C)
       p.ws[(static_cast<int64_t>(blockIdx.x) * (W + 1) + j) * p.C + c] =
           (red[0][l][je] + red[1][l][je]) + (red[2][l][je] + red[3][l][je]);
   }
 }
 
-template <int W>
-__global__ __launch_bounds__(256) void conv_bwd_sum_kernel(ConvParams p, int64_t blocks) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= static_cast<int64_t>(W + 1) * p.C) return;
-  const int j = static_cast<int>(i / p.C), c = static_cast<int>(i % p.C);
-  float s = 0.f;
-  for (int64_t b = 0; b < blocks; ++b) s += p.ws[b * (W + 1) * p.C + i];
-  if (j < W)
-    p.dweight[static_cast<int64_t>(c) * W + j] = s;
-  else if (p.dbias)
-    p.dbias[c] = s;
-}
-
 // dstate0: row r of the state (position r - (W-1)) meets weight j at token r - j.
 template <typename E, int W>
-__global__ __launch_bounds__(256) void conv_dstate0_kernel(ConvParams p, int64_t items) {
+__device__ __forceinline__ void dstate0_rows(const ConvParams& p, int64_t item) {
   constexpr int V = kVec<E>;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= items) return;
   const int nv = p.C / V;
-  const int c0 = static_cast<int>(id % nv) * V;
-  const int n = static_cast<int>(id / nv);
+  const int c0 = static_cast<int>(item % nv) * V;
+  const int n = static_cast<int>(item / nv);
   int64_t bos, len;
   chunk::seq_range(p.seq, n, bos, len);
-  Chan<E, W> ch;
+  Chan<E, W, V> ch;
   ch.load(p, c0);
   float win[W - 1][V], g[W - 1][V];
   ch.window(p, c0, n, bos, 0, win);
@@ -359,14 +377,38 @@ __global__ __launch_bounds__(256) void conv_dstate0_kernel(ConvParams p, int64_t
     store_vec<E, V>(static_cast<E*>(p.dstate0) + (static_cast<int64_t>(n) * (W - 1) + r) * p.C + c0, g[r]);
 }
 
+// dweight and dbias from the workgroups' sums, eight of them in flight; the threads
+// behind the first `sums` form dstate0.
+template <typename E, int W>
+__global__ __launch_bounds__(256) void conv_bwd_finish_kernel(ConvParams p, int64_t blocks, int64_t sums, int64_t items) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= sums) {
+    if (i - sums < items) dstate0_rows<E, W>(p, i - sums);
+    return;
+  }
+  const int64_t n = static_cast<int64_t>(W + 1) * p.C;
+  if (i >= n) return;
+  float part[8] = {};
+  int64_t b = 0;
+  for (; b + 8 <= blocks; b += 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[k] += p.ws[(b + k) * n + i];
+  }
+  for (; b < blocks; ++b) part[0] += p.ws[b * n + i];
+  const float s = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+  const int j = static_cast<int>(i / p.C), c = static_cast<int>(i % p.C);
+  if (j < W)
+    p.dweight[static_cast<int64_t>(c) * W + j] = s;
+  else if (p.dbias)
+    p.dbias[c] = s;
+}
+
 unsigned blocks_of(int64_t threads) { return static_cast<unsigned>((threads + 255) / 256); }
 
 template <typename E, int W, int RT>
 hipError_t fwd_t(const ConvParams& p, hipStream_t s) {
-  const int nv = p.C / kVec<E>;
-  // whole workgroups of walkers first
-  const int64_t walkers = (p.rows + RT - 1) / RT * nv;
-  const int64_t items = p.state_final ? static_cast<int64_t>(p.N) * (W - 1) * nv : 0;
+  const int64_t walkers = (p.rows + RT - 1) / RT * (p.C / kWalkV);
+  const int64_t items = p.state_final ? static_cast<int64_t>(p.N) * (W - 1) * (p.C / kVec<E>) : 0;
   if (walkers + items == 0) return hipSuccess;
   hipLaunchKernelGGL((conv_fwd_kernel<E, W, RT>), dim3(blocks_of(walkers + items)), dim3(256), 0, s, p, walkers, items);
   return hipGetLastError();
@@ -374,24 +416,22 @@ hipError_t fwd_t(const ConvParams& p, hipStream_t s) {
 
 template <typename E, int W>
 hipError_t fwd_w(const ConvParams& p, hipStream_t s) {
-  // runs of 16 rows read each row 1 + (W-1)/16 times; below two waves a SIMD that
-  // way, runs of 4 spread a short prompt over more of the chip
-  if (p.rows * (p.C / kVec<E>) / 16 < 2 * 1024 * 64) return fwd_t<E, W, 4>(p, s);
-  return fwd_t<E, W, 16>(p, s);
+  // runs of eight rows read each row 1 + (W-1)/8 times, from the cache where two runs
+  // meet; below one wave a SIMD that way, runs of two spread a short prompt over more
+  // of the chip
+  if (p.rows * (p.C / kWalkV) / 8 < 1024 * 64) return fwd_t<E, W, 2>(p, s);
+  return fwd_t<E, W, 8>(p, s);
 }
 
 template <typename E, int W>
 hipError_t bwd_w(const ConvParams& p, hipStream_t s) {
-  const int nv = p.C / kVec<E>;
   const int64_t blocks = conv_bwd_blocks(p.rows);
   if (blocks > 0)
-    hipLaunchKernelGGL((conv_bwd_kernel<E, W>), dim3(static_cast<unsigned>(blocks), (nv + 7) / 8), dim3(256), 0, s, p);
-  hipLaunchKernelGGL((conv_bwd_sum_kernel<W>), dim3(blocks_of(static_cast<int64_t>(W + 1) * p.C)), dim3(256), 0, s, p,
-                     blocks);
-  if (p.dstate0 && p.N > 0) {
-    const int64_t items = static_cast<int64_t>(p.N) * nv;
-    hipLaunchKernelGGL((conv_dstate0_kernel<E, W>), dim3(blocks_of(items)), dim3(256), 0, s, p, items);
-  }
+    hipLaunchKernelGGL((conv_bwd_kernel<E, W>),
+                       dim3(static_cast<unsigned>(blocks), (p.C / kBwdV + kBwdLanes - 1) / kBwdLanes), dim3(256), 0, s, p);
+  const int64_t sums = static_cast<int64_t>(blocks_of(static_cast<int64_t>(W + 1) * p.C)) * 256;
+  const int64_t items = p.dstate0 ? static_cast<int64_t>(p.N) * (p.C / kVec<E>) : 0;
+  hipLaunchKernelGGL((conv_bwd_finish_kernel<E, W>), dim3(blocks_of(sums + items)), dim3(256), 0, s, p, blocks, sums, items);
   return hipGetLastError();
 }
 
