@@ -80,8 +80,8 @@ gdn_status step(const gdn_problem* p, const void* q, const void* k, const void* 
   gdn_status st = gdn_workspace_size(p, GDN_PASS_RECURRENT_FWD, &unused);
   if (st != GDN_OK) return st;
   if (p->T != 1 || p->cu_seqlens_host) return GDN_ERR_SHAPE;
-  // one workgroup of 256 threads per (head, column tile), counted in 32 bits along a grid axis
-  if (static_cast<int64_t>(p->B) * p->H >= 1 << 24) return GDN_ERR_UNSUPPORTED;
+  // workgroups of 256 threads, up to Dv / 32 of them a head, counted in 32-bit threads
+  if (static_cast<int64_t>(p->B) * p->H * ((p->Dv + 31) / 32) >= 1 << 24) return GDN_ERR_UNSUPPORTED;
   const size_t io = p->io_dtype == GDN_BF16 ? 2 : 4;
   const size_t heads = static_cast<size_t>(p->B) * p->H;
   const size_t nk = heads * p->Dk, nv = heads * p->Dv;

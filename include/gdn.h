@@ -414,8 +414,8 @@ gdn_status gdn_device_copy(void* dst, const void* src, size_t bytes, void* strea
  *   in    : q, k [B,1,H,Dk], v [B,1,H,Dv] (io dtype); g, beta [B,1,H] fp32
  *   in/out: S [B,H,Dk,Dv] fp32, 16-byte aligned
  *   out   : o [B,1,H,Dv] (io dtype)
- * All arithmetic is fp32 whatever the io dtype; o is rounded once.  B H < 2^24
- * (GDN_ERR_UNSUPPORTED).  No output may
+ * All arithmetic is fp32 whatever the io dtype; o is rounded once.  B H ceil(Dv / 32)
+ * < 2^24 (else GDN_ERR_UNSUPPORTED).  No output may
  * overlap another tensor (GDN_ERR_ALIAS).  No workspace. */
 gdn_status gdn_step(const gdn_problem* problem, const void* q, const void* k, const void* v,
                     const float* g, const float* beta, float* S, void* o, void* stream);
