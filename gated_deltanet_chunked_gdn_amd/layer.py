@@ -21,111 +21,127 @@ once as a ``SeqLens``.  Outputs and gradients that were not asked for are None.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
 
 from . import _native as nat
-from .ops import _IO, SeqLens, _seqlens
+from .ops import _IO, _seqlens
 
-# the current device and the raw current stream, without building Python objects: a
-# single-token call is a few microseconds
+# A single-token call is a few microseconds, so the checks are kept to what costs little:
+# the device as its index, the raw current stream, problems by their sizes.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 _ACT = {None: nat.GDN_ACT_NONE, "none": nat.GDN_ACT_NONE, "silu": nat.GDN_ACT_SILU}
+_F32 = torch.float32
 
 
-def _first(t, name):
+def _first(t, name, dims, what):
+    """Index of the device of the tensor that the others have to share it with."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device (got {t.device})")
     if t.dtype not in _IO:
         raise TypeError(f"{name} must be bfloat16 or float32")
-    return t.device
+    if t.dim() != dims:
+        raise ValueError(what)
+    return t.get_device()
 
 
-def _want(t, shape, dtype, device, name, optional=False):
-    """A contiguous tensor of this shape, dtype and device, as an address (None for an
-    absent optional one).  A host pointer that reached a kernel would be a GPU memory
-    fault, which the C ABI cannot detect."""
-    if t is None and optional:
-        return None
+def _want(t, shape, dtype, dev, name):
+    """The address of a contiguous tensor of this shape, dtype and device (index).  A host
+    pointer that reached a kernel would be a GPU memory fault, which the C ABI cannot
+    detect."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
-        return t.data_ptr()
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} (got {tuple(t.shape)})")
 
 
-def _out(out, like, device, name):
-    if out is None:
-        return torch.empty_like(like)
-    _want(out, like.shape, like.dtype, device, name)
-    return out
+def _may(t, shape, dtype, dev, name):
+    """_want, or None for an absent tensor."""
+    return None if t is None else _want(t, shape, dtype, dev, name)
 
 
-def _call(device, name, *args):
+def _call(dev, name, *args):
     """The library call on the device's current stream, with that device current."""
     fn = getattr(nat.load(), name)
-    index = device.index
-    if index == _current_device():
-        st = fn(*args, _current_stream(index))
+    if dev == _current_device():
+        st = fn(*args, _current_stream(dev))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _current_stream(index))
+        with torch.cuda.device(dev):
+            st = fn(*args, _current_stream(dev))
     if st:
         nat.check(st, name)
 
 
-def _offsets(seqs: Optional[SeqLens], device, batch):
-    """(sequences, host offsets, device offsets)"""
-    if seqs is None:
-        return batch, None, None
-    if seqs.dev.device != device:
-        raise ValueError(f"cu_seqlens must be on {device} (got {seqs.dev.device})")
-    return seqs.num_seqs, seqs.host.ctypes.data, seqs.dev.data_ptr()
+@functools.lru_cache(maxsize=256)
+def _dense(kind, *fields):
+    """A problem of dense tensors: the same sizes give the same (never written) structure."""
+    return kind(*fields)
 
 
-def _buffer(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _packed(cu_seqlens, dev):
+    seqs = _seqlens(cu_seqlens, torch.device("cuda", dev))
+    if seqs.dev.get_device() != dev:
+        raise ValueError(f"cu_seqlens must be on cuda:{dev} (got {seqs.dev.device})")
+    return seqs
 
 
-def _buffer_arg(buf, nbytes, device, name):
-    """A caller's uint8 buffer, or a fresh one of the size the library asks for."""
+def _buffer(buf, nbytes, dev, name):
+    """(buffer, address, bytes) of a caller's uint8 buffer, or of a fresh one of the size
+    the library asks for."""
     if buf is None:
-        buf = _buffer(nbytes, device)
-        return buf, (buf.data_ptr() if buf is not None else None), nbytes
+        if not nbytes:
+            return None, None, 0
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return buf, buf.data_ptr(), nbytes
     if not isinstance(buf, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if buf.device != device:
-        raise ValueError(f"{name} must be on {device} (got {buf.device})")
+    if buf.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} (got {buf.device})")
     if not buf.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return buf, buf.data_ptr(), buf.numel() * buf.element_size()
 
 
+def _result(out, like, dev):
+    """(tensor, address) of the caller's output or a fresh one like `like`."""
+    if out is None:
+        out = torch.empty_like(like)
+        return out, out.data_ptr()
+    return out, _want(out, like.shape, like.dtype, dev, "out")
+
+
 # --------------------------------------------------------------------------- delta rule, one token
 
 def _step(name, q, k, v, g, beta, state, scale, out, channel):
-    dev = _first(q, "q")
-    if q.dim() != 4 or q.shape[1] != 1 or not isinstance(v, torch.Tensor) or v.dim() != 4:
-        raise ValueError("q and k must be (B, 1, H, Dk) and v (B, 1, H, Dv)")
-    B, _, H, Dk = q.shape
+    what = "q and k must be (B, 1, H, Dk) and v (B, 1, H, Dv)"
+    dev = _first(q, "q", 4, what)
+    qs, io = q.shape, q.dtype
+    B, one, H, Dk = qs
+    if one != 1 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError(what)
     Dv = v.shape[3]
-    io, f32 = q.dtype, torch.float32
-    args = (_want(q, q.shape, io, dev, "q"), _want(k, q.shape, io, dev, "k"), _want(v, (B, 1, H, Dv), io, dev, "v"),
-            _want(g, q.shape if channel else (B, 1, H), f32, dev, "g"), _want(beta, (B, 1, H), f32, dev, "beta"),
-            _want(state, (B, H, Dk, Dv), f32, dev, "state"))
-    o = _out(out, v, dev, "out")
-    prob = nat.Problem(B, 1, H, Dk, Dv, B, None, None, _IO[io], scale, 64, 1, nat.GDN_PRECISION_IO)
-    _call(dev, name, prob, *args, o.data_ptr())
+    gs = (B, 1, H)
+    ptrs = (_want(q, qs, io, dev, "q"), _want(k, qs, io, dev, "k"), _want(v, (B, 1, H, Dv), io, dev, "v"),
+            _want(g, qs if channel else gs, _F32, dev, "g"), _want(beta, gs, _F32, dev, "beta"),
+            _want(state, (B, H, Dk, Dv), _F32, dev, "state"))
+    o, optr = _result(out, v, dev)
+    prob = _dense(nat.Problem, B, 1, H, Dk, Dv, B, None, None, _IO[io], float(scale), 64, 1, nat.GDN_PRECISION_IO)
+    _call(dev, name, prob, *ptrs, optr)
     return o
 
 
@@ -143,22 +159,26 @@ def kda_step(q, k, v, g, beta, state, scale: float = 1.0, out=None):
 
 # --------------------------------------------------------------------------- short causal convolution
 
-def _conv_problem(x, weight, seqs, activation, dev):
-    if x.dim() != 3:
-        raise ValueError("x must be (B, T, C)")
+def _conv_problem(x, weight, cu_seqlens, activation):
+    """(device index, offsets, problem)"""
+    dev = _first(x, "x", 3, "x must be (B, T, C)")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a (C, W) tensor")
     if activation not in _ACT:
         raise ValueError(f"activation must be one of {sorted(map(str, _ACT))}")
     B, T, C = x.shape
-    n, host, ptr = _offsets(seqs, dev, B)
-    return nat.ConvProblem(B, T, C, weight.shape[1], n, host, ptr, _IO[x.dtype], _ACT[activation])
+    W, io, act = weight.shape[1], _IO[x.dtype], _ACT[activation]
+    if cu_seqlens is None:
+        return dev, None, _dense(nat.ConvProblem, B, T, C, W, B, None, None, io, act)
+    s = _packed(cu_seqlens, dev)
+    return dev, s, nat.ConvProblem(B, T, C, W, s.num_seqs, s.host.ctypes.data, s.dev.data_ptr(), io, act)
 
 
 def _conv_inputs(x, weight, bias, dev):
-    C, f32 = x.shape[2], torch.float32
-    return (_want(x, x.shape, x.dtype, dev, "x"), _want(weight, (C, weight.shape[1]), f32, dev, "weight"),
-            _want(bias, (C,), f32, dev, "bias", optional=True))
+    xs = x.shape
+    C = xs[2]
+    return (_want(x, xs, x.dtype, dev, "x"), _want(weight, (C, weight.shape[1]), _F32, dev, "weight"),
+            _may(bias, (C,), _F32, dev, "bias"))
 
 
 def conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, activation: Optional[str] = "silu",
@@ -167,18 +187,15 @@ def conv_fwd(x, weight, bias=None, state0=None, cu_seqlens=None, activation: Opt
     weight (C, W) and bias (C,) fp32, W in 2..4; ``activation`` "silu" or None.
     ``state0`` (N, W - 1, C) of the io dtype holds the rows before every sequence
     (oldest first; None: zeros).  Returns (y, state_final or None)."""
-    dev = _first(x, "x")
-    seqs = _seqlens(cu_seqlens, dev)
-    prob = _conv_problem(x, weight, seqs, activation, dev)
+    dev, seqs, prob = _conv_problem(x, weight, cu_seqlens, activation)  # seqs: keeps the offsets alive
     shape = (prob.num_seqs, prob.W - 1, prob.C)
     ins = _conv_inputs(x, weight, bias, dev)
-    s0 = _want(state0, shape, x.dtype, dev, "state0", optional=True)
-    y = _out(out, x, dev, "out")
+    s0 = _may(state0, shape, x.dtype, dev, "state0")
+    y, yptr = _result(out, x, dev)
     last = final_state_out
     if last is None and output_final_state:
-        last = torch.empty(shape, dtype=x.dtype, device=dev)
-    _call(dev, "gdn_conv_fwd", prob, *ins, s0, y.data_ptr(),
-          _want(last, shape, x.dtype, dev, "final_state_out", optional=True))
+        last = x.new_empty(shape)
+    _call(dev, "gdn_conv_fwd", prob, *ins, s0, yptr, _may(last, shape, x.dtype, dev, "final_state_out"))
     return y, last
 
 
@@ -186,17 +203,14 @@ def conv_bwd(x, weight, dy, bias=None, state0=None, dstate_final=None, cu_seqlen
              activation: Optional[str] = "silu", workspace=None):
     """Backward of conv_fwd (gdn_conv_bwd).  Returns dict dx, dweight, dbias (None
     without bias), dstate0 (None without state0)."""
-    dev = _first(x, "x")
-    seqs = _seqlens(cu_seqlens, dev)
-    prob = _conv_problem(x, weight, seqs, activation, dev)
+    dev, seqs, prob = _conv_problem(x, weight, cu_seqlens, activation)  # seqs: keeps the offsets alive
     shape = (prob.num_seqs, prob.W - 1, prob.C)
     ins = _conv_inputs(x, weight, bias, dev)
-    s0 = _want(state0, shape, x.dtype, dev, "state0", optional=True)
-    grads = (_want(dy, x.shape, x.dtype, dev, "dy"),
-             _want(dstate_final, shape, x.dtype, dev, "dstate_final", optional=True))
+    s0 = _may(state0, shape, x.dtype, dev, "state0")
+    grads = (_want(dy, x.shape, x.dtype, dev, "dy"), _may(dstate_final, shape, x.dtype, dev, "dstate_final"))
     n = ctypes.c_size_t(0)
     nat.check(nat.load().gdn_conv_workspace_size(prob, n), "gdn_conv_workspace_size")
-    _, ws, nws = _buffer_arg(workspace, n.value, dev, "workspace")
+    buf, ws, nws = _buffer(workspace, n.value, dev, "workspace")
     out = {"dx": torch.empty_like(x), "dweight": torch.empty_like(weight),
            "dbias": torch.empty_like(bias) if bias is not None else None,
            "dstate0": torch.empty_like(state0) if state0 is not None else None}
@@ -208,32 +222,38 @@ def conv_bwd(x, weight, dy, bias=None, state0=None, dstate_final=None, cu_seqlen
 def conv_step(x, weight, state, bias=None, activation: Optional[str] = "silu", out=None):
     """One token of conv_fwd for every sequence (gdn_conv_step): x (B, 1, C); ``state``
     (B, W - 1, C) is shifted by one row in place.  Returns y."""
-    dev = _first(x, "x")
-    prob = _conv_problem(x, weight, None, activation, dev)
-    if x.shape[1] != 1:
+    dev, _, prob = _conv_problem(x, weight, None, activation)
+    if prob.T != 1:
         raise ValueError("x must be (B, 1, C)")
     ins = _conv_inputs(x, weight, bias, dev)
     s = _want(state, (prob.B, prob.W - 1, prob.C), x.dtype, dev, "state")
-    y = _out(out, x, dev, "out")
-    _call(dev, "gdn_conv_step", prob, *ins, s, y.data_ptr())
+    y, yptr = _result(out, x, dev)
+    _call(dev, "gdn_conv_step", prob, *ins, s, yptr)
     return y
 
 
 # --------------------------------------------------------------------------- selective scan
 
-def _scan_problem(u, A, Bm, seqs, dt_softplus, dev):
-    if u.dim() != 3 or not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
-        raise ValueError("u must be (B, T, D) and Bm, Cm (B, T, G, N)")
+def _scan_problem(u, Bm, cu_seqlens, dt_softplus):
+    """(device index, offsets, problem)"""
+    what = "u must be (B, T, D) and Bm, Cm (B, T, G, N)"
+    dev = _first(u, "u", 3, what)
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != 4:
+        raise ValueError(what)
     B, T, D = u.shape
-    n, host, ptr = _offsets(seqs, dev, B)
-    return nat.ScanProblem(B, T, D, Bm.shape[3], Bm.shape[2], n, host, ptr, _IO[u.dtype], bool(dt_softplus))
+    _, _, G, N = Bm.shape
+    io, softplus = _IO[u.dtype], int(bool(dt_softplus))
+    if cu_seqlens is None:
+        return dev, None, _dense(nat.ScanProblem, B, T, D, N, G, B, None, None, io, softplus)
+    s = _packed(cu_seqlens, dev)
+    return dev, s, nat.ScanProblem(B, T, D, N, G, s.num_seqs, s.host.ctypes.data, s.dev.data_ptr(), io, softplus)
 
 
 def _scan_inputs(p, u, dt, A, Bm, Cm, D, z, dt_bias, dev):
-    io, f32, bc = u.dtype, torch.float32, (p.B, p.T, p.G, p.N)
-    return (_want(u, u.shape, io, dev, "u"), _want(dt, u.shape, io, dev, "dt"), _want(A, (p.D, p.N), f32, dev, "A"),
-            _want(Bm, bc, io, dev, "Bm"), _want(Cm, bc, io, dev, "Cm"), _want(D, (p.D,), f32, dev, "D", optional=True),
-            _want(z, u.shape, io, dev, "z", optional=True), _want(dt_bias, (p.D,), f32, dev, "dt_bias", optional=True))
+    us, io, bc, chan = u.shape, u.dtype, (p.B, p.T, p.G, p.N), (p.D,)
+    return (_want(u, us, io, dev, "u"), _want(dt, us, io, dev, "dt"), _want(A, (p.D, p.N), _F32, dev, "A"),
+            _want(Bm, bc, io, dev, "Bm"), _want(Cm, bc, io, dev, "Cm"), _may(D, chan, _F32, dev, "D"),
+            _may(z, us, io, dev, "z"), _may(dt_bias, chan, _F32, dev, "dt_bias"))
 
 
 def _scan_size(prob, pass_):
@@ -242,33 +262,30 @@ def _scan_size(prob, pass_):
     return n.value
 
 
-def scan_buffers(u, A, Bm, cu_seqlens=None):
+def scan_buffers(u, Bm, cu_seqlens=None):
     """Sizes in bytes of the buffers the scan takes: dict forward (workspace of
     scan_fwd and scan_fwd_save), saved, backward (workspace of scan_bwd_saved)."""
-    dev = _first(u, "u")
-    prob = _scan_problem(u, A, Bm, _seqlens(cu_seqlens, dev), True, dev)
+    _, seqs, prob = _scan_problem(u, Bm, cu_seqlens, True)  # seqs: keeps the offsets alive
     return {"forward": _scan_size(prob, nat.GDN_SCAN_FWD), "saved": _scan_size(prob, nat.GDN_SCAN_SAVED),
             "backward": _scan_size(prob, nat.GDN_SCAN_BWD)}
 
 
 def _scan_fwd(save, u, dt, A, Bm, Cm, D, z, dt_bias, dt_softplus, h0, cu_seqlens, output_final_state, out,
               final_state_out, saved, workspace):
-    dev = _first(u, "u")
-    seqs = _seqlens(cu_seqlens, dev)
-    prob = _scan_problem(u, A, Bm, seqs, dt_softplus, dev)
+    dev, seqs, prob = _scan_problem(u, Bm, cu_seqlens, dt_softplus)  # seqs: keeps the offsets alive
     ins = _scan_inputs(prob, u, dt, A, Bm, Cm, D, z, dt_bias, dev)
     shape = (prob.num_seqs, prob.D, prob.N)
-    h0p = _want(h0, shape, torch.float32, dev, "h0", optional=True)
-    y = _out(out, u, dev, "out")
+    h0p = _may(h0, shape, _F32, dev, "h0")
+    y, yptr = _result(out, u, dev)
     h = final_state_out
     if h is None and output_final_state:
-        h = torch.empty(shape, dtype=torch.float32, device=dev)
-    outs = (y.data_ptr(), _want(h, shape, torch.float32, dev, "final_state_out", optional=True))
-    _, ws, nws = _buffer_arg(workspace, _scan_size(prob, nat.GDN_SCAN_FWD), dev, "workspace")
+        h = A.new_empty(shape)
+    outs = (yptr, _may(h, shape, _F32, dev, "final_state_out"))
+    buf, ws, nws = _buffer(workspace, _scan_size(prob, nat.GDN_SCAN_FWD), dev, "workspace")
     if not save:
         _call(dev, "gdn_scan_fwd", prob, *ins, h0p, *outs, ws, nws)
         return y, h
-    saved, sv, nsv = _buffer_arg(saved, _scan_size(prob, nat.GDN_SCAN_SAVED), dev, "saved")
+    saved, sv, nsv = _buffer(saved, _scan_size(prob, nat.GDN_SCAN_SAVED), dev, "saved")
     _call(dev, "gdn_scan_fwd_save", prob, *ins, h0p, *outs, sv, nsv, ws, nws)
     return y, h, saved
 
@@ -295,22 +312,20 @@ def scan_bwd_saved(u, dt, A, Bm, Cm, dy, saved, D=None, z=None, dt_bias=None, dt
     """Backward of scan_fwd_save (gdn_scan_bwd_saved) with the same inputs and
     cu_seqlens.  Returns dict du, ddt, dA, dB, dC, dD (None without D), dz (None
     without z), ddt_bias (None without dt_bias), dh0."""
-    dev = _first(u, "u")
-    seqs = _seqlens(cu_seqlens, dev)
-    prob = _scan_problem(u, A, Bm, seqs, dt_softplus, dev)
+    dev, seqs, prob = _scan_problem(u, Bm, cu_seqlens, dt_softplus)  # seqs: keeps the offsets alive
     ins = _scan_inputs(prob, u, dt, A, Bm, Cm, D, z, dt_bias, dev)
     shape = (prob.num_seqs, prob.D, prob.N)
     dyp = _want(dy, u.shape, u.dtype, dev, "dy")
-    dhp = _want(dh_final, shape, torch.float32, dev, "dh_final", optional=True)
+    dhp = _may(dh_final, shape, _F32, dev, "dh_final")
     need = _scan_size(prob, nat.GDN_SCAN_SAVED)
     if saved is None and need:
         raise ValueError("saved must be the buffer scan_fwd_save filled")
-    _, sv, nsv = _buffer_arg(saved, 0, dev, "saved")
-    _, ws, nws = _buffer_arg(workspace, _scan_size(prob, nat.GDN_SCAN_BWD), dev, "workspace")
+    _, sv, nsv = _buffer(saved, 0, dev, "saved")
+    buf, ws, nws = _buffer(workspace, _scan_size(prob, nat.GDN_SCAN_BWD), dev, "workspace")
     empty = lambda t: torch.empty_like(t) if t is not None else None  # noqa: E731
     out = {"du": empty(u), "ddt": empty(dt), "dA": empty(A), "dB": empty(Bm), "dC": empty(Cm), "dD": empty(D),
            "dz": empty(z), "ddt_bias": empty(dt_bias),
-           "dh0": torch.empty(shape, dtype=torch.float32, device=dev) if want_dh0 else None}
+           "dh0": A.new_empty(shape) if want_dh0 else None}
     _call(dev, "gdn_scan_bwd_saved", prob, *ins, dyp, dhp, sv, nsv,
           *(t.data_ptr() if t is not None else None for t in out.values()), ws, nws)
     return out
@@ -319,12 +334,11 @@ def scan_bwd_saved(u, dt, A, Bm, Cm, dy, saved, D=None, z=None, dt_bias=None, dt
 def scan_step(u, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, dt_softplus: bool = True, out=None):
     """One token of scan_fwd for every sequence (gdn_scan_step): u, dt, z (B, 1, D),
     Bm, Cm (B, 1, G, N); ``state`` (B, D, N) fp32 is updated in place.  Returns y."""
-    dev = _first(u, "u")
-    prob = _scan_problem(u, A, Bm, None, dt_softplus, dev)
-    if u.shape[1] != 1:
+    dev, _, prob = _scan_problem(u, Bm, None, dt_softplus)
+    if prob.T != 1:
         raise ValueError("u must be (B, 1, D)")
     ins = _scan_inputs(prob, u, dt, A, Bm, Cm, D, z, dt_bias, dev)
-    s = _want(state, (prob.B, prob.D, prob.N), torch.float32, dev, "state")
-    y = _out(out, u, dev, "out")
-    _call(dev, "gdn_scan_step", prob, *ins, s, y.data_ptr())
+    s = _want(state, (prob.B, prob.D, prob.N), _F32, dev, "state")
+    y, yptr = _result(out, u, dev)
+    _call(dev, "gdn_scan_step", prob, *ins, s, yptr)
     return y

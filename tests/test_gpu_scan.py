@@ -72,7 +72,7 @@ def test_scan(B, T, D, N, G, cu, z, skip, bias, state, io):
 def test_split_over_time(T, D, N, cu):
     """Few channels and many tokens: several segments, whose starts are composed."""
     a, h0, dy, dl = _inputs(1, T, D, N, 1, F32, cu=cu)
-    sizes = gdn.scan_buffers(a["u"], a["A"], a["Bm"], cu_seqlens=cu)
+    sizes = gdn.scan_buffers(a["u"], a["Bm"], cu_seqlens=cu)
     assert sizes["forward"] > 0  # segment states: the split is taken
     want = _ref(a, h0, cu, True, dy, dl)
     size = _ref(a, h0, cu, True, dy, dl, size=True)

@@ -258,7 +258,7 @@ def test_host_tensors_are_refused(monkeypatch):
     u, A, B = f(1, 5, 16), f(16, 16), f(1, 5, 1, 16)
     for call in (lambda: layer.scan_fwd(u, u, A, B, B), lambda: layer.scan_fwd_save(u, u, A, B, B),
                  lambda: layer.scan_bwd_saved(u, u, A, B, B, u, f(4)), lambda: layer.scan_step(u, u, A, B, B, f(1, 16, 16)),
-                 lambda: layer.scan_buffers(u, A, B)):
+                 lambda: layer.scan_buffers(u, B)):
         with pytest.raises(ValueError, match="u must be on a GPU"):
             call()
     with pytest.raises(TypeError):
@@ -266,8 +266,9 @@ def test_host_tensors_are_refused(monkeypatch):
 
 
 def test_want_names_what_is_wrong():
-    dev = torch.device("cpu")
+    dev = -1  # what get_device() gives for host tensors
     t = torch.zeros(3, 4)
+    assert layer._want(t, (3, 4), torch.float32, dev, "t") == t.data_ptr()
     with pytest.raises(ValueError, match="shape"):
         layer._want(t, (4, 3), torch.float32, dev, "t")
     with pytest.raises(TypeError, match="bfloat16"):
@@ -275,7 +276,8 @@ def test_want_names_what_is_wrong():
     with pytest.raises(ValueError, match="contiguous"):
         layer._want(t.t(), (4, 3), torch.float32, dev, "t")
     with pytest.raises(ValueError, match="must be on"):
-        layer._want(t, (3, 4), torch.float32, torch.device("cuda", 0), "t")
-    with pytest.raises(TypeError):
-        layer._want(None, (3, 4), torch.float32, dev, "t")
-    assert layer._want(None, (3, 4), torch.float32, dev, "t", optional=True) is None
+        layer._want(t, (3, 4), torch.float32, 0, "t")
+    for bad in (None, [1.0]):
+        with pytest.raises(TypeError):
+            layer._want(bad, (3, 4), torch.float32, dev, "t")
+    assert layer._may(None, (3, 4), torch.float32, dev, "t") is None
