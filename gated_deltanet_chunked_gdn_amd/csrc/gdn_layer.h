@@ -74,6 +74,7 @@ struct ScanParams {
   int32_t softplus;
   int32_t segs;
   int64_t seg_len;
+  int32_t in_time;      // forward: the time axis inside the workgroup (segs == 1)
   // backward
   const void* dy;
   const float* dh_final;
@@ -97,13 +98,18 @@ constexpr int kScanBlock = 16;    // tokens between two kept states
 // bos / block + n + c (distinct, as chunk_slots).
 inline int64_t scan_slots(int64_t rows, int64_t nseq) { return rows / kScanBlock + nseq + 1; }
 inline int scan_tiles(int D, int G) { return G * ((D / G + kScanTile - 1) / kScanTile); }
-// Segments of the longest sequence of max_len tokens, and their length.
+// Segments of the longest sequence of max_len tokens, and their length; `in_time`: the
+// forward's kernel with the time axis inside the workgroup instead.
 struct ScanSplit {
   int32_t segs;
   int64_t len;
+  int32_t in_time;
 };
-ScanSplit scan_split(int64_t max_len, int64_t nseq, int D, int G);
+ScanSplit scan_split_fwd(int64_t max_len, int64_t nseq, int D, int G, int N);
+ScanSplit scan_split_bwd(int64_t max_len, int64_t nseq, int D, int G);
 hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
+inline int scan_time_tiles(int D, int G) { return G * ((D / G + 15) / 16); }
+hipError_t launch_scan_time(const ScanParams& p, int N, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
 // state in p.h_final, updated in place
 hipError_t launch_scan_step(const ScanParams& p, int N, bool bf16, hipStream_t s);

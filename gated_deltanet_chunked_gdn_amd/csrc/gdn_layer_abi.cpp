@@ -139,13 +139,13 @@ gdn::ConvParams conv_params(const gdn_conv_problem* p, const ConvSize& c, const 
 struct ScanSize {
   size_t io = 0, values = 0, bc = 0, a = 0, chan = 0, state = 0;
   int64_t rows = 0;
-  gdn::ScanSplit split{1, 0};
+  gdn::ScanSplit split{1, 0, 0};
   size_t saved = 0;                      // kept states
   size_t seg_end = 0, seg_sum = 0;       // segment states and sums of delta (segs > 1)
   size_t part_bc = 0, part_a = 0;        // backward: partial sums
 };
 
-gdn_status check_scan(const gdn_scan_problem* p, ScanSize* c) {
+gdn_status check_scan(const gdn_scan_problem* p, bool bwd, ScanSize* c) {
   if (!p) return GDN_ERR_NULL;
   if (p->io_dtype != GDN_FP32 && p->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (p->B < 0 || p->T < 0 || p->D <= 0 || p->N <= 0 || p->G <= 0 || p->num_seqs < 0 || p->D % p->G != 0)
@@ -164,7 +164,8 @@ gdn_status check_scan(const gdn_scan_problem* p, ScanSize* c) {
   c->chan = static_cast<size_t>(p->D) * 4;
   c->state = static_cast<size_t>(p->num_seqs) * c->a;
   if (p->num_seqs == 0) return GDN_OK;
-  c->split = gdn::scan_split(max_len, p->num_seqs, p->D, p->G);
+  c->split = bwd ? gdn::scan_split_bwd(max_len, p->num_seqs, p->D, p->G)
+                 : gdn::scan_split_fwd(max_len, p->num_seqs, p->D, p->G, p->N);
   const size_t parts = static_cast<size_t>(c->split.segs) * p->num_seqs;
   c->saved = static_cast<size_t>(gdn::scan_slots(c->rows, p->num_seqs)) * c->a;
   if (c->split.segs > 1) {
@@ -184,7 +185,7 @@ gdn::ScanParams scan_params(const gdn_scan_problem* p, const ScanSize& c, const 
   sp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
   sp.nseq = p->num_seqs; sp.D = p->D; sp.G = p->G;
   sp.softplus = p->dt_softplus != 0;
-  sp.segs = c.split.segs; sp.seg_len = c.split.len;
+  sp.segs = c.split.segs; sp.seg_len = c.split.len; sp.in_time = c.split.in_time;
   sp.rows = c.rows;
   return sp;
 }
@@ -200,7 +201,7 @@ gdn_status scan_fwd(const gdn_scan_problem* p, const void* u, const void* dt, co
                     void* y, float* h_final, bool save, void* saved, size_t saved_bytes, void* ws,
                     size_t ws_bytes, void* stream) {
   ScanSize c;
-  gdn_status st = check_scan(p, &c);
+  gdn_status st = check_scan(p, false, &c);
   if (st != GDN_OK) return st;
   st = check_tensors({{u, c.values, 16, true}, {dt, c.values, 16, true}, {A, c.a, 16, true}, {Bm, c.bc, 16, true},
                       {Cm, c.bc, 16, true}, {Dskip, c.chan, 16, false}, {z, c.values, 16, false},
@@ -293,7 +294,7 @@ gdn_status gdn_scan_workspace_size(const gdn_scan_problem* p, int32_t pass, size
   if (!bytes) return GDN_ERR_NULL;
   if (pass != GDN_SCAN_FWD && pass != GDN_SCAN_SAVED && pass != GDN_SCAN_BWD) return GDN_ERR_UNSUPPORTED;
   ScanSize c;
-  const gdn_status st = check_scan(p, &c);
+  const gdn_status st = check_scan(p, pass == GDN_SCAN_BWD, &c);
   if (st != GDN_OK) return st;
   const size_t segments = c.seg_end + c.seg_sum;
   *bytes = pass == GDN_SCAN_SAVED ? c.saved : pass == GDN_SCAN_FWD ? segments : segments + c.part_bc + c.part_a;
@@ -321,7 +322,7 @@ gdn_status gdn_scan_bwd_saved(const gdn_scan_problem* p, const void* u, const vo
                               float* dDskip, void* dz, float* ddt_bias, float* dh0, void* ws, size_t ws_bytes,
                               void* stream) {
   ScanSize c;
-  gdn_status st = check_scan(p, &c);
+  gdn_status st = check_scan(p, true, &c);
   if (st != GDN_OK) return st;
   if (dz && !z) return GDN_ERR_NULL;
   st = check_tensors({{u, c.values, 16, true}, {dt, c.values, 16, true}, {A, c.a, 16, true}, {Bm, c.bc, 16, true},
@@ -353,7 +354,7 @@ gdn_status gdn_scan_step(const gdn_scan_problem* p, const void* u, const void* d
                          const void* Cm, const float* Dskip, const void* z, const float* dt_bias, float* h,
                          void* y, void* stream) {
   ScanSize c;
-  gdn_status st = check_scan(p, &c);
+  gdn_status st = check_scan(p, false, &c);
   if (st != GDN_OK) return st;
   if (p->T != 1 || p->cu_seqlens_host) return GDN_ERR_SHAPE;
   st = check_tensors({{u, c.values, 16, true}, {dt, c.values, 16, true}, {A, c.a, 16, true}, {Bm, c.bc, 16, true},

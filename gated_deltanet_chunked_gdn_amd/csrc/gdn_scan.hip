@@ -219,6 +219,7 @@ hipError_t step_t(const ScanParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s) {
+  if (p.in_time) return launch_scan_time(p, N, bf16, s);
   GDN_SCAN_DISPATCH(fwd_t)
 }
 hipError_t launch_scan_step(const ScanParams& p, int N, bool bf16, hipStream_t s) { GDN_SCAN_DISPATCH(step_t) }

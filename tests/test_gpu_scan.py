@@ -40,6 +40,8 @@ CASES = [  # B, T, D, N, G, cu, z, skip, bias, state
     (1, 97, 64, 16, 1, [0, 0, 1, 16, 33, 33, 96, 97, 97], True, True, True, True),
     (1, 60, 40, 64, 1, [0, 31, 60], True, True, True, True),
     (1, 66, 136, 8, 1, [0, 2, 66], False, True, True, True),
+    (1, 150, 72, 16, 3, [0, 40, 40, 150], True, True, True, True),
+    (2, 129, 24, 8, 1, None, True, True, False, False),
 ]
 
 
