@@ -98,15 +98,15 @@ constexpr int kScanBlock = 16;    // tokens between two kept states
 // bos / block + n + c (distinct, as chunk_slots).
 inline int64_t scan_slots(int64_t rows, int64_t nseq) { return rows / kScanBlock + nseq + 1; }
 inline int scan_tiles(int D, int G) { return G * ((D / G + kScanTile - 1) / kScanTile); }
-// Segments of the longest sequence of max_len tokens, and their length; `in_time`: the
+// Segments of the longest sequence, of max_len of all the rows, and their length; `in_time`: the
 // forward's kernel with the time axis inside the workgroup instead.
 struct ScanSplit {
   int32_t segs;
   int64_t len;
   int32_t in_time;
 };
-ScanSplit scan_split_fwd(int64_t max_len, int64_t nseq, int D, int G, int N);
-ScanSplit scan_split_bwd(int64_t max_len, int64_t nseq, int D, int G);
+ScanSplit scan_split_fwd(int64_t max_len, int64_t rows, int D, int G, int N);
+ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G);
 hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
 inline int scan_time_tiles(int D, int G) { return G * ((D / G + 15) / 16); }
 hipError_t launch_scan_time(const ScanParams& p, int N, bool bf16, hipStream_t s);

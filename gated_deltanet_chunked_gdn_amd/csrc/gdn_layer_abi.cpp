@@ -164,8 +164,8 @@ gdn_status check_scan(const gdn_scan_problem* p, bool bwd, ScanSize* c) {
   c->chan = static_cast<size_t>(p->D) * 4;
   c->state = static_cast<size_t>(p->num_seqs) * c->a;
   if (p->num_seqs == 0) return GDN_OK;
-  c->split = bwd ? gdn::scan_split_bwd(max_len, p->num_seqs, p->D, p->G)
-                 : gdn::scan_split_fwd(max_len, p->num_seqs, p->D, p->G, p->N);
+  c->split = bwd ? gdn::scan_split_bwd(max_len, c->rows, p->D, p->G)
+                 : gdn::scan_split_fwd(max_len, c->rows, p->D, p->G, p->N);
   const size_t parts = static_cast<size_t>(c->split.segs) * p->num_seqs;
   c->saved = static_cast<size_t>(gdn::scan_slots(c->rows, p->num_seqs)) * c->a;
   if (c->split.segs > 1) {

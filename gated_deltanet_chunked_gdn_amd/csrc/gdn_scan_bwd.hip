@@ -13,9 +13,8 @@
 // states) are added over the 16 channels of its wave by lane swaps that halve the
 // registers each time (rows of 16 lanes hold channels c / 4: two swap steps), then by
 // two DPP adds inside the quad that holds channels c % 4.  Each workgroup writes its
-// 64 channels' sums of dB and dC, and one kernel adds them over the channel tiles in
-// order; the sums of dA, dD and ddt_bias over the tokens are added over the segments
-// and sequences by another.  No atomics: the same inputs give the same bits.
+// 64 channels' sums of dB and dC, and a last kernel adds them over the channel tiles in
+// order, and the sums of dA, dD and ddt_bias over the segments and sequences.  No atomics: the same inputs give the same bits.
 #include <hip/hip_runtime.h>
 
 #include "gdn_scan_device.h"
@@ -101,10 +100,11 @@ struct BwdLoader : Loader<E, N, TT> {
 };
 
 // Gradient of the state before every segment but the first of a sequence, from a zero
-// gradient behind it, and the segment's sum of delta.
+// gradient behind it, and the segment's sum of delta.  Staged per (token, channel): delta
+// and ds; two buffers, one barrier a block of 16 tokens.
 template <typename E, int N>
 __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
-  constexpr int S = N / 4, EL = BwdLoader<E, N>::EL;
+  constexpr int S = N / 4, EL = TT / 4, PC = N > 16 ? N / 16 : 1;
   const int tid = threadIdx.x;
   const Place at;
   const int n = blockIdx.z, seg = blockIdx.y + 1;
@@ -114,10 +114,9 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
   const int64_t begin = seg * p.seg_len, end = min(len, begin + p.seg_len);
   if (begin >= end) return;
 
-  __shared__ Stage<N, TT> st;
-  __shared__ ChannelParams cp;
-  __shared__ float dsb[TT][kScanTile];
-  __shared__ float sums[4][kScanTile];
+  __shared__ float2 dg[2][TT][kScanTile];
+  __shared__ float Cs[2][TT][N];
+  __shared__ float part[4][kScanTile];
   const bool chan = at.c < ct.count;
   const int64_t hd = static_cast<int64_t>(ct.d0 + at.c) * N + at.q * S;
   float A2[S], G[S];
@@ -127,34 +126,90 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
     A2[s] *= kLog2e;
     G[s] = 0.f;
   }
-  float dsum = 0.f, delta[EL], sig[EL], ds[EL];
-  BwdLoader<E, N> ld(p, ct, bos);
-  int64_t t0 = begin + (end - begin - 1) / TT * TT;
-  ld.fetch(t0, end);
-  cp.fill(p, ct);
-  __syncthreads();
-  for (; t0 >= begin; t0 -= TT) {
-    ld.put(st, cp, t0, end, delta, sig);
-    ld.put_ds(dsb, t0, end, ds);
-    if (t0 > begin) ld.fetch(t0 - TT, end);
-    __syncthreads();
+  // a thread's share: four channels of one token, and a piece of its C
+  const int row = tid >> 4, piece = tid & 15, col = piece * EL;
+  const bool live = col < ct.count;
+  const int d = ct.d0 + (live ? col : 0);
+  Raw<float, EL> bias;
+  bias.zero();
+  if (p.dt_bias) bias.load(p.dt_bias + d);
+  Raw<E, EL> rdt, rdy, rz;
+  E rc[PC];
+  auto fetch = [&](int64_t t0) {
+    const int64_t t = bos + min(t0 + row, end - 1);
+    rdt.load(static_cast<const E*>(p.dt) + t * p.D + d);
+    rdy.load(static_cast<const E*>(p.dy) + t * p.D + d);
+    if (p.z) rz.load(static_cast<const E*>(p.z) + t * p.D + d);
+    const int64_t bc = (t * p.G + ct.g) * N + (piece * PC < N ? piece * PC : 0);
 #pragma unroll
-    for (int t = TT - 1; t >= 0; --t) {
-      const float d = st.dd[t][at.c].x, g = dsb[t][at.c];
-      float Cv[S];
-      read_states<S>(&st.C[t][at.q * S], Cv);
+    for (int i = 0; i < PC; ++i) rc[i] = static_cast<const E*>(p.Cm)[bc + i];
+  };
+  auto put = [&](int b, int64_t t0) {
+    const bool ok = t0 + row < end;
+    float delta[EL], ds[EL], sig;
 #pragma unroll
-      for (int s = 0; s < S; ++s) G[s] = exp2_(d * A2[s]) * fmaf(Cv[s], g, G[s]);
-      if (t % 4 == at.q) dsum += d;
+    for (int e = 0; e < EL; ++e) {
+      delta[e] = rdt.get(e) + bias.get(e);
+      ds[e] = rdy.get(e);
     }
+    if (p.softplus) {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) delta[e] = softplus_(delta[e], sig);
+    }
+    if (p.z) {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) {
+        const float z = rz.get(e);
+        ds[e] *= z * sigmoid_(z);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < EL; e += 2) {
+      float4 v = {delta[e], ds[e], delta[e + 1], ds[e + 1]};
+      if (!ok || !live) v = float4{0.f, 0.f, 0.f, 0.f};
+      *reinterpret_cast<float4*>(&dg[b][row][col + e]) = v;
+    }
+    if (piece * PC < N) {
+#pragma unroll
+      for (int i = 0; i < PC; ++i) Cs[b][row][piece * PC + i] = ok ? IoT<E>::ld(&rc[i]) : 0.f;
+    }
+  };
+  int64_t t0 = begin + (end - begin - 1) / TT * TT;
+  fetch(t0);
+  put(0, t0);
+  __syncthreads();
+  float dsum = 0.f;
+  for (int b = 0; t0 >= begin; t0 -= TT, b ^= 1) {
+    if (t0 > begin) fetch(t0 - TT);
+#pragma unroll 2
+    for (int t = TT - 4; t >= 0; t -= 4) {
+      // four tokens' decays first, then the chain through them
+      float a[4][S], g[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = dg[b][t + j][at.c];
+        g[j] = v.y;
+        if (j == at.q) dsum += v.x;
+#pragma unroll
+        for (int s = 0; s < S; ++s) a[j][s] = exp2_(v.x * A2[s]);
+      }
+#pragma unroll
+      for (int j = 3; j >= 0; --j) {
+        float Cv[S];
+        read_states<S>(&Cs[b][t + j][at.q * S], Cv);
+#pragma unroll
+        for (int s = 0; s < S; ++s) G[s] = a[j][s] * fmaf(Cv[s], g[j], G[s]);
+      }
+    }
+    if (t0 > begin) put(b ^ 1, t0 - TT);
     __syncthreads();
   }
-  const int64_t part = static_cast<int64_t>(seg) * p.nseq + n;
-  if (chan) store_states<S>(p.seg_end + part * p.D * N + hd, G);
-  sums[at.q][at.c] = dsum;
+  const int64_t pt = static_cast<int64_t>(seg) * p.nseq + n;
+  if (chan) store_states<S>(p.seg_end + pt * p.D * N + hd, G);
+  part[at.q][at.c] = dsum;
   __syncthreads();
   if (tid < kScanTile && tid < ct.count)
-    p.seg_sum[part * p.D + ct.d0 + tid] = (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
+    p.seg_sum[pt * p.D + ct.d0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
 }
 
 // GATED: dz is wanted, and with it the outputs before the gate.
@@ -388,26 +443,39 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   }
 }
 
-// dB and dC: the channel tiles' sums in order.
-template <typename E, int N>
-__global__ __launch_bounds__(256) void scan_bwd_bc_kernel(ScanParams p, int tiles, int64_t items) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= items) return;
-  float s = 0.f;
-  for (int k = 0; k < tiles; ++k) s += p.part_bc[static_cast<int64_t>(k) * items + i];
-  const int64_t rg = i / (2 * N);
-  const int k = static_cast<int>(i % (2 * N));
-  E* const out = static_cast<E*>(k < N ? p.dBm : p.dCm);
-  IoT<E>::st(out + rg * N + k % N, s);
+// Sum of `count` values `stride` apart, eight in flight, in a fixed order.
+template <typename T>
+__device__ __forceinline__ T strided_sum(const float* p, int64_t count, int64_t stride, T zero) {
+  T s[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = zero;
+  int64_t i = 0;
+  for (; i + 8 <= count; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] += *reinterpret_cast<const T*>(p + (i + k) * stride);
+  }
+  for (; i < count; ++i) s[0] += *reinterpret_cast<const T*>(p + i * stride);
+  return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
 }
 
-// dA, dDskip and ddt_bias: the segments' and sequences' sums in order.
-template <int N>
-__global__ __launch_bounds__(256) void scan_bwd_a_kernel(ScanParams p, int64_t parts) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, items = static_cast<int64_t>(p.D) * (N + 2);
+// dB and dC from the channel tiles' sums, four values a thread; the threads behind the
+// first `bc` form dA, dDskip and ddt_bias from the segments' and sequences' sums.
+template <typename E, int N>
+__global__ __launch_bounds__(256) void scan_bwd_finish_kernel(ScanParams p, int tiles, int64_t bc, int64_t parts) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t values = p.rows * p.G * 2 * N;
+  if (id < bc) {
+    const int64_t i = id * 4;
+    if (i >= values) return;
+    const f32x4_t s = strided_sum<f32x4_t>(p.part_bc + i, tiles, values, zero4());
+    const int64_t rg = i / (2 * N);
+    const int k = static_cast<int>(i % (2 * N));
+    chunk::store4<E>(static_cast<E*>(k < N ? p.dBm : p.dCm) + rg * N + k % N, s[0], s[1], s[2], s[3]);
+    return;
+  }
+  const int64_t i = id - bc, items = static_cast<int64_t>(p.D) * (N + 2);
   if (i >= items) return;
-  float s = 0.f;
-  for (int64_t k = 0; k < parts; ++k) s += p.part_a[k * items + i];
+  const float s = strided_sum<float>(p.part_a + i, parts, items, 0.f);
   const int64_t d = i / (N + 2);
   const int k = static_cast<int>(i % (N + 2));
   if (k < N)
@@ -432,12 +500,9 @@ hipError_t bwd_t(const ScanParams& p, hipStream_t s) {
     else
       hipLaunchKernelGGL((scan_bwd_kernel<E, N, false>), dim3(tiles, p.segs, nseq), dim3(256), 0, s, p);
   }
-  const int64_t items = p.rows * p.G * 2 * N;
-  if (items > 0)
-    hipLaunchKernelGGL((scan_bwd_bc_kernel<E, N>), dim3(blocks_of(items)), dim3(256), 0, s, p,
-                       static_cast<int>(tiles / p.G), items);
-  hipLaunchKernelGGL((scan_bwd_a_kernel<N>), dim3(blocks_of(static_cast<int64_t>(p.D) * (N + 2))), dim3(256), 0, s, p,
-                     static_cast<int64_t>(p.segs) * p.nseq);
+  const int64_t bc = static_cast<int64_t>(blocks_of(p.rows * p.G * N / 2)) * 256;
+  hipLaunchKernelGGL((scan_bwd_finish_kernel<E, N>), dim3(blocks_of(bc + static_cast<int64_t>(p.D) * (N + 2))), dim3(256), 0,
+                     s, p, static_cast<int>(tiles / p.G), bc, static_cast<int64_t>(p.segs) * p.nseq);
   return hipGetLastError();
 }
 
