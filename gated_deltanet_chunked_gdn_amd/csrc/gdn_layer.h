@@ -65,8 +65,8 @@ struct ScanParams {
   void* y;
   float* h_final;
   float* saved;         // [block slot][D][N] states before every block, or nullptr
-  // segments over the time axis: `segs` runs of `seg_len` tokens (a multiple of the
-  // block length) of every sequence
+  // segments over the time axis: `segs` runs of `seg_len` tokens (a multiple of
+  // kScanBlock) of every sequence
   float* seg_end;       // [seg][sequence][D][N]
   float* seg_sum;       // [seg][sequence][D]: sums of delta
   SeqInfo seq;
