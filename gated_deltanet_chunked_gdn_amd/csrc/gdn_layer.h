@@ -106,7 +106,7 @@ struct ScanSplit {
   int32_t in_time;
 };
 ScanSplit scan_split_fwd(int64_t max_len, int64_t rows, int D, int G, int N);
-ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G);
+ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G, int N);
 hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
 inline int scan_time_tiles(int D, int G) { return G * ((D / G + 15) / 16); }
 hipError_t launch_scan_time(const ScanParams& p, int N, bool bf16, hipStream_t s);

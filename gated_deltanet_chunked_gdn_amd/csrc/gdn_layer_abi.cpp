@@ -164,7 +164,7 @@ gdn_status check_scan(const gdn_scan_problem* p, bool bwd, ScanSize* c) {
   c->chan = static_cast<size_t>(p->D) * 4;
   c->state = static_cast<size_t>(p->num_seqs) * c->a;
   if (p->num_seqs == 0) return GDN_OK;
-  c->split = bwd ? gdn::scan_split_bwd(max_len, c->rows, p->D, p->G)
+  c->split = bwd ? gdn::scan_split_bwd(max_len, c->rows, p->D, p->G, p->N)
                  : gdn::scan_split_fwd(max_len, c->rows, p->D, p->G, p->N);
   const size_t parts = static_cast<size_t>(c->split.segs) * p->num_seqs;
   c->saved = static_cast<size_t>(gdn::scan_slots(c->rows, p->num_seqs)) * c->a;

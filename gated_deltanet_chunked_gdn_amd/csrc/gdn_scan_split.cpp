@@ -13,18 +13,20 @@ static int64_t sequences(int64_t max_len, int64_t rows) {
 // Serial needs the fewest instructions; the split runs the state's part of the work
 // twice, and every segment composes the ones before it.  It is taken where the channels
 // alone leave SIMDs idle: segments of at least 64 tokens, as many as give every SIMD four
-// waves (1024 workgroups of four).  Where that leaves fewer than 512 workgroups, the chain
-// of tokens is what takes the time, and segments are shortened, to 16 tokens at least and
-// 32 of them at most, for up to 512 workgroups.  Measured, bf16 (us), at least 64 / 16:
+// waves (1024 workgroups of four; two waves, 512, for 64 states, whose registers allow no
+// more).  Where that leaves fewer than half as many workgroups, the chain of tokens is
+// what takes the time, and segments are shortened, to 16 tokens at least and 32 of them at
+// most, for up to half as many.  Measured, bf16 (us), at least 64 / 16:
 //   16 states, backward, 1 x 64 x 256    22 / 15     1 x 128 x 2048   36 / 20
 //   64 states, forward,  1 x 128 x 256   39 / 18     backward 88 / 35
 // but 64 states, forward, 1 x 512 x 2048 44 / 69 with 1024 workgroups of 16 tokens.
-ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G) {
+ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G, int N) {
+  const int64_t want = N == 64 ? 512 : 1024;
   const int64_t groups = sequences(max_len, rows) * scan_tiles(D, G);
-  int64_t segs = std::min<int64_t>((1024 + groups - 1) / groups, max_len / 64);
-  if (segs * groups < 512) {
+  int64_t segs = std::min<int64_t>((want + groups - 1) / groups, max_len / 64);
+  if (segs * groups < want / 2) {
     const int64_t least = std::min<int64_t>(64, ((max_len + 31) / 32 + 15) / 16 * 16);
-    segs = std::min<int64_t>((512 + groups - 1) / groups, max_len / std::max<int64_t>(least, 16));
+    segs = std::min<int64_t>((want / 2 + groups - 1) / groups, max_len / std::max<int64_t>(least, 16));
   }
   if (segs < 2) return ScanSplit{1, std::max<int64_t>(max_len, 64), 0};
   const int64_t len = ((max_len + segs - 1) / segs + 15) / 16 * 16;
@@ -46,7 +48,7 @@ ScanSplit scan_split_fwd(int64_t max_len, int64_t rows, int D, int G, int N) {
   const int64_t narrow = sequences(max_len, rows) * scan_time_tiles(D, G);
   if (N <= 16 && max_len > (groups < 512 ? 16 : 64) && groups < 1024 && (max_len <= 320 || narrow >= 384))
     return ScanSplit{1, std::max<int64_t>(max_len, 64), 1};
-  return scan_split_bwd(max_len, rows, D, G);
+  return scan_split_bwd(max_len, rows, D, G, N);
 }
 
 }  // namespace gdn
