@@ -67,8 +67,8 @@ struct ScanParams {
   float* saved;         // [block slot][D][N] states before every block, or nullptr
   // segments over the time axis: `segs` runs of `seg_len` tokens (a multiple of
   // kScanBlock) of every sequence
-  float* seg_end;       // [seg][sequence][D][N]
-  float* seg_sum;       // [seg][sequence][D]: sums of delta
+  float* seg_end;       // [slot][D][N], slot bos / seg_len + n + segment (as the kept states)
+  float* seg_sum;       // [slot][D]: sums of delta
   SeqInfo seq;
   int32_t nseq, D, G;
   int32_t softplus;
@@ -88,7 +88,8 @@ struct ScanParams {
   float* ddt_bias;
   float* dh0;
   float* part_bc;       // [channel tile][row][2][N] partial dB, dC
-  float* part_a;        // [sequence, segment][D][N + 2] partial dA, dDskip, ddt_bias
+  float* part_a;        // [slot][D][N + 2] partial dA, dDskip, ddt_bias
+  int64_t parts;        // slots of segments: rows / seg_len + sequences
   int64_t rows;         // B * T
 };
 

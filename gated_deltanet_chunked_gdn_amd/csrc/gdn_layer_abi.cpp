@@ -140,6 +140,7 @@ struct ScanSize {
   size_t io = 0, values = 0, bc = 0, a = 0, chan = 0, state = 0;
   int64_t rows = 0;
   gdn::ScanSplit split{1, 0, 0};
+  int64_t parts = 0;                     // slots of segments
   size_t saved = 0;                      // kept states
   size_t seg_end = 0, seg_sum = 0;       // segment states and sums of delta (segs > 1)
   size_t part_bc = 0, part_a = 0;        // backward: partial sums
@@ -157,7 +158,8 @@ gdn_status check_scan(const gdn_scan_problem* p, bool bwd, ScanSize* c) {
   if (st != GDN_OK) return st;
   c->io = p->io_dtype == GDN_BF16 ? 2 : 4;
   c->rows = static_cast<int64_t>(p->B) * p->T;
-  if (c->rows > INT32_MAX || c->rows * p->G > INT32_MAX || p->D > 1 << 20) return GDN_ERR_UNSUPPORTED;
+  // threads (two values of dBm or dCm each, in the backward) are counted in 32 bits
+  if (c->rows > INT32_MAX || c->rows * p->G * p->N >= INT64_C(1) << 32 || p->D > 1 << 20) return GDN_ERR_UNSUPPORTED;
   c->values = static_cast<size_t>(c->rows) * p->D * c->io;
   c->bc = static_cast<size_t>(c->rows) * p->G * p->N * c->io;
   c->a = static_cast<size_t>(p->D) * p->N * 4;
@@ -166,7 +168,8 @@ gdn_status check_scan(const gdn_scan_problem* p, bool bwd, ScanSize* c) {
   if (p->num_seqs == 0) return GDN_OK;
   c->split = bwd ? gdn::scan_split_bwd(max_len, c->rows, p->D, p->G, p->N)
                  : gdn::scan_split_fwd(max_len, c->rows, p->D, p->G, p->N);
-  const size_t parts = static_cast<size_t>(c->split.segs) * p->num_seqs;
+  c->parts = c->rows / c->split.len + p->num_seqs;
+  const size_t parts = static_cast<size_t>(c->parts);
   c->saved = static_cast<size_t>(gdn::scan_slots(c->rows, p->num_seqs)) * c->a;
   if (c->split.segs > 1) {
     c->seg_end = up256(parts * c->a);
@@ -186,6 +189,7 @@ gdn::ScanParams scan_params(const gdn_scan_problem* p, const ScanSize& c, const 
   sp.nseq = p->num_seqs; sp.D = p->D; sp.G = p->G;
   sp.softplus = p->dt_softplus != 0;
   sp.segs = c.split.segs; sp.seg_len = c.split.len; sp.in_time = c.split.in_time;
+  sp.parts = c.parts;
   sp.rows = c.rows;
   return sp;
 }

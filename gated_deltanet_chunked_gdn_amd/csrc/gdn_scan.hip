@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
   if (FULL) {
     load_states<S>(p.h0 + static_cast<int64_t>(n) * p.D * N + hd, chan && p.h0, h);
     for (int g = 0; g < seg; ++g) {
-      const int64_t part = static_cast<int64_t>(g) * p.nseq + n;
+      const int64_t part = part_slot(p, bos, n, g);
       const float sum = chan ? p.seg_sum[part * p.D + ct.d0 + c] : 0.f;
       float e[S];
       load_states<S>(p.seg_end + part * p.D * N + hd, chan, e);
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
   if (FULL) {
     if (seg == last && p.h_final && chan) store_states<S>(p.h_final + static_cast<int64_t>(n) * p.D * N + hd, h);
   } else {
-    const int64_t part = static_cast<int64_t>(seg) * p.nseq + n;
+    const int64_t part = part_slot(p, bos, n, seg);
     if (chan) store_states<S>(p.seg_end + part * p.D * N + hd, h);
     sums[q][c] = dsum;
     __syncthreads();

@@ -204,7 +204,7 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
     if (t0 > begin) put(b ^ 1, t0 - TT);
     __syncthreads();
   }
-  const int64_t pt = static_cast<int64_t>(seg) * p.nseq + n;
+  const int64_t pt = part_slot(p, bos, n, seg);
   if (chan) store_states<S>(p.seg_end + pt * p.D * N + hd, G);
   part[at.q][at.c] = dsum;
   __syncthreads();
@@ -229,7 +229,8 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   chunk::seq_range(p.seq, n, bos, len);
   const int last = len > 0 ? static_cast<int>((len - 1) / p.seg_len) : 0;
   const int64_t begin = seg * p.seg_len, end = min(len, begin + p.seg_len);
-  const int64_t part = static_cast<int64_t>(seg) * p.nseq + n;
+  if (seg > last) return;
+  const int64_t part = part_slot(p, bos, n, seg);
 
   __shared__ Stage<N, TT> st;
   __shared__ ChannelParams cp;
@@ -254,7 +255,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
       dA[s] = 0.f;
     }
     for (int g = last; g > seg; --g) {
-      const int64_t pt = static_cast<int64_t>(g) * p.nseq + n;
+      const int64_t pt = part_slot(p, bos, n, g);
       const float sum = chan ? p.seg_sum[pt * p.D + ct.d0 + at.c] : 0.f;
       float e[SG];
       load_states<SG>(p.seg_end + pt * p.D * N + hd + k * NW, chan, e);
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
     }
   }
   // what goes over the tokens: dA of this lane's states, dD and ddt_bias of the tile's channels
-  const int64_t pa = (part * p.D + ct.d0) * (N + 2);
+  float* const sums_a = p.part_a + (part * p.D + ct.d0) * (N + 2);
 #pragma unroll
   for (int k = 0; k < NG; ++k) {
     if constexpr (NG > 1) {
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
     }
     if (chan) {
 #pragma unroll
-      for (int s = 0; s < SG; ++s) p.part_a[pa + at.c * (N + 2) + k * NW + at.q * SG + s] = dA[s];
+      for (int s = 0; s < SG; ++s) sums_a[at.c * (N + 2) + k * NW + at.q * SG + s] = dA[s];
       if (seg == 0 && p.dh0) store_states<SG>(p.dh0 + static_cast<int64_t>(n) * p.D * N + hd + k * NW, G);
     }
   }
@@ -439,7 +440,12 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
     float sum = 0.f;
 #pragma unroll
     for (int r = 0; r < TT; ++r) sum += sums[k][r][c];
-    if (c < ct.count) p.part_a[pa + c * (N + 2) + N + k] = sum;
+    if (c < ct.count) sums_a[c * (N + 2) + N + k] = sum;
+  }
+  if (seg == last) {  // slots that no segment has, up to the next sequence's
+    const int64_t next = (bos + len) / p.seg_len + n + 1;
+    for (int64_t s = part + 1; s < next; ++s)
+      for (int i = tid; i < ct.count * (N + 2); i += 256) p.part_a[(s * p.D + ct.d0) * (N + 2) + i] = 0.f;
   }
 }
 
@@ -502,7 +508,7 @@ hipError_t bwd_t(const ScanParams& p, hipStream_t s) {
   }
   const int64_t bc = static_cast<int64_t>(blocks_of(p.rows * p.G * N / 2)) * 256;
   hipLaunchKernelGGL((scan_bwd_finish_kernel<E, N>), dim3(blocks_of(bc + static_cast<int64_t>(p.D) * (N + 2))), dim3(256), 0,
-                     s, p, static_cast<int>(tiles / p.G), bc, static_cast<int64_t>(p.segs) * p.nseq);
+                     s, p, static_cast<int>(tiles / p.G), bc, p.parts);
   return hipGetLastError();
 }
 

@@ -46,6 +46,12 @@ __device__ __forceinline__ int64_t saved_slot(int64_t bos, int n, int64_t t) {
   return bos / kScanBlock + n + t / kScanBlock;
 }
 
+// Slot of segment `seg` of sequence n in the buffers of segments; its slots and those of
+// the next sequence (the slots behind its last segment are at most two).
+__device__ __forceinline__ int64_t part_slot(const ScanParams& p, int64_t bos, int n, int seg) {
+  return bos / p.seg_len + n + seg;
+}
+
 template <int S>
 __device__ __forceinline__ void load_states(const float* p, bool ok, float (&f)[S]) {
 #pragma unroll

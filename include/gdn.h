@@ -480,8 +480,8 @@ gdn_status gdn_conv_step(const gdn_conv_problem* problem, const void* x, const f
  * where grp(d) = d / (D / G).  Tensors: u, dt, z, y [B,T,D], Bm, Cm [B,T,G,N] (io
  * dtype); A [D,N], Dskip, dt_bias [D], h0, h_final [num_seqs,D,N] fp32.  All of them
  * 16-byte aligned.  Supported: N in {8, 16, 32, 64}, D / G a multiple of 8, D up to
- * 2^20, B T G < 2^31, up to 65535 sequences, else GDN_ERR_UNSUPPORTED.  A <= 0 and delta >= 0 are
- * documented, not checked.  All arithmetic is fp32; io outputs are rounded once. */
+ * 2^20, B T < 2^31, B T G N < 2^32, up to 65535 sequences, else GDN_ERR_UNSUPPORTED.
+ * Finite A <= 0 and delta >= 0 are documented, not checked.  All arithmetic is fp32; io outputs are rounded once. */
 typedef struct gdn_scan_problem {
   int32_t B, T, D, N, G;
   int32_t num_seqs;                /* == B for dense input, else len(cu_seqlens) - 1        */

@@ -87,6 +87,59 @@ def test_split_over_time(T, D, N, cu):
         ref.check(key, got[key], want[key], size[key], 6 * T + N + D + T + 128)
 
 
+def test_many_short_sequences_and_a_long_one():
+    """Slots of segments that no sequence has, between those that have one."""
+    cu = [0, 0]
+    for n in range(60):
+        cu.append(cu[-1] + (1, 0, 17, 5, 63, 2)[n % 6])
+    cu += [cu[-1] + 700, cu[-1] + 701, cu[-1] + 701]
+    T, D, N = cu[-1], 40, 32
+    a, h0, dy, dl = _inputs(1, T, D, N, 1, F32, cu=cu)
+    want, size = _ref(a, h0, cu, True, dy, dl), _ref(a, h0, cu, True, dy, dl, size=True)
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0, cu_seqlens=cu)
+    ws = torch.full((gdn.scan_buffers(a["u"], a["Bm"], cu_seqlens=cu)["backward"],), 255, dtype=torch.uint8, device=DEV)  # NaN
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu, workspace=ws)
+    ref.check("y", y, want["y"], size["y"], 3 * 700 + N + 64)
+    ref.check("state", h, want["state"], size["state"], 3 * 700 + 64)
+    for key in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"):
+        ref.check(key, got[key], want[key], size[key], 6 * 700 + N + D + T + 128)
+
+
+def test_optional_outputs_of_the_c_abi():
+    """dDskip without Dskip and ddt_bias without dt_bias may be asked for; dDskip, dz,
+    ddt_bias and dh0 need not be."""
+    import ctypes
+
+    from gated_deltanet_chunked_gdn_amd import _native as nat
+
+    B, T, D, N = 2, 40, 72, 16
+    a, _, dy, _ = _inputs(B, T, D, N, 1, F32, skip=False, bias=False, state=False)
+    _, _, saved = gdn.scan_fwd_save(**a)
+    full = gdn.scan_bwd_saved(**a, dy=dy, saved=saved)
+    want = _ref(a, None, None, True, dy)
+    size = _ref(a, None, None, True, dy, size=True)
+    lib, prob = nat.load(), nat.ScanProblem(B, T, D, N, 1, B, None, None, nat.GDN_FP32, 1)
+    ws = torch.empty(gdn.scan_buffers(a["u"], a["Bm"])["backward"], dtype=torch.uint8, device=DEV)
+
+    def call(**asked):
+        out = {k: torch.empty_like(full[k]) for k in ("du", "ddt", "dA", "dB", "dC")}
+        out.update(asked)
+        names = ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0")
+        ins = [a[k] for k in ("u", "dt", "A", "Bm", "Cm", "D", "z", "dt_bias")] + [dy, None, saved]
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        st = lib.gdn_scan_bwd_saved(ctypes.byref(prob), *map(p, ins), saved.numel(), *(p(out.get(k)) for k in names), p(ws), ws.numel(),
+                                    torch.cuda.current_stream().cuda_stream)
+        assert st == nat.GDN_OK
+        return out
+
+    none = call()
+    for k in ("du", "ddt", "dA", "dB", "dC"):
+        assert torch.equal(none[k], full[k]), k
+    more = call(dD=torch.empty(D, device=DEV), ddt_bias=torch.empty(D, device=DEV))
+    for k in ("dD", "ddt_bias"):
+        ref.check(k, more[k], want[k], size[k], 7 * T + N + D + 128)
+
+
 @pytest.mark.parametrize("io", [BF, F32])
 def test_raw_steps_and_extremes(io):
     """No softplus; steps of zero (the state stays), large steps (it is forgotten), and

@@ -21,7 +21,8 @@ def _inputs(B, H, Dk, Dv, io, channel, seed=0):
 
 @pytest.mark.parametrize("channel", [False, True])
 @pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("B,H,Dk,Dv", [(1, 1, 64, 16), (1, 8, 128, 128), (3, 5, 64, 80), (2, 3, 128, 256), (17, 2, 128, 48)])
+@pytest.mark.parametrize("B,H,Dk,Dv", [(1, 1, 64, 16), (1, 8, 128, 128), (3, 5, 64, 80), (2, 3, 128, 256), (17, 2, 128, 48),
+                                       (64, 10, 128, 112), (300, 9, 64, 80)])  # the last two: states past the caches (32 MB)
 def test_step(B, H, Dk, Dv, io, channel):
     t, S = _inputs(B, H, Dk, Dv, io, channel)
     o_ref, S_ref = ref.delta_step(**t, S=S, scale=0.7)

@@ -158,6 +158,7 @@ def scan_size(p, pass_):
     (dict(num_seqs=1), nat.GDN_ERR_SHAPE), (dict(B=70000, num_seqs=70000, T=1), nat.GDN_ERR_UNSUPPORTED),
     (dict(B=50000, num_seqs=50000, T=50000), nat.GDN_ERR_UNSUPPORTED),
     (dict(B=40000, num_seqs=40000, T=40000, D=64, G=8), nat.GDN_ERR_UNSUPPORTED),
+    (dict(B=4000, num_seqs=4000, T=100000), nat.GDN_ERR_UNSUPPORTED),
 ])
 def test_scan_problem(lib, kw, status):
     p = scan_problem(**kw)
@@ -183,8 +184,13 @@ def test_scan_sizes():
     # no sequences and no tokens need next to nothing
     assert scan_size(scan_problem(B=0, num_seqs=0), nat.GDN_SCAN_BWD) == (nat.GDN_OK, 0)
     # a large batch stays within 64-bit sizes
-    st, n = scan_size(scan_problem(B=4000, num_seqs=4000, T=100000, D=8192), nat.GDN_SCAN_BWD)
+    st, n = scan_size(scan_problem(B=2000, num_seqs=2000, T=100000, D=8192), nat.GDN_SCAN_BWD)
     assert st == nat.GDN_OK and n > 1 << 40
+    # many short packed sequences beside a long one: slots by tokens, not by the longest
+    cu = [0] + list(range(8192, 8192 + 5001))
+    p = scan_problem(B=1, T=cu[-1], num_seqs=len(cu) - 1, D=1024, cu_seqlens_host=offsets(cu), cu_seqlens_dev=P)
+    st, n = scan_size(p, nat.GDN_SCAN_FWD)
+    assert st == nat.GDN_OK and n < 5600 * 1024 * 17 * 4
 
 
 def test_scan_pointers(lib):
