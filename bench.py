@@ -73,7 +73,58 @@ def event_times(call, n_calls, warmup, stream):
     return np.array([a.elapsed_time(b) for a, b in ev]) * 1e-3
 
 
+# the operators around the delta rule, timed with --extra only
+LAYER_EXTRAS = ("step", "conv", "scan")
 EXTRAS = ("bwd", "segment_split", "prologue", "epilogue", "kda", "kda_bwd", "kda_segment_split", "policy")
+
+
+def layer_measurements(gdn, dev, steps, warmup, which):
+    """The single-token delta rule step, the short convolution and the selective scan at
+    a decoding, a prompt and a training shape each: milliseconds a call (HIP events) and
+    the bytes that a call cannot do without."""
+    import torch
+
+    stream = torch.cuda.current_stream(dev)
+    gen = torch.Generator(device=dev).manual_seed(0)
+    bf = torch.bfloat16
+
+    def rand(*s, std=1.0, dtype=bf):
+        return (torch.randn(*s, generator=gen, device=dev) * std).to(dtype)
+
+    f32 = torch.float32
+
+    def timed(call, nbytes):
+        kt = float(event_times(lambda i: call(), steps, warmup, stream).mean())
+        return {"ms_mean": kt * 1e3, "alg_bytes": nbytes, "alg_GBps": nbytes / kt / 1e9}
+
+    out = {}
+    if which == "step":
+        for B, H in ((1, 8), (128, 16)):
+            D = 128
+            q, k, v = (rand(B, 1, H, D, std=D ** -0.5) for _ in range(3))
+            g, beta, S = -rand(B, 1, H, dtype=f32).abs(), torch.rand(B, 1, H, device=dev), rand(B, H, D, D, std=0.1, dtype=f32)
+            out[f"B{B}_H{H}_d128_bf16"] = timed(lambda: gdn.step(q, k, v, g, beta, S), 2 * S.numel() * 4)
+    elif which == "conv":
+        B, T, C, W = 4, 4096, 2048, 4
+        x, dy, w, b = rand(B, T, C), rand(B, T, C), rand(C, W, dtype=f32), rand(C, dtype=f32)
+        xs, state = rand(256, 1, C), rand(256, W - 1, C)
+        out["fwd_B4_T4096_C2048_bf16"] = timed(lambda: gdn.conv_fwd(x, w, bias=b), 2 * x.numel() * 2)
+        out["bwd_B4_T4096_C2048_bf16"] = timed(lambda: gdn.conv_bwd(x, w, dy, bias=b), 3 * x.numel() * 2)
+        out["step_B256_C2048_bf16"] = timed(lambda: gdn.conv_step(xs, w, state, bias=b), 2 * W * xs.numel() * 2)
+    else:
+        B, T, D, N = 4, 2048, 2048, 16
+        u, dt, z, dy = rand(B, T, D), rand(B, T, D), rand(B, T, D), rand(B, T, D)
+        A, Bm, Cm = -torch.rand(D, N, device=dev) - 0.1, rand(B, T, 1, N), rand(B, T, 1, N)
+        kw = dict(D=rand(D, dtype=f32), z=z, dt_bias=rand(D, dtype=f32) - 3)
+        _, _, saved = gdn.scan_fwd_save(u, dt, A, Bm, Cm, **kw)
+        kept = saved.numel()
+        out["fwd_B4_T2048_D2048_N16_bf16"] = timed(lambda: gdn.scan_fwd(u, dt, A, Bm, Cm, **kw), 4 * u.numel() * 2)
+        out["fwd_save"] = timed(lambda: gdn.scan_fwd_save(u, dt, A, Bm, Cm, saved=saved, **kw), 4 * u.numel() * 2 + kept)
+        out["bwd_saved"] = timed(lambda: gdn.scan_bwd_saved(u, dt, A, Bm, Cm, dy, saved, **kw), 7 * u.numel() * 2 + kept)
+        us, zs, h = rand(64, 1, D), rand(64, 1, D), rand(64, D, N, dtype=f32)
+        Bs, Cs = rand(64, 1, 1, N), rand(64, 1, 1, N)
+        out["step_B64_D2048_N16_bf16"] = timed(lambda: gdn.scan_step(us, us, A, Bs, Cs, h, **dict(kw, z=zs)), 2 * h.numel() * 4)
+    return out
 
 
 def extra_measurements(gdn, generate, WORKLOADS, dev, steps, warmup, which=EXTRAS):
@@ -372,7 +423,7 @@ def parse():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-extras", action="store_true",
                     help="skip the measurements of the other passes")
-    ap.add_argument("--extra", choices=EXTRAS, default=None,
+    ap.add_argument("--extra", choices=EXTRAS + LAYER_EXTRAS, default=None,
                     help="time only this other pass (HIP events) and print its JSON object")
     ap.add_argument("--cpu-seconds", type=float, default=10.0,
                     help="approximate CPU time budget of the oracle baseline")
@@ -504,6 +555,10 @@ def main():
         sys.exit(1)
     if args.extra:
         dev = torch.device("cuda:0")
+        if args.extra in LAYER_EXTRAS:
+            res = layer_measurements(gdn, dev, args.steps, args.warmup, args.extra)
+            print(json.dumps({"extra": args.extra, **res}), flush=True)
+            return
         res = extra_measurements(gdn, generate, WORKLOADS, dev, args.steps, args.warmup, (args.extra,))
         print(json.dumps({"extra": args.extra, **res[args.extra]}), flush=True)
         return

@@ -257,7 +257,17 @@ def _scan_inputs(p, u, dt, A, Bm, Cm, D, z, dt_bias, dev):
 
 
 def _scan_size(prob, pass_):
+    if not prob.cu_seqlens_host:
+        return _dense_scan_size(prob.B, prob.T, prob.D, prob.N, prob.G, prob.io_dtype, pass_)
     n = ctypes.c_size_t(0)
+    nat.check(nat.load().gdn_scan_workspace_size(prob, pass_, n), "gdn_scan_workspace_size")
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _dense_scan_size(B, T, D, N, G, io, pass_):
+    n = ctypes.c_size_t(0)
+    prob = nat.ScanProblem(B, T, D, N, G, B, None, None, io, 1)
     nat.check(nat.load().gdn_scan_workspace_size(prob, pass_, n), "gdn_scan_workspace_size")
     return n.value
 
