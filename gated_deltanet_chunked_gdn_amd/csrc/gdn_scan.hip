@@ -10,7 +10,7 @@
 //   * four lanes share a channel, each holding N / 4 of its states in registers; the
 //     states of one lane are contiguous, so B and C come from LDS as wide reads that
 //     sixteen channels share;
-//   * a workgroup of four waves (64 channels) stages a tile of 32 tokens: delta and
+//   * a workgroup of four waves (64 channels) stages a tile of 16 tokens: delta and
 //     delta u are formed once per (token, channel), the softplus with them;
 //   * the four partial outputs of a channel are reduced for four tokens at a time by
 //     two lane swaps (v_permlane32_swap, v_permlane16_swap): three swaps and three
@@ -160,7 +160,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
 
 // One token: four lanes a channel, N / 4 contiguous states each (a wave covers 16
 // channels' states as one contiguous piece).  The state is read and written once: 64 x
-// 4096 x 16, 36 MB, takes 9.2 us (3.9 TB/s); two, four or eight sequences a thread take
+// 4096 x 16, 36 MB, takes 9.1 us (4.0 TB/s); two, four or eight sequences a thread take
 // as long or longer.
 template <typename E, int N>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanParams p) {

@@ -22,10 +22,7 @@ namespace scan {
 
 using namespace layer;
 
-#ifndef KT
-#define KT 16
-#endif
-constexpr int kTile = KT;     // tokens staged at a time
+constexpr int kTile = 16;     // tokens staged at a time
 constexpr int kYStride = 80;  // row stride of output tiles: the four token rows a wave writes fall in other banks
 
 // A workgroup's channels d0 .. d0 + count - 1, all of group g.
