@@ -19,7 +19,9 @@ template <typename E>
 constexpr int kVec = 16 / static_cast<int>(sizeof(E));
 // Channels of a thread in the forward: eight-byte bf16 loads leave registers for more
 // waves (runs of eight rows of 4 x 4096 x 2048 bf16, 134 MB: 29 us, 4.6 TB/s; 33 us
-// with eight channels).
+// with eight channels).  The rows two runs share cost 25 MB more reads; neighbouring runs
+// on one XCD take most of that back but no time (29 us in groups of up to 32, 34 us with
+// a contiguous eighth of the rows on each XCD).
 constexpr int kWalkV = 4;
 
 // One thread's channels: weights, bias, and the reading of input and state rows.
@@ -187,9 +189,9 @@ __device__ __forceinline__ float silu_grad(float p, float dy) {
 // their dp alone), two rows at a time with the next two in flight; four channels
 // rather than eight halve the registers of the weights and their gradients, for four
 // waves a SIMD (4 x 4096 x 2048 bf16, 201 MB: 51 us, 3.9 TB/s; with eight channels and two
-// waves 80 us, with four rows ahead and three waves 61 us).  A workgroup covers 512 rows of 64 channels: its sums of dp x and dp are
-// reduced over the runs (lanes, then waves) and written once, and a second kernel adds
-// the workgroups' sums in order.
+// waves 80 us, with four rows ahead and three waves 61 us).  A workgroup covers 512 rows
+// of 64 channels: its sums of dp x and dp are reduced over the runs (lanes, then waves)
+// and written once, and a second kernel adds the workgroups' sums in order.
 constexpr int kBwdV = 4, kBwdRun = 32, kBwdLanes = 16, kBwdAhead = 2;
 static_assert(256 / kBwdLanes * kBwdRun == kConvBwdRows, "rows of a workgroup");
 

@@ -19,7 +19,7 @@
 // Bound by vector instructions, as the forward, with the sums over the channels on top:
 // 23.5 a token, channel and state.  4 x 2048 tokens, 2048 channels, 16 states, bf16, with
 // z: main kernel 219 us (its waves issue a vector instruction in 87 % of the cycles; the
-// 240 MB it moves would take 47), summary of the segments 63, last kernel 11.  Measured
+// 345 MB it moves would take 67), summary of the segments 63, last kernel 11.  Measured
 // and not kept: those sums by fp32 matrix instructions (381 us: the operands' layout
 // costs more moves than the adds it saves), decays formed twice instead of kept, at three
 // waves a SIMD (252).
