@@ -220,6 +220,34 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
     p.seg_sum[pt * p.D + ct.d0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
 }
 
+// G through the segments at `slot`, slot - 1, ... (`count` of them): sum and end are this
+// lane's places in a slot of seg_sum and seg_end, its states NG pieces NW apart.  The
+// loads of several segments are in flight together.
+template <int NG, int SG>
+__device__ __forceinline__ void compose(const ScanParams& p, const float* sum, const float* end, int64_t slot,
+                                        int count, const float (&A2)[NG][SG], float (&G)[NG][SG]) {
+  constexpr int M = NG * SG > 8 ? 2 : 4, NW = 4 * SG;
+  const int64_t state = static_cast<int64_t>(p.D) * NG * NW;
+  for (int i = 0; i < count; i += M) {
+    float x[M], e[M][NG][SG];
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int64_t at = slot - min(i + j, count - 1);
+      x[j] = sum[at * p.D];
+#pragma unroll
+      for (int k = 0; k < NG; ++k) load_states<SG>(end + at * state + k * NW, true, e[j][k]);
+    }
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      if (i + j >= count) break;
+#pragma unroll
+      for (int k = 0; k < NG; ++k)
+#pragma unroll
+        for (int s = 0; s < SG; ++s) G[k][s] = fmaf(exp2_(A2[k][s] * x[j]), G[k][s], e[j][k][s]);
+    }
+  }
+}
+
 // GATED: dz is wanted, and with it the outputs before the gate.
 template <typename E, int N, bool GATED>
 __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
@@ -253,26 +281,29 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   // the lane's states of pass k: q SG + NW k .. + SG - 1
   const int64_t hd = static_cast<int64_t>(ct.d0 + at.c) * N + at.q * SG;
   float A2[SG], G[SG], dA[SG];
+  {
+    float Ak[NG][SG], Gk[NG][SG];
 #pragma unroll
-  for (int k = NG - 1; k >= 0; --k) {
-    load_states<SG>(p.A + hd + k * NW, chan, A2);
-    load_states<SG>(p.dh_final + static_cast<int64_t>(n) * p.D * N + hd + k * NW, chan && p.dh_final, G);
+    for (int k = 0; k < NG; ++k) {
+      load_states<SG>(p.A + hd + k * NW, chan, Ak[k]);
+      load_states<SG>(p.dh_final + static_cast<int64_t>(n) * p.D * N + hd + k * NW, chan && p.dh_final, Gk[k]);
+#pragma unroll
+      for (int s = 0; s < SG; ++s) Ak[k][s] *= kLog2e;
+    }
+    if (chan)
+      compose<NG, SG>(p, p.seg_sum + ct.d0 + at.c, p.seg_end + hd, part_slot(p, bos, n, last), last - seg, Ak, Gk);
 #pragma unroll
     for (int s = 0; s < SG; ++s) {
-      A2[s] *= kLog2e;
+      A2[s] = Ak[0][s];
+      G[s] = Gk[0][s];
       dA[s] = 0.f;
     }
-    for (int g = last; g > seg; --g) {
-      const int64_t pt = part_slot(p, bos, n, g);
-      const float sum = chan ? p.seg_sum[pt * p.D + ct.d0 + at.c] : 0.f;
-      float e[SG];
-      load_states<SG>(p.seg_end + pt * p.D * N + hd + k * NW, chan, e);
-#pragma unroll
-      for (int s = 0; s < SG; ++s) G[s] = fmaf(exp2_(A2[s] * sum), G[s], e[s]);
-    }
     if constexpr (NG > 1) {
-      carry[2 * k][tid] = f32x4_t{G[0], G[1], G[2], G[3]};
-      carry[2 * k + 1][tid] = zero4();
+#pragma unroll
+      for (int k = 0; k < NG; ++k) {
+        carry[2 * k][tid] = f32x4_t{Gk[k][0], Gk[k][1], Gk[k][2], Gk[k][3]};
+        carry[2 * k + 1][tid] = zero4();
+      }
     }
   }
 
