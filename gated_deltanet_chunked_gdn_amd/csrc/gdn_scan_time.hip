@@ -1,7 +1,7 @@
-// The selective scan's forward with the time axis inside the workgroup, on gfx950, for 8
-// and 16 states a channel.
+// The selective scan's forward with the time axis inside the workgroup, on gfx950.
 //
-// Four waves hold the same 16 channels and take 16 consecutive tokens each, 64 a step.
+// Four waves hold the same 16 channels (8 of 32 states, 4 of 64: four states a lane) and
+// take 16 consecutive tokens each, 64 a step.
 // A wave forms its tokens' decays a and writes w = delta u B once, keeps them in
 // registers (16 tokens x N / 4 states x 2) while it runs h <- a h + w from zero to its
 // end, and passes (product of the decays, end state) through LDS.  Every wave then folds
@@ -14,12 +14,15 @@
 // Measured, bf16, 16 states, forward: 2 x 2048 x 4096 110 us (137 us split over segments),
 // 1 x 128 x 1024 7.1 us (19 us: one launch instead of two); 73 % of the cycles issue vector
 // instructions, 9.7 a token, channel and state with the staging and the gate, at the two
-// waves a SIMD that the registers leave.
+// waves a SIMD that the registers leave.  64 states: six packed prompts, 3001 x 1024, 75 us
+// (93 us split).
 //
 // Each wave stages its own tokens; one barrier a step, for the pairs.  Workgroups of
-// neighbouring channels share cache lines (32-byte row pieces), so eight of them in a row
+// neighbouring channels share cache lines (row pieces of 8 to 64 bytes), so eight in a row
 // of the grid lie 64 channels apart, and the neighbours follow on the same XCD.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "gdn_scan_device.h"
 
@@ -29,15 +32,30 @@ namespace {
 using namespace layer;
 using namespace scan;
 
-constexpr int kCh = 16;    // channels of a workgroup
 constexpr int kTok = 16;   // tokens of a wave
 constexpr int kStep = 64;  // tokens of a step
 
+// One or two values as loaded (Raw takes whole vectors of 8 or 16 bytes).
+template <typename E, int NV>
+struct alignas(NV * sizeof(E)) Few {
+  E v[NV];
+  __device__ __forceinline__ void load(const E* p) { *this = *reinterpret_cast<const Few*>(p); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = E(0);
+  }
+  __device__ __forceinline__ float get(int e) const { return IoT<E>::ld(&v[e]); }
+};
+template <typename E, int NV>
+using Vals = std::conditional_t<NV * sizeof(E) >= 8, Raw<E, NV>, Few<E, NV>>;
+
 template <typename E, int N>
 __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int tiles) {
-  constexpr int S = N / 4, P = N / 4;  // states of a lane; a lane's values of one token's B and C
+  constexpr int kCh = scan_time_channels(N), EL = kCh / 4;
+  constexpr int S = kCh * N / 64, P = N / 4;  // states of a lane; a lane's values of one token's B and C
+  constexpr int kRow = N > 16 ? N + 4 : N;    // stride of B and C rows: the rows that a wave writes at once fall in other banks
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, q = lane >> 4;
+  const int c = lane % kCh, q = lane / kCh;
   const int n = blockIdx.y;
   // tile: 8 XCDs take workgroups in turn, so workgroups x, x + 8, ... share one
   const int x = blockIdx.x, per = (tiles + 7) / 8, tile = (x & 7) * per + (x >> 3);
@@ -47,9 +65,9 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
   int64_t bos, len;
   chunk::seq_range(p.seq, n, bos, len);
 
-  __shared__ float2 dd[4][kTok][kCh];
-  __shared__ float Bs[4][kTok][N], Cs[4][kTok][N];
-  __shared__ float ys[4][kTok][kCh + 4];
+  __shared__ alignas(16) float2 dd[4][kTok][kCh];
+  __shared__ alignas(16) float Bs[4][kTok][kRow], Cs[4][kTok][kRow];
+  __shared__ alignas(16) float ys[4][kTok][kCh + 4];
   __shared__ float pair[2][4][2][64][S];  // decay product, end state of each wave
 
   const bool chan = c < count;
@@ -60,52 +78,53 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
 #pragma unroll
   for (int s = 0; s < S; ++s) A2[s] *= kLog2e;
 
-  // this lane's share of the wave's tile: four channels of one token
-  const int row = lane >> 2, piece = lane & 3, col = piece * 4;
+  // this lane's share of the wave's tile: a quarter of the channels of one token
+  const int row = lane >> 2, piece = lane & 3, col = piece * EL;
   const bool live = col < count;
   const int d = d0 + (live ? col : 0);
-  Raw<float, 4> bias, skip;
+  Vals<float, EL> bias, skip;
   bias.zero();
   skip.zero();
   if (p.dt_bias) bias.load(p.dt_bias + d);
   if (p.Dskip) skip.load(p.Dskip + d);
-  Raw<E, 4> ru, rdt, rz;
-  E rb[P], rc[P];
+  Vals<E, EL> ru, rdt, rz;
+  Vals<E, P> rb, rc;
   auto fetch = [&](int64_t t0) {
     const int64_t t = bos + min(t0 + wave * kTok + row, len - 1);
     ru.load(static_cast<const E*>(p.u) + t * p.D + d);
     rdt.load(static_cast<const E*>(p.dt) + t * p.D + d);
     if (p.z) rz.load(static_cast<const E*>(p.z) + t * p.D + d);
     const int64_t bc = (t * p.G + g) * N + piece * P;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      rb[i] = static_cast<const E*>(p.Bm)[bc + i];
-      rc[i] = static_cast<const E*>(p.Cm)[bc + i];
-    }
+    rb.load(static_cast<const E*>(p.Bm) + bc);
+    rc.load(static_cast<const E*>(p.Cm) + bc);
   };
   if (len > 0) fetch(0);
   int buf = 0;
   for (int64_t t0 = 0; t0 < len; t0 += kStep, buf ^= 1) {
     const int64_t t = t0 + wave * kTok + row;
     const bool ok = t < len;
-    const Raw<E, 4> cu = ru, cz = rz;
-    float delta[4], sig;
+    const Vals<E, EL> cu = ru, cz = rz;
+    float delta[EL], sig;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) delta[e] = rdt.get(e) + bias.get(e);
+    for (int e = 0; e < EL; ++e) delta[e] = rdt.get(e) + bias.get(e);
     if (p.softplus) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) delta[e] = softplus_(delta[e], sig);
+      for (int e = 0; e < EL; ++e) delta[e] = softplus_(delta[e], sig);
     }
+    if constexpr (EL == 1) {
+      dd[wave][row][col] = ok && live ? float2{delta[0], delta[0] * cu.get(0)} : float2{0.f, 0.f};
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      float4 v = {delta[e], delta[e] * cu.get(e), delta[e + 1], delta[e + 1] * cu.get(e + 1)};
-      if (!ok || !live) v = float4{0.f, 0.f, 0.f, 0.f};
-      *reinterpret_cast<float4*>(&dd[wave][row][col + e]) = v;
+      for (int e = 0; e < EL; e += 2) {
+        float4 v = {delta[e], delta[e] * cu.get(e), delta[e + 1], delta[e + 1] * cu.get(e + 1)};
+        if (!ok || !live) v = float4{0.f, 0.f, 0.f, 0.f};
+        *reinterpret_cast<float4*>(&dd[wave][row][col + e]) = v;
+      }
     }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      Bs[wave][row][piece * P + i] = ok ? IoT<E>::ld(&rb[i]) : 0.f;
-      Cs[wave][row][piece * P + i] = ok ? IoT<E>::ld(&rc[i]) : 0.f;
+      Bs[wave][row][piece * P + i] = ok ? rb.get(i) : 0.f;
+      Cs[wave][row][piece * P + i] = ok ? rc.get(i) : 0.f;
     }
     if (t0 + kStep < len) fetch(t0 + kStep);
     __builtin_amdgcn_wave_barrier();
@@ -162,21 +181,33 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
           acc[i] = fmaf(h[s], Cv[s], acc[i]);
         }
       }
-      ys[wave][j + q][c] = reduce_rows4(acc[0], acc[1], acc[2], acc[3]);
+      float sum = reduce_rows4(acc[0], acc[1], acc[2], acc[3]);  // lanes of row t: token j + t
+      if (kCh < 16) sum += dpp_f32<0x128, 0xf>(sum);
+      if (kCh < 8) sum += dpp_f32<0x124, 0xf>(sum);
+      if ((lane & 15) < kCh) ys[wave][j + (lane >> 4)][c] = sum;
     }
     __builtin_amdgcn_wave_barrier();
     if (ok && live) {
-      const float4 yv = *reinterpret_cast<const float4*>(&ys[wave][row][col]);
-      float y[4] = {yv.x, yv.y, yv.z, yv.w};
+      Vals<float, EL> yv;
+      yv.load(&ys[wave][row][col]);
+      float y[EL];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = fmaf(skip.get(e), cu.get(e), y[e]);
+      for (int e = 0; e < EL; ++e) {
+        y[e] = fmaf(skip.get(e), cu.get(e), yv.get(e));
         if (p.z) {
           const float z = cz.get(e);
           y[e] *= z * sigmoid_(z);
         }
       }
-      store_vec<E, 4>(static_cast<E*>(p.y) + (bos + t) * p.D + d, y);
+      E* const to = static_cast<E*>(p.y) + (bos + t) * p.D + d;
+      if constexpr (EL == 4) {
+        store_vec<E, EL>(to, y);
+      } else {
+        Few<E, EL> out;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) IoT<E>::st(&out.v[e], y[e]);
+        *reinterpret_cast<Few<E, EL>*>(to) = out;
+      }
     }
   }
   if (wave == 0 && p.h_final && chan) store_states<S>(p.h_final + static_cast<int64_t>(n) * p.D * N + hd, carry);
@@ -184,7 +215,7 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
 
 template <typename E, int N>
 hipError_t launch_t(const ScanParams& p, hipStream_t s) {
-  const int tiles = scan_time_tiles(p.D, p.G);
+  const int tiles = scan_time_tiles(p.D, p.G, N);
   hipLaunchKernelGGL((scan_time_kernel<E, N>), dim3((tiles + 7) / 8 * 8, static_cast<unsigned>(p.nseq)), dim3(256), 0, s, p, tiles);
   return hipGetLastError();
 }
@@ -192,8 +223,7 @@ hipError_t launch_t(const ScanParams& p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_scan_time(const ScanParams& p, int N, bool bf16, hipStream_t s) {
-  if (N == 8) return bf16 ? launch_t<uint16_t, 8>(p, s) : launch_t<float, 8>(p, s);
-  return bf16 ? launch_t<uint16_t, 16>(p, s) : launch_t<float, 16>(p, s);
+  GDN_SCAN_DISPATCH(launch_t)
 }
 
 }  // namespace gdn

@@ -200,3 +200,31 @@ def test_no_tokens_and_no_sequences():
     y, h, saved = gdn.scan_fwd_save(**a, h0=h0)
     got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl)
     assert y.shape == (0, 4, 16) and float(got["dA"].abs().max()) == 0
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("B,T,D,N,G,cu,split", [
+    (1, 1100, 24, 8, 1, None, True),
+    (1, 1100, 72, 16, 3, None, True),
+    (2, 1030, 40, 32, 1, None, True),
+    (1, 1500, 80, 32, 2, [0, 1000, 1003, 1003, 1500], True),
+    (1, 1100, 72, 64, 1, None, True),
+    (1, 1700, 16, 64, 2, [0, 0, 990, 1000, 1700], True),
+    (2, 16, 136, 32, 1, None, False),
+    (1, 45, 48, 64, 2, [0, 16, 16, 29, 45], False),
+    (1, 77, 24, 32, 1, [0, 77], False),
+    (1, 200, 12 * 8, 64, 3, [0, 64, 129, 200], False),
+])
+def test_every_form_and_width(B, T, D, N, G, cu, split, io):
+    """The forms over segments, over the time axis inside a workgroup, and serial, with
+    every number of states and both types."""
+    a, h0, dy, dl = _inputs(B, T, D, N, G, io, cu=cu, seed=5)
+    sizes = gdn.scan_buffers(a["u"], a["Bm"], cu_seqlens=cu)
+    assert (sizes["forward"] > 0) == split
+    want, size = _ref(a, h0, cu, True, dy, dl), _ref(a, h0, cu, True, dy, dl, size=True)
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0, cu_seqlens=cu)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl, cu_seqlens=cu)
+    ref.check("y", y, want["y"], size["y"], 3 * T + N + 64)
+    ref.check("state", h, want["state"], size["state"], 3 * T + 64)
+    for key in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"):
+        ref.check(key, got[key], want[key], size[key], 6 * T + N + D + T + 128)
