@@ -1,9 +1,8 @@
 // The selective scan's forward with the time axis inside the workgroup, on gfx950.
 //
 // Four waves hold the same 16 channels (8 of 32 states, 4 of 64: four states a lane) and
-// take 16 consecutive tokens each, 64 a step.
-// A wave forms its tokens' decays a and writes w = delta u B once, keeps them in
-// registers (16 tokens x N / 4 states x 2) while it runs h <- a h + w from zero to its
+// take 16 consecutive tokens each, 64 a step.  A wave forms its tokens' decays a and
+// writes w = delta u B once, keeps them in registers (16 tokens x 4 states x 2) while it runs h <- a h + w from zero to its
 // end, and passes (product of the decays, end state) through LDS.  Every wave then folds
 // the four pairs onto the carried state, which gives its own start and the next step's
 // carry, and runs its tokens again from the start: two more multiply-adds a state (the
@@ -18,8 +17,8 @@
 // (93 us split).
 //
 // Each wave stages its own tokens; one barrier a step, for the pairs.  Workgroups of
-// neighbouring channels share cache lines (row pieces of 8 to 64 bytes), so eight in a row
-// of the grid lie 64 channels apart, and the neighbours follow on the same XCD.
+// neighbouring channels share cache lines (row pieces of 8 to 64 bytes), so each XCD takes
+// an eighth of the channels: its workgroups follow each other eight apart in the grid.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

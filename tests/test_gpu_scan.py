@@ -228,3 +228,13 @@ def test_every_form_and_width(B, T, D, N, G, cu, split, io):
     ref.check("state", h, want["state"], size["state"], 3 * T + 64)
     for key in ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"):
         ref.check(key, got[key], want[key], size[key], 6 * T + N + D + T + 128)
+
+
+@pytest.mark.parametrize("T,D,N", [(16, 4112, 32), (13, 2064, 64)])
+def test_many_channels_and_few_tokens(T, D, N):
+    """Wide states in the serial form."""
+    a, h0, dy, dl = _inputs(1, T, D, N, 1, BF, seed=6)
+    want, size = _ref(a, h0, None, True), _ref(a, h0, None, True, size=True)
+    y, h = gdn.scan_fwd(**a, h0=h0)
+    ref.check("y", y, want["y"], size["y"], 3 * T + N + 64)
+    ref.check("state", h, want["state"], size["state"], 3 * T + 64)
