@@ -14,7 +14,8 @@
 // 1 x 128 x 1024 7.1 us (19 us: one launch instead of two); 73 % of the cycles issue vector
 // instructions, 9.7 a token, channel and state with the staging and the gate, at the two
 // waves a SIMD that the registers leave.  64 states: six packed prompts, 3001 x 1024, 75 us
-// (93 us split).
+// (93 us split).  Eight waves of eight tokens, at four waves a SIMD, gain nothing (131 us
+// for the first, the same for the last): they fold twice as often.
 //
 // Each wave stages its own tokens; one barrier a step, for the pairs.  Workgroups of
 // neighbouring channels share cache lines (row pieces of 8 to 64 bytes), so each XCD takes

@@ -238,3 +238,15 @@ def test_many_channels_and_few_tokens(T, D, N):
     y, h = gdn.scan_fwd(**a, h0=h0)
     ref.check("y", y, want["y"], size["y"], 3 * T + N + 64)
     ref.check("state", h, want["state"], size["state"], 3 * T + 64)
+
+
+@pytest.mark.parametrize("N", [8, 32, 64])
+def test_no_tokens_of_other_widths(N):
+    a, h0, dy, dl = _inputs(3, 0, 16, N, 1, BF)
+    y, h, saved = gdn.scan_fwd_save(**a, h0=h0)
+    got = gdn.scan_bwd_saved(**a, dy=dy, saved=saved, dh_final=dl)
+    assert y.shape == (3, 0, 16) and torch.equal(h, h0) and torch.equal(got["dh0"], dl)
+    a, h0, dy, dl = _inputs(1, 3, 16, N, 1, BF, cu=[0, 0, 3, 3])
+    y, h = gdn.scan_fwd(**a, h0=h0, cu_seqlens=[0, 0, 3, 3])
+    alone = gdn.scan_fwd(**a, h0=h0[1:2].contiguous())
+    assert torch.equal(h[[0, 2]], h0[[0, 2]]) and torch.equal(y, alone[0]) and torch.equal(h[1:2], alone[1])
