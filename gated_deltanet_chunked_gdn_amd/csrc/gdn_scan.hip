@@ -90,6 +90,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
     const Stage<N, kTile>& st = stage[b];
 #pragma unroll 2
     for (int t = 0; t < kTile; t += 4) {
+      __builtin_amdgcn_s_setprio(2);
       if (FULL && t % kScanBlock == 0 && p.saved && t0 + t < end && chan)
         store_states<S>(p.saved + saved_slot(bos, n, t0 + t) * p.D * N + hd, h);
       // four tokens' decays and writes first, then the chain through them: a wave
@@ -110,6 +111,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int s = 0; s < S; ++s) a[j][s] = exp2_(a[j][s]);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float Cv[S];
@@ -123,6 +125,7 @@ __global__ __launch_bounds__(256) void scan_fwd_kernel(ScanParams p) {
       }
       if (FULL) ybuf[b][t + q][c] = reduce_rows4(acc[0], acc[1], acc[2], acc[3]);
     }
+    __builtin_amdgcn_s_setprio(0);
     if (!FULL) {
 #pragma unroll
       for (int t = 0; t < kTile; t += 4) dsum += st.dd[t + q][c].x;

@@ -18,8 +18,8 @@
 //
 // Bound by vector instructions, as the forward, with the sums over the channels on top:
 // 23.5 a token, channel and state.  4 x 2048 tokens, 2048 channels, 16 states, bf16, with
-// z: main kernel 219 us (its waves issue a vector instruction in 87 % of the cycles; the
-// 345 MB it moves would take 67), summary of the segments 63, last kernel 11.  Measured
+// z: main kernel 205 us (222 without the wave priorities; the 345 MB it moves would take
+// 67), summary of the segments 60, last kernel 11.  Measured
 // and not kept: those sums by fp32 matrix instructions (381 us: the operands' layout
 // costs more moves than the adds it saves), decays formed twice instead of kept, at three
 // waves a SIMD (252).
@@ -189,6 +189,7 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
   float dsum = 0.f;
   for (int b = 0; t0 >= begin; t0 -= TT, b ^= 1) {
     if (t0 > begin) fetch(t0 - TT);
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll 2
     for (int t = TT - 4; t >= 0; t -= 4) {
       // four tokens' decays first, then the chain through them
@@ -209,6 +210,7 @@ __global__ __launch_bounds__(256) void scan_bwd_summary_kernel(ScanParams p) {
         for (int s = 0; s < S; ++s) G[s] = a[j][s] * fmaf(Cv[s], g[j], G[s]);
       }
     }
+    __builtin_amdgcn_s_setprio(0);
     if (t0 > begin) put(b ^ 1, t0 - TT);
     __syncthreads();
   }
@@ -351,6 +353,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
       // indexes the compiler cannot see through: on the way back the staged values are
       // read again rather than kept in (96) registers
       int ci = at.c, qi = at.q * SG + k * NW;
+      __builtin_amdgcn_s_setprio(2);
 #pragma unroll
       for (int tg = 0; tg < TT; tg += TG) {
         float v[16];
@@ -380,6 +383,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
         __builtin_amdgcn_sched_barrier(0);
       }
       asm volatile("" : "+v"(ci), "+v"(qi));
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int tg = TT - TG; tg >= 0; tg -= TG) {
         float v[16];
@@ -412,6 +416,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
         bc[wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
         __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_s_setprio(0);
       if constexpr (NG > 1) {
         carry[2 * k][tid] = f32x4_t{G[0], G[1], G[2], G[3]};
         carry[2 * k + 1][tid] = f32x4_t{dA[0], dA[1], dA[2], dA[3]};

@@ -43,28 +43,27 @@ ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G, int N) {
 }
 
 // The forward has a kernel with the time axis inside the workgroup.  It has no second pass
-// over the exponentials, but takes 64 tokens in 2.4 us however few its workgroups, 512 of
+// over the exponentials, but takes 64 tokens in 2.3 us however few its workgroups, 512 of
 // which the chip holds (a workgroup: 256 pairs of channel and state).  Measured against the
-// split, bf16, one sequence (us, time axis inside / split), for W workgroups (64 states: 64
-// in the first column):
-//                     W = 128      256        512        1024       2048       4096
-//   16 states   17   4.6 / 6.2  4.6 / 6.2  5.5 / 6.3  9.3 / 6.5   16 / 5.8
-//               64   4.7 / 8.9  4.8 / 9.1  5.9 / 10   9.8 / 14    17 / 14
-//              256    12 / 13    13 / 16    16 / 25    30 / 34    55 / 59
-//              512    22 / 17    23 / 25    29 / 37    52 / 58   101 / 109
-//             2048    84 / 43    84 / 66   101 / 118  217 / 210  383 / 392   754 / 584
-//   32 states   16   4.5 / 5.5  4.6 / 5.5  5.5 / 5.5  9.2 / 5.5   16 / 5.7
-//              512    22 / 24    22 / 25    27 / 36    51 / 58    97 / 95
-//             1024    40 / 31    42 / 40    51 / 62    96 / 105  188 / 179
-//             2048    81 / 46    83 / 70    96 / 108  188 / 198  405 / 350
-//   64 states   16   4.5 / 7.3  4.5 / 7.3  5.4 / 7.4  9.1 / 7.4
-//               64   4.6 / 15   4.6 / 15   5.5 / 16   9.2 / 16    16 / 23    30 / 22
-//              512    20 / 30    22 / 30    27 / 42    51 / 59    94 / 102  183 / 164
-//             1024    38 / 38    40 / 45    51 / 64    95 / 104  183 / 192  355 / 319
-//             2048    75 / 53    78 / 75    95 / 109  185 / 194  359 / 372  717 / 631
+// split, bf16, one sequence (us, time axis inside / split), for W workgroups:
+//          tokens    W = 64      128        256        512        1024       2048       4096
+//   16 states  16   4.4 / 4.4  4.4 / 4.5  4.5 / 4.5  5.1 / 4.7  8.7 / 4.7   15 / 5.3   28 / 7.2
+//              64   4.4 / 8.7  4.4 / 9.0  4.6 / 9.0  5.3 / 10   9.0 / 13    18 / 14    32 / 19
+//             256    11 / 11    11 / 12    12 / 15    15 / 24    26 / 32    47 / 49    91 / 61
+//             512    20 / 15    20 / 16    21 / 24    26 / 35    46 / 53    87 / 88   177 / 122
+//            2048    72 / 28    73 / 40    74 / 60    87 / 104  167 / 182  329 / 324  652 / 435
+//   32 states  16   4.4 / 5.4  4.4 / 5.4  4.5 / 5.4  5.2 / 5.4  8.9 / 5.5   16 / 5.7   29 / 6.9
+//              64   4.5 / 11   4.5 / 11   4.7 / 11   5.5 / 11   9.3 / 14    17 / 18    34 / 19
+//             512    20 / 18    21 / 24    22 / 24    26 / 35    48 / 57    92 / 93   181 / 171
+//            2048    74 / 33    80 / 44    81 / 68    89 / 105  174 / 190  382 / 338  766 / 619
+//   64 states  16   4.4 / 7.1  4.5 / 7.2  4.6 / 7.2  5.2 / 7.2  8.8 / 7.3   16 / 7.6   29 / 7.8
+//              64   4.5 / 15   4.5 / 15   4.7 / 15   5.5 / 16   9.2 / 16    17 / 23    30 / 22
+//             512    20 / 30    21 / 29    22 / 29    26 / 41    48 / 55    91 / 92   179 / 154
+//            1024    38 / 37    39 / 37    40 / 45    47 / 60    90 / 95   176 / 172  347 / 297
+//            2048    74 / 53    76 / 53    77 / 71    89 / 101  174 / 175  345 / 331  690 / 586
 ScanSplit scan_split_fwd(int64_t max_len, int64_t rows, int D, int G, int N) {
   const int64_t wgs = sequences(max_len, rows) * scan_time_tiles(D, G, N);
-  const bool fills = wgs >= 384, over = wgs >= (N == 32 && max_len > 256 ? 2048 : 4096);
+  const bool fills = wgs >= 384, over = wgs >= (max_len > 256 ? 2048 : 4096);
   const bool long_enough = max_len > std::max<int64_t>(16, wgs / 32) || (N > 16 && wgs <= 512);
   if (long_enough && !over && (fills || max_len <= std::max(320, 15 * N)))
     return ScanSplit{1, std::max<int64_t>(max_len, 64), 1};

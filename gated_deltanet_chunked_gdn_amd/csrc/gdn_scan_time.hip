@@ -10,12 +10,13 @@
 // parallel at six vector instructions per token, channel and state, where the split
 // over segments (gdn_scan.hip) spends nine, and the staging twice.
 //
-// Measured, bf16, 16 states, forward: 2 x 2048 x 4096 110 us (137 us split over segments),
-// 1 x 128 x 1024 7.1 us (19 us: one launch instead of two); 73 % of the cycles issue vector
-// instructions, 9.7 a token, channel and state with the staging and the gate, at the two
-// waves a SIMD that the registers leave.  64 states: six packed prompts, 3001 x 1024, 75 us
-// (93 us split).  Eight waves of eight tokens, at four waves a SIMD, gain nothing (131 us
-// for the first, the same for the last): they fold twice as often.
+// Measured, bf16, 16 states, forward: 2 x 2048 x 4096 99 us (112 without the wave
+// priorities; 9.6 vector instructions a token, channel and state with the staging and the
+// gate, at the two waves a SIMD that the registers leave), 1 x 128 x 1024 7 us (10 us
+// split: one launch instead of two).  64 states, six
+// packed prompts, 3001 x 1024: 75 us (93 us split).  Eight waves of eight tokens, at four
+// waves a SIMD, gain nothing (131 us for the first, the same for the last): they fold twice
+// as often.
 //
 // Each wave stages its own tokens; one barrier a step, for the pairs.  Workgroups of
 // neighbouring channels share cache lines (row pieces of 8 to 64 bytes), so each XCD takes
@@ -130,6 +131,7 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
     __builtin_amdgcn_wave_barrier();
 
     // decays and writes, and the run from zero
+    __builtin_amdgcn_s_setprio(1);
     float a[kTok][S], w[kTok][S], h[S], sum = 0.f;
 #pragma unroll
     for (int s = 0; s < S; ++s) h[s] = 0.f;
@@ -151,6 +153,7 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
     for (int s = 0; s < S; ++s) prod[s] = exp2_(A2[s] * sum);
     store_states<S>(pair[buf][wave][0][lane], prod);
     store_states<S>(pair[buf][wave][1][lane], h);
+    __builtin_amdgcn_s_setprio(0);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
