@@ -109,8 +109,11 @@ struct ScanSplit {
 ScanSplit scan_split_fwd(int64_t max_len, int64_t rows, int D, int G, int N);
 ScanSplit scan_split_bwd(int64_t max_len, int64_t rows, int D, int G, int N);
 hipError_t launch_scan_fwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
+// Channels of a workgroup of that kernel, and workgroups of a sequence.
 constexpr int scan_time_channels(int N) { return N <= 16 ? 16 : 256 / N; }
-inline int scan_time_tiles(int D, int G, int N) { return G * ((D / G + scan_time_channels(N) - 1) / scan_time_channels(N)); }
+inline int scan_time_tiles(int D, int G, int N) {
+  return G * ((D / G + scan_time_channels(N) - 1) / scan_time_channels(N));
+}
 hipError_t launch_scan_time(const ScanParams& p, int N, bool bf16, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanParams& p, int N, bool bf16, hipStream_t s);
 // state in p.h_final, updated in place

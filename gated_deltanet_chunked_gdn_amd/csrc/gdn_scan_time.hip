@@ -54,7 +54,8 @@ template <typename E, int N>
 __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int tiles) {
   constexpr int kCh = scan_time_channels(N), EL = kCh / 4;
   constexpr int S = kCh * N / 64, P = N / 4;  // states of a lane; a lane's values of one token's B and C
-  constexpr int kRow = N > 16 ? N + 4 : N;    // stride of B and C rows: the rows that a wave writes at once fall in other banks
+  // stride of B and C rows: the rows that a wave writes at once fall in other banks
+  constexpr int kRow = N > 16 ? N + 4 : N;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane % kCh, q = lane / kCh;
   const int n = blockIdx.y;
@@ -184,10 +185,11 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
           acc[i] = fmaf(h[s], Cv[s], acc[i]);
         }
       }
-      float sum = reduce_rows4(acc[0], acc[1], acc[2], acc[3]);  // lanes of row t: token j + t
-      if (kCh < 16) sum += dpp_f32<0x128, 0xf>(sum);
-      if (kCh < 8) sum += dpp_f32<0x124, 0xf>(sum);
-      if ((lane & 15) < kCh) ys[wave][j + (lane >> 4)][c] = sum;
+      // lanes of row t: token j + t; rotations by 8 and 4 lanes add the quarters of a row
+      float yj = reduce_rows4(acc[0], acc[1], acc[2], acc[3]);
+      if (kCh < 16) yj += dpp_f32<0x128, 0xf>(yj);
+      if (kCh < 8) yj += dpp_f32<0x124, 0xf>(yj);
+      if ((lane & 15) < kCh) ys[wave][j + (lane >> 4)][c] = yj;
     }
     __builtin_amdgcn_wave_barrier();
     if (ok && live) {
@@ -219,7 +221,8 @@ __global__ __launch_bounds__(256, 2) void scan_time_kernel(ScanParams p, int til
 template <typename E, int N>
 hipError_t launch_t(const ScanParams& p, hipStream_t s) {
   const int tiles = scan_time_tiles(p.D, p.G, N);
-  hipLaunchKernelGGL((scan_time_kernel<E, N>), dim3((tiles + 7) / 8 * 8, static_cast<unsigned>(p.nseq)), dim3(256), 0, s, p, tiles);
+  hipLaunchKernelGGL((scan_time_kernel<E, N>), dim3((tiles + 7) / 8 * 8, static_cast<unsigned>(p.nseq)), dim3(256), 0, s,
+                     p, tiles);
   return hipGetLastError();
 }
 

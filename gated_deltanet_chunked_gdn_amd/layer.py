@@ -16,7 +16,9 @@ current stream, and every step of the computation runs in libgdn's HIP kernels.
 Tensors are contiguous; activations are bf16 or fp32 (one dtype a call), parameters
 and recurrent states fp32, the convolution's state the io dtype (it keeps input
 rows).  Packed sequences: B == 1 and ``cu_seqlens`` the N + 1 offsets, best built
-once as a ``SeqLens``.  Outputs and gradients that were not asked for are None.
+once as a ``SeqLens``.  Outputs and gradients that were not asked for are None.  A
+``workspace`` holds nothing between calls, but calls that may overlap (on two streams,
+in graphs replayed at once) need one each; without one a call takes a fresh buffer.
 """
 from __future__ import annotations
 
