@@ -21,8 +21,9 @@
 // z: main kernel 205 us (222 without the wave priorities; the 345 MB it moves would take
 // 67), summary of the segments 60, last kernel 11.  Measured
 // and not kept: those sums by fp32 matrix instructions (381 us: the operands' layout
-// costs more moves than the adds it saves), decays formed twice instead of kept, at three
-// waves a SIMD (252).
+// costs more moves than the adds it saves), the rows of lanes added in LDS instead of by
+// lane swaps (205 against 201), decays formed twice instead of kept, at three waves a SIMD
+// (252).
 #include <hip/hip_runtime.h>
 
 #include "gdn_scan_device.h"
@@ -37,7 +38,7 @@ constexpr int TT = kScanBlock;
 // v[i], i < 16, summed over the wave's 16 channels: lane (cg, c3, q) gets value 4 cg + c3
 // of its quarter q of the states.  Two lane swaps halve the registers while they add the
 // rows of lanes (cg = c / 4), exchanges between the quads halve them over c % 4 = c3.
-__device__ __forceinline__ float channels_sum16(float (&v)[16], bool c_hi, bool c_lo) {
+__device__ __forceinline__ float channels_sum16(float (&v)[16]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     swap32(v[i], v[i + 8]);
@@ -48,13 +49,21 @@ __device__ __forceinline__ float channels_sum16(float (&v)[16], bool c_hi, bool 
     swap16(v[i], v[i + 4]);
     v[i] += v[i + 4];
   }
-  const float x = (c_hi ? v[2] : v[0]) + dpp_f32<0x128, 0xf>(c_hi ? v[0] : v[2]);
-  const float y = (c_hi ? v[3] : v[1]) + dpp_f32<0x128, 0xf>(c_hi ? v[1] : v[3]);
-  // the neighbouring quad's: shl:4 into quads 0 and 2, shr:4 into 1 and 3
-  const int give = __float_as_int(c_lo ? x : y);
-  int got = __builtin_amdgcn_update_dpp(0, give, 0x104, 0xf, 0x5, false);
-  got = __builtin_amdgcn_update_dpp(got, give, 0x114, 0xf, 0xa, false);
-  return (c_lo ? y : x) + __int_as_float(got);
+  // adds that write two of the four quads of a row each: quads 0, 1 keep v[0] and v[1] with
+  // those of the quad two on, quads 2, 3 v[2] and v[3]; then the same between neighbours.
+  // (A DPP operand may be read two wait states after it was written.)
+  float x, y, sum;
+  asm("s_nop 1\n\t"
+      "v_add_f32_dpp %0, %3, %3 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %1, %4, %4 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+      "v_add_f32_dpp %0, %5, %5 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "v_add_f32_dpp %1, %6, %6 row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+      "s_nop 1\n\t"
+      "v_add_f32_dpp %2, %0, %0 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+      "v_add_f32_dpp %2, %1, %1 row_shr:4 row_mask:0xf bank_mask:0xa"
+      : "=&v"(x), "=&v"(y), "=&v"(sum)
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]));
+  return sum;
 }
 // x[i], i < 4, summed over the four lanes of a channel (a quad): lane q gets x[q].
 __device__ __forceinline__ float states_sum4(const float (&x)[4], bool q_hi, bool q_lo) {
@@ -277,7 +286,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   __shared__ float bc[4][TT][2][NW];         // dB, dC of each wave's channels, a pass
   __shared__ f32x4_t carry[NG > 1 ? 2 * NG : 1][NG > 1 ? 256 : 1];  // G and dA between a lane's passes
 
-  const bool q_lo = lane & 1, q_hi = lane & 2, c_lo = lane & 4, c_hi = lane & 8;
+  const bool q_lo = lane & 1, q_hi = lane & 2;
   const int v16 = lane >> 2;  // the value of a group of 16 this lane gets
   const bool chan = at.c < ct.count;
   // the lane's states of pass k: q SG + NW k .. + SG - 1
@@ -379,7 +388,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
           }
           if (GATED) add_sum<NG>(&sums[2][tg + t4 + at.q][at.c], states_sum4(sC, q_hi, q_lo), k);
         }
-        bc[wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
+        bc[wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v);
         __builtin_amdgcn_sched_barrier(0);
       }
       asm volatile("" : "+v"(ci), "+v"(qi));
@@ -413,7 +422,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
           add_sum<NG>(&sums[0][tg + t4 + at.q][at.c], states_sum4(sB, q_hi, q_lo), k);
           add_sum<NG>(&sums[1][tg + t4 + at.q][at.c], states_sum4(sA, q_hi, q_lo), k);
         }
-        bc[wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v, c_hi, c_lo);
+        bc[wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v);
         __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_s_setprio(0);
