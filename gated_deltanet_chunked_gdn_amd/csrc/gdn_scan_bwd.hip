@@ -17,8 +17,8 @@
 // over the segments and sequences.  No atomics: the same inputs give the same bits.
 //
 // Bound by vector instructions, as the forward, with the sums over the channels on top:
-// 23.5 a token, channel and state.  4 x 2048 tokens, 2048 channels, 16 states, bf16, with
-// z: main kernel 205 us (222 without the wave priorities; the 345 MB it moves would take
+// 22.7 a token, channel and state.  4 x 2048 tokens, 2048 channels, 16 states, bf16, with
+// z: main kernel 201 us (222 without the wave priorities; the 345 MB it moves would take
 // 67), summary of the segments 60, last kernel 11.  Measured
 // and not kept: those sums by fp32 matrix instructions (381 us: the operands' layout
 // costs more moves than the adds it saves), the rows of lanes added in LDS instead of by
