@@ -259,12 +259,18 @@ __device__ __forceinline__ void compose(const ScanParams& p, const float* sum, c
   }
 }
 
-// GATED: dz is wanted, and with it the outputs before the gate.  RAGGED: a group's last
-// tile has fewer than 64 channels.  The lanes behind them hold zeros but meet the real B and
-// C, so an infinity there makes NaN of them; nothing of theirs is stored, but their terms in
-// the sums over the channels are cleared: 2.6 % of the training step of five packed
-// sequences, 6001 x 1000 channels, 16 states (177 -> 182 us), none where tiles are full.
-template <typename E, int N, bool GATED, bool RAGGED>
+// Where tiles of 64 channels or blocks of 16 tokens are not full, what stands behind the end
+// is zero, and infinities would make NaN of it:
+//  - kTokens: tokens behind a sequence's end leave the state and G as they are and add
+//    delta G a h = 0 to dA, so their states (the last one) are set to zero;
+//  - kChannels: lanes behind a group's channels meet the real B and C.  Nothing of theirs is
+//    stored, but their terms in the sums over the channels are cleared.  (kTokens as well.)
+// Training steps, without / kTokens / kChannels: 4 x 1999 x 1024 channels, 32 states, 360 / 361 /
+// 375 us; five packed sequences, 6001 x 1000, 16 states, 176 / - / 181 us.
+enum Ragged { kFullBlocks, kTokens, kChannels };
+
+// GATED: dz is wanted, and with it the outputs before the gate.
+template <typename E, int N, bool GATED, Ragged R>
 __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   constexpr int S = N / 4;
   constexpr int SG = S < 4 ? S : 4;  // states of a lane taken at a time
@@ -294,7 +300,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   const int v16 = lane >> 2;  // the value of a group of 16 this lane gets
   const bool chan = at.c < ct.count;
   auto only_channels = [&](float (&v)[16]) {
-    if (!RAGGED) return;
+    if (R != kChannels) return;
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = chan ? v[i] : 0.f;
   };
@@ -400,6 +406,12 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
         only_channels(v);
         bc[wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v);
         __builtin_amdgcn_sched_barrier(0);
+      }
+      if (R != kFullBlocks && t0 + TT > end) {
+#pragma unroll
+        for (int t = 1; t < TT; ++t)
+#pragma unroll
+          for (int s = 0; s < SG; ++s) hb[t][s] = t0 + t < end ? hb[t][s] : 0.f;
       }
       asm volatile("" : "+v"(ci), "+v"(qi));
       __builtin_amdgcn_s_setprio(1);
@@ -562,9 +574,11 @@ unsigned blocks_of(int64_t threads) { return static_cast<unsigned>((threads + 25
 template <typename E, int N, bool GATED>
 void launch_main(const ScanParams& p, dim3 grid, hipStream_t s) {
   if (p.D / p.G % kScanTile != 0)
-    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, true>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, kChannels>), grid, dim3(256), 0, s, p);
+  else if (p.seq.cu || p.seq.T % TT != 0)
+    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, kTokens>), grid, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, false>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, kFullBlocks>), grid, dim3(256), 0, s, p);
 }
 
 template <typename E, int N>

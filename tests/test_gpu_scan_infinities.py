@@ -61,3 +61,18 @@ def test_infinite_write_or_read_vector(D, N, G, z, name, io):
     got = _case(a, h0, dy, dl, None)
     key, rows = ("dC", slice(21, 32)) if name == "Bm" else ("dB", slice(0, 22))
     assert bool((got[key][0, rows, G - 1, N - 3] == INF).all())
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("value", [INF, float("nan")])
+@pytest.mark.parametrize("T,D,N,cu", [(37, 64, 16, None), (37, 24, 8, None), (49, 64, 32, None), (31, 72, 64, None),
+                                      (60, 64, 16, [0, 21, 32, 60])])
+def test_a_last_token_that_is_not_finite(T, D, N, cu, value, io):
+    """The last state of a sequence enters dC of the last token and no other gradient: dA
+    holds the states before the tokens, so it stays finite, wherever the sequence ends."""
+    a, h0, dy, dl = _inputs(T, D, N, 1, io, True, n=len(cu) - 1 if cu else 1)
+    for end in (cu or [0, T])[1:]:
+        a["u"][0, end - 1] = value
+    got = _case(a, h0, dy, dl, cu)
+    assert bool(got["dA"].isfinite().all())
+    assert bool((got["dC"][0, -1].isnan() if value != value else got["dC"][0, -1] == INF).all())
