@@ -113,9 +113,15 @@ gdn_status check_conv(const gdn_conv_problem* p, ConvSize* c) {
   if (st != GDN_OK) return st;
   c->io = p->io_dtype == GDN_BF16 ? 2 : 4;
   c->rows = static_cast<int64_t>(p->B) * p->T;
-  // threads (one per token and channel vector at most) are counted in 32 bits
-  if (c->rows > INT32_MAX || (c->rows + (p->W - 1) * static_cast<int64_t>(p->num_seqs)) * (p->C / 4) >= INT64_C(1) << 32)
-    return GDN_ERR_UNSUPPORTED;
+  if (c->rows > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  // A launch counts its threads in 32 bits.  Vectors of V channels: the forward takes one
+  // thread for 8 rows of 4 channels (for 2 rows where those are below 2^16) and one for each
+  // vector of the kept rows; the step and the backward's last kernel one for each vector of
+  // the sequences, the latter (W + 1) C more.  2^23 covers what is rounded up, those (W + 1) C
+  // (at most 5 2^20) and the threads of two rows (at most 2^18 + 2^17 more).
+  const int64_t vec = 16 / static_cast<int64_t>(c->io);
+  const int64_t threads = c->rows * p->C / 32 + static_cast<int64_t>(p->num_seqs) * (p->W - 1) * (p->C / vec);
+  if (threads > (INT64_C(1) << 32) - (1 << 23)) return GDN_ERR_UNSUPPORTED;
   c->values = static_cast<size_t>(c->rows) * p->C * c->io;
   c->state = static_cast<size_t>(p->num_seqs) * (p->W - 1) * p->C * c->io;
   c->weight = static_cast<size_t>(p->C) * p->W * 4;

@@ -434,8 +434,9 @@ typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activatio
  * Tensors: x, y, dy, dx [B,T,C]; state0, state_final, state, dstate_final, dstate0
  * [N,W-1,C], oldest row first (io dtype; state rows are input rows, kept exactly);
  * weight, dweight [C,W] and bias, dbias [C] fp32.  All of them 16-byte aligned.
- * Supported: C a multiple of 8 up to 2^20, W in {2, 3, 4}, N <= 65535, B T < 2^31,
- * else GDN_ERR_UNSUPPORTED.  Sums are fp32; io outputs are rounded once. */
+ * Supported: C a multiple of 8 up to 2^20, W in {2, 3, 4}, N <= 65535, B T < 2^31, and
+ * B T C / 32 + N (W - 1) C / V <= 2^32 - 2^23 (the threads of a launch; V = 8 for bf16, 4
+ * for fp32), else GDN_ERR_UNSUPPORTED.  Sums are fp32; io outputs are rounded once. */
 typedef struct gdn_conv_problem {
   int32_t B, T, C, W;
   int32_t num_seqs;                /* N: == B for dense input, else len(cu_seqlens) - 1     */
