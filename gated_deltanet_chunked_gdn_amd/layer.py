@@ -89,10 +89,15 @@ def _call(dev, name, *args):
         nat.check(st, name)
 
 
-@functools.lru_cache(maxsize=256)
-def _dense(kind, *fields):
-    """A problem of dense tensors: the same sizes give the same (never written) structure."""
+def _problem(kind, *fields):
+    """A problem, its first five fields sizes that 32 bits hold (ctypes would cut them off)."""
+    if max(fields[:5]) >= 1 << 31:
+        raise ValueError(f"a size of {max(fields[:5])} is more than the library's 32 bits hold")
     return kind(*fields)
+
+
+# a problem of dense tensors: the same sizes give the same (never written) structure
+_dense = functools.lru_cache(maxsize=256)(_problem)
 
 
 def _packed(cu_seqlens, dev):
@@ -173,7 +178,7 @@ def _conv_problem(x, weight, cu_seqlens, activation):
     if cu_seqlens is None:
         return dev, None, _dense(nat.ConvProblem, B, T, C, W, B, None, None, io, act)
     s = _packed(cu_seqlens, dev)
-    return dev, s, nat.ConvProblem(B, T, C, W, s.num_seqs, s.host.ctypes.data, s.dev.data_ptr(), io, act)
+    return dev, s, _problem(nat.ConvProblem, B, T, C, W, s.num_seqs, s.host.ctypes.data, s.dev.data_ptr(), io, act)
 
 
 def _conv_inputs(x, weight, bias, dev):
@@ -248,7 +253,7 @@ def _scan_problem(u, Bm, cu_seqlens, dt_softplus):
     if cu_seqlens is None:
         return dev, None, _dense(nat.ScanProblem, B, T, D, N, G, B, None, None, io, softplus)
     s = _packed(cu_seqlens, dev)
-    return dev, s, nat.ScanProblem(B, T, D, N, G, s.num_seqs, s.host.ctypes.data, s.dev.data_ptr(), io, softplus)
+    return dev, s, _problem(nat.ScanProblem, B, T, D, N, G, s.num_seqs, s.host.ctypes.data, s.dev.data_ptr(), io, softplus)
 
 
 def _scan_inputs(p, u, dt, A, Bm, Cm, D, z, dt_bias, dev):

@@ -4,8 +4,10 @@ import ctypes
 import itertools
 
 import pytest
+import torch
 
 from gated_deltanet_chunked_gdn_amd import _native as nat
+from gated_deltanet_chunked_gdn_amd import layer
 
 LIMIT = (1 << 32) - (1 << 23)
 
@@ -54,3 +56,35 @@ def test_more_threads_than_a_launch_has_are_refused():
     """Last kernel of the backward: 3 2^20 threads for the sums and 16383 2^18 for dstate0."""
     assert launches(16383, 0, 1 << 20, 2, nat.GDN_FP32)[2] >= 1 << 32
     assert status(16383, 0, 1 << 20, 2, nat.GDN_FP32) == nat.GDN_ERR_UNSUPPORTED
+
+
+def _calls():
+    many = (1 << 32) + 1  # one sequence, counted in 32 bits
+    z = torch.zeros
+    x, w = z(many, 0, 8), z(8, 4)
+    u, A, Bm = z(many, 0, 8), z(8, 8), z(many, 0, 1, 8)
+    q, v, g, S = z(many, 1, 0, 64), z(many, 1, 0, 16), z(many, 1, 0), z(many, 0, 64, 16)
+    return {"conv_fwd": lambda: layer.conv_fwd(x, w), "conv_bwd": lambda: layer.conv_bwd(x, w, x),
+            "conv_step": lambda: layer.conv_step(z(many, 1, 0), z(0, 4), z(many, 3, 0)),
+            "conv_packed": lambda: layer.conv_fwd(z(1, many, 0), z(0, 4), cu_seqlens=layer_seqs([0, 1])),
+            "scan_fwd": lambda: layer.scan_fwd(u, u, A, Bm, Bm), "scan_buffers": lambda: layer.scan_buffers(u, Bm),
+            "scan_packed": lambda: layer.scan_buffers(z(1, many, 0), z(1, many, 0, 8), cu_seqlens=layer_seqs([0, 1])),
+            "scan_step": lambda: layer.scan_step(z(many, 1, 0), z(many, 1, 0), z(0, 8), z(many, 1, 0, 8), z(many, 1, 0, 8), z(many, 0, 8)),
+            "step": lambda: layer.step(q, q, v, g, g, S), "kda_step": lambda: layer.kda_step(q, q, v, q, g, S)}
+
+
+def layer_seqs(offsets):
+    from gated_deltanet_chunked_gdn_amd.ops import SeqLens
+
+    return SeqLens(offsets, "cpu")
+
+
+@pytest.mark.parametrize("name", sorted(_calls()))
+def test_sizes_beyond_32_bits_are_refused(monkeypatch, name):
+    """The library's sizes are 32-bit: 2^32 + 1 sequences or tokens must not be taken for one
+    (host tensors without elements, on which no call gets past its checks)."""
+    monkeypatch.setattr(layer, "_first", lambda t, *_: t.get_device())
+    monkeypatch.setattr(layer, "_packed", lambda cu, dev: cu)
+    monkeypatch.setattr(layer, "_call", lambda *a: pytest.fail("the library call was reached"))
+    with pytest.raises(ValueError, match="4294967297"):
+        _calls()[name]()
