@@ -1,5 +1,6 @@
 // How the selective scan is split over the time axis (host only).
 #include <algorithm>
+#include <cmath>
 
 #include "gdn_layer.h"
 
@@ -32,6 +33,14 @@ static ScanSplit split(int64_t max_len, int64_t rows, int D, int G, int N, bool 
     const int64_t least = std::min<int64_t>(64, ((max_len + 31) / 32 + 15) / 16 * 16);
     segs = std::min<int64_t>((want / 2 + groups - 1) / groups, max_len / std::max<int64_t>(least, 16));
   }
+  // A segment's start is composed of the others of its sequence one after another, 0.35 us
+  // (forward) or 0.4 us (backward) each; a token takes 0.2 us (forward, both kernels) or 0.35
+  // us for every 16 states that the backward takes at a time.  The sum of both is least near
+  // segs^2 = tokens (times those passes).  Without this bound / with it, bf16, us:
+  //   64 channels, 16 states: 8192 tokens, forward 60 / 51, backward 74 / 72 (128 / 85 segments);
+  //   65536 tokens, 370 / 144 and 444 / 193 (1024 / 256).  Up to 64 segments it changes nothing.
+  const int64_t passes = nearest ? std::max(1, N / 16) : 1;
+  segs = std::min(segs, std::max<int64_t>(64, static_cast<int64_t>(std::sqrt(static_cast<double>(max_len * passes)))));
   if (segs < 2) return ScanSplit{1, std::max<int64_t>(max_len, 64), 0};
   const int64_t len = nearest ? std::max<int64_t>((max_len / segs + 8) / 16 * 16, 16)
                               : ((max_len + segs - 1) / segs + 15) / 16 * 16;

@@ -88,3 +88,24 @@ def test_sizes_beyond_32_bits_are_refused(monkeypatch, name):
     monkeypatch.setattr(layer, "_call", lambda *a: pytest.fail("the library call was reached"))
     with pytest.raises(ValueError, match="4294967297"):
         _calls()[name]()
+
+
+def _segments(T, D, N, pass_):
+    """Slots of segments that the workspace of one sequence has: its end states and sums."""
+    p = nat.ScanProblem(1, T, D, N, 1, 1, None, None, nat.GDN_FP32, 1)
+    n = ctypes.c_size_t(0)
+    assert nat.load().gdn_scan_workspace_size(p, pass_, n) == nat.GDN_OK
+    if pass_ == nat.GDN_SCAN_BWD:  # and the partial sums of dB and dC, of dA, dD and ddt_bias
+        return (n.value - -(-D // 64) * T * 2 * N * 4) // (D * (2 * N + 3) * 4)
+    return n.value // (D * (N + 1) * 4)
+
+
+@pytest.mark.parametrize("T", [4096, 5000, 8192, 16384, 65536, 262144, 1 << 20])
+@pytest.mark.parametrize("D,N", [(64, 8), (64, 16), (256, 16), (64, 32), (64, 64), (1024, 64)])
+def test_scan_segments_do_not_outgrow_their_tokens(T, D, N):
+    """Every segment composes all the others of its sequence, so their number squared stays
+    near the sequence's tokens (times the backward's passes over wide states; a third more
+    where lengths are rounded to 16 tokens), and the split is still taken."""
+    for pass_, tokens in ((nat.GDN_SCAN_FWD, T), (nat.GDN_SCAN_BWD, T * max(1, N // 16))):
+        segs = _segments(T, D, N, pass_)
+        assert 16 <= segs <= 4 / 3 * max(64, tokens ** 0.5) + 1, (pass_, segs)
