@@ -81,7 +81,8 @@ EXTRAS = ("bwd", "segment_split", "prologue", "epilogue", "kda", "kda_bwd", "kda
 def layer_measurements(gdn, dev, steps, warmup, which):
     """The single-token delta rule step, the short convolution and the selective scan at
     a decoding, a prompt and a training shape each: milliseconds a call (HIP events) and
-    the bytes that a call cannot do without."""
+    the bytes that a call cannot do without.  Every call has the same inputs, much of which
+    stays in the caches between calls."""
     import torch
 
     stream = torch.cuda.current_stream(dev)

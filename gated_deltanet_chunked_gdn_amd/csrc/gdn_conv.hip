@@ -189,7 +189,10 @@ __device__ __forceinline__ float silu_grad(float p, float dy) {
 // their dp alone), two rows at a time with the next two in flight; four channels
 // rather than eight halve the registers of the weights and their gradients, for four
 // waves a SIMD (4 x 4096 x 2048 bf16, 201 MB: 51 us, 3.9 TB/s; with eight channels and two
-// waves 80 us, with four rows ahead and three waves 61 us).  A workgroup covers 512 rows
+// waves 80 us, with four rows ahead and three waves 61 us).  At width 4 those waves leave 4
+// (bf16) and 6 (fp32, three waves) registers too few, which the compiler keeps in scratch.  A
+// thread has 32 rows however few there are: 512 x 512 bf16, eight workgroups, takes 26 us
+// forward and backward.  A workgroup covers 512 rows
 // of 64 channels: its sums of dp x and dp are reduced over the runs (lanes, then waves)
 // and written once, and a second kernel adds the workgroups' sums in order.
 constexpr int kBwdV = 4, kBwdRun = 32, kBwdLanes = 16, kBwdAhead = 2;

@@ -66,9 +66,10 @@ __device__ __forceinline__ float sigmoid_(float x) { return rcp_(1.f + exp2_(-kL
 
 // softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1].  With w = 1 + e rounded,
 // log1p(e) = log(w) + (e - (w - 1)) / w up to the square of the second term, the
-// rounding of w; dividing it by w <= 2 is left out: it is at most 2^-24, next to a
-// logarithm that is above w - 1 >= 1/2 of e wherever it is not zero.  `sig` gets the
-// derivative, sigmoid(x).
+// rounding of w, r = |e - (w - 1)| <= 2^-24 (w lies in [1, 2]).  Dividing it by w is left
+// out, which adds r (w - 1) / w.  On [1, 2] log(w) >= (w - 1) log 2, so where w > 1 that is
+// at most r / (w log 2) <= 1.45 2^-24 of the logarithm; where w == 1 nothing is added and
+// the sum is e itself.  `sig` gets the derivative, sigmoid(x).
 __device__ __forceinline__ float softplus_(float x, float& sig) {
   const float e = exp2_(-kLog2e * fabsf(x)), w = 1.f + e;
   const float r = rcp_(w);

@@ -8,7 +8,11 @@
 // Blocks of 16 tokens go from the last to the first.  Of a block, every lane forms its
 // states and decays forward from the kept state (they stay in registers: 16 tokens x 4
 // states x 2) and then walks back; wider states take the block four states a lane at a
-// time, and G and dA wait in LDS between their passes.  The four lanes of a quad share a
+// time, and G and dA wait in LDS between their passes.  All 256 registers of two waves a SIMD
+// are taken from 16 states on, and what is held for a block's end goes to scratch in part:
+// of the instances that form dz 0 (bf16) and 9 (fp32) registers with 16 states, 7 and 21 with
+// 32, 7 and 27 with 64 (up to five more where blocks or tiles are not full); of the others 7
+// with 64 fp32 states (up to 12).  The four lanes of a quad share a
 // channel, so its sums over the states are two DPP exchanges; a lane's 16 values of dB
 // (four tokens, four states) are added over the wave's 16 channels by steps that halve
 // the values each time: two lane swaps over the rows of lanes, two exchanges between the
@@ -18,8 +22,8 @@
 //
 // Bound by vector instructions, as the forward, with the sums over the channels on top:
 // 22.7 a token, channel and state.  4 x 2048 tokens, 2048 channels, 16 states, bf16, with
-// z: main kernel 201 us (222 without the wave priorities; the 345 MB it moves would take
-// 67), summary of the segments 60, last kernel 11.  Measured
+// z: main kernel 201 to 204 us (222 without the wave priorities; the 345 MB it moves would
+// take 67), summary of the segments 60, last kernel 11.  Measured
 // and not kept: those sums by fp32 matrix instructions (381 us: the operands' layout
 // costs more moves than the adds it saves), the rows of lanes added in LDS instead of by
 // lane swaps (205 against 201), decays formed twice instead of kept, at three waves a SIMD

@@ -13,9 +13,14 @@ static int64_t sequences(int64_t max_len, int64_t rows) {
 
 // Serial needs the fewest instructions; the split runs the state's part of the work
 // twice, and every segment composes the ones before it.  It is taken where the channels
-// alone leave SIMDs idle: segments of at least 64 tokens, as many as give every SIMD four
-// waves (1024 workgroups of four; two waves, 512, for 64 states, whose registers allow no
-// more).  Where that leaves fewer than half as many workgroups, the chain of tokens is
+// alone leave SIMDs idle: segments of at least 64 tokens, as many as make 1024 workgroups of
+// four waves (512 for 64 states, whose registers allow two waves a SIMD).  That is one round
+// of workgroups in the forward with 8 and 16 states (four waves a SIMD and more), one and a
+// third with 32, where the kernel of the outputs has three waves, and two in the backward,
+// which has two with every number of states.  32 states with 768 instead, forward / backward,
+// us: 1 x 2048 x 16384 347 -> 312 / 978 -> 1220, 1 x 16384 x 2048 389 -> 356 / 982 -> 1240,
+// 1 x 2048 x 32768 629 -> 630 / 1879 -> 1883; with 512 347 -> 364, 389 -> 403, 629 -> 455 and
+// 978 -> 1007, 982 -> 999, 1879 -> 1677.  Where that leaves fewer than half as many workgroups, the chain of tokens is
 // what takes the time, and segments are shortened, to 16 tokens at least and 32 of them at
 // most, for up to half as many.  Measured, bf16 (us), at least 64 / 16:
 //   16 states, backward, 1 x 64 x 256    22 / 15     1 x 128 x 2048   36 / 20

@@ -19,6 +19,10 @@ rows).  Packed sequences: B == 1 and ``cu_seqlens`` the N + 1 offsets, best buil
 once as a ``SeqLens``.  Outputs and gradients that were not asked for are None.  A
 ``workspace`` holds nothing between calls, but calls that may overlap (on two streams,
 in graphs replayed at once) need one each; without one a call takes a fresh buffer.
+
+As in ``ops``, no call records anything for autograd: outputs carry no history, whatever
+requires gradients, a tensor that is updated in place keeps its version, and gradients come
+from the ``_bwd`` calls.
 """
 from __future__ import annotations
 

@@ -74,6 +74,8 @@
 extern "C" {
 #endif
 
+/* The operators of the layer (gdn_step and all that follows it below) are additions within
+ * version 6: the number does not tell whether a library has them, their symbols do. */
 #define GDN_ABI_VERSION 6
 
 typedef enum gdn_status {
@@ -482,7 +484,11 @@ gdn_status gdn_conv_step(const gdn_conv_problem* problem, const void* x, const f
  * dtype); A [D,N], Dskip, dt_bias [D], h0, h_final [num_seqs,D,N] fp32.  All of them
  * 16-byte aligned.  Supported: N in {8, 16, 32, 64}, D / G a multiple of 8, D up to
  * 2^20, B T < 2^31, B T G N < 2^32, up to 65535 sequences, else GDN_ERR_UNSUPPORTED.
- * Finite A <= 0 and delta >= 0 are documented, not checked.  All arithmetic is fp32; io outputs are rounded once. */
+ * Finite A <= 0 and delta >= 0 are documented, not checked.  All arithmetic is fp32; io outputs are rounded once.
+ * NaN and Inf reach what the definition makes of them and nothing that it leaves finite.  Where it
+ * gives an infinity NaN may stand instead: a state that is infinite while the decays over 16
+ * tokens or more underflow to zero, and dA where dh_final is infinite and the sequence's length is no
+ * multiple of 16. */
 typedef struct gdn_scan_problem {
   int32_t B, T, D, N, G;
   int32_t num_seqs;                /* == B for dense input, else len(cu_seqlens) - 1        */
