@@ -10,9 +10,9 @@
 // states x 2) and then walks back; wider states take the block four states a lane at a
 // time, and G and dA wait in LDS between their passes.  All 256 registers of two waves a SIMD
 // are taken from 16 states on, and what is held for a block's end goes to scratch in part:
-// of the instances that form dz 0 (bf16) and 9 (fp32) registers with 16 states, 7 and 21 with
-// 32, 7 and 27 with 64 (up to five more where blocks or tiles are not full); of the others 7
-// with 64 fp32 states (up to 12).  The four lanes of a quad share a
+// of the instances that form dz 0 (bf16) and 6 (fp32) registers with 16 states, 7 and 22 with
+// 32, 7 and 34 with 64; of the others 1 and 9 with 16 and 64 fp32 states (up to four more in the
+// instances for blocks that are not full).  The four lanes of a quad share a
 // channel, so its sums over the states are two DPP exchanges; a lane's 16 values of dB
 // (four tokens, four states) are added over the wave's 16 channels by steps that halve
 // the values each time: two lane swaps over the rows of lanes, two exchanges between the
@@ -263,18 +263,13 @@ __device__ __forceinline__ void compose(const ScanParams& p, const float* sum, c
   }
 }
 
-// Where tiles of 64 channels or blocks of 16 tokens are not full, what stands behind the end
-// is zero, and infinities would make NaN of it:
-//  - kTokens: tokens behind a sequence's end leave the state and G as they are and add
-//    delta G a h = 0 to dA, so their states (the last one) are set to zero;
-//  - kChannels: lanes behind a group's channels meet the real B and C.  Nothing of theirs is
-//    stored, but their terms in the sums over the channels are cleared.  (kTokens as well.)
-// Training steps, without / kTokens / kChannels: 4 x 1999 x 1024 channels, 32 states, 360 / 361 /
-// 375 us; five packed sequences, 6001 x 1000, 16 states, 176 / - / 181 us.
-enum Ragged { kFullBlocks, kTokens, kChannels };
-
 // GATED: dz is wanted, and with it the outputs before the gate.
-template <typename E, int N, bool GATED, Ragged R>
+// TAIL: a sequence's last block may have fewer than 16 tokens.  Tokens behind the end leave the
+// state and G as they are and add delta G a h = 0 to dA, which a last state that is not finite
+// would make NaN of: their states are set to zero.  Training steps without / with: 4 x 1999 x 1024
+// channels, 32 states, bf16, 360 / 362 us; 4 x 1023 x 1000, 64 states, fp32, 369 / 383 us; four
+// packed sequences, 777 x 320, 32 states, fp32, 52.9 / 54.0 us.
+template <typename E, int N, bool GATED, bool TAIL>
 __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   constexpr int S = N / 4;
   constexpr int SG = S < 4 ? S : 4;  // states of a lane taken at a time
@@ -293,7 +288,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   if (seg > last) return;
   const int64_t part = part_slot(p, bos, n, seg);
 
-  __shared__ Stage<N, TT> st;
+  __shared__ Stage<N, TT, 4> st;
   __shared__ ChannelParams cp;
   __shared__ float dsb[TT][kScanTile];
   __shared__ float sums[3][TT][kScanTile];   // over a channel's states: G B, A q, C h
@@ -303,11 +298,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
   const bool q_lo = lane & 1, q_hi = lane & 2;
   const int v16 = lane >> 2;  // the value of a group of 16 this lane gets
   const bool chan = at.c < ct.count;
-  auto only_channels = [&](float (&v)[16]) {
-    if (R != kChannels) return;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = chan ? v[i] : 0.f;
-  };
   // the lane's states of pass k: q SG + NW k .. + SG - 1
   const int64_t hd = static_cast<int64_t>(ct.d0 + at.c) * N + at.q * SG;
   float A2[SG], G[SG], dA[SG];
@@ -350,6 +340,12 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
     load_states<SG>(kept, chan, hn);
   }
   cp.fill(p, ct);
+  // Lanes behind the tile's channels read B and C from four zeros behind each row: with the
+  // real ones an infinity would make NaN of their zeros and reach the sums over the channels.
+  if (tid < 4 * TT) {
+    st.B[tid / 4][N + tid % 4] = 0.f;
+    st.C[tid / 4][N + tid % 4] = 0.f;
+  }
   __syncthreads();
   for (; begin < end && t0 >= begin; t0 -= TT) {
     ld.put(st, cp, t0, end, delta, sig);
@@ -380,7 +376,7 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
       }
       // indexes the compiler cannot see through: on the way back the staged values are
       // read again rather than kept in (96) registers
-      int ci = at.c, qi = at.q * SG + k * NW;
+      int ci = at.c, qi = chan ? at.q * SG + k * NW : N;
       __builtin_amdgcn_s_setprio(2);
 #pragma unroll
       for (int tg = 0; tg < TT; tg += TG) {
@@ -407,11 +403,10 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
           }
           if (GATED) add_sum<NG>(&sums[2][tg + t4 + at.q][at.c], states_sum4(sC, q_hi, q_lo), k);
         }
-        only_channels(v);
         bc[wave][tg + v16 / SG][1][at.q * SG + v16 % SG] = channels_sum16(v);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (R != kFullBlocks && t0 + TT > end) {
+      if (TAIL && t0 + TT > end) {
 #pragma unroll
         for (int t = 1; t < TT; ++t)
 #pragma unroll
@@ -448,7 +443,6 @@ __global__ __launch_bounds__(256, 2) void scan_bwd_kernel(ScanParams p) {
           add_sum<NG>(&sums[0][tg + t4 + at.q][at.c], states_sum4(sB, q_hi, q_lo), k);
           add_sum<NG>(&sums[1][tg + t4 + at.q][at.c], states_sum4(sA, q_hi, q_lo), k);
         }
-        only_channels(v);
         bc[wave][tg + v16 / SG][0][at.q * SG + v16 % SG] = channels_sum16(v);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -577,12 +571,10 @@ unsigned blocks_of(int64_t threads) { return static_cast<unsigned>((threads + 25
 
 template <typename E, int N, bool GATED>
 void launch_main(const ScanParams& p, dim3 grid, hipStream_t s) {
-  if (p.D / p.G % kScanTile != 0)
-    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, kChannels>), grid, dim3(256), 0, s, p);
-  else if (p.seq.cu || p.seq.T % TT != 0)
-    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, kTokens>), grid, dim3(256), 0, s, p);
+  if (p.seq.cu || p.seq.T % TT != 0)
+    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, true>), grid, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, kFullBlocks>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((scan_bwd_kernel<E, N, GATED, false>), grid, dim3(256), 0, s, p);
 }
 
 template <typename E, int N>

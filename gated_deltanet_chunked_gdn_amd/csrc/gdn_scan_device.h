@@ -107,12 +107,13 @@ __device__ __forceinline__ float reduce_rows4(float x0, float x1, float x2, floa
 }
 
 // A tile of TT tokens in LDS: (delta, delta u) of every channel, B and C rows in
-// fp32.  Tokens behind the end hold zeros, which leave the state as it is.
-template <int N, int TT>
+// fp32, PAD more values a row.  Tokens behind the end hold zeros, which leave the state as it
+// is.
+template <int N, int TT, int PAD = 0>
 struct Stage {
   float2 dd[TT][kScanTile];
-  float B[TT][N];
-  float C[TT][N];
+  float B[TT][N + PAD];
+  float C[TT][N + PAD];
 };
 
 // dt_bias and D of the tile's channels (zero where there is none), in LDS: registers
@@ -164,7 +165,8 @@ struct Loader {
     }
   }
   // `delta` and its derivative `sig` by dt of this thread's channels (zero behind the end)
-  __device__ __forceinline__ void put(Stage<N, TT>& st, const ChannelParams& cp, int64_t t0, int64_t end,
+  template <int PAD>
+  __device__ __forceinline__ void put(Stage<N, TT, PAD>& st, const ChannelParams& cp, int64_t t0, int64_t end,
                                       float (&delta)[EL], float (&sig)[EL]) const {
     const bool ok = t0 + row < end, both = ok && live;
     float2 v[EL];

@@ -11,7 +11,7 @@
 // over segments (gdn_scan.hip) spends nine, and the staging twice.
 //
 // Measured, bf16, 16 states, forward: 2 x 2048 x 4096 90 us a call where calls queue up (100
-// without the wave priorities), 104 us a launch by itself in a trace (9.6 vector instructions a token, channel and state with the staging and the
+// without the wave priorities), 98 to 109 us a launch by itself in a trace (9.6 vector instructions a token, channel and state with the staging and the
 // gate, at the two waves a SIMD that the registers leave), 1 x 128 x 1024 7 us (10 us
 // split: one launch instead of two).  64 states, six
 // packed prompts, 3001 x 1024: 75 us (93 us split).  Eight waves of eight tokens, at four
