@@ -260,7 +260,7 @@ def _plain_glr(s):
         return out
     dy = s["dy"].reshape(rows, C).float()
     dlast = s["dstate"] if s["dstate"] is not None else torch.zeros_like(h0)
-    d = dy if z is None else dy * z * sig
+    d = dy.clone() if z is None else dy * z * sig
     d[ends] += dlast[some]
     after = torch.cat([cut[1:], torch.zeros_like(cut[:1])])
     grad = _running(after.flip(0), d.flip(0)).flip(0)
