@@ -53,6 +53,10 @@ GDN_ACT_SILU = 1
 GDN_SCAN_FWD = 0
 GDN_SCAN_SAVED = 1
 GDN_SCAN_BWD = 2
+# gdn_glr_pass
+GDN_GLR_FWD = 0
+GDN_GLR_SAVED = 1
+GDN_GLR_BWD = 2
 
 # Every symbol include/gdn.h declares.
 EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chunk_fwd",
@@ -60,7 +64,8 @@ EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chun
             "gdn_kda_chunk_fwd", "gdn_chunk_fwd_noalloc", "gdn_device_copy", "gdn_chunk_fwd_save",
             "gdn_chunk_bwd_saved", "gdn_kda_chunk_bwd", "gdn_kda_chunk_fwd_save", "gdn_kda_chunk_bwd_saved",
             "gdn_step", "gdn_kda_step", "gdn_conv_fwd", "gdn_conv_workspace_size", "gdn_conv_bwd", "gdn_conv_step",
-            "gdn_scan_workspace_size", "gdn_scan_fwd", "gdn_scan_fwd_save", "gdn_scan_bwd_saved", "gdn_scan_step")
+            "gdn_scan_workspace_size", "gdn_scan_fwd", "gdn_scan_fwd_save", "gdn_scan_bwd_saved", "gdn_scan_step",
+            "gdn_glr_workspace_size", "gdn_glr_fwd", "gdn_glr_fwd_save", "gdn_glr_bwd_saved", "gdn_glr_step")
 
 
 class GdnLibraryMissing(RuntimeError):
@@ -108,6 +113,17 @@ class ScanProblem(ctypes.Structure):
         ("cu_seqlens_dev", ctypes.c_void_p),
         ("io_dtype", ctypes.c_int32),
         ("dt_softplus", ctypes.c_int32),
+    ]
+
+
+class GlrProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("io_dtype", ctypes.c_int32),
+        ("c", ctypes.c_float),
     ]
 
 
@@ -159,7 +175,7 @@ def load():
     lib.gdn_kda_chunk_fwd_save.restype = ctypes.c_int
     lib.gdn_kda_chunk_bwd_saved.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.gdn_kda_chunk_bwd_saved.restype = ctypes.c_int
-    PC, PS, Z = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.c_size_t
+    PC, PS, PG, Z = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.POINTER(GlrProblem), ctypes.c_size_t
     for name, args in (
             ("gdn_step", [PP] + [P] * 8), ("gdn_kda_step", [PP] + [P] * 8),
             ("gdn_conv_fwd", [PC] + [P] * 7), ("gdn_conv_step", [PC] + [P] * 6),
@@ -169,7 +185,12 @@ def load():
             ("gdn_scan_fwd", [PS] + [P] * 12 + [Z, P]),
             ("gdn_scan_fwd_save", [PS] + [P] * 12 + [Z, P, Z, P]),
             ("gdn_scan_bwd_saved", [PS] + [P] * 11 + [Z] + [P] * 10 + [Z, P]),
-            ("gdn_scan_step", [PS] + [P] * 11)):
+            ("gdn_scan_step", [PS] + [P] * 11),
+            ("gdn_glr_workspace_size", [PG, ctypes.c_int32, ctypes.POINTER(Z)]),
+            ("gdn_glr_fwd", [PG] + [P] * 9 + [Z, P]),
+            ("gdn_glr_fwd_save", [PG] + [P] * 9 + [Z, P, Z, P]),
+            ("gdn_glr_bwd_saved", [PG] + [P] * 8 + [Z] + [P] * 7 + [Z, P]),
+            ("gdn_glr_step", [PG] + [P] * 8)):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int

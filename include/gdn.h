@@ -550,6 +550,81 @@ gdn_status gdn_scan_step(const gdn_scan_problem* problem, const void* u, const v
                          const void* Bm, const void* Cm, const float* Dskip, const void* z,
                          const float* dt_bias, float* h, void* y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators that hybrid models put next to the delta rule: the gated linear
+ * recurrence, the norm and rotation of queries and keys, and attention over a
+ * sliding window.  The conventions above hold; what differs is said at each entry
+ * point.
+ * ------------------------------------------------------------------------- */
+
+/* Gated linear recurrence: per sequence and channel, with a state h (initially h0, or
+ * zero) and for every token t in order
+ *     la = -c softplus(lam) sigmoid(r_t);  a = exp(la)
+ *     h <- a h + sqrt(1 - a^2) sigmoid(i_t) x_t
+ *     y_t = h   or, with z,   h z_t sigmoid(z_t)
+ * Tensors: x, r, i, z, y and their gradients [B,T,C] (io dtype); lam, dlam [C], h0,
+ * h_final, dh_final, dh0, h [num_seqs,C] fp32.  All of them 16-byte aligned.  Supported: C a
+ * multiple of 8 up to 2^20, B T < 2^31, up to 65535 sequences, c >= 0, and fewer than 2^32
+ * threads in a launch, else GDN_ERR_UNSUPPORTED.  A launch has 64 threads for 1, 4 or 8 (the
+ * fewest that hold the longest sequence at 64 tokens, in the backward 32; else 8), for every
+ * 32 channels (rounded up to 256), every sequence and every segment of the longest one (one
+ * segment wherever sequences and channels alone are 256 workgroups).  Finite lam is documented,
+ * not checked.  All arithmetic is fp32; io outputs are rounded once.  NaN and Inf reach what
+ * the definition makes of them and nothing that it leaves finite; where it gives an infinity
+ * NaN may stand instead (a state that is infinite while the decays over several tokens
+ * underflow to zero). */
+typedef struct gdn_glr_problem {
+  int32_t B, T, C;
+  int32_t num_seqs;                /* == B for dense input, else len(cu_seqlens) - 1        */
+  const int32_t* cu_seqlens_host;  /* host, num_seqs + 1 offsets, or NULL (dense)           */
+  const int32_t* cu_seqlens_dev;   /* device copy of the same values, or NULL               */
+  int32_t io_dtype;                /* gdn_dtype                                             */
+  float c;                         /* factor of the log-decay                               */
+} gdn_glr_problem;
+
+typedef enum gdn_glr_pass {
+  GDN_GLR_FWD = 0,   /* workspace of gdn_glr_fwd and gdn_glr_fwd_save */
+  GDN_GLR_SAVED = 1, /* the `saved` buffer                            */
+  GDN_GLR_BWD = 2    /* workspace of gdn_glr_bwd_saved                */
+} gdn_glr_pass;
+
+/* Bytes of the device buffer `pass` needs (0 is possible; the pointer may then be
+ * NULL); GDN_ERR_UNSUPPORTED for another pass.  The sizes depend on the problem's
+ * sizes and offsets alone. */
+gdn_status gdn_glr_workspace_size(const gdn_glr_problem* problem, int32_t pass, size_t* bytes);
+
+/* Forward.  in: x, r, i, lam; z, h0 (each may be NULL: no gate, zero); out: y, h_final
+ * (NULL: not wanted; a sequence of no tokens keeps h0).  The time axis is composed of runs
+ * and, where the channels are few, of segments: results are those of the serial order up to
+ * fp32 rounding, bit-identical from call to call. */
+gdn_status gdn_glr_fwd(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
+                       const float* lam, const void* z, const float* h0, void* y, float* h_final,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Training: gdn_glr_fwd_save computes what gdn_glr_fwd computes (bit-identical) and keeps
+ * the state every few tokens in `saved` (GDN_GLR_SAVED bytes, 16-byte aligned);
+ * gdn_glr_bwd_saved forms from it the gradients of L = <y, dy> + <h_final, dh_final>.
+ * The problem and the inputs must be those of the save call and `saved` unmodified (not
+ * checked).  `saved` is only read by the backward.
+ *   in : x, r, i, lam, z as gdn_glr_fwd; dy; dh_final (NULL: zero)
+ *   out: dx, dr, di (io dtype), dlam (fp32); dz, dh0 (NULL: not wanted; dz needs z,
+ *        GDN_ERR_NULL otherwise)
+ * dlam is summed in a fixed order (bit-identical from call to call). */
+gdn_status gdn_glr_fwd_save(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
+                            const float* lam, const void* z, const float* h0, void* y, float* h_final,
+                            void* saved, size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                            void* stream);
+gdn_status gdn_glr_bwd_saved(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
+                             const float* lam, const void* z, const void* dy, const float* dh_final,
+                             const void* saved, size_t saved_bytes, void* dx, void* dr, void* di,
+                             float* dlam, void* dz, float* dh0, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* One token of every sequence (decoding; dense with T == 1): y, and the state h [B,C] fp32
+ * updated in place.  y and h must not overlap another tensor.  No workspace. */
+gdn_status gdn_glr_step(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
+                        const float* lam, const void* z, float* h, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

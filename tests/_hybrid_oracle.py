@@ -1,0 +1,116 @@
+"""float64 definitions of the operators of hybrid models (CPU), their gradients, and
+bounds on the error of an fp32 evaluation.
+
+The bounds are running error analyses: next to each value stands the sum of the absolute
+values of its terms and what the roundings on the way of each term can add up to, in
+units of 2^-24, with the true values of decays and gates.  ``check`` adds the final
+rounding to the output's type, half a step of it.
+"""
+import torch
+
+U = 2.0 ** -24
+
+
+def spans(B, T, cu):
+    """(first row, last row + 1) of every sequence of the flattened (B T) rows."""
+    if cu is None:
+        return [(i * T, (i + 1) * T) for i in range(B)]
+    return [(int(a), int(b)) for a, b in zip(cu[:-1], cu[1:])]
+
+
+def f64(*ts):
+    return [None if t is None else t.detach().double().cpu() for t in ts]
+
+
+def check(name, got, want, bound):
+    """|got - want| <= bound + half a step of got's type."""
+    assert tuple(got.shape) == tuple(want.shape), (name, got.shape, want.shape)
+    half = torch.finfo(got.dtype).eps / 2 if got.dtype != torch.float32 else 0.0
+    off = (got.detach().double().cpu() - want).abs()
+    # the rounded value may be of a size that the bound has moved
+    room = bound + half * (want.abs() + bound) + torch.finfo(torch.float32).tiny
+    bad = ~(off <= room)
+    assert not bool(bad.any()), f"{name}: {int(bad.sum())} of {bad.numel()} off, worst {float((off / room).nan_to_num(9e9).max()):.3g} of the bound"
+
+
+# --------------------------------------------------------------------------- gated linear recurrence
+
+def glr(x, r, i, lam, z, h0, cu, c=8.0, dy=None, dlast=None):
+    """(values, bounds): dicts y, state and, with dy, the gradients of <y, dy> + <state,
+    dlast>, by the written-out formulas, token by token.
+
+    Roundings: a sigmoid of v (|v| + 4: the exponent's, of the exponential's argument, and
+    the quotient's), la that of r's sigmoid and 8 more (softplus, factors), kl in all; a
+    kl |la| + 3; m half of kl and 14 for the difference (1 - a^2 >= 0.39 where it is taken,
+    and the exponential's derivative is at most 1 over the rest), at most 12 + kl / 2; a state one for the
+    multiply-add, and 100 for the joins of runs, waves and segments."""
+    x, r, i, lam, z, h0, dy, dlast = f64(x, r, i, lam, z, h0, dy, dlast)
+    B, T, C = x.shape
+    shape = x.shape
+    x, r, i, z, dy = [None if t is None else t.reshape(B * T, C) for t in (x, r, i, z, dy)]
+    soft = torch.clamp(lam, min=0) + torch.log1p(torch.exp(-lam.abs()))
+    sr, si = torch.sigmoid(r), torch.sigmoid(i)
+    la = -c * soft * sr
+    kl = r.abs() + 12
+    a, m = torch.exp(la), torch.sqrt(-torch.expm1(2 * la))
+    ka, km = kl * la.abs() + 3, 12 + kl / 2
+    ki = i.abs() + 4
+    b = m * si * x
+    kb = km + ki + 3
+    seqs = spans(B, T, cu)
+    n = len(seqs)
+    h, hp = torch.zeros_like(x), torch.zeros_like(x)
+    hs, hps, eh, ehp = (torch.zeros_like(x) for _ in range(4))  # sums of absolute terms, errors
+    last, elast = x.new_zeros(n, C), x.new_zeros(n, C)
+    for q, (t0, t1) in enumerate(seqs):
+        v = h0[q] if h0 is not None else x.new_zeros(C)
+        s, e = v.abs(), torch.zeros_like(v)
+        for t in range(t0, t1):
+            hp[t], hps[t], ehp[t] = v, s, e + 100 * U * s
+            v = a[t] * v + b[t]
+            e = a[t] * e + (ka[t] + 1) * U * a[t] * s + (kb[t] + 1) * U * b[t].abs()
+            s = a[t] * s + b[t].abs()
+            h[t], hs[t], eh[t] = v, s, e + 100 * U * s
+        last[q], elast[q] = v, e + 100 * U * s
+    if z is not None:
+        sz = torch.sigmoid(z)
+        gate, kz = z * sz, z.abs() + 7
+        y, ey = h * gate, (eh + kz * U * hs) * gate.abs()
+    else:
+        y, ey = h, eh
+    out, err = {"y": y.reshape(shape), "state": last}, {"y": ey.reshape(shape), "state": elast}
+    if dy is None:
+        return out, err
+    ds = dy * gate if z is not None else dy
+    kd = kz if z is not None else torch.zeros_like(x)
+    G, Gs, eG = (torch.zeros_like(x) for _ in range(3))
+    dh0, edh0 = x.new_zeros(n, C), x.new_zeros(n, C)
+    for q, (t0, t1) in enumerate(seqs):
+        v = dlast[q] if dlast is not None else x.new_zeros(C)
+        s, e = v.abs(), torch.zeros_like(v)
+        for t in range(t1 - 1, t0 - 1, -1):
+            v, e = ds[t] + v, e + (kd[t] + 1) * U * ds[t].abs() + U * s
+            s = ds[t].abs() + s
+            G[t], Gs[t], eG[t] = v, s, e + 100 * U * s
+            v, e, s = a[t] * v, a[t] * e + (ka[t] + 1) * U * a[t] * s, a[t] * s
+        dh0[q], edh0[q] = v, e + 100 * U * s
+    xs = x.abs()
+    dx, edx = G * m * si, (eG + (km + ki + 3) * U * Gs) * m * si
+    di = G * m * x * si * (1 - si)
+    edi = (eG * (1 - si) + Gs * ((km + ki + 5) * (1 - si) + 4) * U) * m * xs * si  # 1 - s: off by roundings of 1
+    lm = torch.where(m > 0, la / m, 0)
+    one, two = a * la * hp, a * a * lm * si * x
+    E = G * (one - two)
+    both = (a * la.abs() * hps + a * a * lm.abs() * si * xs)
+    eE = eG * both + Gs * (a * la.abs() * (ehp + (ka + kl + 6) * U * hps) + (2 * ka + kl + km + ki + 8) * U * a * a * lm.abs() * si * xs)
+    Es = Gs * both
+    dr, edr = E * (1 - sr), eE * (1 - sr) + 6 * U * Es
+    ratio = torch.sigmoid(lam) / soft
+    dlam, edlam = E.sum(0) * ratio, (eE.sum(0) + (min(B * T, 4096) + 40) * U * Es.sum(0)) * ratio
+    out.update(dx=dx.reshape(shape), dr=dr.reshape(shape), di=di.reshape(shape), dlam=dlam, dh0=dh0)
+    err.update(dx=edx.reshape(shape), dr=edr.reshape(shape), di=edi.reshape(shape), dlam=edlam, dh0=edh0)
+    if z is not None:
+        slope, wide = sz * (1 + z * (1 - sz)), sz * (1 + z.abs() * (1 - sz) + z.abs())
+        out["dz"] = (dy * h * slope).reshape(shape)
+        err["dz"] = (dy.abs() * (eh * slope.abs() + hs * (z.abs() + 16) * U * wide)).reshape(shape)
+    return out, err

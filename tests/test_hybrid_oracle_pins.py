@@ -1,0 +1,70 @@
+"""The float64 definitions of the hybrid operators against differences, closed forms and
+planted mistakes (CPU)."""
+import torch
+
+import _hybrid_oracle as ref
+
+
+def _glr_args(B=2, T=9, C=3, seed=0, z=True):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    return [r(B, T, C), r(B, T, C), r(B, T, C), r(C) - 2, r(B, T, C) if z else None], r, B
+
+
+def test_glr_gradients_against_differences():
+    for z, cu in ((True, None), (False, None), (True, [0, 4, 4, 9])):
+        args, r, B = _glr_args(B=1 if cu else 2, z=z)
+        n = len(cu) - 1 if cu else B
+        h0, dy, dl = r(n, 3), r(*args[0].shape), r(n, 3)
+        out, _ = ref.glr(*args, h0, cu, dy=dy, dlast=dl)
+
+        def loss(*leaves):
+            o, _ = ref.glr(*leaves[:4], leaves[4] if z else None, leaves[-1], cu)
+            return (o["y"] * dy).sum() + (o["state"] * dl).sum()
+
+        leaves = [t for t in args if t is not None] + [h0]
+        names = ["dx", "dr", "di", "dlam"] + (["dz"] if z else []) + ["dh0"]
+        for k, name in enumerate(names):
+            flat = leaves[k].reshape(-1)
+            for j in range(0, flat.numel(), max(1, flat.numel() // 12)):
+                keep, step = float(flat[j]), 1e-6
+                flat[j] = keep + step
+                up = loss(*leaves)
+                flat[j] = keep - step
+                down = loss(*leaves)
+                flat[j] = keep
+                assert abs(float(up - down) / (2 * step) - float(out[name].reshape(-1)[j])) <= 1e-7 * (1 + abs(float(up))), name
+
+
+def test_glr_closed_forms():
+    args, r, B = _glr_args(z=False)
+    h0 = r(B, 3)
+    shut = [args[0], torch.full_like(args[1], -60.0), *args[2:]]  # a gate that is shut keeps the state
+    out, _ = ref.glr(*shut, h0, None)
+    assert float((out["y"] - h0.unsqueeze(1)).abs().max()) <= 1e-11
+    # one token of an open gate: a = exp(-c softplus(lam))
+    out, _ = ref.glr(args[0][:, :1], torch.full((B, 1, 3), 60.0, dtype=torch.float64), torch.full((B, 1, 3), 60.0, dtype=torch.float64), args[3],
+                     None, h0, None, c=2.0)
+    a = (1 + torch.exp(args[3])) ** -2
+    assert float((out["y"][:, 0] - (a * h0 + torch.sqrt(1 - a * a) * args[0][:, 0])).abs().max()) <= 1e-14
+    # packed = each alone
+    x, rr, i, lam, _ = args
+    whole, _ = ref.glr(x[:1], rr[:1], i[:1], lam, None, h0, [0, 4, 9])
+    for n, s in enumerate((slice(0, 4), slice(4, 9))):
+        part, _ = ref.glr(x[:1, s], rr[:1, s], i[:1, s], lam, None, h0[n:n + 1], None)
+        assert torch.equal(part["y"], whole["y"][:, s]) and torch.equal(part["state"][0], whole["state"][n])
+
+
+def test_glr_bounds_notice_a_planted_mistake():
+    """A state taken one token late, or sqrt(1 - a) for sqrt(1 - a^2), is far outside the bounds."""
+    args, r, B = _glr_args(T=20)
+    out, err = ref.glr(*args, r(B, 3), None, dy=r(*args[0].shape))
+    for name in out:
+        assert float((err[name] / out[name].abs().mean()).max()) <= 1e-3, name
+        ref.check(name, out[name].float(), out[name], err[name] + 2 * ref.U * out[name].abs())
+    bad = torch.cat([out["y"][:, 1:], out["y"][:, :1]], 1)
+    try:
+        ref.check("late", bad.float(), out["y"], err["y"])
+    except AssertionError:
+        return
+    raise AssertionError("a planted mistake passed")
