@@ -10,5 +10,6 @@ from .ops import (SeqLens, chunk_bwd, chunk_bwd_saved, chunk_fwd, chunk_fwd_noal
                   prologue, recurrent_ref, saved_buffer)
 from .layer import (conv_bwd, conv_fwd, conv_step, kda_step, scan_buffers, scan_bwd_saved,  # noqa: F401
                     scan_fwd, scan_fwd_save, scan_step, step)
-from .hybrid import glr_buffers, glr_bwd_saved, glr_fwd, glr_fwd_save, glr_step  # noqa: F401
+from .hybrid import (glr_buffers, glr_bwd_saved, glr_fwd, glr_fwd_save, glr_step, rope_bwd,  # noqa: F401
+                     rope_fwd)
 from ._native import GdnError, GdnLibraryMissing  # noqa: F401

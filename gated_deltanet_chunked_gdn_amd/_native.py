@@ -57,6 +57,10 @@ GDN_SCAN_BWD = 2
 GDN_GLR_FWD = 0
 GDN_GLR_SAVED = 1
 GDN_GLR_BWD = 2
+# gdn_rope_norm
+GDN_ROPE_NONE = 0
+GDN_ROPE_RMS = 1
+GDN_ROPE_L2 = 2
 
 # Every symbol include/gdn.h declares.
 EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chunk_fwd",
@@ -65,7 +69,8 @@ EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chun
             "gdn_chunk_bwd_saved", "gdn_kda_chunk_bwd", "gdn_kda_chunk_fwd_save", "gdn_kda_chunk_bwd_saved",
             "gdn_step", "gdn_kda_step", "gdn_conv_fwd", "gdn_conv_workspace_size", "gdn_conv_bwd", "gdn_conv_step",
             "gdn_scan_workspace_size", "gdn_scan_fwd", "gdn_scan_fwd_save", "gdn_scan_bwd_saved", "gdn_scan_step",
-            "gdn_glr_workspace_size", "gdn_glr_fwd", "gdn_glr_fwd_save", "gdn_glr_bwd_saved", "gdn_glr_step")
+            "gdn_glr_workspace_size", "gdn_glr_fwd", "gdn_glr_fwd_save", "gdn_glr_bwd_saved", "gdn_glr_step",
+            "gdn_rope_fwd", "gdn_rope_workspace_size", "gdn_rope_bwd")
 
 
 class GdnLibraryMissing(RuntimeError):
@@ -127,6 +132,18 @@ class GlrProblem(ctypes.Structure):
     ]
 
 
+class RopeProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("R", ctypes.c_int32),
+        ("norm", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("io_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -176,6 +193,7 @@ def load():
     lib.gdn_kda_chunk_bwd_saved.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.gdn_kda_chunk_bwd_saved.restype = ctypes.c_int
     PC, PS, PG, Z = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.POINTER(GlrProblem), ctypes.c_size_t
+    PR = ctypes.POINTER(RopeProblem)
     for name, args in (
             ("gdn_step", [PP] + [P] * 8), ("gdn_kda_step", [PP] + [P] * 8),
             ("gdn_conv_fwd", [PC] + [P] * 7), ("gdn_conv_step", [PC] + [P] * 6),
@@ -190,7 +208,9 @@ def load():
             ("gdn_glr_fwd", [PG] + [P] * 9 + [Z, P]),
             ("gdn_glr_fwd_save", [PG] + [P] * 9 + [Z, P, Z, P]),
             ("gdn_glr_bwd_saved", [PG] + [P] * 8 + [Z] + [P] * 7 + [Z, P]),
-            ("gdn_glr_step", [PG] + [P] * 8)):
+            ("gdn_glr_step", [PG] + [P] * 8),
+            ("gdn_rope_fwd", [PR] + [P] * 9), ("gdn_rope_workspace_size", [PR, ctypes.POINTER(Z)]),
+            ("gdn_rope_bwd", [PR] + [P] * 13 + [Z, P])):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int

@@ -52,4 +52,41 @@ hipError_t launch_glr_fwd(const GlrParams& p, bool bf16, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrParams& p, bool bf16, hipStream_t s);
 hipError_t launch_glr_step(const GlrParams& p, bool bf16, hipStream_t s);
 
+// ---------------------------------------------------------------------------- norm and rotation
+
+struct RopeParams {
+  const void* q;         // [tokens] rows of Hq D values, q_stride apart
+  const void* k;
+  const float* inv_freq; // [R / 2]
+  const int32_t* pos;    // [tokens] or nullptr: the place in the row of T
+  const float* wq;       // [D] or nullptr
+  const float* wk;
+  void* q_out;           // contiguous; backward: dq, dk
+  void* k_out;
+  const void* dq_out;    // backward, contiguous
+  const void* dk_out;
+  float* dwq;            // or nullptr
+  float* dwk;
+  float* part;           // backward: [workgroup][2][D] partial sums
+  int64_t q_stride, k_stride;
+  int64_t tokens;
+  int32_t T, Hq, Hk, R;
+  int32_t norm;          // gdn_rope_norm
+  float eps;
+  int32_t per_group;     // tokens that a workgroup takes at a time
+  int32_t groups;        // workgroups
+};
+
+// Tokens of a workgroup at a time: four where that leaves every CU several workgroups.
+constexpr int kRopeMost = 4;
+inline int rope_tokens(int64_t tokens) { return tokens >= 1024 * kRopeMost ? kRopeMost : 1; }
+// The backward's workgroups go on to further tokens, so that few partial sums are left.
+constexpr int kRopeBwdGroups = 1024;
+inline int64_t rope_bwd_groups(int64_t tokens) {
+  const int64_t n = (tokens + rope_tokens(tokens) - 1) / rope_tokens(tokens);
+  return n < kRopeBwdGroups ? n : kRopeBwdGroups;
+}
+hipError_t launch_rope_fwd(const RopeParams& p, int D, bool bf16, bool interleaved, hipStream_t s);
+hipError_t launch_rope_bwd(const RopeParams& p, int D, bool bf16, bool interleaved, hipStream_t s);
+
 }  // namespace gdn

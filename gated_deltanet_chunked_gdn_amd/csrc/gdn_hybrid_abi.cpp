@@ -94,6 +94,63 @@ gdn_status glr_fwd(const gdn_glr_problem* p, const void* x, const void* r, const
   return hip_status(gdn::launch_glr_fwd(gp, c.io == 2, static_cast<hipStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------------------- norm and rotation
+
+struct RopeSize {
+  size_t io = 0, qin = 0, kin = 0, q = 0, k = 0, freq = 0, pos = 0, weight = 0, ws = 0;
+  int64_t tokens = 0, q_stride = 0, k_stride = 0;
+};
+
+// Bytes from the first to the last value of `rows` rows of `row` values, `stride` apart.
+size_t extent(int64_t rows, int64_t stride, int64_t row, size_t io) {
+  return rows ? static_cast<size_t>((rows - 1) * stride + row) * io : 0;
+}
+
+// A row stride in values (0: the row itself): whole 16 bytes, rows that do not overlap.
+gdn_status check_stride(int64_t given, int64_t row, size_t io, int64_t* stride) {
+  *stride = given ? given : row;
+  if (*stride < row) return GDN_ERR_SHAPE;
+  // 2^31 rows of 2^31 values of 4 bytes would pass 64 bits
+  if (*stride > INT64_C(1) << 28) return GDN_ERR_UNSUPPORTED;
+  return *stride * static_cast<int64_t>(io) % 16 ? GDN_ERR_ALIGN : GDN_OK;
+}
+
+gdn_status check_rope(const gdn_rope_problem* p, RopeSize* c) {
+  if (!p) return GDN_ERR_NULL;
+  if (p->io_dtype != GDN_FP32 && p->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (p->B < 0 || p->T < 0 || p->Hq <= 0 || p->Hk <= 0 || p->D <= 0 || p->R < 0 || p->R > p->D) return GDN_ERR_SHAPE;
+  if ((p->D != 64 && p->D != 128 && p->D != 256) || p->R % 16 != 0 || p->Hq > 4096 || p->Hk > 4096) return GDN_ERR_UNSUPPORTED;
+  if (p->norm != GDN_ROPE_NONE && p->norm != GDN_ROPE_RMS && p->norm != GDN_ROPE_L2) return GDN_ERR_UNSUPPORTED;
+  c->io = p->io_dtype == GDN_BF16 ? 2 : 4;
+  c->tokens = static_cast<int64_t>(p->B) * p->T;
+  if (c->tokens > INT32_MAX || c->tokens * (p->Hq + p->Hk) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  // 256 threads for every four tokens and more (one below 4096), counted in 32 bits
+  if (c->tokens / gdn::kRopeMost >= INT64_C(1) << 24) return GDN_ERR_UNSUPPORTED;
+  const int64_t qrow = static_cast<int64_t>(p->Hq) * p->D, krow = static_cast<int64_t>(p->Hk) * p->D;
+  gdn_status st = check_stride(p->q_stride, qrow, c->io, &c->q_stride);
+  if (st == GDN_OK) st = check_stride(p->k_stride, krow, c->io, &c->k_stride);
+  if (st != GDN_OK) return st;
+  c->qin = extent(c->tokens, c->q_stride, qrow, c->io);
+  c->kin = extent(c->tokens, c->k_stride, krow, c->io);
+  c->q = static_cast<size_t>(c->tokens) * qrow * c->io;
+  c->k = static_cast<size_t>(c->tokens) * krow * c->io;
+  c->freq = static_cast<size_t>(p->R) / 2 * 4;
+  c->pos = static_cast<size_t>(c->tokens) * 4;
+  c->weight = static_cast<size_t>(p->D) * 4;
+  c->ws = static_cast<size_t>(gdn::rope_bwd_groups(c->tokens)) * 2 * c->weight;
+  return GDN_OK;
+}
+
+gdn::RopeParams rope_params(const gdn_rope_problem* p, const RopeSize& c, const void* q, const void* k, const float* inv_freq,
+                            const int32_t* positions, const float* wq, const float* wk) {
+  gdn::RopeParams rp{};
+  rp.q = q; rp.k = k; rp.inv_freq = inv_freq; rp.pos = positions; rp.wq = wq; rp.wk = wk;
+  rp.q_stride = c.q_stride; rp.k_stride = c.k_stride; rp.tokens = c.tokens;
+  rp.T = p->T; rp.Hq = p->Hq; rp.Hk = p->Hk; rp.R = p->R; rp.norm = p->norm; rp.eps = p->eps;
+  rp.per_group = gdn::rope_tokens(c.tokens);
+  return rp;
+}
+
 }  // namespace
 
 extern "C" {
@@ -157,6 +214,52 @@ gdn_status gdn_glr_step(const gdn_glr_problem* p, const void* x, const void* r, 
   gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z);
   gp.h_final = h; gp.y = y;
   return hip_status(gdn::launch_glr_step(gp, c.io == 2, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k, const float* inv_freq,
+                        const int32_t* positions, const float* wq, const float* wk, void* q_out, void* k_out, void* stream) {
+  RopeSize c;
+  gdn_status st = check_rope(p, &c);
+  if (st != GDN_OK) return st;
+  if ((wq || wk) && p->norm != GDN_ROPE_RMS) return GDN_ERR_UNSUPPORTED;
+  st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {inv_freq, c.freq, 4, true}, {positions, c.pos, 4, false},
+                      {wq, c.weight, 16, false}, {wk, c.weight, 16, false}},
+                     {{q_out, c.q, 16, true}, {k_out, c.k, 16, true}});
+  if (st != GDN_OK || c.tokens == 0) return st;
+  gdn::RopeParams rp = rope_params(p, c, q, k, inv_freq, positions, wq, wk);
+  rp.q_out = q_out; rp.k_out = k_out;
+  rp.groups = static_cast<int32_t>((c.tokens + rp.per_group - 1) / rp.per_group);
+  return hip_status(gdn::launch_rope_fwd(rp, p->D, c.io == 2, p->interleaved != 0, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_rope_workspace_size(const gdn_rope_problem* p, size_t* bytes) {
+  if (!bytes) return GDN_ERR_NULL;
+  RopeSize c;
+  const gdn_status st = check_rope(p, &c);
+  if (st != GDN_OK) return st;
+  *bytes = c.ws;
+  return GDN_OK;
+}
+
+gdn_status gdn_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k, const float* inv_freq,
+                        const int32_t* positions, const float* wq, const float* wk, const void* dq_out, const void* dk_out,
+                        void* dq, void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+  RopeSize c;
+  gdn_status st = check_rope(p, &c);
+  if (st != GDN_OK) return st;
+  if ((wq || wk || dwq || dwk) && p->norm != GDN_ROPE_RMS) return GDN_ERR_UNSUPPORTED;
+  st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {inv_freq, c.freq, 4, true}, {positions, c.pos, 4, false},
+                      {wq, c.weight, 16, false}, {wk, c.weight, 16, false}, {dq_out, c.q, 16, true}, {dk_out, c.k, 16, true}},
+                     {{dq, c.q, 16, true}, {dk, c.k, 16, true}, {dwq, c.weight, 16, false}, {dwk, c.weight, 16, false},
+                      {ws, ws_bytes, 16, false}});
+  if (st != GDN_OK) return st;
+  if ((dwq || dwk) && c.ws && (!ws || ws_bytes < c.ws)) return GDN_ERR_WORKSPACE;
+  if (c.tokens == 0 && !dwq && !dwk) return GDN_OK;
+  gdn::RopeParams rp = rope_params(p, c, q, k, inv_freq, positions, wq, wk);
+  rp.q_out = dq; rp.k_out = dk; rp.dq_out = dq_out; rp.dk_out = dk_out; rp.dwq = dwq; rp.dwk = dwk;
+  rp.part = static_cast<float*>(ws);
+  rp.groups = static_cast<int32_t>(gdn::rope_bwd_groups(c.tokens));
+  return hip_status(gdn::launch_rope_bwd(rp, p->D, c.io == 2, p->interleaved != 0, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,14 +1,17 @@
 """Python entry points of the operators that hybrid models put next to the delta rule,
-over libgdn's C ABI (include/gdn.h): the gated linear recurrence.  As in ``layer``,
-PyTorch supplies device memory and the current stream, and every step of the computation
-runs in libgdn's HIP kernels.
+over libgdn's C ABI (include/gdn.h): the gated linear recurrence, and the norm and rotation
+of queries and keys.  As in ``layer``, PyTorch supplies device memory and the current
+stream, and every step of the computation runs in libgdn's HIP kernels.
 
     y, h     = glr_fwd(x, r, i, lam, z=None, h0=None)
     y, h, saved = glr_fwd_save(...)
     grads    = glr_bwd_saved(x, r, i, lam, dy, saved, ...)
     y        = glr_step(x, r, i, lam, state, z=None)  # one token, state updated in place
 
-Activations are bf16 or fp32 (one dtype a call), parameters and recurrent states fp32.
+    q, k     = rope_fwd(q, k, inv_freq, positions=None, norm="rms", wq=None, wk=None)
+    grads    = rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, ...)
+
+Tensors are contiguous, but for q and k (see there).  Activations are bf16 or fp32 (one dtype a call), parameters and recurrent states fp32.
 Packed sequences: B == 1 and ``cu_seqlens`` the N + 1 offsets, best built once as a
 ``SeqLens``.  Outputs and gradients that were not asked for are None.  A ``workspace``
 holds nothing between calls, but calls that may overlap (on two streams, in graphs
@@ -147,3 +150,88 @@ def glr_step(x, r, i, lam, state, z=None, c: float = 8.0, out=None):
     y, yptr = _result(out, x, dev)
     _call(dev, "gdn_glr_step", prob, *ins, s, yptr)
     return y
+
+
+# --------------------------------------------------------------------------- norm and rotation
+
+_NORM = {None: nat.GDN_ROPE_NONE, "none": nat.GDN_ROPE_NONE, "rms": nat.GDN_ROPE_RMS, "l2": nat.GDN_ROPE_L2}
+_I32 = torch.int32
+
+
+def _rows(t, shape, dtype, dev, name):
+    """(address, values from token to token) of a (B, T, H, D) tensor whose tokens' heads and
+    values are contiguous and whose tokens lie evenly apart: a contiguous one, or a view of
+    the columns of a contiguous (B, T, more) one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[2] * shape[3]
+    B, T, H, D = shape
+    sb, st, sh, sd = t.stride()
+    if T == 1:  # a token's own stride says nothing: the rows of the batch count
+        st = sb if B > 1 else H * D
+    if (sd != 1 and D > 1) or (sh != D and H > 1) or st < H * D or (B > 1 and sb != T * st):
+        raise ValueError(f"{name} must be contiguous, or a view of the columns of contiguous rows (strides {t.stride()})")
+    return t.data_ptr(), st
+
+
+def _rope_problem(q, k, inv_freq, norm, eps, interleaved):
+    """(device index, problem, addresses of q and k)"""
+    what = "q must be (B, T, Hq, D) and k (B, T, Hk, D)"
+    dev = _first(q, "q", 4, what)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError(what)
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be an (R / 2,) tensor")
+    if norm not in _NORM:
+        raise ValueError(f"norm must be one of {sorted(map(str, _NORM))}")
+    B, T, Hq, D = q.shape
+    Hk, io = k.shape[2], q.dtype
+    qp, qs = _rows(q, q.shape, io, dev, "q")
+    kp, ks = _rows(k, (B, T, Hk, D), io, dev, "k")
+    prob = _dense(nat.RopeProblem, (B, T, Hq, Hk, D, 2 * inv_freq.shape[0]), _NORM[norm], int(bool(interleaved)), _IO[io],
+                  float(eps), qs, ks)
+    return dev, prob, qp, kp
+
+
+def _rope_inputs(p, inv_freq, positions, wq, wk, dev):
+    return (_want(inv_freq, (p.R // 2,), _F32, dev, "inv_freq") or None, _may(positions, (p.B, p.T), _I32, dev, "positions"),
+            _may(wq, (p.D,), _F32, dev, "wq"), _may(wk, (p.D,), _F32, dev, "wk"))
+
+
+def rope_fwd(q, k, inv_freq, positions=None, norm="rms", eps: float = 1e-6, wq=None, wk=None, interleaved: bool = False,
+             q_out=None, k_out=None):
+    """Norm of queries and keys per head and rotation by position (gdn_rope_fwd): q
+    (B, T, Hq, D), k (B, T, Hk, D) of the io dtype, contiguous or columns of contiguous
+    rows; inv_freq (R / 2,) fp32; ``positions`` (B, T) int32 or None (0 .. T - 1); ``norm``
+    "rms" (with weights wq, wk (D,) fp32 or None), "l2" or None.  Returns (q, k)."""
+    dev, prob, qp, kp = _rope_problem(q, k, inv_freq, norm, eps, interleaved)
+    ins = _rope_inputs(prob, inv_freq, positions, wq, wk, dev)
+    outs = []
+    for out, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        out = torch.empty(like.shape, dtype=like.dtype, device=dev) if out is None else out
+        outs.append((out, _want(out, like.shape, like.dtype, dev, name)))
+    _call(dev, "gdn_rope_fwd", prob, qp, kp, *ins, outs[0][1], outs[1][1])
+    return outs[0][0], outs[1][0]
+
+
+def rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, norm="rms", eps: float = 1e-6, wq=None, wk=None,
+             interleaved: bool = False, workspace=None):
+    """Backward of rope_fwd (gdn_rope_bwd).  Returns dict dq, dk, dwq, dwk (None without
+    their weights)."""
+    dev, prob, qp, kp = _rope_problem(q, k, inv_freq, norm, eps, interleaved)
+    ins = _rope_inputs(prob, inv_freq, positions, wq, wk, dev)
+    grads = (_want(dq_out, q.shape, q.dtype, dev, "dq_out"), _want(dk_out, k.shape, q.dtype, dev, "dk_out"))
+    need = _size("gdn_rope_workspace_size", prob) if wq is not None or wk is not None else 0
+    buf, ws, nws = _buffer(workspace, need, dev, "workspace")
+    fresh = lambda t: torch.empty(t.shape, dtype=t.dtype, device=dev) if t is not None else None  # noqa: E731
+    out = {"dq": fresh(q), "dk": fresh(k), "dwq": fresh(wq), "dwk": fresh(wk)}
+    _call(dev, "gdn_rope_bwd", prob, qp, kp, *ins, *grads, *(t.data_ptr() if t is not None else None for t in out.values()),
+          ws, nws)
+    return out

@@ -625,6 +625,57 @@ gdn_status gdn_glr_bwd_saved(const gdn_glr_problem* problem, const void* x, cons
 gdn_status gdn_glr_step(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
                         const float* lam, const void* z, float* h, void* y, void* stream);
 
+typedef enum gdn_rope_norm {
+  GDN_ROPE_NONE = 0, /* n = x                                           */
+  GDN_ROPE_RMS = 1,  /* n = x / sqrt(mean(x^2) + eps) w                 */
+  GDN_ROPE_L2 = 2    /* n = x / max(||x||_2, 1e-30), as gdn_prologue    */
+} gdn_rope_norm;
+
+/* Norm of queries and keys per head (over its D values) with the rotation by position in
+ * the same pass.  The first R values of a head are R / 2 pairs (j, j'), with j' = j + R / 2,
+ * or, interleaved, (2 j, 2 j + 1); pair j is turned by the angle position inv_freq[j]
+ * (radians):
+ *     out_j = n_j cos - n_j' sin;  out_j' = n_j' cos + n_j sin
+ * and the values behind the first R are n.
+ *   in : q [B,T,Hq,D], k [B,T,Hk,D] (io dtype): a token's heads and values contiguous,
+ *        tokens q_stride and k_stride values apart (0: Hq D and Hk D), so that both may be
+ *        views of one projection's rows; inv_freq [R / 2] fp32 (NULL with R == 0);
+ *        positions [B,T] int32 (NULL: 0 .. T - 1 in every row); wq, wk [D] fp32 (each NULL:
+ *        ones; only with GDN_ROPE_RMS, else GDN_ERR_UNSUPPORTED)
+ *   out: q_out, k_out, contiguous
+ * 16-byte aligned but for inv_freq and positions (4 bytes); strides of whole 16 bytes
+ * (GDN_ERR_ALIGN), at least Hq D and Hk D (GDN_ERR_SHAPE).  Supported: D in {64, 128, 256},
+ * R a multiple of 16 up to D, Hq and Hk up to 4096, B T (Hq + Hk) < 2^31, else
+ * GDN_ERR_UNSUPPORTED.  Angles are reduced in fp64 (2^-52 of the angle); all else is fp32,
+ * squares included, and outputs are rounded once.  eps >= 0 and finite frequencies are
+ * documented, not checked. */
+typedef struct gdn_rope_problem {
+  int32_t B, T, Hq, Hk, D, R;
+  int32_t norm;             /* gdn_rope_norm; another value: GDN_ERR_UNSUPPORTED */
+  int32_t interleaved;      /* nonzero: pairs (2 j, 2 j + 1)                     */
+  int32_t io_dtype;         /* gdn_dtype                                         */
+  float eps;                /* GDN_ROPE_RMS                                      */
+  int64_t q_stride, k_stride;
+} gdn_rope_problem;
+
+gdn_status gdn_rope_fwd(const gdn_rope_problem* problem, const void* q, const void* k,
+                        const float* inv_freq, const int32_t* positions, const float* wq,
+                        const float* wk, void* q_out, void* k_out, void* stream);
+
+/* Bytes of workspace gdn_rope_bwd needs where dwq or dwk is wanted (their partial sums). */
+gdn_status gdn_rope_workspace_size(const gdn_rope_problem* problem, size_t* bytes);
+
+/* Backward: gradients of <q_out, dq_out> + <k_out, dk_out>.
+ *   in : as gdn_rope_fwd; dq_out [B,T,Hq,D], dk_out [B,T,Hk,D] (io dtype), contiguous
+ *   out: dq, dk (io dtype), contiguous; dwq, dwk [D] fp32 (each NULL: not wanted; only with
+ *        GDN_ROPE_RMS, else GDN_ERR_UNSUPPORTED; without a weight it is that of ones)
+ * A row whose norm the L2 form cuts off at 1e-30 has the gradient of the product that is
+ * left.  Weights' gradients are summed in a fixed order (bit-identical from call to call). */
+gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const void* k,
+                        const float* inv_freq, const int32_t* positions, const float* wq,
+                        const float* wk, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                        float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -114,3 +114,61 @@ def glr(x, r, i, lam, z, h0, cu, c=8.0, dy=None, dlast=None):
         out["dz"] = (dy * h * slope).reshape(shape)
         err["dz"] = (dy.abs() * (eh * slope.abs() + hs * (z.abs() + 16) * U * wide)).reshape(shape)
     return out, err
+
+
+# --------------------------------------------------------------------------- norm and rotation
+
+def turned(x, angle, inter, back=False):
+    """The first pairs of x (..., H, D) turned by angle (..., R / 2), or back; with |sin| and
+    |cos| as given where angle is a pair of tensors."""
+    cos, sin = (torch.cos(angle), torch.sin(angle)) if isinstance(angle, torch.Tensor) else angle
+    cos, sin = cos.unsqueeze(-2), sin.unsqueeze(-2)
+    if back:
+        sin = -sin
+    n = cos.shape[-1]
+    out = x.clone()
+    a, b = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if inter else (slice(0, n), slice(n, 2 * n))
+    out[..., a] = x[..., a] * cos - x[..., b] * sin
+    out[..., b] = x[..., b] * cos + x[..., a] * sin
+    return out
+
+
+def _mixed(x, pairs, inter):
+    """|x_j| + |x_j'| of every turned channel, |x| of the others."""
+    one = torch.ones(*x.shape[:-2], pairs, dtype=x.dtype)
+    return turned(x.abs(), (one, -one), inter).abs().maximum(turned(x.abs(), (one, one), inter).abs())
+
+
+def rope(x, w, freq, pos, norm, eps, inter, d=None):
+    """(values, bounds) of one of q, k: dicts out and, with d, dx, dw.
+
+    Roundings: a row's sum of squares 20 (16 values a lane at most, six joins), inv 14 (half
+    of that, a root, a quotient), n 17; a cosine or sine 6 of one and 2^-50 of the angle; the
+    turned value two more.  Weights' gradients: an eighth of the rows one after another (16
+    rows of a workgroup share them, or 8 of 256 values) and 150 for the joins."""
+    x, w, freq, d = f64(x, w, freq, d)
+    pos = pos.detach().double().cpu()
+    angle = pos.unsqueeze(-1) * freq
+    D, pairs = x.shape[-1], freq.numel()
+    lost = 30 * U + angle.abs().amax() * 2.0 ** -50 if pairs else 30 * U
+    ss = (x * x).sum(-1, keepdim=True)
+    if norm == "rms":
+        inv, share = 1 / torch.sqrt(ss / D + eps), 1 / D
+    elif norm == "l2":
+        inv, share = 1 / torch.sqrt(ss).clamp(min=1e-30), (ss.sqrt() > 1e-30).double()
+    else:
+        inv, share = torch.ones_like(ss), 0.0
+    ww = w if w is not None else torch.ones(D, dtype=torch.float64)
+    n = x * inv * ww
+    out, err = {"out": turned(n, angle, inter)}, {"out": lost * _mixed(n, pairs, inter)}
+    if d is None:
+        return out, err
+    g, gs = turned(d, angle, inter, back=True), _mixed(d, pairs, inter)
+    u, us = g * ww, gs * ww.abs()
+    dot, dots = (u * x).sum(-1, keepdim=True), (us * x.abs()).sum(-1, keepdim=True)
+    out["dx"] = inv * (u - x * inv * inv * share * dot)
+    err["dx"] = inv * ((lost + 20 * U) * us + (lost + 80 * U) * x.abs() * inv * inv * share * dots)
+    rows = x.numel() // D
+    out["dw"] = (g * x * inv).reshape(rows, D).sum(0)
+    err["dw"] = ((lost + (rows / 8 + 150) * U) * gs * x.abs() * inv).reshape(rows, D).sum(0)
+    return out, err

@@ -68,3 +68,42 @@ def test_glr_bounds_notice_a_planted_mistake():
     except AssertionError:
         return
     raise AssertionError("a planted mistake passed")
+
+
+def test_rope_gradients_against_differences():
+    g = torch.Generator().manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    freq, pos = r(4).abs(), torch.tensor([[3, -7]], dtype=torch.int32)
+    for norm in ("rms", "l2", None):
+        for inter in (False, True):
+            x, w, d = r(1, 2, 3, 12), r(12), r(1, 2, 3, 12)
+            w = w if norm == "rms" else None
+            out, _ = ref.rope(x, w, freq, pos, norm, 1e-3, inter, d)
+            for leaf, name in ((x, "dx"), (w, "dw")):
+                if leaf is None:
+                    continue
+                flat = leaf.reshape(-1)
+                for j in range(0, flat.numel(), 5):
+                    keep, vals = float(flat[j]), []
+                    for sign in (1, -1):
+                        flat[j] = keep + sign * 1e-6
+                        vals.append(float((ref.rope(x, w, freq, pos, norm, 1e-3, inter)[0]["out"] * d).sum()))
+                    flat[j] = keep
+                    assert abs((vals[0] - vals[1]) / 2e-6 - float(out[name].reshape(-1)[j])) <= 1e-7, (norm, inter, name)
+
+
+def test_rope_is_a_rotation():
+    """Pairs as complex numbers; scores depend on the distance of the positions alone."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(1, 2, 1, 8, generator=g, dtype=torch.float64)
+    freq = torch.tensor([1.0, 0.25, 0.01], dtype=torch.float64)
+    pos = torch.tensor([[5, 11]])
+    y, _ = ref.rope(x, None, freq, pos, None, 0.0, True)
+    z = torch.view_as_complex(x[..., :6].reshape(1, 2, 1, 3, 2)) * torch.polar(torch.ones(1, 2, 1, 3, dtype=torch.float64),
+                                                                                  pos[..., None, None] * freq)
+    assert float((y["out"][..., :6] - torch.view_as_real(z).flatten(-2)).abs().max()) <= 1e-15
+    assert torch.equal(y["out"][..., 6:], x[..., 6:])
+    for inter in (False, True):
+        near = ref.rope(x, None, freq, pos, None, 0.0, inter)[0]["out"]
+        far = ref.rope(x, None, freq, pos + 1000, None, 0.0, inter)[0]["out"]
+        assert abs(float((near[0, 0] * near[0, 1]).sum() - (far[0, 0] * far[0, 1]).sum())) <= 1e-12
