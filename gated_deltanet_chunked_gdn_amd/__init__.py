@@ -11,5 +11,5 @@ from .ops import (SeqLens, chunk_bwd, chunk_bwd_saved, chunk_fwd, chunk_fwd_noal
 from .layer import (conv_bwd, conv_fwd, conv_step, kda_step, scan_buffers, scan_bwd_saved,  # noqa: F401
                     scan_fwd, scan_fwd_save, scan_step, step)
 from .hybrid import (glr_buffers, glr_bwd_saved, glr_fwd, glr_fwd_save, glr_step, rope_bwd,  # noqa: F401
-                     rope_fwd)
+                     rope_fwd, swa_bwd, swa_fill, swa_fwd, swa_step)
 from ._native import GdnError, GdnLibraryMissing  # noqa: F401

@@ -61,6 +61,9 @@ GDN_GLR_BWD = 2
 GDN_ROPE_NONE = 0
 GDN_ROPE_RMS = 1
 GDN_ROPE_L2 = 2
+# gdn_swa_pass
+GDN_SWA_BWD = 0
+GDN_SWA_STEP = 1
 
 # Every symbol include/gdn.h declares.
 EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chunk_fwd",
@@ -70,7 +73,8 @@ EXPORTED = ("gdn_abi_version", "gdn_status_str", "gdn_workspace_size", "gdn_chun
             "gdn_step", "gdn_kda_step", "gdn_conv_fwd", "gdn_conv_workspace_size", "gdn_conv_bwd", "gdn_conv_step",
             "gdn_scan_workspace_size", "gdn_scan_fwd", "gdn_scan_fwd_save", "gdn_scan_bwd_saved", "gdn_scan_step",
             "gdn_glr_workspace_size", "gdn_glr_fwd", "gdn_glr_fwd_save", "gdn_glr_bwd_saved", "gdn_glr_step",
-            "gdn_rope_fwd", "gdn_rope_workspace_size", "gdn_rope_bwd")
+            "gdn_rope_fwd", "gdn_rope_workspace_size", "gdn_rope_bwd",
+            "gdn_swa_workspace_size", "gdn_swa_fwd", "gdn_swa_bwd", "gdn_swa_fill", "gdn_swa_step")
 
 
 class GdnLibraryMissing(RuntimeError):
@@ -144,6 +148,19 @@ class RopeProblem(ctypes.Structure):
     ]
 
 
+class SwaProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+        ("num_seqs", ctypes.c_int32),
+        ("cu_seqlens_host", ctypes.c_void_p),
+        ("cu_seqlens_dev", ctypes.c_void_p),
+        ("io_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -193,7 +210,7 @@ def load():
     lib.gdn_kda_chunk_bwd_saved.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.gdn_kda_chunk_bwd_saved.restype = ctypes.c_int
     PC, PS, PG, Z = ctypes.POINTER(ConvProblem), ctypes.POINTER(ScanProblem), ctypes.POINTER(GlrProblem), ctypes.c_size_t
-    PR = ctypes.POINTER(RopeProblem)
+    PR, PW = ctypes.POINTER(RopeProblem), ctypes.POINTER(SwaProblem)
     for name, args in (
             ("gdn_step", [PP] + [P] * 8), ("gdn_kda_step", [PP] + [P] * 8),
             ("gdn_conv_fwd", [PC] + [P] * 7), ("gdn_conv_step", [PC] + [P] * 6),
@@ -210,7 +227,10 @@ def load():
             ("gdn_glr_bwd_saved", [PG] + [P] * 8 + [Z] + [P] * 7 + [Z, P]),
             ("gdn_glr_step", [PG] + [P] * 8),
             ("gdn_rope_fwd", [PR] + [P] * 9), ("gdn_rope_workspace_size", [PR, ctypes.POINTER(Z)]),
-            ("gdn_rope_bwd", [PR] + [P] * 13 + [Z, P])):
+            ("gdn_rope_bwd", [PR] + [P] * 13 + [Z, P]),
+            ("gdn_swa_workspace_size", [PW, ctypes.c_int32, ctypes.POINTER(Z)]),
+            ("gdn_swa_fwd", [PW] + [P] * 6), ("gdn_swa_bwd", [PW] + [P] * 10 + [Z, P]),
+            ("gdn_swa_fill", [PW] + [P] * 5), ("gdn_swa_step", [PW] + [P] * 8 + [Z, P])):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int

@@ -23,7 +23,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["gdn_abi.cpp", "gdn_noalloc.cpp", "gdn_chunk_fwd.hip", "gdn_chunk_chain.hip", "gdn_chunk_bwd.hip", "gdn_recurrent.hip", "gdn_prologue.hip",
            "gdn_epilogue.hip", "gdn_layer_abi.cpp", "gdn_scan_split.cpp", "gdn_step.hip", "gdn_conv.hip", "gdn_scan.hip", "gdn_scan_time.hip", "gdn_scan_bwd.hip", "gdn_kda.hip", "gdn_kda_bwd.hip", "gdn_copy.hip",
-           "gdn_hybrid_abi.cpp", "gdn_glr.hip", "gdn_rope.hip"]
+           "gdn_hybrid_abi.cpp", "gdn_glr.hip", "gdn_rope.hip", "gdn_swa_fwd.hip", "gdn_swa_bwd.hip", "gdn_swa_step.hip"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
           "-Wall", "-Wno-unused-parameter", f"-I{INCLUDE}", f"-I{CSRC}"]

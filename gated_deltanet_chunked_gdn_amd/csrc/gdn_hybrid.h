@@ -89,4 +89,44 @@ inline int64_t rope_bwd_groups(int64_t tokens) {
 hipError_t launch_rope_fwd(const RopeParams& p, int D, bool bf16, bool interleaved, hipStream_t s);
 hipError_t launch_rope_bwd(const RopeParams& p, int D, bool bf16, bool interleaved, hipStream_t s);
 
+// ---------------------------------------------------------------------------- window attention
+
+struct SwaParams {
+  const void* q;       // rows of Hq D values, q_stride apart
+  const void* k;       // rows of Hk D values
+  const void* v;
+  void* o;             // contiguous
+  float* lse;          // [rows][Hq], or nullptr in the forward
+  const void* dout;    // backward, contiguous
+  void* dq;
+  void* dk;
+  void* dv;
+  float* delta;        // backward: [rows][Hq] sums of dout o
+  float* first_win;    // backward: [N][Hk][S][2][D] the first tokens' dk, dv from inside the window
+  float* first_far;    // backward: [slot][4][Hk][S][2][D] those from queries further on, by runs of them
+  int64_t q_stride, k_stride, v_stride;
+  SeqInfo seq;
+  int32_t N, Hq, Hk;
+  int32_t W, S;        // W at most the longest sequence; S 0 where no window leaves a token behind
+  int32_t max_len;
+  float scale;
+  // cache
+  void* kc;            // [N][slots][Hk][D]
+  void* vc;
+  const int32_t* lens; // step: tokens before this one, negative: an idle place
+  int32_t slots;       // S + W
+  int32_t splits;      // step: runs of slots, a workgroup each
+  int32_t run;         // step: slots of a run
+  float* part;         // step: [split][N][Hq] (maximum, sum), then [split][N][Hq][D] values
+};
+constexpr int kSwaQueries = 128;  // queries of a workgroup
+constexpr int kSwaKeys = 128;     // keys of a workgroup of the backward
+constexpr int kSwaFar = 512;      // queries of a run for the first tokens' gradients
+// Run c of a sequence that starts at row bos uses slot bos / kSwaFar + n + c (distinct).
+inline int64_t swa_far_slots(int64_t rows, int64_t n) { return rows / kSwaFar + n; }
+hipError_t launch_swa_fwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
+hipError_t launch_swa_bwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
+hipError_t launch_swa_fill(const SwaParams& p, int D, bool bf16, hipStream_t s);
+hipError_t launch_swa_step(const SwaParams& p, int D, bool bf16, hipStream_t s);
+
 }  // namespace gdn

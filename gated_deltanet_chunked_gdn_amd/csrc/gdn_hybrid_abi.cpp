@@ -151,6 +151,87 @@ gdn::RopeParams rope_params(const gdn_rope_problem* p, const RopeSize& c, const 
   return rp;
 }
 
+// ---------------------------------------------------------------------------- window attention
+
+struct SwaSize {
+  size_t io = 0, qin = 0, kin = 0, vin = 0, q = 0, k = 0, lse = 0, cache = 0, lens = 0;
+  size_t delta = 0, win = 0, far = 0, step = 0;
+  int64_t rows = 0, q_stride = 0, k_stride = 0, v_stride = 0;
+  int32_t W = 0, S = 0, max_len = 0, splits = 1, run = 0;
+};
+
+gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
+  if (!p) return GDN_ERR_NULL;
+  if (p->io_dtype != GDN_FP32 && p->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
+  if (p->B < 0 || p->T < 0 || p->Hq <= 0 || p->Hk <= 0 || p->D <= 0 || p->num_seqs < 0 || p->Hq % p->Hk != 0 || p->window <= 0 || p->sinks < 0)
+    return GDN_ERR_SHAPE;
+  if ((p->D != 64 && p->D != 128) || p->Hq > 4096 || p->sinks > 1024) return GDN_ERR_UNSUPPORTED;
+  int64_t max_len = 0;
+  gdn_status st = check_seqs(p, &max_len);
+  if (st != GDN_OK) return st;
+  c->io = p->io_dtype == GDN_BF16 ? 2 : 4;
+  c->rows = static_cast<int64_t>(p->B) * p->T;
+  if (c->rows > 1 << 30) return GDN_ERR_UNSUPPORTED;
+  const int64_t qrow = static_cast<int64_t>(p->Hq) * p->D, krow = static_cast<int64_t>(p->Hk) * p->D;
+  st = check_stride(p->q_stride, qrow, c->io, &c->q_stride);
+  if (st == GDN_OK) st = check_stride(p->k_stride, krow, c->io, &c->k_stride);
+  if (st == GDN_OK) st = check_stride(p->v_stride, krow, c->io, &c->v_stride);
+  if (st != GDN_OK) return st;
+  c->max_len = static_cast<int32_t>(max_len);
+  // a window as long as every sequence leaves nothing behind it
+  c->W = static_cast<int32_t>(std::min<int64_t>(p->window, std::max<int64_t>(max_len, 1)));
+  c->S = c->W >= max_len ? 0 : static_cast<int32_t>(std::min<int64_t>(p->sinks, max_len));
+  c->qin = extent(c->rows, c->q_stride, qrow, c->io);
+  c->kin = extent(c->rows, c->k_stride, krow, c->io);
+  c->vin = extent(c->rows, c->v_stride, krow, c->io);
+  c->q = static_cast<size_t>(c->rows) * qrow * c->io;
+  c->k = static_cast<size_t>(c->rows) * krow * c->io;
+  c->lse = static_cast<size_t>(c->rows) * p->Hq * 4;
+  c->delta = up256(c->lse);
+  const size_t first = static_cast<size_t>(p->Hk) * c->S * 2 * p->D * 4;
+  c->win = up256(p->num_seqs * first);
+  c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs)) * 4 * first;
+  // Workgroups of 256 threads, counted in 32 bits: blocks of queries of every query head (the
+  // backward's blocks of keys are as long), rounded up to eight.
+  const int64_t blocks = (max_len + gdn::kSwaQueries - 1) / gdn::kSwaQueries;
+  if ((blocks * p->Hq + 7) / 8 * 8 * p->num_seqs >= 1 << 24) return GDN_ERR_UNSUPPORTED;
+  const int64_t runs = (max_len + gdn::kSwaFar - 1) / gdn::kSwaFar;
+  if ((runs * p->Hk + 7) / 8 * 8 * p->num_seqs * ((c->S + 31) / 32) >= 1 << 24 || static_cast<int64_t>(c->S) * p->Hk * p->num_seqs >= 1 << 24)
+    return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+// What the cache adds: its slots, and the step's runs of them.
+gdn_status check_cache(const gdn_swa_problem* p, SwaSize* c) {
+  const gdn_status st = check_swa(p, c);
+  if (st != GDN_OK) return st;
+  const int64_t slots = static_cast<int64_t>(p->sinks) + p->window, row = static_cast<int64_t>(p->Hk) * p->D;
+  if (slots > 1 << 30) return GDN_ERR_UNSUPPORTED;
+  // threads of the filling: a piece of 16 bytes each; workgroups of the step
+  const int64_t fill = (slots * (row * static_cast<int64_t>(c->io) / 16) + 255) / 256 * p->num_seqs;
+  if (fill >= 1 << 24) return GDN_ERR_UNSUPPORTED;
+  c->cache = static_cast<size_t>(p->num_seqs) * slots * row * c->io;
+  c->lens = static_cast<size_t>(p->num_seqs) * 4;
+  const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(p->num_seqs) * p->Hk * ((p->Hq / p->Hk + 15) / 16));
+  // runs of at least 128 slots (32 a wave), as many as make 1024 workgroups
+  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>((1024 + groups - 1) / groups, (slots + 127) / 128));
+  c->run = static_cast<int32_t>(((slots + splits - 1) / splits + 127) / 128 * 128);
+  c->splits = static_cast<int32_t>((slots + c->run - 1) / c->run);
+  if (groups * c->splits >= 1 << 24) return GDN_ERR_UNSUPPORTED;
+  c->step = c->splits > 1 ? static_cast<size_t>(c->splits) * p->num_seqs * p->Hq * (p->D + 2) * 4 : 0;
+  return GDN_OK;
+}
+
+gdn::SwaParams swa_params(const gdn_swa_problem* p, const SwaSize& c, const void* q, const void* k, const void* v) {
+  gdn::SwaParams sp{};
+  sp.q = q; sp.k = k; sp.v = v;
+  sp.q_stride = c.q_stride; sp.k_stride = c.k_stride; sp.v_stride = c.v_stride;
+  sp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
+  sp.N = p->num_seqs; sp.Hq = p->Hq; sp.Hk = p->Hk; sp.W = c.W; sp.S = c.S; sp.max_len = c.max_len;
+  sp.scale = p->scale;
+  return sp;
+}
+
 }  // namespace
 
 extern "C" {
@@ -260,6 +341,74 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k,
   rp.part = static_cast<float*>(ws);
   rp.groups = static_cast<int32_t>(gdn::rope_bwd_groups(c.tokens));
   return hip_status(gdn::launch_rope_bwd(rp, p->D, c.io == 2, p->interleaved != 0, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_swa_workspace_size(const gdn_swa_problem* p, int32_t pass, size_t* bytes) {
+  if (!bytes) return GDN_ERR_NULL;
+  if (pass != GDN_SWA_BWD && pass != GDN_SWA_STEP) return GDN_ERR_UNSUPPORTED;
+  SwaSize c;
+  const gdn_status st = pass == GDN_SWA_BWD ? check_swa(p, &c) : check_cache(p, &c);
+  if (st != GDN_OK) return st;
+  *bytes = pass == GDN_SWA_BWD ? c.delta + c.win + c.far : c.step;
+  return GDN_OK;
+}
+
+gdn_status gdn_swa_fwd(const gdn_swa_problem* p, const void* q, const void* k, const void* v, void* o, float* lse, void* stream) {
+  SwaSize c;
+  gdn_status st = check_swa(p, &c);
+  if (st != GDN_OK) return st;
+  st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {v, c.vin, 16, true}}, {{o, c.q, 16, true}, {lse, c.lse, 4, false}});
+  if (st != GDN_OK || c.rows == 0) return st;
+  gdn::SwaParams sp = swa_params(p, c, q, k, v);
+  sp.o = o; sp.lse = lse;
+  return hip_status(gdn::launch_swa_fwd(sp, p->D, c.io == 2, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_swa_bwd(const gdn_swa_problem* p, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                       const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
+  SwaSize c;
+  gdn_status st = check_swa(p, &c);
+  if (st != GDN_OK) return st;
+  st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {v, c.vin, 16, true}, {o, c.q, 16, true}, {lse, c.lse, 4, true},
+                      {dout, c.q, 16, true}},
+                     {{dq, c.q, 16, true}, {dk, c.k, 16, true}, {dv, c.k, 16, true}, {ws, ws_bytes, 16, false}});
+  if (st != GDN_OK) return st;
+  if (c.rows == 0) return GDN_OK;
+  if (!ws || ws_bytes < c.delta + c.win + c.far) return GDN_ERR_WORKSPACE;
+  gdn::SwaParams sp = swa_params(p, c, q, k, v);
+  sp.o = const_cast<void*>(o); sp.lse = const_cast<float*>(lse); sp.dout = dout;
+  sp.dq = dq; sp.dk = dk; sp.dv = dv;
+  sp.delta = static_cast<float*>(ws);
+  sp.first_win = reinterpret_cast<float*>(static_cast<char*>(ws) + c.delta);
+  sp.first_far = reinterpret_cast<float*>(static_cast<char*>(ws) + c.delta + c.win);
+  return hip_status(gdn::launch_swa_bwd(sp, p->D, c.io == 2, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_swa_fill(const gdn_swa_problem* p, const void* k, const void* v, void* kcache, void* vcache, void* stream) {
+  SwaSize c;
+  gdn_status st = check_cache(p, &c);
+  if (st != GDN_OK) return st;
+  st = check_tensors({{k, c.kin, 16, true}, {v, c.vin, 16, true}}, {{kcache, c.cache, 16, true}, {vcache, c.cache, 16, true}});
+  if (st != GDN_OK || p->num_seqs == 0 || c.rows == 0) return st;
+  gdn::SwaParams sp = swa_params(p, c, nullptr, k, v);
+  sp.S = p->sinks; sp.slots = p->sinks + p->window; sp.kc = kcache; sp.vc = vcache;
+  return hip_status(gdn::launch_swa_fill(sp, p->D, c.io == 2, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_swa_step(const gdn_swa_problem* p, const void* q, const void* k, const void* v, void* kcache, void* vcache,
+                        const int32_t* lens, void* o, void* ws, size_t ws_bytes, void* stream) {
+  SwaSize c;
+  gdn_status st = check_cache(p, &c);
+  if (st != GDN_OK) return st;
+  if (p->T != 1 || p->cu_seqlens_host) return GDN_ERR_SHAPE;
+  st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {v, c.vin, 16, true}, {lens, c.lens, 4, true}},
+                     {{kcache, c.cache, 16, true}, {vcache, c.cache, 16, true}, {o, c.q, 16, true}, {ws, ws_bytes, 16, false}});
+  if (st != GDN_OK || p->B == 0) return st;
+  if (c.step && (!ws || ws_bytes < c.step)) return GDN_ERR_WORKSPACE;
+  gdn::SwaParams sp = swa_params(p, c, q, k, v);
+  sp.S = p->sinks; sp.slots = p->sinks + p->window; sp.kc = kcache; sp.vc = vcache; sp.lens = lens; sp.o = o;
+  sp.splits = c.splits; sp.run = c.run; sp.part = static_cast<float*>(ws);
+  return hip_status(gdn::launch_swa_step(sp, p->D, c.io == 2, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

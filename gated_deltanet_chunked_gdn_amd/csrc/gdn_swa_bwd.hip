@@ -1,0 +1,368 @@
+// Backward of the window attention on gfx950.  With P from the kept log-sums and
+//   delta_i = sum_d do_i o_i,  dP = do v^T,  dS = scale P (dP - delta)
+//   dv_j = sum_i P_ij do_i,  dk_j = sum_i dS_ij q_i,  dq_i = sum_j dS_ij k_j
+//
+// Two kernels form the scores again, each with its own sum in registers, so no sum needs
+// an atomic and every result is bit-identical from call to call:
+//   * dq: a block of queries over its keys, scores transposed as in the forward; it also
+//     forms delta, which the other reads;
+//   * dk, dv: a block of keys over the queries whose window holds it, for every query head
+//     of its key head; here the scores stand with queries down the accumulator, a key a
+//     lane, which makes P and dS the operands of the sums over queries.
+// The first tokens are seen by all later queries too: a few keys with long sums.  Their
+// part from behind the window is summed by runs of 512 queries (the same kernel, its four
+// waves sharing the keys and parting the queries) and joined in order by a last kernel.
+#include <hip/hip_runtime.h>
+
+#include "gdn_swa_device.h"
+
+namespace gdn {
+namespace {
+
+using namespace swa;
+
+// ---------------------------------------------------------------------------- dq
+
+template <typename Op, int D>
+__global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
+  using E = typename Op::elem;
+  constexpr int CT = 2, KT = 64, NS = D / Op::kCols, ND = D / 16, KB = Op::kBlocks;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int item = xcd_item(blockIdx.x, items);
+  if (item >= items) return;
+  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
+  const int block = rest / group, h = hk * group + rest - block * group;
+  int64_t bos, len64;
+  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
+  const int len = static_cast<int>(len64), q0 = block * kSwaQueries;
+  if (q0 >= len) return;
+
+  __shared__ alignas(16) E Ks[KT * D];
+  __shared__ alignas(16) E Vs[KT * D];
+
+  const int wq0 = q0 + 32 * wave, wq1 = min(wq0 + 31, len - 1);
+  u32x4_t qf[CT][NS], df[CT][NS];
+  float lse2[CT], delta[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    const int i = min(wq0 + 16 * t + c, len - 1);
+    const int64_t at = (bos + i) * p.Hq + h;
+    const E* const row = static_cast<const E*>(p.q) + (bos + i) * p.q_stride + h * D;
+    const E* const drow = static_cast<const E*>(p.dout) + at * D;
+    const E* const orow = static_cast<const E*>(p.o) + at * D;
+    float dot = 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      qf[t][s] = load_row<Op>(row, s, lane);
+      df[t][s] = load_row<Op>(drow, s, lane);
+      const u32x4_t of = load_row<Op>(orow, s, lane);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if constexpr (sizeof(E) == 2) {
+          dot = fmaf(__uint_as_float(df[t][s][w] << 16), __uint_as_float(of[w] << 16), dot);
+          dot = fmaf(__uint_as_float(df[t][s][w] & 0xffff0000u), __uint_as_float(of[w] & 0xffff0000u), dot);
+        } else {
+          dot = fmaf(__uint_as_float(df[t][s][w]), __uint_as_float(of[w]), dot);
+        }
+      }
+    }
+    dot += __shfl_xor(dot, 16, 64);
+    dot += __shfl_xor(dot, 32, 64);
+    delta[t] = dot;
+    lse2[t] = p.lse[at] * kLog2e;
+    if (g == 0 && wq0 + 16 * t + c < len) p.delta[at] = dot;
+  }
+  const E* const kb = static_cast<const E*>(p.k) + bos * p.k_stride + hk * D;
+  const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
+  const int win = max(0, q0 - p.W + 1) / KT * KT, last = min(q0 + kSwaQueries, len) - 1;
+  const int nfirst = (min(p.S, win) + KT - 1) / KT, tiles = nfirst + (last - win) / KT + 1;
+  auto start = [&](int t) { return t < nfirst ? t * KT : win + (t - nfirst) * KT; };
+
+  f32x4_t acc[ND][CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t)
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[d][t] = zero4();
+  const float scale2 = p.scale * kLog2e;
+  Stage<E, D, KT> sk, sv;
+  sk.load(kb, p.k_stride, start(0), len);
+  sv.load(vb, p.v_stride, start(0), len);
+  for (int t = 0; t < tiles; ++t) {
+    const int j0 = start(t);
+    __syncthreads();
+    sk.store(Ks);
+    sv.store(Vs);
+    __syncthreads();
+    if (t + 1 < tiles) {
+      sk.load(kb, p.k_stride, start(t + 1), len);
+      sv.load(vb, p.v_stride, start(t + 1), len);
+    }
+    if (wq0 >= len || j0 > wq1 || (j0 + KT - 1 <= wq0 - p.W && j0 >= p.S)) continue;
+    const bool whole = j0 + KT - 1 <= wq0 && j0 > wq1 - p.W;
+#pragma unroll
+    for (int b0 = 0; b0 < 4; b0 += KB) {
+      f32x4_t s[KB][CT], dp[KB][CT];
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+#pragma unroll
+        for (int u = 0; u < CT; ++u) s[b][u] = dp[b][u] = zero4();
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const u32x4_t ka = read_row<Op, D>(Ks, 16 * (b0 + b), n, lane);
+          const u32x4_t va = read_row<Op, D>(Vs, 16 * (b0 + b), n, lane);
+#pragma unroll
+          for (int u = 0; u < CT; ++u) {
+            s[b][u] = Op::mma(ka, qf[u][n], s[b][u]);
+            dp[b][u] = Op::mma(va, df[u][n], dp[b][u]);
+          }
+        }
+      }
+      u32x4_t sf[CT];
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        f32x4_t ds[KB];
+        const int i = wq0 + 16 * u + c;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = exp2_(fmaf(s[b][u][r], scale2, -lse2[u])) * (dp[b][u][r] - delta[u]);
+            ds[b][r] = whole || sees(i, j0 + 16 * (b0 + b) + 4 * g + r, p.W, p.S) ? x : 0.f;
+          }
+        sf[u] = Op::operand(ds);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const u32x4_t a = Op::template read_tr<D>(Ks, 16 * b0, 16 * d, lane);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) acc[d][u] = Op::mma(a, sf[u], acc[d][u]);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    const int i = wq0 + 16 * u + c;
+    if (i >= len) continue;
+    E* const row = static_cast<E*>(p.dq) + ((bos + i) * p.Hq + h) * D;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+      chunk::store4<E>(row + 16 * d + 4 * g, acc[d][u][0] * p.scale, acc[d][u][1] * p.scale, acc[d][u][2] * p.scale, acc[d][u][3] * p.scale);
+  }
+}
+
+// ---------------------------------------------------------------------------- dk, dv
+
+// FAR: the first tokens' sums over the queries of a run whose window has left them behind;
+// the waves hold the same 32 keys and take a step's queries of a tile each (32, fp32 16).  Else 32 keys a wave
+// and the queries whose window holds them.
+template <typename Op, int D, bool FAR>
+__global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items, int blocks) {
+  using E = typename Op::elem;
+  constexpr int CT = 2, KB = Op::kBlocks, NS = D / Op::kCols, ND = D / 16;
+  constexpr int QT = FAR ? 64 * KB : sizeof(E) == 2 ? 64 : 32;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int item = xcd_item(blockIdx.x, items);
+  if (item >= items) return;
+  const int group = p.Hq / p.Hk, hk = item / blocks, block = item - hk * blocks;
+  int64_t bos, len64;
+  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
+  const int len = static_cast<int>(len64);
+  const int k0 = FAR ? 32 * blockIdx.z : block * kSwaKeys, wk0 = FAR ? k0 : k0 + 32 * wave;
+  if (k0 >= len || (FAR && len <= p.W)) return;
+  // queries i0 .. i1
+  int i0, i1;
+  if (FAR) {
+    i0 = block * kSwaFar;
+    i1 = min(i0 + kSwaFar, len) - 1;
+    if (i1 < k0 + p.W) return;  // none of them is so far behind
+  } else {
+    i0 = k0;
+    i1 = min(static_cast<int64_t>(len), static_cast<int64_t>(k0) + kSwaKeys - 1 + p.W) - 1;
+  }
+
+  __shared__ alignas(16) E Qs[QT * D];
+  __shared__ alignas(16) E Ds[QT * D];
+  __shared__ alignas(16) float ls[QT], dl[QT];
+
+  u32x4_t kf[CT][NS], vf[CT][NS];
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    const int j = min(wk0 + 16 * u + c, len - 1);
+    const E* const krow = static_cast<const E*>(p.k) + (bos + j) * p.k_stride + hk * D;
+    const E* const vrow = static_cast<const E*>(p.v) + (bos + j) * p.v_stride + hk * D;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      kf[u][n] = load_row<Op>(krow, n, lane);
+      vf[u][n] = load_row<Op>(vrow, n, lane);
+    }
+  }
+  f32x4_t ak[ND][CT], av[ND][CT];
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int u = 0; u < CT; ++u) ak[d][u] = av[d][u] = zero4();
+
+  const int tiles = (i1 - i0) / QT + 1, steps = group * tiles;
+  const float scale2 = p.scale * kLog2e;
+  Stage<E, D, QT> sq, sd;
+  float rl = 0.f, rd = 0.f;
+  auto fetch = [&](int step) {
+    const int h = hk * group + step / tiles, row = i0 + (step % tiles) * QT;
+    sq.load(static_cast<const E*>(p.q) + bos * p.q_stride + h * D, p.q_stride, row, len);
+    sd.load(static_cast<const E*>(p.dout) + (bos * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, row, len);
+    if (threadIdx.x < QT) {
+      const int64_t at = (bos + min(row + static_cast<int>(threadIdx.x), len - 1)) * p.Hq + h;
+      rl = p.lse[at] * kLog2e;
+      rd = p.delta[at];
+    }
+  };
+  fetch(0);
+  for (int step = 0; step < steps; ++step) {
+    const int r0 = i0 + (step % tiles) * QT;
+    __syncthreads();
+    sq.store(Qs);
+    sd.store(Ds);
+    if (threadIdx.x < QT) {
+      ls[threadIdx.x] = rl;
+      dl[threadIdx.x] = rd;
+    }
+    __syncthreads();
+    if (step + 1 < steps) fetch(step + 1);
+#pragma unroll
+    for (int b1 = 0; b1 < (FAR ? KB : QT / 16); b1 += KB) {
+      const int b0 = FAR ? KB * wave : b1;
+      const int first = r0 + 16 * b0, end = first + 16 * KB - 1;
+      // no query here sees a key of this wave's
+      if (wk0 >= len || first >= len || (FAR ? end < wk0 + p.W : end < wk0 || first - (wk0 + 31) >= p.W)) continue;
+      const bool whole = !FAR && first >= wk0 + 31 && end - wk0 < p.W && end < len && wk0 + 31 < len;
+      f32x4_t s[KB][CT], dp[KB][CT];
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+#pragma unroll
+        for (int u = 0; u < CT; ++u) s[b][u] = dp[b][u] = zero4();
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const u32x4_t qa = read_row<Op, D>(Qs, 16 * (b0 + b), n, lane);
+          const u32x4_t da = read_row<Op, D>(Ds, 16 * (b0 + b), n, lane);
+#pragma unroll
+          for (int u = 0; u < CT; ++u) {
+            s[b][u] = Op::mma(qa, kf[u][n], s[b][u]);
+            dp[b][u] = Op::mma(da, vf[u][n], dp[b][u]);
+          }
+        }
+      }
+      u32x4_t pf[CT], sf[CT];
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(&ls[16 * (b0 + b) + 4 * g]);
+        const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(&dl[16 * (b0 + b) + 4 * g]);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          const int j = wk0 + 16 * u + c;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = first + 16 * b + 4 * g + r;
+            const bool ok = whole || (i < len && j < len && (FAR ? j < p.S && i - j >= p.W : j <= i && i - j < p.W));
+            const float w = exp2_(fmaf(s[b][u][r], scale2, -l4[r]));
+            dp[b][u][r] = ok ? w * (dp[b][u][r] - d4[r]) : 0.f;
+            s[b][u][r] = ok ? w : 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        const f32x4_t two[2] = {s[0][u], s[KB - 1][u]}, ds[2] = {dp[0][u], dp[KB - 1][u]};
+        pf[u] = Op::operand(two);
+        sf[u] = Op::operand(ds);
+      }
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const u32x4_t da = Op::template read_tr<D>(Ds, 16 * b0, 16 * d, lane);
+        const u32x4_t qa = Op::template read_tr<D>(Qs, 16 * b0, 16 * d, lane);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          av[d][u] = Op::mma(da, pf[u], av[d][u]);
+          ak[d][u] = Op::mma(qa, sf[u], ak[d][u]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    const int j = wk0 + 16 * u + c;
+    if (j >= len) continue;
+    float* part = nullptr;  // of the first tokens
+    if (FAR) {
+      if (j >= p.S) continue;
+      const int64_t slot = bos / kSwaFar + blockIdx.y + block;
+      part = p.first_far + (((slot * 4 + wave) * p.Hk + hk) * p.S + j) * 2 * D;
+    } else if (j < p.S && len > p.W) {
+      part = p.first_win + ((static_cast<int64_t>(blockIdx.y) * p.Hk + hk) * p.S + j) * 2 * D;
+    }
+    if (part) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        chunk::store4<float>(part + 16 * d + 4 * g, ak[d][u][0], ak[d][u][1], ak[d][u][2], ak[d][u][3]);
+        chunk::store4<float>(part + D + 16 * d + 4 * g, av[d][u][0], av[d][u][1], av[d][u][2], av[d][u][3]);
+      }
+    } else {
+      const int64_t at = ((bos + j) * p.Hk + hk) * D;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        chunk::store4<E>(static_cast<E*>(p.dk) + at + 16 * d + 4 * g, ak[d][u][0] * p.scale, ak[d][u][1] * p.scale, ak[d][u][2] * p.scale,
+                         ak[d][u][3] * p.scale);
+        chunk::store4<E>(static_cast<E*>(p.dv) + at + 16 * d + 4 * g, av[d][u][0], av[d][u][1], av[d][u][2], av[d][u][3]);
+      }
+    }
+  }
+}
+
+// The first tokens' dk and dv: the sums from inside the window, then those of the runs in order.
+template <typename E, int D>
+__global__ __launch_bounds__(2 * D) void swa_first_kernel(SwaParams p) {
+  const int j = blockIdx.x / p.Hk, hk = blockIdx.x % p.Hk, n = blockIdx.y, x = threadIdx.x;
+  int64_t bos, len;
+  chunk::seq_range(p.seq, n, bos, len);
+  if (len <= p.W || j >= len) return;
+  float sum = p.first_win[((static_cast<int64_t>(n) * p.Hk + hk) * p.S + j) * 2 * D + x];
+  const int64_t slot = bos / kSwaFar + n, runs = (len + kSwaFar - 1) / kSwaFar;
+  // as in the kernel above: the keys' block of 32 says which runs were formed
+  for (int64_t r = 0; r < runs; ++r) {
+    if (min((r + 1) * kSwaFar, len) - 1 < (j / 32 * 32) + p.W) continue;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum += p.first_far[((((slot + r) * 4 + w) * p.Hk + hk) * p.S + j) * 2 * D + x];
+  }
+  const int64_t at = ((bos + j) * p.Hk + hk) * D;
+  if (x < D)
+    IoT<E>::st(static_cast<E*>(p.dk) + at + x, sum * p.scale);
+  else
+    IoT<E>::st(static_cast<E*>(p.dv) + at + x - D, sum);
+}
+
+unsigned of8(int items) { return static_cast<unsigned>((items + 7) / 8 * 8); }
+
+template <typename Op, int D>
+hipError_t launch_t(const SwaParams& p, hipStream_t s) {
+  const unsigned N = static_cast<unsigned>(p.N);
+  const int qblocks = (p.max_len + kSwaQueries - 1) / kSwaQueries, qitems = p.Hq * qblocks;
+  hipLaunchKernelGGL((swa_dq_kernel<Op, D>), dim3(of8(qitems), N), dim3(256), 0, s, p, qitems, qblocks);
+  const int kblocks = (p.max_len + kSwaKeys - 1) / kSwaKeys, kitems = p.Hk * kblocks;
+  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, false>), dim3(of8(kitems), N), dim3(256), 0, s, p, kitems, kblocks);
+  if (p.S > 0) {
+    const int runs = (p.max_len + kSwaFar - 1) / kSwaFar, items = p.Hk * runs;
+    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, true>), dim3(of8(items), N, static_cast<unsigned>((p.S + 31) / 32)), dim3(256), 0, s, p, items, runs);
+    hipLaunchKernelGGL((swa_first_kernel<typename Op::elem, D>), dim3(static_cast<unsigned>(p.S * p.Hk), N), dim3(2 * D), 0, s, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_swa_bwd(const SwaParams& p, int D, bool bf16, hipStream_t s) {
+  if (bf16) return D == 64 ? launch_t<MmaBf16, 64>(p, s) : launch_t<MmaBf16, 128>(p, s);
+  return D == 64 ? launch_t<MmaF32, 64>(p, s) : launch_t<MmaF32, 128>(p, s);
+}
+
+}  // namespace gdn

@@ -1,0 +1,135 @@
+// Device helpers of the window attention's kernels: tiles of rows in LDS, operands of the
+// matrix instructions, the window's mask.
+//
+// Products are formed on 16x16 tiles.  What a lane (c = lane % 16, g = lane / 16) gives to
+// one "step" of a product is 16 bytes: bf16 8 values of the reduction (one instruction over
+// 32), fp32 4 values (four instructions over 16).  The order of the reduction is free as long as both
+// operands share it, and two orders are used:
+//   * along a row of values (d): column COLS step + EPP g + e; both operands are pieces of
+//     16 bytes of rows, from memory or from LDS;
+//   * along rows (keys or queries): row 16 b + 4 g + r of the step's blocks b, the rows that
+//     an accumulator holds in lane (c, g), so scores go from the accumulators of one product
+//     into the operand of the next without leaving their registers.  The other operand
+//     comes from LDS by transposing reads (bf16) or down a column (fp32).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_chunk_common.h"
+#include "gdn_device.h"
+#include "gdn_hybrid.h"
+
+namespace gdn {
+namespace swa {
+
+using chunk::u32x4_t;
+constexpr float kLog2e = chunk::kLog2e;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A tile of rows of D values in LDS.  The piece of 16 bytes u of row t stands at u ^ swizzle(t), which
+// spreads both ways of reading evenly over the banks: 16 rows at one piece, and 16 rows
+// (four a lane group) at two neighbouring pieces (bf16) or four (fp32).
+template <typename E, int D>
+struct Tile {
+  static constexpr int kEpp = 16 / static_cast<int>(sizeof(E));  // values of a piece
+  static constexpr int kPieces = D / kEpp;                       // pieces of a row: 8, 16 or 32
+  static __device__ __forceinline__ int swizzle(int row) { return kPieces == 8 ? (row >> 1) & 7 : row & 15; }
+  static __device__ __forceinline__ int at(int row, int piece) { return row * D + ((piece ^ swizzle(row)) * kEpp); }
+};
+
+struct MmaBf16 {
+  using elem = uint16_t;
+  static constexpr int kCols = 32;  // columns of a step along a row
+  static constexpr int kBlocks = 2; // 16-row blocks of a step along rows
+  static __device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  }
+  // Rounding to bf16: the operands of the second products are probabilities and the scores'
+  // gradients, off by at most 2^-8 of each, as the inputs they are multiplied with are.
+  static __device__ __forceinline__ u32x4_t operand(const f32x4_t* acc) {
+    return u32x4_t{pack_bf16x2(acc[0][0], acc[0][1]), pack_bf16x2(acc[0][2], acc[0][3]), pack_bf16x2(acc[1][0], acc[1][1]),
+                   pack_bf16x2(acc[1][2], acc[1][3])};
+  }
+  // Columns d0 .. d0 + 15 of the 32 rows from row0 on, as the operand whose lane (c, g) holds
+  // column d0 + c of rows 4 g + 0..3 of both blocks.  ds_read_b64_tr_b16: within 16 lanes, lane s names
+  // row s / 4, columns 4 (s % 4) .. + 3, and lane i receives column i of the four rows.
+  template <int D>
+  static __device__ __forceinline__ u32x4_t read_tr(const elem* tile, int row0, int d0, int lane) {
+    const int s = lane & 15, row = row0 + 4 * (lane >> 4) + (s >> 2);
+    const elem* const p = tile + Tile<elem, D>::at(row, (d0 >> 3) + ((s & 3) >> 1)) + 4 * (s & 1);
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p));
+    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(p + 16 * D));
+    typedef short i16x8_t __attribute__((ext_vector_type(8)));
+    return __builtin_bit_cast(u32x4_t, static_cast<i16x8_t>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)));
+  }
+};
+
+struct MmaF32 {
+  using elem = float;
+  static constexpr int kCols = 16;
+  static constexpr int kBlocks = 1;
+  static __device__ __forceinline__ f32x4_t mma(u32x4_t a, u32x4_t b, f32x4_t c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
+    return c;
+  }
+  static __device__ __forceinline__ u32x4_t operand(const f32x4_t* acc) { return __builtin_bit_cast(u32x4_t, acc[0]); }
+  template <int D>
+  static __device__ __forceinline__ u32x4_t read_tr(const elem* tile, int row0, int d0, int lane) {
+    const int col = d0 + (lane & 15);
+    u32x4_t v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      v[r] = __float_as_uint(tile[Tile<elem, D>::at(row0 + 4 * (lane >> 4) + r, col >> 2) + (col & 3)]);
+    return v;
+  }
+};
+
+// A row's operand: 16 bytes of row `row0 + lane % 16`, step `s` along it.
+template <typename Op, int D>
+__device__ __forceinline__ u32x4_t read_row(const typename Op::elem* tile, int row0, int s, int lane) {
+  return *reinterpret_cast<const u32x4_t*>(tile + Tile<typename Op::elem, D>::at(row0 + (lane & 15), 4 * s + (lane >> 4)));
+}
+template <typename Op>
+__device__ __forceinline__ u32x4_t load_row(const typename Op::elem* row, int s, int lane) {
+  constexpr int epp = 16 / static_cast<int>(sizeof(typename Op::elem));
+  return *reinterpret_cast<const u32x4_t*>(row + s * Op::kCols + epp * (lane >> 4));
+}
+
+// 64 or 128 rows of D values on their way from memory to a tile, 256 threads.
+template <typename E, int D, int ROWS>
+struct Stage {
+  using T = Tile<E, D>;
+  static constexpr int kStep = 256 / T::kPieces;  // rows that the workgroup takes at once
+  static constexpr int kN = ROWS / kStep;
+  u32x4_t w[kN];
+  // rows row0 .. row0 + ROWS - 1 of those that start at `base`, `stride` values apart; zeros
+  // where there is no row
+  __device__ __forceinline__ void load(const E* base, int64_t stride, int row0, int rows) {
+    const int piece = threadIdx.x % T::kPieces, first = row0 + threadIdx.x / T::kPieces;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int row = first + i * kStep;
+      const bool in = row >= 0 && row < rows;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(base + static_cast<int64_t>(in ? row : rows - 1) * stride + piece * T::kEpp);
+      w[i] = in ? v : u32x4_t(0u);
+    }
+  }
+  __device__ __forceinline__ void store(E* tile) const {
+    const int piece = threadIdx.x % T::kPieces, first = threadIdx.x / T::kPieces;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) *reinterpret_cast<u32x4_t*>(tile + T::at(first + i * kStep, piece)) = w[i];
+  }
+};
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Query i sees key j: no later one, and of the earlier ones the last W (itself among them)
+// and the first S.
+__device__ __forceinline__ bool sees(int i, int j, int W, int S) { return j <= i && (j > i - W || j < S); }
+
+// Workgroups x, x + 8, ... share an XCD and its L2: items in order, an eighth of them each.
+__device__ __forceinline__ int xcd_item(int x, int items) { return (x & 7) * ((items + 7) / 8) + (x >> 3); }
+
+}  // namespace swa
+}  // namespace gdn

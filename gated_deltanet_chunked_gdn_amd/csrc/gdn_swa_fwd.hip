@@ -1,0 +1,179 @@
+// Causal attention over a sliding window whose first tokens stay visible, forward, on
+// gfx950:  o_i = sum_j p_ij v_j,  p_i = softmax over the visible j of scale q_i . k_j.
+//
+// One pass over the keys that a block of queries sees, with the running maximum and sum of
+// the softmax (in base 2, fp32).  A workgroup holds 128 queries of a head, 32 a wave; keys
+// and values come in tiles of 64 rows through LDS, loaded while the tile before is worked
+// on.  Scores are formed transposed (keys down the accumulator, a query a lane), so the
+// softmax runs inside lanes but for two exchanges of the maximum, and the probabilities are
+// the operand of the second product as they stand.  Tiles that all of a wave's queries see
+// whole take no mask, those that none sees no product.
+#include <hip/hip_runtime.h>
+
+#include "gdn_swa_device.h"
+
+namespace gdn {
+namespace {
+
+using namespace swa;
+
+template <typename Op, int D>
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int blocks) {
+  using E = typename Op::elem;
+  constexpr int CT = 2, KT = 64, NS = D / Op::kCols, NR = 4 / Op::kBlocks, ND = D / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int item = xcd_item(blockIdx.x, items);
+  if (item >= items) return;
+  // a key head's query heads next to each other, then its blocks of queries
+  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
+  const int block = rest / group, h = hk * group + rest - block * group;
+  int64_t bos, len64;
+  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
+  const int len = static_cast<int>(len64), q0 = block * kSwaQueries;
+  if (q0 >= len) return;
+
+  __shared__ alignas(16) E Ks[KT * D];
+  __shared__ alignas(16) E Vs[KT * D];
+
+  const int wq0 = q0 + 32 * wave, wq1 = min(wq0 + 31, len - 1);  // this wave's queries; none if wq0 >= len
+  u32x4_t qf[CT][NS];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    const int i = min(wq0 + 16 * t + c, len - 1);
+    const E* const row = static_cast<const E*>(p.q) + (bos + i) * p.q_stride + h * D;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[t][s] = load_row<Op>(row, s, lane);
+  }
+  const E* const kb = static_cast<const E*>(p.k) + bos * p.k_stride + hk * D;
+  const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
+
+  // tiles: the first tokens' as far as they lie before the window's, then the window's
+  const int win = max(0, q0 - p.W + 1) / KT * KT, last = min(q0 + kSwaQueries, len) - 1;
+  const int nfirst = (min(p.S, win) + KT - 1) / KT, tiles = nfirst + (last - win) / KT + 1;
+  auto start = [&](int t) { return t < nfirst ? t * KT : win + (t - nfirst) * KT; };
+
+  f32x4_t acc[ND][CT];
+  float top[CT], sum[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    top[t] = -INFINITY;
+    sum[t] = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[d][t] = zero4();
+  }
+  const float scale2 = p.scale * kLog2e;
+  Stage<E, D, KT> sk, sv;
+  sk.load(kb, p.k_stride, start(0), len);
+  sv.load(vb, p.v_stride, start(0), len);
+  for (int t = 0; t < tiles; ++t) {
+    const int j0 = start(t);
+    __syncthreads();
+    sk.store(Ks);
+    sv.store(Vs);
+    __syncthreads();
+    if (t + 1 < tiles) {
+      sk.load(kb, p.k_stride, start(t + 1), len);
+      sv.load(vb, p.v_stride, start(t + 1), len);
+    }
+    if (wq0 >= len || j0 > wq1 || (j0 + KT - 1 <= wq0 - p.W && j0 >= p.S)) continue;
+    f32x4_t s[4][CT];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      s[b][0] = s[b][1] = zero4();
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const u32x4_t a = read_row<Op, D>(Ks, 16 * b, n, lane);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) s[b][u] = Op::mma(a, qf[u][n], s[b][u]);
+      }
+    }
+    const bool whole = j0 + KT - 1 <= wq0 && j0 > wq1 - p.W;
+    u32x4_t pf[NR][CT];
+#pragma unroll
+    for (int u = 0; u < CT; ++u) {
+      float high = -INFINITY;
+      if (whole) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            s[b][u][r] *= scale2;
+            high = fmaxf(high, s[b][u][r]);
+          }
+      } else {
+        const int i = wq0 + 16 * u + c;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            s[b][u][r] = sees(i, j0 + 16 * b + 4 * g + r, p.W, p.S) ? s[b][u][r] * scale2 : -INFINITY;
+            high = fmaxf(high, s[b][u][r]);
+          }
+      }
+      high = fmaxf(high, __shfl_xor(high, 16, 64));
+      high = fmaxf(high, __shfl_xor(high, 32, 64));
+      const float now = fmaxf(top[u], high);
+      const float base = now == -INFINITY ? 0.f : now;  // nothing seen yet
+      const float fade = exp2_(top[u] - base);
+      top[u] = now;
+      float part = 0.f;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          s[b][u][r] = exp2_(s[b][u][r] - base);
+          part += s[b][u][r];
+        }
+      sum[u] = fmaf(sum[u], fade, part);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[d][u] *= fade;
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        const f32x4_t two[2] = {s[n * Op::kBlocks][u], s[n * Op::kBlocks + Op::kBlocks - 1][u]};
+        pf[n][u] = Op::operand(two);
+      }
+#pragma unroll
+    for (int n = 0; n < NR; ++n)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const u32x4_t a = Op::template read_tr<D>(Vs, n * 16 * Op::kBlocks, 16 * d, lane);
+#pragma unroll
+        for (int u = 0; u < CT; ++u) acc[d][u] = Op::mma(a, pf[n][u], acc[d][u]);
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    const int i = wq0 + 16 * u + c;
+    float total = sum[u];
+    total += __shfl_xor(total, 16, 64);
+    total += __shfl_xor(total, 32, 64);
+    if (i >= len) continue;
+    const float inv = 1.f / total;
+    E* const row = static_cast<E*>(p.o) + ((bos + i) * p.Hq + h) * D;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+      chunk::store4<E>(row + 16 * d + 4 * g, acc[d][u][0] * inv, acc[d][u][1] * inv, acc[d][u][2] * inv, acc[d][u][3] * inv);
+    if (p.lse && g == 0) p.lse[(bos + i) * p.Hq + h] = kLn2 * (top[u] + __builtin_amdgcn_logf(total));
+  }
+}
+
+template <typename Op, int D>
+hipError_t launch_t(const SwaParams& p, hipStream_t s) {
+  const int blocks = (p.max_len + kSwaQueries - 1) / kSwaQueries, items = p.Hq * blocks;
+  hipLaunchKernelGGL((swa_fwd_kernel<Op, D>), dim3(static_cast<unsigned>((items + 7) / 8 * 8), static_cast<unsigned>(p.N)), dim3(256), 0, s, p,
+                     items, blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_swa_fwd(const SwaParams& p, int D, bool bf16, hipStream_t s) {
+  if (bf16) return D == 64 ? launch_t<MmaBf16, 64>(p, s) : launch_t<MmaBf16, 128>(p, s);
+  return D == 64 ? launch_t<MmaF32, 64>(p, s) : launch_t<MmaF32, 128>(p, s);
+}
+
+}  // namespace gdn

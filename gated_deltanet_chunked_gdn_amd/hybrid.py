@@ -1,7 +1,8 @@
 """Python entry points of the operators that hybrid models put next to the delta rule,
-over libgdn's C ABI (include/gdn.h): the gated linear recurrence, and the norm and rotation
-of queries and keys.  As in ``layer``, PyTorch supplies device memory and the current
-stream, and every step of the computation runs in libgdn's HIP kernels.
+over libgdn's C ABI (include/gdn.h): the gated linear recurrence, the norm and rotation of
+queries and keys, and attention over a sliding window.  As in ``layer``, PyTorch supplies
+device memory and the current stream, and every step of the computation runs in libgdn's
+HIP kernels.
 
     y, h     = glr_fwd(x, r, i, lam, z=None, h0=None)
     y, h, saved = glr_fwd_save(...)
@@ -11,7 +12,13 @@ stream, and every step of the computation runs in libgdn's HIP kernels.
     q, k     = rope_fwd(q, k, inv_freq, positions=None, norm="rms", wq=None, wk=None)
     grads    = rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, ...)
 
-Tensors are contiguous, but for q and k (see there).  Activations are bf16 or fp32 (one dtype a call), parameters and recurrent states fp32.
+    o        = swa_fwd(q, k, v, window, sinks=0)      # with return_lse: (o, lse)
+    grads    = swa_bwd(q, k, v, o, lse, do, window, sinks=0)
+    swa_fill(k, v, kcache, vcache, sinks=0)           # a prompt's keys and values
+    o        = swa_step(q, k, v, kcache, vcache, lens, sinks=0)  # one token, cache updated in place
+
+Tensors are contiguous; q, k and v of the last two operators may also be columns of
+contiguous rows, as a projection leaves them side by side.  Activations are bf16 or fp32 (one dtype a call), parameters and recurrent states fp32.
 Packed sequences: B == 1 and ``cu_seqlens`` the N + 1 offsets, best built once as a
 ``SeqLens``.  Outputs and gradients that were not asked for are None.  A ``workspace``
 holds nothing between calls, but calls that may overlap (on two streams, in graphs
@@ -235,3 +242,86 @@ def rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, norm="rms", eps: fl
     _call(dev, "gdn_rope_bwd", prob, qp, kp, *ins, *grads, *(t.data_ptr() if t is not None else None for t in out.values()),
           ws, nws)
     return out
+
+
+# --------------------------------------------------------------------------- window attention
+
+def _swa_problem(q, k, v, window, sinks, scale, cu_seqlens):
+    """(device index, offsets, problem, addresses of q, k, v)"""
+    what = "q must be (B, T, Hq, D) and k, v (B, T, Hk, D)"
+    dev = _first(q, "q", 4, what)
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError(what)
+    B, T, Hq, D = q.shape
+    Hk, io = k.shape[2], q.dtype
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(q, q.shape, io, dev, "q"), _rows(k, (B, T, Hk, D), io, dev, "k"),
+                                    _rows(v, (B, T, Hk, D), io, dev, "v"))
+    sizes, rest = (B, T, Hq, Hk, D, int(window), int(sinks)), (_IO[io], float(scale), qs, ks, vs)
+    if cu_seqlens is None:
+        return dev, None, _dense(nat.SwaProblem, sizes + (B,), None, None, *rest), (qp, kp, vp)
+    s = _packed(cu_seqlens, dev)
+    return dev, s, _problem(nat.SwaProblem, sizes + (s.num_seqs,), s.host.ctypes.data, s.dev.data_ptr(), *rest), (qp, kp, vp)
+
+
+def swa_fwd(q, k, v, window: int, sinks: int = 0, scale: float = 1.0, cu_seqlens=None, out=None, return_lse: bool = False):
+    """Causal attention over a sliding window whose first tokens stay visible
+    (gdn_swa_fwd): q (B, T, Hq, D), k, v (B, T, Hk, D) of the io dtype, Hq a multiple of Hk,
+    D 64 or 128.  A query sees the last ``window`` tokens, itself among them, and the first
+    ``sinks`` of its sequence.  Returns o, or (o, lse) with lse (B, T, Hq) fp32."""
+    dev, seqs, prob, ptrs = _swa_problem(q, k, v, window, sinks, scale, cu_seqlens)  # seqs: keeps the offsets alive
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+    optr = _want(o, q.shape, q.dtype, dev, "out")
+    lse = torch.empty(q.shape[:3], dtype=_F32, device=dev) if return_lse else None
+    _call(dev, "gdn_swa_fwd", prob, *ptrs, optr, lse.data_ptr() if return_lse else None)
+    return (o, lse) if return_lse else o
+
+
+def swa_bwd(q, k, v, o, lse, do, window: int, sinks: int = 0, scale: float = 1.0, cu_seqlens=None, workspace=None):
+    """Backward of swa_fwd (gdn_swa_bwd) from its o and lse.  Returns dict dq, dk, dv."""
+    dev, seqs, prob, ptrs = _swa_problem(q, k, v, window, sinks, scale, cu_seqlens)  # seqs: keeps the offsets alive
+    ins = (_want(o, q.shape, q.dtype, dev, "o"), _want(lse, q.shape[:3], _F32, dev, "lse"), _want(do, q.shape, q.dtype, dev, "do"))
+    buf, ws, nws = _buffer(workspace, _size("gdn_swa_workspace_size", prob, nat.GDN_SWA_BWD), dev, "workspace")
+    out = {name: torch.empty(t.shape, dtype=t.dtype, device=dev) for name, t in (("dq", q), ("dk", k), ("dv", v))}
+    _call(dev, "gdn_swa_bwd", prob, *ptrs, *ins, *(t.data_ptr() for t in out.values()), ws, nws)
+    return out
+
+
+def _cache_slots(kcache, sinks):
+    if not isinstance(kcache, torch.Tensor) or kcache.dim() != 4 or kcache.shape[1] <= sinks:
+        raise ValueError("kcache must be (sequences, sinks + window, Hk, D)")
+    return kcache.shape[1]
+
+
+def swa_fill(k, v, kcache, vcache, sinks: int = 0, cu_seqlens=None):
+    """Writes the keys and values of prompts into the caches that swa_step continues
+    (gdn_swa_fill): kcache, vcache (sequences, sinks + window, Hk, D) of the io dtype, whose
+    size says the window.  Slots that the prompts do not reach are left as they were."""
+    slots = _cache_slots(kcache, sinks)
+    dev, seqs, prob, ptrs = _swa_problem(k, k, v, slots - sinks, sinks, 1.0, cu_seqlens)  # seqs: keeps the offsets alive
+    shape = (prob.num_seqs, slots, prob.Hk, prob.D)
+    _call(dev, "gdn_swa_fill", prob, *ptrs[1:], _want(kcache, shape, k.dtype, dev, "kcache"), _want(vcache, shape, k.dtype, dev, "vcache"))
+
+
+def swa_step(q, k, v, kcache, vcache, lens, sinks: int = 0, scale: float = 1.0, out=None, workspace=None):
+    """One token of swa_fwd for every sequence (gdn_swa_step): q (B, 1, Hq, D), k, v
+    (B, 1, Hk, D); kcache, vcache (B, sinks + window, Hk, D), updated in place; ``lens``
+    (B,) int32: the tokens that each sequence had before, negative where its place is idle
+    (o is zero there).  The caller adds one to lens behind its last layer.  Returns o."""
+    slots = _cache_slots(kcache, sinks)
+    dev, _, prob, ptrs = _swa_problem(q, k, v, slots - sinks, sinks, scale, None)
+    if prob.T != 1:
+        raise ValueError("q must be (B, 1, Hq, D)")
+    shape = (prob.B, slots, prob.Hk, prob.D)
+    caches = (_want(kcache, shape, q.dtype, dev, "kcache"), _want(vcache, shape, q.dtype, dev, "vcache"))
+    lp = _want(lens, (prob.B,), _I32, dev, "lens")
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+    optr = _want(o, q.shape, q.dtype, dev, "out")
+    need = _step_size(prob.B, prob.Hq, prob.Hk, prob.D, prob.window, prob.sinks, prob.io_dtype)
+    buf, ws, nws = _buffer(workspace, need, dev, "workspace")
+    _call(dev, "gdn_swa_step", prob, *ptrs, *caches, lp, optr, ws, nws)
+    return o
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_size(B, Hq, Hk, D, window, sinks, io):
+    return _size("gdn_swa_workspace_size", nat.SwaProblem(B, 1, Hq, Hk, D, window, sinks, B, None, None, io, 1.0, 0, 0, 0), nat.GDN_SWA_STEP)

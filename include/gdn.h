@@ -676,6 +676,72 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
                         const float* wk, const void* dq_out, const void* dk_out, void* dq, void* dk,
                         float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Causal attention over a sliding window whose first tokens stay visible: query i of a
+ * sequence sees key j <= i where j > i - window or j < sinks, and
+ *     o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i),
+ *     lse_i = log sum_j exp(scale q_i . k_j)       over the keys it sees
+ * (at least its own).  Query head h attends to key head h / (Hq / Hk).
+ * Tensors: q, o, dout, dq [B,T,Hq,D], k, v, dk, dv [B,T,Hk,D] (io dtype), lse [B,T,Hq] fp32.
+ * q, k and v may have their tokens q_stride, k_stride, v_stride values apart as in
+ * gdn_rope_problem (0: contiguous); all else is contiguous.  16-byte aligned, lse and lens
+ * 4-byte.  Supported: D in {64, 128}, Hq a multiple of Hk up to 4096, window >= 1 (as long as
+ * wanted), sinks up to 1024, B T up to 2^30, up to 65535 sequences, and fewer than 2^24
+ * workgroups in a launch (one for 128 tokens of the longest sequence, every query head and
+ * every sequence), else GDN_ERR_UNSUPPORTED.
+ * Scores, sums and statistics of the softmax are fp32; with bf16 io the probabilities and
+ * the scores' gradients are rounded to bf16 as operands of the products that sum over them.
+ * Outputs are rounded once.  Sums run in a fixed order (bit-identical from call to call). */
+typedef struct gdn_swa_problem {
+  int32_t B, T, Hq, Hk, D;
+  int32_t window, sinks;
+  int32_t num_seqs;                /* == B for dense input, else len(cu_seqlens) - 1        */
+  const int32_t* cu_seqlens_host;  /* host, num_seqs + 1 offsets, or NULL (dense)           */
+  const int32_t* cu_seqlens_dev;   /* device copy of the same values, or NULL               */
+  int32_t io_dtype;                /* gdn_dtype                                             */
+  float scale;
+  int64_t q_stride, k_stride, v_stride;
+} gdn_swa_problem;
+
+typedef enum gdn_swa_pass {
+  GDN_SWA_BWD = 0, /* workspace of gdn_swa_bwd  */
+  GDN_SWA_STEP = 1 /* workspace of gdn_swa_step */
+} gdn_swa_pass;
+
+/* Bytes of the device buffer `pass` needs (0 is possible; the pointer may then be NULL);
+ * GDN_ERR_UNSUPPORTED for another pass.  The sizes depend on the problem alone. */
+gdn_status gdn_swa_workspace_size(const gdn_swa_problem* problem, int32_t pass, size_t* bytes);
+
+/* Forward.  out: o; lse (NULL: not wanted).  No workspace. */
+gdn_status gdn_swa_fwd(const gdn_swa_problem* problem, const void* q, const void* k, const void* v,
+                       void* o, float* lse, void* stream);
+
+/* Backward: gradients of <o, dout>, from the forward's o and lse (of the same problem and
+ * inputs, not checked). */
+gdn_status gdn_swa_bwd(const gdn_swa_problem* problem, const void* q, const void* k, const void* v,
+                       const void* o, const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* The cache of a sequence: sinks + window slots of Hk D values for keys and as many for
+ * values, [num_seqs, sinks + window, Hk, D] (io dtype).  Token j < sinks stands in slot j,
+ * any other in slot sinks + (j - sinks) mod window: the slots that n tokens have left hold
+ * exactly what token n - 1 sees.
+ *
+ * gdn_swa_fill writes the slots of prompts of their own (dense or packed): for every
+ * sequence its first tokens and the last of the others; slots that it does not reach are
+ * left as they were. */
+gdn_status gdn_swa_fill(const gdn_swa_problem* problem, const void* k, const void* v, void* kcache,
+                        void* vcache, void* stream);
+
+/* One token of every sequence (decoding; dense with T == 1): its key and value are written
+ * to their slot, and o is what the token sees.  lens [B] int32 on the device holds the
+ * tokens that each sequence had before (the caller adds one behind its last layer); a
+ * negative one marks an idle place of the batch: its cache is left alone, its o is zero.
+ * Slots that have not been written are not read.  The caches and o must not overlap another
+ * tensor. */
+gdn_status gdn_swa_step(const gdn_swa_problem* problem, const void* q, const void* k, const void* v,
+                        void* kcache, void* vcache, const int32_t* lens, void* o, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -172,3 +172,103 @@ def rope(x, w, freq, pos, norm, eps, inter, d=None):
     out["dw"] = (g * x * inv).reshape(rows, D).sum(0)
     err["dw"] = ((lost + (rows / 8 + 150) * U) * gs * x.abs() * inv).reshape(rows, D).sum(0)
     return out, err
+
+
+# --------------------------------------------------------------------------- window attention
+
+def seen(Tq, W, S):
+    i = torch.arange(Tq)
+    return (i <= i[:, None]) & ((i > i[:, None] - W) | (i < S))
+
+
+def _attend(q, k, v, mask, scale, half):
+    """(o, lse, p, bound of o, relative bounds of p) of one head: q (n, D), k, v (m, D).
+
+    Roundings: a score's D products summed (D + 3 of the absolute terms), the exponent's (its
+    size, the maximum's and the sum's, twice, and 8); a probability that of its own score and
+    the mean over its row's; `half` for its rounding as an operand; a sum over n keys n + 16."""
+    n = mask.sum(-1, keepdim=True).double()
+    s = (q @ k.T) * scale
+    e = (q.shape[-1] + 3) * U * (q.abs() @ k.abs().T) * abs(scale)
+    s = s.masked_fill(~mask, -torch.inf)
+    lse = torch.logsumexp(s, -1, keepdim=True)
+    p = torch.exp(s - lse)
+    e = torch.where(mask, e + 2 * U * (s.abs().nan_to_num(posinf=0) + lse.abs() + 8), 0)
+    mean = (p * e).sum(-1, keepdim=True)
+    eta = torch.where(mask, e + mean + (n + 8) * U, 0)
+    bound = (p * (eta + half + (n + 16) * U)) @ v.abs()
+    return p @ v, lse, p, bound, eta
+
+
+def swa(q, k, v, W, S, scale, cu, do=None):
+    """(values, bounds): dicts o, lse and, with do, dq, dk, dv; every sequence and head alone."""
+    io = q.dtype
+    half = 0.0 if io == torch.float32 else torch.finfo(io).eps / 2
+    q, k, v, do = f64(q, k, v, do)
+    B, T, Hq, D = q.shape
+    Hk = k.shape[2]
+    group = Hq // Hk
+    rows = lambda t: None if t is None else t.reshape(B * T, t.shape[2], D)  # noqa: E731
+    q, k, v, do = rows(q), rows(k), rows(v), rows(do)
+    out = {"o": torch.zeros_like(q), "lse": torch.zeros(B * T, Hq, dtype=torch.float64)}
+    if do is not None:
+        out.update(dq=torch.zeros_like(q), dk=torch.zeros_like(k), dv=torch.zeros_like(v))
+    err = {name: torch.zeros_like(t) for name, t in out.items()}
+    for t0, t1 in spans(B, T, cu):
+        if t1 == t0:
+            continue
+        mask = seen(t1 - t0, W, S)
+        n, m = mask.sum(-1, keepdim=True).double(), mask.sum(0).double().unsqueeze(-1) * group
+        for h in range(Hq):
+            qs, ks, vs = q[t0:t1, h], k[t0:t1, h // group], v[t0:t1, h // group]
+            o, lse, p, bo, eta = _attend(qs, ks, vs, mask, scale, half)
+            out["o"][t0:t1, h], err["o"][t0:t1, h] = o, bo
+            out["lse"][t0:t1, h] = lse[:, 0]
+            err["lse"][t0:t1, h] = ((p * eta).sum(-1) + 8 * U * (lse[:, 0].abs() + 1))
+            if do is None:
+                continue
+            d = do[t0:t1, h]
+            dp, dps = d @ vs.T, d.abs() @ vs.abs().T
+            delta = (d * o).sum(-1, keepdim=True)
+            deltas = (d.abs() * o.abs()).sum(-1, keepdim=True)
+            # from the stored o: its own bound, its rounding, the sum
+            edelta = (d.abs() * (bo + half * (o.abs() + bo))).sum(-1, keepdim=True) + (D + 8) * U * deltas
+            ds = p * (dp - delta) * scale
+            eds = p * abs(scale) * (eta * (dp - delta).abs() + (D + 11) * U * dps + edelta + 8 * U * deltas) + half * ds.abs()
+            eds = torch.where(mask, eds * (1 + half), 0)
+            out["dq"][t0:t1, h] = ds @ ks
+            err["dq"][t0:t1, h] = (eds + (n + 16) * U * ds.abs()) @ ks.abs()
+            out["dk"][t0:t1, h // group] += ds.T @ qs
+            err["dk"][t0:t1, h // group] += (eds.T + (m + 64) * U * ds.abs().T) @ qs.abs()
+            out["dv"][t0:t1, h // group] += p.T @ d
+            err["dv"][t0:t1, h // group] += (p * (eta + half)).T @ d.abs() + ((m + 64) * U * p.T) @ d.abs()
+    shape = lambda t, H: t.reshape(B, T, H, *t.shape[2:])  # noqa: E731
+    heads = {"o": Hq, "lse": Hq, "dq": Hq, "dk": Hk, "dv": Hk}
+    return {x: shape(t, heads[x]) for x, t in out.items()}, {x: shape(t, heads[x]) for x, t in err.items()}
+
+
+def slot_of(token, W, S):
+    return token if token < S else S + (token - S) % W
+
+
+def swa_step(q, k, v, kc, vc, lens, S, scale):
+    """(o, its bound, keys' cache, values' cache) after one token of every sequence."""
+    io = q.dtype
+    half = 0.0 if io == torch.float32 else torch.finfo(io).eps / 2
+    q, k, v, kc, vc = (t.clone() for t in f64(q, k, v, kc, vc))
+    B, _, Hq, _ = q.shape
+    W, group = kc.shape[1] - S, Hq // k.shape[2]
+    o, err = torch.zeros_like(q), torch.zeros_like(q)
+    for n, before in enumerate(lens.tolist()):
+        if before < 0:
+            continue
+        slot = slot_of(before, W, S)
+        kc[n, slot], vc[n, slot] = k[n, 0], v[n, 0]
+        tokens = sorted(set(range(min(S, before + 1))) | set(range(max(0, before + 1 - W), before + 1)))
+        slots = [slot_of(t, W, S) for t in tokens]
+        assert len(set(slots)) == len(slots)
+        for h in range(Hq):
+            got, _, _, bound, _ = _attend(q[n, :, h], kc[n, slots, h // group], vc[n, slots, h // group],
+                                          torch.ones(1, len(slots), dtype=torch.bool), scale, half)
+            o[n, :, h], err[n, :, h] = got, bound
+    return o, err, kc, vc

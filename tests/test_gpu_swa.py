@@ -1,0 +1,135 @@
+"""Window attention on the GPU against its float64 definition: forward and backward over
+dense and packed sequences (marked gpu).  The bounds are counted in _hybrid_oracle.swa."""
+import math
+
+import pytest
+import torch
+
+import gated_deltanet_chunked_gdn_amd as gdn
+import _hybrid_oracle as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def inputs(B, T, Hq, Hk, D, io, seed=0, views=False):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(io)  # noqa: E731
+    if views:
+        rows = r(B, T, (Hq + 2 * Hk) * D)
+        q, k, v = (t.unflatten(-1, (-1, D)) for t in rows.split([Hq * D, Hk * D, Hk * D], dim=-1))
+        return q, k, v, r(B, T, Hq, D)
+    return r(B, T, Hq, D), r(B, T, Hk, D), r(B, T, Hk, D), r(B, T, Hq, D)
+
+
+def compare(q, k, v, do, W, S, scale, cu):
+    want, err = ref.swa(q, k, v, W, S, scale, cu, do)
+    how = dict(sinks=S, scale=scale, cu_seqlens=cu)
+    B, T = q.shape[:2]
+    room = torch.full((1, T + 2, *q.shape[2:]), 7.0, device=DEV, dtype=q.dtype) if B == 1 else None
+    o, lse = gdn.swa_fwd(q, k, v, W, return_lse=True, out=room[:, 1:T + 1] if room is not None else None, **how)
+    assert torch.equal(gdn.swa_fwd(q, k, v, W, **how), o)
+    got = gdn.swa_bwd(q, k, v, o, lse, do, W, **how)
+    again = gdn.swa_bwd(q, k, v, o, lse, do, W, **how)
+    torch.cuda.synchronize()
+    if room is not None:
+        assert bool((room[:, 0] == 7).all()) and bool((room[:, T + 1] == 7).all())
+    ref.check("o", o, want["o"], err["o"])
+    ref.check("lse", lse, want["lse"], err["lse"])
+    for key in ("dq", "dk", "dv"):
+        ref.check(key, got[key], want[key], err[key])
+        assert torch.equal(got[key], again[key]), key
+
+
+CASES = [  # B, T, Hq, Hk, D, W, S, cu, views
+    (1, 1, 1, 1, 64, 1, 0, None, False),
+    (2, 5, 2, 1, 64, 3, 0, None, False),
+    (1, 65, 2, 2, 128, 1, 0, None, False),
+    (1, 129, 4, 2, 128, 64, 0, None, True),
+    (2, 200, 3, 1, 64, 65, 1, None, False),
+    (1, 300, 2, 1, 128, 33, 4, None, True),
+    (1, 260, 1, 1, 64, 1000, 3, None, False),
+    (1, 290, 2, 1, 64, 17, 70, None, False),
+    (1, 400, 2, 2, 64, 100, 130, None, False),
+    (3, 64, 8, 1, 64, 64, 2, None, False),
+    (1, 333, 4, 2, 64, 40, 3, [0, 0, 1, 65, 193, 193, 332, 333, 333], False),
+    (1, 350, 2, 1, 128, 129, 2, [0, 130, 350], True),
+]
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,W,S,cu,views", CASES)
+def test_swa(B, T, Hq, Hk, D, W, S, cu, views, io):
+    q, k, v, do = inputs(B, T, Hq, Hk, D, io, views=views)
+    compare(q, k, v, do, W, S, D ** -0.5, cu)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("T,W,S,D,cu", [(1100, 60, 5, 64, None), (700, 31, 40, 128, None), (1300, 512, 33, 64, [0, 600, 601, 1300])])
+def test_first_tokens_of_long_sequences(T, W, S, D, cu, io):
+    """Several runs of queries behind the first tokens' window, more of them than one block of keys."""
+    q, k, v, do = inputs(1, T, 2, 1, D, io, seed=1)
+    compare(q, k, v, do, W, S, D ** -0.5, cu)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 4.0])
+def test_scales(scale):
+    """Scores of up to a hundred and more, rising where the maximum moves, and none at all."""
+    q, k, v, do = inputs(1, 150, 2, 1, 64, F32, seed=2)
+    compare(q, k, v, do, 50, 2, scale, None)
+
+
+def test_large_scores_first():
+    """The largest score comes first, or last: the running maximum falls behind or jumps."""
+    for at in (0, 149):
+        q, k, v, do = inputs(1, 150, 1, 1, 64, F32, seed=3)
+        k[0, at] *= 30
+        compare(q, k, v, do, 150, 0, 0.125, None)
+
+
+def test_dense_rows_are_packed_sequences():
+    q, k, v, do = inputs(3, 70, 4, 2, 64, BF, seed=4)
+    o, lse = gdn.swa_fwd(q, k, v, 20, sinks=2, scale=0.1, return_lse=True)
+    got = gdn.swa_bwd(q, k, v, o, lse, do, 20, sinks=2, scale=0.1)
+    flat = lambda t: t.reshape(1, 210, *t.shape[2:])  # noqa: E731
+    cu = [0, 70, 140, 210]
+    o2, lse2 = gdn.swa_fwd(flat(q), flat(k), flat(v), 20, sinks=2, scale=0.1, cu_seqlens=cu, return_lse=True)
+    got2 = gdn.swa_bwd(flat(q), flat(k), flat(v), o2, lse2, flat(do), 20, sinks=2, scale=0.1, cu_seqlens=cu)
+    assert torch.equal(flat(o), o2) and torch.equal(flat(lse), lse2)
+    for key in got:
+        assert torch.equal(flat(got[key]), got2[key]), key
+
+
+def test_empty():
+    for B, T, cu in ((0, 5, None), (2, 0, None), (1, 0, [0]), (1, 0, [0, 0, 0])):
+        q, k, v, do = inputs(B, T, 2, 1, 64, BF)
+        o, lse = gdn.swa_fwd(q, k, v, 4, sinks=1, cu_seqlens=cu, return_lse=True)
+        got = gdn.swa_bwd(q, k, v, o, lse, do, 4, sinks=1, cu_seqlens=cu)
+        assert o.shape == q.shape and got["dk"].shape == k.shape
+
+
+def test_gradients_against_differences():
+    """The fp32 chain against central differences of its own forward: step 2^-6, whose square
+    times a third derivative stays below 1e-3 here; roundings of 200 2^-24 sum |o do| over the step."""
+    q, k, v, do = inputs(1, 20, 2, 1, 64, F32, seed=5)
+    how = dict(sinks=2, scale=0.125)
+    o, lse = gdn.swa_fwd(q, k, v, 6, return_lse=True, **how)
+    got = gdn.swa_bwd(q, k, v, o, lse, do, 6, **how)
+    for name, t in (("dq", q), ("dk", k), ("dv", v)):
+        for j in (0, 65, 999):
+            vals = []
+            for sign in (1, -1):
+                w = [x.clone() for x in (q, k, v)]
+                w[("dq", "dk", "dv").index(name)].view(-1)[j] += sign * 2.0 ** -6
+                vals.append(float((gdn.swa_fwd(*w, 6, **how).double() * do).sum()))
+            assert abs((vals[0] - vals[1]) * 32 - float(got[name].view(-1)[j])) <= 5e-3, name
+
+
+def test_infinite_scores_are_nan_in_their_row_alone():
+    q, k, v, _ = inputs(1, 100, 1, 1, 64, F32, seed=6)
+    clean = gdn.swa_fwd(q, k, v, 30)
+    q[0, 40, 0, 3] = math.inf
+    o = gdn.swa_fwd(q, k, v, 30)
+    assert (~torch.isfinite(o)).any(-1).nonzero()[:, 1].unique().tolist() == [40]
+    assert torch.equal(o[:, :40], clean[:, :40]) and torch.equal(o[:, 41:], clean[:, 41:])

@@ -107,3 +107,39 @@ def test_rope_is_a_rotation():
         near = ref.rope(x, None, freq, pos, None, 0.0, inter)[0]["out"]
         far = ref.rope(x, None, freq, pos + 1000, None, 0.0, inter)[0]["out"]
         assert abs(float((near[0, 0] * near[0, 1]).sum() - (far[0, 0] * far[0, 1]).sum())) <= 1e-12
+
+
+def test_swa_gradients_against_differences():
+    g = torch.Generator().manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    for W, S, cu in ((3, 0, None), (2, 2, None), (4, 1, [0, 0, 3, 10]), (50, 5, None)):
+        q, k, v, do = r(1, 10, 4, 5), r(1, 10, 2, 5), r(1, 10, 2, 5), r(1, 10, 4, 5)
+        out, _ = ref.swa(q, k, v, W, S, 0.7, cu, do)
+        for leaf, name in ((q, "dq"), (k, "dk"), (v, "dv")):
+            flat = leaf.reshape(-1)
+            for j in range(0, flat.numel(), 7):
+                keep, vals = float(flat[j]), []
+                for sign in (1, -1):
+                    flat[j] = keep + sign * 1e-6
+                    vals.append(float((ref.swa(q, k, v, W, S, 0.7, cu)[0]["o"] * do).sum()))
+                flat[j] = keep
+                assert abs((vals[0] - vals[1]) / 2e-6 - float(out[name].reshape(-1)[j])) <= 1e-7, (W, S, name)
+
+
+def test_swa_masks():
+    assert ref.seen(5, 2, 1).int().tolist() == [[1, 0, 0, 0, 0], [1, 1, 0, 0, 0], [1, 1, 1, 0, 0], [1, 0, 1, 1, 0], [1, 0, 0, 1, 1]]
+    assert torch.equal(ref.seen(6, 6, 0), torch.ones(6, 6).tril().bool())
+    assert torch.equal(ref.seen(6, 1, 0), torch.eye(6).bool())
+
+
+def test_swa_step_continues_the_sequence():
+    """Token by token through the cache = the rows of the whole sequence."""
+    g = torch.Generator().manual_seed(6)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    for W, S in ((1, 0), (3, 0), (3, 2), (20, 4)):
+        q, k, v = r(2, 11, 2, 4), r(2, 11, 1, 4), r(2, 11, 1, 4)
+        want, _ = ref.swa(q, k, v, W, S, 0.5, None)
+        kc, vc = r(2, S + W, 1, 4), r(2, S + W, 1, 4)
+        for t in range(11):
+            o, _, kc, vc = ref.swa_step(q[:, t:t + 1], k[:, t:t + 1], v[:, t:t + 1], kc, vc, torch.tensor([t, t]), S, 0.5)
+            assert float((o - want["o"][:, t:t + 1]).abs().max()) <= 1e-14, (W, S, t)
