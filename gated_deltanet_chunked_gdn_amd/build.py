@@ -31,7 +31,8 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
 
 # The state pass keeps its MFMA accumulators in VGPRs: it touches them with VALU
 # code between products, which AGPR accumulators would turn into copies.
-EXTRA = {"gdn_chunk_chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# So do the window attention's kernels.
+EXTRA = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in ("gdn_chunk_chain.hip", "gdn_swa_fwd.hip", "gdn_swa_bwd.hip", "gdn_swa_step.hip")}
 
 
 def _compile(src: str) -> str:

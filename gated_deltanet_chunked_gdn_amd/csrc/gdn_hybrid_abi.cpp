@@ -110,8 +110,8 @@ size_t extent(int64_t rows, int64_t stride, int64_t row, size_t io) {
 gdn_status check_stride(int64_t given, int64_t row, size_t io, int64_t* stride) {
   *stride = given ? given : row;
   if (*stride < row) return GDN_ERR_SHAPE;
-  // 2^31 rows of 2^31 values of 4 bytes would pass 64 bits
-  if (*stride > INT64_C(1) << 28) return GDN_ERR_UNSUPPORTED;
+  // the kernels address up to 128 rows from one of them in 32 bits
+  if (*stride > INT64_C(1) << 21) return GDN_ERR_UNSUPPORTED;
   return *stride * static_cast<int64_t>(io) % 16 ? GDN_ERR_ALIGN : GDN_OK;
 }
 

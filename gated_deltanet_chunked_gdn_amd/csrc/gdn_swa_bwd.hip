@@ -24,7 +24,7 @@ using namespace swa;
 // ---------------------------------------------------------------------------- dq
 
 template <typename Op, int D>
-__global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
   using E = typename Op::elem;
   constexpr int CT = 2, KT = 64, NS = D / Op::kCols, ND = D / 16, KB = Op::kBlocks;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -38,8 +38,7 @@ __global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, 
   const int len = static_cast<int>(len64), q0 = block * kSwaQueries;
   if (q0 >= len) return;
 
-  __shared__ alignas(16) E Ks[KT * D];
-  __shared__ alignas(16) E Vs[KT * D];
+  __shared__ alignas(16) E Kt[2][KT * D], Vt[2][KT * D];
 
   const int wq0 = q0 + 32 * wave, wq1 = min(wq0 + 31, len - 1);
   u32x4_t qf[CT][NS], df[CT][NS];
@@ -71,7 +70,6 @@ __global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, 
     dot += __shfl_xor(dot, 32, 64);
     delta[t] = dot;
     lse2[t] = p.lse[at] * kLog2e;
-    if (g == 0 && wq0 + 16 * t + c < len) p.delta[at] = dot;
   }
   const E* const kb = static_cast<const E*>(p.k) + bos * p.k_stride + hk * D;
   const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
@@ -85,18 +83,34 @@ __global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, 
 #pragma unroll
     for (int d = 0; d < ND; ++d) acc[d][t] = zero4();
   const float scale2 = p.scale * kLog2e;
-  Stage<E, D, KT> sk, sv;
-  sk.load(kb, p.k_stride, start(0), len);
-  sv.load(vb, p.v_stride, start(0), len);
-  for (int t = 0; t < tiles; ++t) {
-    const int j0 = start(t);
-    __syncthreads();
-    sk.store(Ks);
-    sv.store(Vs);
-    __syncthreads();
-    if (t + 1 < tiles) {
-      sk.load(kb, p.k_stride, start(t + 1), len);
-      sv.load(vb, p.v_stride, start(t + 1), len);
+  // Where queries see few keys, o is as large as the values and its rounding to bf16 is most of the
+  // error of delta (and a third of dq's and dk's): there delta is the sum of P dP, by a pass
+  // of its own over the few tiles.
+  const bool exact = sizeof(E) == 2 && tiles <= 4;
+  const int steps = exact ? 2 * tiles : tiles;
+  float own[CT];
+#pragma unroll
+  for (int u = 0; u < CT; ++u) own[u] = 0.f;
+  auto fetch = [&](int t) {
+    const int j0 = start(t >= tiles ? t - tiles : t);
+    Stage<E, D, KT>::load(Kt[t & 1], kb + j0 * p.k_stride, p.k_stride, len - j0);
+    Stage<E, D, KT>::load(Vt[t & 1], vb + j0 * p.v_stride, p.v_stride, len - j0);
+  };
+  fetch(0);
+  for (int t = 0; t < steps; ++t) {
+    const bool sums = exact && t < tiles;  // the pass that forms delta
+    const int j0 = start(t >= tiles ? t - tiles : t);
+    const E* const Ks = Kt[t & 1];
+    const E* const Vs = Vt[t & 1];
+    landed();
+    __syncthreads();  // and the other buffer is read
+    if (t + 1 < steps) fetch(t + 1);
+    if (exact && t == tiles) {
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        delta[u] = own[u] + __shfl_xor(own[u], 16, 64);
+        delta[u] += __shfl_xor(delta[u], 32, 64);
+      }
     }
     if (wq0 >= len || j0 > wq1 || (j0 + KT - 1 <= wq0 - p.W && j0 >= p.S)) continue;
     const bool whole = j0 + KT - 1 <= wq0 && j0 > wq1 - p.W;
@@ -118,19 +132,38 @@ __global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, 
           }
         }
       }
-      u32x4_t sf[CT];
 #pragma unroll
       for (int u = 0; u < CT; ++u) {
-        f32x4_t ds[KB];
-        const int i = wq0 + 16 * u + c;
+        const float less = sums ? 0.f : delta[u];
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = exp2_(fmaf(s[b][u][r], scale2, -lse2[u])) * (dp[b][u][r] - delta[u]);
-            ds[b][r] = whole || sees(i, j0 + 16 * (b0 + b) + 4 * g + r, p.W, p.S) ? x : 0.f;
-          }
-        sf[u] = Op::operand(ds);
+          for (int r = 0; r < 4; ++r) s[b][u][r] = exp2_(fmaf(s[b][u][r], scale2, -lse2[u])) * (dp[b][u][r] - less);
+      }
+      if (!whole) {
+        seldom();
+#pragma unroll
+        for (int u = 0; u < CT; ++u)
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              s[b][u][r] = sees(wq0 + 16 * u + c, j0 + 16 * (b0 + b) + 4 * g + r, p.W, p.S) ? s[b][u][r] : 0.f;
+      }
+      if (sums) {
+#pragma unroll
+        for (int u = 0; u < CT; ++u)
+#pragma unroll
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) own[u] += s[b][u][r];
+        continue;
+      }
+      u32x4_t sf[CT];
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        const f32x4_t two[2] = {s[0][u], s[KB - 1][u]};
+        sf[u] = Op::operand(two);
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
@@ -140,6 +173,9 @@ __global__ __launch_bounds__(256, 1) void swa_dq_kernel(SwaParams p, int items, 
       }
     }
   }
+#pragma unroll
+  for (int u = 0; u < CT; ++u)
+    if (g == 0 && wq0 + 16 * u + c < len) p.delta[(bos + wq0 + 16 * u + c) * p.Hq + h] = delta[u];
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
     const int i = wq0 + 16 * u + c;
@@ -182,9 +218,8 @@ __global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items,
     i1 = min(static_cast<int64_t>(len), static_cast<int64_t>(k0) + kSwaKeys - 1 + p.W) - 1;
   }
 
-  __shared__ alignas(16) E Qs[QT * D];
-  __shared__ alignas(16) E Ds[QT * D];
-  __shared__ alignas(16) float ls[QT], dl[QT];
+  __shared__ alignas(16) E Qt[2][QT * D], Dt[2][QT * D];
+  __shared__ alignas(16) float lt[2][QT], dt[2][QT];
 
   u32x4_t kf[CT][NS], vf[CT][NS];
 #pragma unroll
@@ -206,12 +241,11 @@ __global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items,
 
   const int tiles = (i1 - i0) / QT + 1, steps = group * tiles;
   const float scale2 = p.scale * kLog2e;
-  Stage<E, D, QT> sq, sd;
   float rl = 0.f, rd = 0.f;
   auto fetch = [&](int step) {
     const int h = hk * group + step / tiles, row = i0 + (step % tiles) * QT;
-    sq.load(static_cast<const E*>(p.q) + bos * p.q_stride + h * D, p.q_stride, row, len);
-    sd.load(static_cast<const E*>(p.dout) + (bos * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, row, len);
+    Stage<E, D, QT>::load(Qt[step & 1], static_cast<const E*>(p.q) + (bos + row) * p.q_stride + h * D, p.q_stride, len - row);
+    Stage<E, D, QT>::load(Dt[step & 1], static_cast<const E*>(p.dout) + ((bos + row) * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, len - row);
     if (threadIdx.x < QT) {
       const int64_t at = (bos + min(row + static_cast<int>(threadIdx.x), len - 1)) * p.Hq + h;
       rl = p.lse[at] * kLog2e;
@@ -221,14 +255,16 @@ __global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items,
   fetch(0);
   for (int step = 0; step < steps; ++step) {
     const int r0 = i0 + (step % tiles) * QT;
-    __syncthreads();
-    sq.store(Qs);
-    sd.store(Ds);
+    const E* const Qs = Qt[step & 1];
+    const E* const Ds = Dt[step & 1];
+    const float* const ls = lt[step & 1];
+    const float* const dl = dt[step & 1];
+    landed();
     if (threadIdx.x < QT) {
-      ls[threadIdx.x] = rl;
-      dl[threadIdx.x] = rd;
+      lt[step & 1][threadIdx.x] = rl;
+      dt[step & 1][threadIdx.x] = rd;
     }
-    __syncthreads();
+    __syncthreads();  // and the other buffer is read
     if (step + 1 < steps) fetch(step + 1);
 #pragma unroll
     for (int b1 = 0; b1 < (FAR ? KB : QT / 16); b1 += KB) {
@@ -259,16 +295,27 @@ __global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items,
         const f32x4_t l4 = *reinterpret_cast<const f32x4_t*>(&ls[16 * (b0 + b) + 4 * g]);
         const f32x4_t d4 = *reinterpret_cast<const f32x4_t*>(&dl[16 * (b0 + b) + 4 * g]);
 #pragma unroll
+        for (int u = 0; u < CT; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            s[b][u][r] = exp2_(fmaf(s[b][u][r], scale2, -l4[r]));
+            dp[b][u][r] = s[b][u][r] * (dp[b][u][r] - d4[r]);
+          }
+      }
+      if (!whole) {
+        seldom();
+#pragma unroll
         for (int u = 0; u < CT; ++u) {
           const int j = wk0 + 16 * u + c;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = first + 16 * b + 4 * g + r;
-            const bool ok = whole || (i < len && j < len && (FAR ? j < p.S && i - j >= p.W : j <= i && i - j < p.W));
-            const float w = exp2_(fmaf(s[b][u][r], scale2, -l4[r]));
-            dp[b][u][r] = ok ? w * (dp[b][u][r] - d4[r]) : 0.f;
-            s[b][u][r] = ok ? w : 0.f;
-          }
+          for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int i = first + 16 * b + 4 * g + r;
+              const bool ok = i < len && j < len && (FAR ? j < p.S && i - j >= p.W : j <= i && i - j < p.W);
+              s[b][u][r] = ok ? s[b][u][r] : 0.f;
+              dp[b][u][r] = ok ? dp[b][u][r] : 0.f;
+            }
         }
       }
 #pragma unroll

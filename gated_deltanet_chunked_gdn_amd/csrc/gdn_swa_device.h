@@ -27,13 +27,17 @@ constexpr float kLog2e = chunk::kLog2e;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // A tile of rows of D values in LDS.  The piece of 16 bytes u of row t stands at u ^ swizzle(t), which
-// spreads both ways of reading evenly over the banks: 16 rows at one piece, and 16 rows
-// (four a lane group) at two neighbouring pieces (bf16) or four (fp32).
+// spreads both ways of reading over the banks: 16 rows at one piece (eight at a time), and,
+// down the rows, four rows at two neighbouring pieces (bf16, a lane group) or 16 rows at
+// four (fp32).
 template <typename E, int D>
 struct Tile {
   static constexpr int kEpp = 16 / static_cast<int>(sizeof(E));  // values of a piece
   static constexpr int kPieces = D / kEpp;                       // pieces of a row: 8, 16 or 32
-  static __device__ __forceinline__ int swizzle(int row) { return kPieces == 8 ? (row >> 1) & 7 : row & 15; }
+  static __device__ __forceinline__ int swizzle(int row) {
+    if (sizeof(E) == 4) return row & 15;
+    return ((row & 3) << 1) | ((row >> 2) & 1) | (kPieces > 8 ? row & 8 : 0);
+  }
   static __device__ __forceinline__ int at(int row, int piece) { return row * D + ((piece ^ swizzle(row)) * kEpp); }
 };
 
@@ -96,33 +100,45 @@ __device__ __forceinline__ u32x4_t load_row(const typename Op::elem* row, int s,
   return *reinterpret_cast<const u32x4_t*>(row + s * Op::kCols + epp * (lane >> 4));
 }
 
-// 64 or 128 rows of D values on their way from memory to a tile, 256 threads.
+// ROWS rows of D values from memory to a tile, by 256 threads, without a stop in registers: a
+// wave's load puts its lanes' 16 bytes one behind another into LDS, so the lane takes the
+// piece that belongs where it stands.  Rows are read through a resource that ends with the
+// last one, so those behind it come as zeros.  Who reads the tile waits for `landed` and then
+// for the workgroup.
 template <typename E, int D, int ROWS>
 struct Stage {
   using T = Tile<E, D>;
-  static constexpr int kStep = 256 / T::kPieces;  // rows that the workgroup takes at once
-  static constexpr int kN = ROWS / kStep;
-  u32x4_t w[kN];
-  // rows row0 .. row0 + ROWS - 1 of those that start at `base`, `stride` values apart; zeros
-  // where there is no row
-  __device__ __forceinline__ void load(const E* base, int64_t stride, int row0, int rows) {
-    const int piece = threadIdx.x % T::kPieces, first = row0 + threadIdx.x / T::kPieces;
+  static constexpr int kRows = 64 / T::kPieces;      // rows of a wave's load
+  static constexpr int kN = ROWS / (4 * kRows);      // loads of a wave
+  // `rows` rows (any number; those of the tile count) from `base` on, `stride` values apart
+  static __device__ __forceinline__ void load(E* tile, const E* base, int64_t stride, int rows) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = min(rows, ROWS), step = static_cast<int>(stride) * static_cast<int>(sizeof(E));
+    // as chunk::buffer_rsrc
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    const u32x4_t r = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu,
+                       static_cast<uint32_t>(n > 0 ? (n - 1) * step + D * static_cast<int>(sizeof(E)) : 0), 0x00020000u};
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int row = first + i * kStep;
-      const bool in = row >= 0 && row < rows;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(base + static_cast<int64_t>(in ? row : rows - 1) * stride + piece * T::kEpp);
-      w[i] = in ? v : u32x4_t(0u);
+      const int first = (4 * i + wave) * kRows, row = first + lane / T::kPieces;
+      const int off = row * step + ((lane % T::kPieces) ^ T::swizzle(row)) * 16;
+      const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(tile + first * D)));
+      // In assembly, since the compiler would wait for the next tile's loads before it reads this
+      // one: it cannot tell the two buffers apart.  Nothing is written to a register; M0 names
+      // the place in LDS (a wait state between its write and the load).  The compiler keeps
+      // nothing in M0 from one instruction to another; the kernels here have no other use of it.
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "memory");
     }
   }
-  __device__ __forceinline__ void store(E* tile) const {
-    const int piece = threadIdx.x % T::kPieces, first = threadIdx.x / T::kPieces;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) *reinterpret_cast<u32x4_t*>(tile + T::at(first + i * kStep, piece)) = w[i];
-  }
 };
+// This wave's loads have arrived (vmcnt 0), those above among them, which the compiler does not count.
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// At the head of a branch that few tiles take: keeps the compiler from computing it always
+// and selecting (it does not move what stands behind this).
+__device__ __forceinline__ void seldom() { __builtin_amdgcn_wave_barrier(); }
 
 // Query i sees key j: no later one, and of the earlier ones the last W (itself among them)
 // and the first S.

@@ -33,8 +33,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   const int len = static_cast<int>(len64), q0 = block * kSwaQueries;
   if (q0 >= len) return;
 
-  __shared__ alignas(16) E Ks[KT * D];
-  __shared__ alignas(16) E Vs[KT * D];
+  __shared__ alignas(16) E Kt[2][KT * D], Vt[2][KT * D];
 
   const int wq0 = q0 + 32 * wave, wq1 = min(wq0 + 31, len - 1);  // this wave's queries; none if wq0 >= len
   u32x4_t qf[CT][NS];
@@ -43,7 +42,11 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     const int i = min(wq0 + 16 * t + c, len - 1);
     const E* const row = static_cast<const E*>(p.q) + (bos + i) * p.q_stride + h * D;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) qf[t][s] = load_row<Op>(row, s, lane);
+    for (int s = 0; s < NS; ++s) {
+      qf[t][s] = load_row<Op>(row, s, lane);
+      // a negative scale turns the queries, so that the largest product has the largest score
+      if (p.scale < 0.f) qf[t][s] ^= u32x4_t(sizeof(E) == 2 ? 0x80008000u : 0x80000000u);
+    }
   }
   const E* const kb = static_cast<const E*>(p.k) + bos * p.k_stride + hk * D;
   const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
@@ -54,7 +57,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   auto start = [&](int t) { return t < nfirst ? t * KT : win + (t - nfirst) * KT; };
 
   f32x4_t acc[ND][CT];
-  float top[CT], sum[CT];
+  float top[CT], sum[CT];  // the exponents' base, in base 2, and the sum of this lane's keys
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
     top[t] = -INFINITY;
@@ -62,25 +65,26 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 #pragma unroll
     for (int d = 0; d < ND; ++d) acc[d][t] = zero4();
   }
-  const float scale2 = p.scale * kLog2e;
-  Stage<E, D, KT> sk, sv;
-  sk.load(kb, p.k_stride, start(0), len);
-  sv.load(vb, p.v_stride, start(0), len);
+  const float scale2 = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);  // not zero: -inf stays what is masked
+  auto fetch = [&](int t) {
+    const int j0 = start(t);
+    Stage<E, D, KT>::load(Kt[t & 1], kb + j0 * p.k_stride, p.k_stride, len - j0);
+    Stage<E, D, KT>::load(Vt[t & 1], vb + j0 * p.v_stride, p.v_stride, len - j0);
+  };
+  fetch(0);
   for (int t = 0; t < tiles; ++t) {
     const int j0 = start(t);
-    __syncthreads();
-    sk.store(Ks);
-    sv.store(Vs);
-    __syncthreads();
-    if (t + 1 < tiles) {
-      sk.load(kb, p.k_stride, start(t + 1), len);
-      sv.load(vb, p.v_stride, start(t + 1), len);
-    }
+    const E* const Ks = Kt[t & 1];
+    const E* const Vs = Vt[t & 1];
+    landed();
+    __syncthreads();  // and the other buffer is read
+    if (t + 1 < tiles) fetch(t + 1);
     if (wq0 >= len || j0 > wq1 || (j0 + KT - 1 <= wq0 - p.W && j0 >= p.S)) continue;
     f32x4_t s[4][CT];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      s[b][0] = s[b][1] = zero4();
+#pragma unroll
+      for (int u = 0; u < CT; ++u) s[b][u] = zero4();
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         const u32x4_t a = read_row<Op, D>(Ks, 16 * b, n, lane);
@@ -88,46 +92,53 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
         for (int u = 0; u < CT; ++u) s[b][u] = Op::mma(a, qf[u][n], s[b][u]);
       }
     }
-    const bool whole = j0 + KT - 1 <= wq0 && j0 > wq1 - p.W;
+    if (!(j0 + KT - 1 <= wq0 && j0 > wq1 - p.W)) {
+      seldom();
+#pragma unroll
+      for (int u = 0; u < CT; ++u)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            s[b][u][r] = sees(wq0 + 16 * u + c, j0 + 16 * b + 4 * g + r, p.W, p.S) ? s[b][u][r] : -INFINITY;
+    }
+    float high[CT];
+    bool rise = false;
+#pragma unroll
+    for (int u = 0; u < CT; ++u) {
+      high[u] = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) high[u] = fmaxf(high[u], s[b][u][r]);
+      // a score may pass the base by 2^8 before all that has been summed is brought to a new
+      // one: powers of two change no rounding, and after a few tiles no base moves
+      rise |= high[u] * scale2 > top[u] + 8.f;
+    }
+    if (__any(rise)) {
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        float m = fmaxf(high[u], __shfl_xor(high[u], 16, 64));
+        m = fmaxf(m, __shfl_xor(m, 32, 64));
+        const float now = fmaxf(top[u], m * scale2);
+        const float fade = now == -INFINITY ? 1.f : exp2_(top[u] - now);
+        top[u] = now;
+        sum[u] *= fade;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d][u] *= fade;
+      }
+    }
     u32x4_t pf[NR][CT];
 #pragma unroll
     for (int u = 0; u < CT; ++u) {
-      float high = -INFINITY;
-      if (whole) {
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[b][u][r] *= scale2;
-            high = fmaxf(high, s[b][u][r]);
-          }
-      } else {
-        const int i = wq0 + 16 * u + c;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[b][u][r] = sees(i, j0 + 16 * b + 4 * g + r, p.W, p.S) ? s[b][u][r] * scale2 : -INFINITY;
-            high = fmaxf(high, s[b][u][r]);
-          }
-      }
-      high = fmaxf(high, __shfl_xor(high, 16, 64));
-      high = fmaxf(high, __shfl_xor(high, 32, 64));
-      const float now = fmaxf(top[u], high);
-      const float base = now == -INFINITY ? 0.f : now;  // nothing seen yet
-      const float fade = exp2_(top[u] - base);
-      top[u] = now;
-      float part = 0.f;
+      const float base = top[u] == -INFINITY ? 0.f : top[u];  // nothing seen yet
 #pragma unroll
       for (int b = 0; b < 4; ++b)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          s[b][u][r] = exp2_(s[b][u][r] - base);
-          part += s[b][u][r];
+          s[b][u][r] = exp2_(fmaf(s[b][u][r], scale2, -base));
+          sum[u] += s[b][u][r];
         }
-      sum[u] = fmaf(sum[u], fade, part);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d][u] *= fade;
     }
 #pragma unroll
     for (int n = 0; n < NR; ++n)

@@ -644,7 +644,7 @@ typedef enum gdn_rope_norm {
  *        ones; only with GDN_ROPE_RMS, else GDN_ERR_UNSUPPORTED)
  *   out: q_out, k_out, contiguous
  * 16-byte aligned but for inv_freq and positions (4 bytes); strides of whole 16 bytes
- * (GDN_ERR_ALIGN), at least Hq D and Hk D (GDN_ERR_SHAPE).  Supported: D in {64, 128, 256},
+ * (GDN_ERR_ALIGN), at least Hq D and Hk D (GDN_ERR_SHAPE), up to 2^21.  Supported: D in {64, 128, 256},
  * R a multiple of 16 up to D, Hq and Hk up to 4096, B T (Hq + Hk) < 2^31, else
  * GDN_ERR_UNSUPPORTED.  Angles are reduced in fp64 (2^-52 of the angle); all else is fp32,
  * squares included, and outputs are rounded once.  eps >= 0 and finite frequencies are
@@ -683,8 +683,8 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
  * (at least its own).  Query head h attends to key head h / (Hq / Hk).
  * Tensors: q, o, dout, dq [B,T,Hq,D], k, v, dk, dv [B,T,Hk,D] (io dtype), lse [B,T,Hq] fp32.
  * q, k and v may have their tokens q_stride, k_stride, v_stride values apart as in
- * gdn_rope_problem (0: contiguous); all else is contiguous.  16-byte aligned, lse and lens
- * 4-byte.  Supported: D in {64, 128}, Hq a multiple of Hk up to 4096, window >= 1 (as long as
+ * gdn_rope_problem (0: contiguous; up to 2^21); all else is contiguous.  16-byte aligned,
+ * lse and lens 4-byte.  Supported: D in {64, 128}, Hq a multiple of Hk up to 4096, window >= 1 (as long as
  * wanted), sinks up to 1024, B T up to 2^30, up to 65535 sequences, and fewer than 2^24
  * workgroups in a launch (one for 128 tokens of the longest sequence, every query head and
  * every sequence), else GDN_ERR_UNSUPPORTED.
