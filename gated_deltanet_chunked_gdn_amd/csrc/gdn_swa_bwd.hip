@@ -193,10 +193,10 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 // the waves hold the same 32 keys and take a step's queries of a tile each (32, fp32 16).  Else 32 keys a wave
 // and the queries whose window holds them.
 template <typename Op, int D, bool FAR>
-__global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items, int blocks) {
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dkv_kernel(SwaParams p, int items, int blocks) {
   using E = typename Op::elem;
   constexpr int CT = 2, KB = Op::kBlocks, NS = D / Op::kCols, ND = D / 16;
-  constexpr int QT = FAR ? 64 * KB : sizeof(E) == 2 ? 64 : 32;
+  constexpr int QT = FAR ? 64 * KB : 32, KT = FAR ? 32 : kSwaKeys;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int item = xcd_item(blockIdx.x, items);
@@ -218,20 +218,19 @@ __global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items,
     i1 = min(static_cast<int64_t>(len), static_cast<int64_t>(k0) + kSwaKeys - 1 + p.W) - 1;
   }
 
+  // the keys stay in LDS, the values in registers: both in registers would leave a SIMD one wave
+  __shared__ alignas(16) E Ks[KT * D];
   __shared__ alignas(16) E Qt[2][QT * D], Dt[2][QT * D];
   __shared__ alignas(16) float lt[2][QT], dt[2][QT];
 
-  u32x4_t kf[CT][NS], vf[CT][NS];
+  Stage<E, D, KT>::load(Ks, static_cast<const E*>(p.k) + (bos + k0) * p.k_stride + hk * D, p.k_stride, len - k0);
+  u32x4_t vf[CT][NS];
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
     const int j = min(wk0 + 16 * u + c, len - 1);
-    const E* const krow = static_cast<const E*>(p.k) + (bos + j) * p.k_stride + hk * D;
     const E* const vrow = static_cast<const E*>(p.v) + (bos + j) * p.v_stride + hk * D;
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-      kf[u][n] = load_row<Op>(krow, n, lane);
-      vf[u][n] = load_row<Op>(vrow, n, lane);
-    }
+    for (int n = 0; n < NS; ++n) vf[u][n] = load_row<Op>(vrow, n, lane);
   }
   f32x4_t ak[ND][CT], av[ND][CT];
 #pragma unroll
@@ -275,16 +274,21 @@ __global__ __launch_bounds__(256, 1) void swa_dkv_kernel(SwaParams p, int items,
       const bool whole = !FAR && first >= wk0 + 31 && end - wk0 < p.W && end < len && wk0 + 31 < len;
       f32x4_t s[KB][CT], dp[KB][CT];
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
+      for (int b = 0; b < KB; ++b)
 #pragma unroll
         for (int u = 0; u < CT; ++u) s[b][u] = dp[b][u] = zero4();
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
+      for (int n = 0; n < NS; ++n) {
+        u32x4_t kf[CT];
+#pragma unroll
+        for (int u = 0; u < CT; ++u) kf[u] = read_row<Op, D>(Ks, wk0 - k0 + 16 * u, n, lane);
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
           const u32x4_t qa = read_row<Op, D>(Qs, 16 * (b0 + b), n, lane);
           const u32x4_t da = read_row<Op, D>(Ds, 16 * (b0 + b), n, lane);
 #pragma unroll
           for (int u = 0; u < CT; ++u) {
-            s[b][u] = Op::mma(qa, kf[u][n], s[b][u]);
+            s[b][u] = Op::mma(qa, kf[u], s[b][u]);
             dp[b][u] = Op::mma(da, vf[u][n], dp[b][u]);
           }
         }

@@ -26,17 +26,22 @@ using chunk::u32x4_t;
 constexpr float kLog2e = chunk::kLog2e;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A tile of rows of D values in LDS.  The piece of 16 bytes u of row t stands at u ^ swizzle(t), which
-// spreads both ways of reading over the banks: 16 rows at one piece (eight at a time), and,
-// down the rows, four rows at two neighbouring pieces (bf16, a lane group) or 16 rows at
-// four (fp32).
+// A tile of rows of D values in LDS.  The piece of 16 bytes u of row t stands at u ^ swizzle(t).
+// LDS serves 256 bytes at a time.  Along rows those are 16 lanes' pieces, of rows 0-3 and
+// 12-15 from one lane group and 4-11 from the next; down the rows (bf16) two lane groups', of
+// rows 0-7 or 8-15 and two neighbouring pieces.  So the eight pairs of pieces go to rows 0-7
+// in order and again to rows 12-15 and 8-11 with the two swapped, which keeps both ways apart
+// (half as many pieces: rows two by two).  In fp32 four lane groups read one row each of
+// four, 16 bytes a lane's four: rows one piece apart.
 template <typename E, int D>
 struct Tile {
   static constexpr int kEpp = 16 / static_cast<int>(sizeof(E));  // values of a piece
   static constexpr int kPieces = D / kEpp;                       // pieces of a row: 8, 16 or 32
   static __device__ __forceinline__ int swizzle(int row) {
     if (sizeof(E) == 4) return row & 15;
-    return ((row & 3) << 1) | ((row >> 2) & 1) | (kPieces > 8 ? row & 8 : 0);
+    constexpr int half = kPieces / 2;
+    const int e = kPieces == 8 ? row >> 1 : row;
+    return (((e & (half - 1)) << 1) | ((e / half) & 1)) ^ (e & half);
   }
   static __device__ __forceinline__ int at(int row, int piece) { return row * D + ((piece ^ swizzle(row)) * kEpp); }
 };
