@@ -5,8 +5,8 @@
 //
 // A linear recurrence composes: a run of tokens takes h to A h + B, with A the product of
 // its decays and B its end from zero.  A workgroup holds 32 channels (rows of 64 or 128
-// bytes) and walks over its tokens in tiles; a thread takes a run of eight tokens of four
-// channels (two in the backward), so the tile's runs are composed by lane shifts inside a
+// bytes) and walks over its tokens in tiles; a thread takes a run of eight tokens of two or
+// four channels, so the tile's runs are composed by lane shifts inside a
 // wave and through LDS between waves, and the run is gone through once more from its own
 // start.  Inputs are read once, while the tile before is worked on.  Where the channels
 // alone are too few workgroups, sequences are cut into segments whose (A, B) come from a
@@ -40,6 +40,22 @@ struct Row {
   typedef uint32_t vec_t __attribute__((ext_vector_type(kWords)));
   vec_t w;
   __device__ __forceinline__ void load(const E* p) { w = *reinterpret_cast<const vec_t*>(p); }
+  // through a resource: zeros behind its end, and stores there are dropped
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t byte) {
+    if constexpr (kWords == 1)
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, byte, 0, 0);
+    else
+      w = __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b64(r, byte, 0, 0));
+  }
+  static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t byte, const float* f) {
+    vec_t v;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) v[i] = sizeof(E) == 2 ? pack_bf16x2(f[2 * i], f[2 * i + 1]) : __float_as_uint(f[i]);
+    if constexpr (kWords == 1)
+      __builtin_amdgcn_raw_buffer_store_b32(v[0], r, byte, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(chunk::u32x2v_t, v), r, byte, 0, 0);
+  }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (sizeof(E) == 2) {
       const uint32_t x = w[e >> 1];
@@ -80,19 +96,13 @@ __device__ __forceinline__ float rate_(float lam, float c) {
   return -c * softplus_(lam, sig) * kLog2e;
 }
 
-// m^2 = 1 - a^2 = -expm1(2 la).  Near la = 0 the difference loses what matters: the series
-// of expm1 there (nine terms: below 2^-28 of the sum for |2 la| <= 1/2).
+// m^2 = 1 - a^2 = 2 a sinh(-la).  Near la = 0 the difference loses what matters, and the
+// series of sinh is short (four terms: the fifth is below 2^-26 of the sum for -la <= 1/2);
+// beyond, 1 - a^2 is 0.63 and more.
 __device__ __forceinline__ float one_minus_square(float la2, float a) {
-  const float x = la2 * (2.f * kLn2);
-  float s = fmaf(x, 1.f / 362880.f, 1.f / 40320.f);
-  s = fmaf(x, s, 1.f / 5040.f);
-  s = fmaf(x, s, 1.f / 720.f);
-  s = fmaf(x, s, 1.f / 120.f);
-  s = fmaf(x, s, 1.f / 24.f);
-  s = fmaf(x, s, 1.f / 6.f);
-  s = fmaf(x, s, 0.5f);
-  s = fmaf(x, s, 1.f);
-  return x > -0.5f ? -x * s : fmaf(-a, a, 1.f);
+  const float x = la2 * -kLn2, y = x * x;
+  const float s = fmaf(y, fmaf(y, fmaf(y, 2.f / 5040.f, 2.f / 120.f), 2.f / 6.f), 2.f);
+  return x < 0.5f ? a * x * s : fmaf(-a, a, 1.f);
 }
 __device__ __forceinline__ float root_(float x) { return __builtin_amdgcn_sqrtf(x); }
 
@@ -116,23 +126,15 @@ struct Place {
   __device__ __forceinline__ int token() const { return (wave * kRuns + run) * kRun; }
 };
 
-// A thread's run in a tile that starts `left` tokens before the segment's end: offsets in
-// values from the tile's first row, where tokens behind the end read the last one, and how
-// many of its tokens there are.  32 bits hold 512 rows of 2^20 values.
-struct Run {
-  uint32_t first, last, step;
-  int count;
-  __device__ __forceinline__ Run(int token, int64_t left, int C) {
-    const int rows = static_cast<int>(min(left, static_cast<int64_t>(512)));
-    step = C;
-    first = static_cast<uint32_t>(token) * C;
-    last = static_cast<uint32_t>(rows - 1) * C;
-    count = rows - token;
-  }
-  __device__ __forceinline__ uint32_t read(int j) const { return min(first + j * step, last); }
-  __device__ __forceinline__ uint32_t write(int j) const { return first + j * step; }
-  __device__ __forceinline__ bool has(int j) const { return j < count; }
-};
+// A tile's rows of one tensor, as a resource that ends with the segment, which is `left` rows
+// off: at most 2^30 bytes (512 rows of bf16 or 256 of fp32, of 2^20 values).
+template <typename E, int ROWS>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_of(const void* base, int64_t row, int64_t left, int C) {
+  static_assert(ROWS * sizeof(E) <= 1024, "2^30 bytes");
+  const int64_t rows = min(left, static_cast<int64_t>(ROWS));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(static_cast<const E*>(base) + row * C), 0,
+                                           static_cast<int>(static_cast<uint32_t>(rows) * C * sizeof(E)), 0x00020000);
+}
 
 // (A, B) of the runs before this lane's in the wave, (1, 0) in front of the first; `A`, `B`
 // become the wave's up to and with this lane.
@@ -182,8 +184,8 @@ __device__ __forceinline__ void scan_runs_back(float* A, float* B, float* eA, fl
 
 // ---------------------------------------------------------------------------- forward
 
-// SUM: the segments' (A, B) alone.
-template <typename E, int V, int NW, bool SUM>
+// Z: there is a gate.  SUM: the segments' (A, B) alone.
+template <typename E, int V, int NW, bool Z, bool SUM>
 __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles) {
   using P = Place<V, NW>;
   const P at;
@@ -220,46 +222,59 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles
     }
   }
 
+  // offset of this thread's run in a tile; of channels behind the last, behind every tile's end
+  const uint32_t step = static_cast<uint32_t>(p.C) * sizeof(E);
+  const uint32_t first = chan ? static_cast<uint32_t>(at.token()) * step + static_cast<uint32_t>(d * sizeof(E)) : 0x7ffffff0u - kRun * step;
   Row<E, V> rx[kRun], rr[kRun], ri[kRun], rz[kRun];
   auto fetch = [&](int64_t t0) {
-    const Run run(at.token(), t_end - t0, p.C);
-    const int64_t base = (bos + t0) * p.C;
-    const E* const x = static_cast<const E*>(p.x) + base;
-    const E* const r = static_cast<const E*>(p.r) + base;
-    const E* const gi = static_cast<const E*>(p.i) + base;
+    const __amdgpu_buffer_rsrc_t x = tile_of<E, P::kTokens>(p.x, bos + t0, t_end - t0, p.C), r = tile_of<E, P::kTokens>(p.r, bos + t0, t_end - t0, p.C),
+                                 gi = tile_of<E, P::kTokens>(p.i, bos + t0, t_end - t0, p.C);
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const uint32_t o = run.read(j) + d;
-      rx[j].load(x + o);
-      rr[j].load(r + o);
-      ri[j].load(gi + o);
+      rr[j].load(r, first + j * step);
+      ri[j].load(gi, first + j * step);
+      rx[j].load(x, first + j * step);
+    }
+    if constexpr (Z) {
+      const __amdgpu_buffer_rsrc_t z = tile_of<E, P::kTokens>(p.z, bos + t0, t_end - t0, p.C);
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) rz[j].load(z, first + j * step);
     }
   };
-  if (t_begin < t_end) fetch(t_begin);
+  // The pass for the sums goes from the segment's end to its start, so that the cache that all
+  // XCDs share holds the first of what the next pass reads.
+  const int64_t count = (t_end - t_begin + P::kTokens - 1) / P::kTokens;
+  if (count > 0) fetch(SUM ? t_begin + (count - 1) * P::kTokens : t_begin);
   int buf = 0;
-  for (int64_t t0 = t_begin; t0 < t_end; t0 += P::kTokens, buf ^= 1) {
-    const Run run(at.token(), t_end - t0, p.C);
-    const int64_t base = (bos + t0) * p.C;
+  for (int64_t k = 0; k < count; ++k, buf ^= 1) {
+    const int64_t t0 = t_begin + (SUM ? count - 1 - k : k) * P::kTokens;
+    const int have = static_cast<int>(min(t_end - t0, static_cast<int64_t>(512))) - at.token();  // tokens of the run and behind it
+    Row<E, V> cx[kRun], cr[kRun], ci[kRun], cz[kRun];
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      cx[j] = rx[j];
+      cr[j] = rr[j];
+      ci[j] = ri[j];
+      if constexpr (Z) cz[j] = rz[j];
+    }
+    if (k + 1 < count) fetch(SUM ? t0 - P::kTokens : t0 + P::kTokens);
     float a[kRun][V], b[kRun][V];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const bool ok = run.has(j);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float la2 = rate[e] * sigmoid_(rr[j].get(e));
+        const float la2 = rate[e] * sigmoid_(cr[j].get(e));
         const float decay = exp2_(la2);
-        const float w = root_(one_minus_square(la2, decay)) * sigmoid_(ri[j].get(e)) * rx[j].get(e);
-        // behind the end a token changes nothing
-        a[j][e] = ok ? decay : 1.f;
-        b[j][e] = ok ? w : 0.f;
+        a[j][e] = decay;
+        b[j][e] = root_(one_minus_square(la2, decay)) * sigmoid_(ci[j].get(e)) * cx[j].get(e);
       }
     }
-    if (!SUM && p.z) {
-      const E* const z = static_cast<const E*>(p.z) + base;
+    if (t_end - t0 < P::kTokens) {  // behind the end a token changes nothing (b is zero, as x there)
 #pragma unroll
-      for (int j = 0; j < kRun; ++j) rz[j].load(z + (run.read(j) + d));
+      for (int j = 0; j < kRun; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[j][e] = j < have ? a[j][e] : 1.f;
     }
-    if (t0 + P::kTokens < t_end) fetch(t0 + P::kTokens);
     float A[V], B[V], eA[V], eB[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -272,7 +287,7 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles
       }
     }
     scan_runs<V, P::kLanes>(A, B, eA, eB, at.lane);
-    float start[V];
+    float start[V], tile_a[V], tile_b[V];
     if constexpr (NW > 1) {
       if (at.run == P::kRuns - 1) {
         Row<float, V>::store(&pair[buf][at.wave][0][at.ch], A);
@@ -290,8 +305,12 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles
         load_f32<V>(&pair[buf][w][1][at.ch], true, wb);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          carry[e] = fmaf(wa[e], carry[e], wb[e]);
-          if (SUM) prod[e] *= wa[e];
+          if (SUM) {
+            tile_b[e] = w == 0 ? wb[e] : fmaf(wa[e], tile_b[e], wb[e]);
+            tile_a[e] = w == 0 ? wa[e] : tile_a[e] * wa[e];
+          } else {
+            carry[e] = fmaf(wa[e], carry[e], wb[e]);
+          }
         }
       }
     } else {
@@ -300,17 +319,25 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles
         start[e] = carry[e];
         const int last = (P::kRuns - 1) * P::kLanes + at.lane % P::kLanes;
         const float wa = __shfl(A[e], last, 64), wb = __shfl(B[e], last, 64);
-        carry[e] = fmaf(wa, carry[e], wb);
-        if (SUM) prod[e] *= wa;
+        tile_a[e] = wa;
+        tile_b[e] = wb;
+        if (!SUM) carry[e] = fmaf(wa, carry[e], wb);
+      }
+    }
+    if (SUM) {  // in front of the tiles so far
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        carry[e] = fmaf(prod[e], tile_b[e], carry[e]);
+        prod[e] *= tile_a[e];
       }
     }
     if constexpr (!SUM) {
       float h[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) h[e] = fmaf(eA[e], start[e], eB[e]);
-      if (p.saved && chan && run.has(0))
+      if (p.saved && chan && have > 0)
         Row<float, V>::store(p.saved + (bos / kRun + n + (t0 + at.token()) / kRun) * p.C + d, h);
-      E* const y = static_cast<E*>(p.y) + base;
+      const __amdgpu_buffer_rsrc_t y = tile_of<E, P::kTokens>(p.y, bos + t0, t_end - t0, p.C);
 #pragma unroll
       for (int j = 0; j < kRun; ++j) {
         float out[V];
@@ -318,12 +345,12 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles
         for (int e = 0; e < V; ++e) {
           h[e] = fmaf(a[j][e], h[e], b[j][e]);
           out[e] = h[e];
-          if (p.z) {
-            const float g = rz[j].get(e);
+          if constexpr (Z) {
+            const float g = cz[j].get(e);
             out[e] = h[e] * (g * sigmoid_(g));
           }
         }
-        if (chan && run.has(j)) Row<E, V>::store(y + (run.write(j) + d), out);
+        Row<E, V>::store(y, first + j * step, out);
       }
     }
   }
@@ -339,8 +366,8 @@ __global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles
 
 // ---------------------------------------------------------------------------- backward
 
-// SUM: the segments' (A, B) of K alone.
-template <typename E, int V, int NW, bool SUM>
+// Z: there is a gate.  SUM: the segments' (A, B) of K alone.
+template <typename E, int V, int NW, bool Z, bool SUM>
 __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles) {
   using P = Place<V, NW>;
   const P at;
@@ -377,52 +404,83 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles
     }
   }
 
-  const int64_t tiles_t = (t_end - t_begin + P::kTokens - 1) / P::kTokens;
-  int buf = 0;
-  for (int64_t tt = tiles_t - 1; tt >= 0; --tt, buf ^= 1) {
-    const int64_t t0 = t_begin + tt * P::kTokens, base = (bos + t0) * p.C;
-    const Run run(at.token(), t_end - t0, p.C);
-    const E* const x = static_cast<const E*>(p.x) + base;
-    const E* const r = static_cast<const E*>(p.r) + base;
-    const E* const gi = static_cast<const E*>(p.i) + base;
-    const E* const z = static_cast<const E*>(p.z) + base;
-    const E* const dy = static_cast<const E*>(p.dy) + base;
-    Row<E, V> rx[kRun], rr[kRun], ri[kRun], rz[kRun], rd[kRun];
+  const uint32_t step = static_cast<uint32_t>(p.C) * sizeof(E);
+  const uint32_t first = chan ? static_cast<uint32_t>(at.token()) * step + static_cast<uint32_t>(d * sizeof(E)) : 0x7ffffff0u - kRun * step;
+  // fp32 leaves no registers for a tile ahead
+  constexpr bool kAhead = SUM || sizeof(E) == 2;
+  Row<E, V> rx[kRun], rr[kRun], ri[kRun], rz[kRun], rd[kRun];
+  Row<float, V> rh;
+  auto fetch = [&](int64_t t0) {
+    const __amdgpu_buffer_rsrc_t r = tile_of<E, P::kTokens>(p.r, bos + t0, t_end - t0, p.C), dy = tile_of<E, P::kTokens>(p.dy, bos + t0, t_end - t0, p.C);
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const uint32_t o = run.read(j) + d;
-      rr[j].load(r + o);
-      rd[j].load(dy + o);
-      if (p.z) rz[j].load(z + o);
-      if constexpr (!SUM) {
-        rx[j].load(x + o);
-        ri[j].load(gi + o);
-      }
+      rr[j].load(r, first + j * step);
+      rd[j].load(dy, first + j * step);
     }
+    if constexpr (Z) {
+      const __amdgpu_buffer_rsrc_t z = tile_of<E, P::kTokens>(p.z, bos + t0, t_end - t0, p.C);
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) rz[j].load(z, first + j * step);
+    }
+    if constexpr (!SUM) {
+      const __amdgpu_buffer_rsrc_t x = tile_of<E, P::kTokens>(p.x, bos + t0, t_end - t0, p.C), gi = tile_of<E, P::kTokens>(p.i, bos + t0, t_end - t0, p.C);
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) {
+        rx[j].load(x, first + j * step);
+        ri[j].load(gi, first + j * step);
+      }
+      rh.load(p.saved + (bos / kRun + n + min(t0 + at.token(), t_end - 1) / kRun) * p.C + d);
+    }
+  };
+  // The pass for the sums goes from the segment's start to its end, as the next does not.
+  const int64_t count = (t_end - t_begin + P::kTokens - 1) / P::kTokens;
+  if (kAhead && count > 0) fetch(SUM ? t_begin : t_begin + (count - 1) * P::kTokens);
+  int buf = 0;
+  for (int64_t k = 0; k < count; ++k, buf ^= 1) {
+    const int64_t t0 = t_begin + (SUM ? k : count - 1 - k) * P::kTokens;
+    const int have = static_cast<int>(min(t_end - t0, static_cast<int64_t>(512))) - at.token();
+    if (!kAhead) fetch(t0);
+    Row<E, V> cx[kRun], cr[kRun], ci[kRun], cz[kRun], cd[kRun];
     float h[V];
-    if constexpr (!SUM)
-      load_f32<V>(p.saved + (bos / kRun + n + min(t0 + at.token(), t_end - 1) / kRun) * p.C + d, true, h);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) {
+      cx[j] = rx[j];
+      cr[j] = rr[j];
+      ci[j] = ri[j];
+      if constexpr (Z) cz[j] = rz[j];
+      cd[j] = rd[j];
+    }
+    if constexpr (!SUM) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) h[e] = rh.get(e);
+    }
+    if (kAhead && k + 1 < count) fetch(SUM ? t0 + P::kTokens : t0 - P::kTokens);
     float a[kRun][V], before[kRun][V], ds[kRun][V];
     float A[V], B[V], eA[V], eB[V];
 #pragma unroll
     for (int j = 0; j < kRun; ++j) {
-      const bool ok = run.has(j);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float la2 = rate[e] * sigmoid_(rr[j].get(e));
+        const float la2 = rate[e] * sigmoid_(cr[j].get(e));
         const float decay = exp2_(la2);
-        a[j][e] = ok ? decay : 1.f;
-        float g = rd[j].get(e);
-        if (p.z) {
-          const float zz = rz[j].get(e);
+        a[j][e] = decay;
+        float g = cd[j].get(e);
+        if constexpr (Z) {
+          const float zz = cz[j].get(e);
           g *= zz * sigmoid_(zz);
         }
-        ds[j][e] = ok ? g : 0.f;
+        ds[j][e] = g;
         if constexpr (!SUM) {
           before[j][e] = h[e];
-          h[e] = fmaf(decay, h[e], root_(one_minus_square(la2, decay)) * sigmoid_(ri[j].get(e)) * rx[j].get(e));
+          h[e] = fmaf(decay, h[e], root_(one_minus_square(la2, decay)) * sigmoid_(ci[j].get(e)) * cx[j].get(e));
         }
       }
+    }
+    if (t_end - t0 < P::kTokens) {  // behind the end a token changes nothing (ds is zero, as dy there)
+#pragma unroll
+      for (int j = 0; j < kRun; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) a[j][e] = j < have ? a[j][e] : 1.f;
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -435,7 +493,7 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles
       }
     }
     scan_runs_back<V, P::kLanes>(A, B, eA, eB, at.lane);
-    float start[V];
+    float start[V], tile_a[V], tile_b[V];
     if constexpr (NW > 1) {
       if (at.run == 0) {
         Row<float, V>::store(&pair[buf][at.wave][0][at.ch], A);
@@ -453,8 +511,12 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles
         load_f32<V>(&pair[buf][w][1][at.ch], true, wb);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          carry[e] = fmaf(wa[e], carry[e], wb[e]);
-          if (SUM) prod[e] *= wa[e];
+          if (SUM) {
+            tile_b[e] = w == NW - 1 ? wb[e] : fmaf(wa[e], tile_b[e], wb[e]);
+            tile_a[e] = w == NW - 1 ? wa[e] : tile_a[e] * wa[e];
+          } else {
+            carry[e] = fmaf(wa[e], carry[e], wb[e]);
+          }
         }
       }
     } else {
@@ -462,28 +524,37 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles
       for (int e = 0; e < V; ++e) {
         start[e] = carry[e];
         const float wa = __shfl(A[e], at.lane % P::kLanes, 64), wb = __shfl(B[e], at.lane % P::kLanes, 64);
-        carry[e] = fmaf(wa, carry[e], wb);
-        if (SUM) prod[e] *= wa;
+        tile_a[e] = wa;
+        tile_b[e] = wb;
+        if (!SUM) carry[e] = fmaf(wa, carry[e], wb);
+      }
+    }
+    if (SUM) {  // behind the tiles so far
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        carry[e] = fmaf(prod[e], tile_b[e], carry[e]);
+        prod[e] *= tile_a[e];
       }
     }
     if constexpr (!SUM) {
       float K[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) K[e] = fmaf(eA[e], start[e], eB[e]);
+      const __amdgpu_buffer_rsrc_t bx = tile_of<E, P::kTokens>(p.dx, bos + t0, t_end - t0, p.C), br = tile_of<E, P::kTokens>(p.dr, bos + t0, t_end - t0, p.C),
+                                   bi = tile_of<E, P::kTokens>(p.di, bos + t0, t_end - t0, p.C);
 #pragma unroll
       for (int j = kRun - 1; j >= 0; --j) {
-        const bool ok = run.has(j);
-        rr[j].forget();
-        ri[j].forget();
-        rx[j].forget();
-        if (p.z) {
-          rz[j].forget();
-          rd[j].forget();
+        cr[j].forget();
+        ci[j].forget();
+        cx[j].forget();
+        if constexpr (Z) {
+          cz[j].forget();
+          cd[j].forget();
         }
         float ox[V], orr[V], oi[V], oz[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float sr = sigmoid_(rr[j].get(e)), si = sigmoid_(ri[j].get(e)), xv = rx[j].get(e);
+          const float sr = sigmoid_(cr[j].get(e)), si = sigmoid_(ci[j].get(e)), xv = cx[j].get(e);
           const float la2 = rate[e] * sr, la = la2 * kLn2;
           const float decay = a[j][e], m = root_(one_minus_square(la2, decay));
           const float G = ds[j][e] + K[e];
@@ -493,20 +564,17 @@ __global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles
           ox[e] = G * m * si;
           orr[e] = E1 * (1.f - sr);
           oi[e] = G * m * six * (1.f - si);
-          if (p.z) {
-            const float zz = rz[j].get(e), sz = sigmoid_(zz);
+          if constexpr (Z) {
+            const float zz = cz[j].get(e), sz = sigmoid_(zz);
             const float hn = fmaf(decay, hp, m * six);
-            oz[e] = rd[j].get(e) * hn * sz * (1.f + zz * (1.f - sz));
+            oz[e] = cd[j].get(e) * hn * sz * (1.f + zz * (1.f - sz));
           }
-          if (ok) total[e] += E1;
+          total[e] += j < have ? E1 : 0.f;
         }
-        if (chan && ok) {
-          const uint32_t o = run.write(j) + d;
-          Row<E, V>::store(static_cast<E*>(p.dx) + base + o, ox);
-          Row<E, V>::store(static_cast<E*>(p.dr) + base + o, orr);
-          Row<E, V>::store(static_cast<E*>(p.di) + base + o, oi);
-          if (p.dz) Row<E, V>::store(static_cast<E*>(p.dz) + base + o, oz);
-        }
+        Row<E, V>::store(bx, first + j * step, ox);
+        Row<E, V>::store(br, first + j * step, orr);
+        Row<E, V>::store(bi, first + j * step, oi);
+        if (Z && p.dz) Row<E, V>::store(tile_of<E, P::kTokens>(p.dz, bos + t0, t_end - t0, p.C), first + j * step, oz);
       }
     }
   }
@@ -596,39 +664,49 @@ dim3 grid_of(const GlrParams& p, int tiles) {
   return dim3(static_cast<unsigned>((tiles + 7) / 8 * 8), static_cast<unsigned>(p.N), static_cast<unsigned>(p.segs));
 }
 
-template <typename E, int NW>
-hipError_t fwd(const GlrParams& p, hipStream_t s) {
+template <typename E, int NW, bool Z>
+void fwd(const GlrParams& p, hipStream_t s) {
+  constexpr int V = glr_vec(false, sizeof(E) == 2);
   const int tiles = glr_tiles(p.C);
-  if (p.segs > 1) hipLaunchKernelGGL((glr_fwd_kernel<E, 4, NW, true>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-  hipLaunchKernelGGL((glr_fwd_kernel<E, 4, NW, false>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
+  if (p.segs > 1) hipLaunchKernelGGL((glr_fwd_kernel<E, V, NW, false, true>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
+  hipLaunchKernelGGL((glr_fwd_kernel<E, V, NW, Z, false>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
+}
+
+template <typename E, int NW, bool Z>
+void bwd(const GlrParams& p, hipStream_t s) {
+  constexpr int V = glr_vec(true, sizeof(E) == 2);
+  const int tiles = glr_tiles(p.C);
+  if (p.segs > 1) hipLaunchKernelGGL((glr_bwd_kernel<E, V, NW, Z, true>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
+  if (p.N > 0) hipLaunchKernelGGL((glr_bwd_kernel<E, V, NW, Z, false>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
+  hipLaunchKernelGGL(glr_lam_kernel, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(256), 0, s, p);
+}
+
+template <typename E, int NW, bool BWD>
+hipError_t launch(const GlrParams& p, hipStream_t s) {
+  if constexpr (BWD)
+    p.z ? bwd<E, NW, true>(p, s) : bwd<E, NW, false>(p, s);
+  else
+    p.z ? fwd<E, NW, true>(p, s) : fwd<E, NW, false>(p, s);
   return hipGetLastError();
 }
 
-template <typename E, int NW>
-hipError_t bwd(const GlrParams& p, hipStream_t s) {
-  const int tiles = glr_tiles(p.C);
-  if (p.segs > 1) hipLaunchKernelGGL((glr_bwd_kernel<E, 2, NW, true>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-  if (p.N > 0) hipLaunchKernelGGL((glr_bwd_kernel<E, 2, NW, false>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-  hipLaunchKernelGGL(glr_lam_kernel, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(256), 0, s, p);
-  return hipGetLastError();
+template <typename E, bool BWD>
+hipError_t launch_waves(const GlrParams& p, hipStream_t s) {
+  switch (p.waves) {
+    case 1: return launch<E, 1, BWD>(p, s);
+    case 4: return launch<E, 4, BWD>(p, s);
+    default: return launch<E, 8, BWD>(p, s);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_glr_fwd(const GlrParams& p, bool bf16, hipStream_t s) {
-  switch (p.waves) {
-    case 1: return bf16 ? fwd<uint16_t, 1>(p, s) : fwd<float, 1>(p, s);
-    case 4: return bf16 ? fwd<uint16_t, 4>(p, s) : fwd<float, 4>(p, s);
-    default: return bf16 ? fwd<uint16_t, 8>(p, s) : fwd<float, 8>(p, s);
-  }
+  return bf16 ? launch_waves<uint16_t, false>(p, s) : launch_waves<float, false>(p, s);
 }
 
 hipError_t launch_glr_bwd(const GlrParams& p, bool bf16, hipStream_t s) {
-  switch (p.waves) {
-    case 1: return bf16 ? bwd<uint16_t, 1>(p, s) : bwd<float, 1>(p, s);
-    case 4: return bf16 ? bwd<uint16_t, 4>(p, s) : bwd<float, 4>(p, s);
-    default: return bf16 ? bwd<uint16_t, 8>(p, s) : bwd<float, 8>(p, s);
-  }
+  return bf16 ? launch_waves<uint16_t, true>(p, s) : launch_waves<float, true>(p, s);
 }
 
 hipError_t launch_glr_step(const GlrParams& p, bool bf16, hipStream_t s) {

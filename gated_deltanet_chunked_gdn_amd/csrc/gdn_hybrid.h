@@ -44,6 +44,10 @@ struct GlrParams {
 
 constexpr int kGlrRun = 8;    // tokens that a thread takes one after another
 constexpr int kGlrTile = 32;  // channels of a workgroup
+// Channels of a lane: 8 bytes, in the backward 4 (bf16) or 8.
+constexpr int glr_vec(bool bwd, bool bf16) { return bf16 && !bwd ? 4 : 2; }
+// Tokens of a wave: its 64 lanes over those of a row, a run each.
+constexpr int glr_wave_tokens(bool bwd, bool bf16) { return 64 / (kGlrTile / glr_vec(bwd, bf16)) * kGlrRun; }
 inline int glr_tiles(int C) { return (C + kGlrTile - 1) / kGlrTile; }
 // Run c of a sequence that starts at row bos uses slot bos / run + n + c (distinct).
 inline int64_t glr_slots(int64_t rows, int64_t n) { return rows / kGlrRun + n + 1; }
@@ -103,12 +107,14 @@ struct SwaParams {
   void* dv;
   float* delta;        // backward: [rows][Hq] sums of dout o
   float* first_win;    // backward: [N][Hk][S][2][D] the first tokens' dk, dv from inside the window
-  float* first_far;    // backward: [slot][4][Hk][S][2][D] those from queries further on, by runs of them
+  float* first_far;    // backward: [slot][Hk][S][2][D] those from queries further on, by runs of them
   int64_t q_stride, k_stride, v_stride;
   SeqInfo seq;
   int32_t N, Hq, Hk;
   int32_t W, S;        // W at most the longest sequence; S 0 where no window leaves a token behind
   int32_t max_len;
+  int32_t few;         // blocks of 128 queries are too few workgroups
+  int32_t few_keys;    // blocks of 128 keys are
   float scale;
   // cache
   void* kc;            // [N][slots][Hk][D]
@@ -121,7 +127,7 @@ struct SwaParams {
 };
 constexpr int kSwaQueries = 128;  // queries of a workgroup
 constexpr int kSwaKeys = 128;     // keys of a workgroup of the backward
-constexpr int kSwaFar = 512;      // queries of a run for the first tokens' gradients
+constexpr int kSwaFar = 256;      // queries of a run for the first tokens' gradients
 // Run c of a sequence that starts at row bos uses slot bos / kSwaFar + n + c (distinct).
 inline int64_t swa_far_slots(int64_t rows, int64_t n) { return rows / kSwaFar + n; }
 hipError_t launch_swa_fwd(const SwaParams& p, int D, bool bf16, hipStream_t s);

@@ -26,10 +26,6 @@ struct GlrSize {
   int32_t segs = 1, waves = 1;
 };
 
-// Tokens of a wave: 64 lanes over the lanes of a row (eight in the forward, of four channels;
-// sixteen in the backward, of two), eight tokens each.
-constexpr int64_t kFwdWave = 64, kBwdWave = 32;
-
 gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
   if (!p) return GDN_ERR_NULL;
   if (p->io_dtype != GDN_FP32 && p->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
@@ -46,7 +42,7 @@ gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
   c->state = static_cast<size_t>(p->num_seqs) * c->chan;
   c->saved = static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs)) * c->chan;
   // A tile as long as the longest sequence needs, up to eight waves.
-  const int64_t wave = bwd ? kBwdWave : kFwdWave;
+  const int64_t wave = gdn::glr_wave_tokens(bwd, c->io == 2);
   c->waves = max_len <= wave ? 1 : max_len <= 4 * wave ? 4 : 8;
   // Segments where the channels leave CUs idle, of two tiles at least.
   const int64_t tile = wave * c->waves, tiles = gdn::glr_tiles(p->C);
@@ -157,7 +153,7 @@ struct SwaSize {
   size_t io = 0, qin = 0, kin = 0, vin = 0, q = 0, k = 0, lse = 0, cache = 0, lens = 0;
   size_t delta = 0, win = 0, far = 0, step = 0;
   int64_t rows = 0, q_stride = 0, k_stride = 0, v_stride = 0;
-  int32_t W = 0, S = 0, max_len = 0, splits = 1, run = 0;
+  int32_t W = 0, S = 0, max_len = 0, few = 0, few_keys = 0, splits = 1, run = 0;
 };
 
 gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
@@ -190,13 +186,18 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   c->delta = up256(c->lse);
   const size_t first = static_cast<size_t>(p->Hk) * c->S * 2 * p->D * 4;
   c->win = up256(p->num_seqs * first);
-  c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs)) * 4 * first;
+  c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs)) * first;
+  // Blocks of half as many queries, or of a quarter as many keys, where whole ones are fewer
+  // than two a CU (packed sequences of other lengths count as so many of the rows).
+  const int64_t whole = c->rows / gdn::kSwaQueries;
+  c->few = whole * p->Hq < 512;
+  c->few_keys = whole * p->Hk < 512;
   // Workgroups of 256 threads, counted in 32 bits: blocks of queries of every query head (the
   // backward's blocks of keys are as long), rounded up to eight.
-  const int64_t blocks = (max_len + gdn::kSwaQueries - 1) / gdn::kSwaQueries;
+  const int64_t blocks = (max_len + 31) / 32;
   if ((blocks * p->Hq + 7) / 8 * 8 * p->num_seqs >= 1 << 24) return GDN_ERR_UNSUPPORTED;
   const int64_t runs = (max_len + gdn::kSwaFar - 1) / gdn::kSwaFar;
-  if ((runs * p->Hk + 7) / 8 * 8 * p->num_seqs * ((c->S + 31) / 32) >= 1 << 24 || static_cast<int64_t>(c->S) * p->Hk * p->num_seqs >= 1 << 24)
+  if ((runs * p->Hk + 7) / 8 * 8 * p->num_seqs * ((c->S + 15) / 16) >= 1 << 24 || static_cast<int64_t>(c->S) * p->Hk * p->num_seqs >= 1 << 24)
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
@@ -228,6 +229,7 @@ gdn::SwaParams swa_params(const gdn_swa_problem* p, const SwaSize& c, const void
   sp.q_stride = c.q_stride; sp.k_stride = c.k_stride; sp.v_stride = c.v_stride;
   sp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
   sp.N = p->num_seqs; sp.Hq = p->Hq; sp.Hk = p->Hk; sp.W = c.W; sp.S = c.S; sp.max_len = c.max_len;
+  sp.few = c.few; sp.few_keys = c.few_keys;
   sp.scale = p->scale;
   return sp;
 }

@@ -10,8 +10,8 @@
 //     of its key head; here the scores stand with queries down the accumulator, a key a
 //     lane, which makes P and dS the operands of the sums over queries.
 // The first tokens are seen by all later queries too: a few keys with long sums.  Their
-// part from behind the window is summed by runs of 512 queries (the same kernel, its four
-// waves sharing the keys and parting the queries) and joined in order by a last kernel.
+// part from behind the window is summed by runs of queries (the same kernel, its four waves
+// sharing the keys and parting the queries) and joined in order by a last kernel.
 #include <hip/hip_runtime.h>
 
 #include "gdn_swa_device.h"
@@ -23,10 +23,11 @@ using namespace swa;
 
 // ---------------------------------------------------------------------------- dq
 
-template <typename Op, int D>
+// CT: 16-query columns of a wave, as in the forward.
+template <typename Op, int D, int CT>
 __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
   using E = typename Op::elem;
-  constexpr int CT = 2, KT = 64, NS = D / Op::kCols, ND = D / 16, KB = Op::kBlocks;
+  constexpr int KT = 64, QB = 64 * CT, NS = D / Op::kCols, ND = D / 16, KB = Op::kBlocks;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int item = xcd_item(blockIdx.x, items);
@@ -35,12 +36,12 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   const int block = rest / group, h = hk * group + rest - block * group;
   int64_t bos, len64;
   chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64), q0 = block * kSwaQueries;
+  const int len = static_cast<int>(len64), q0 = block * QB;
   if (q0 >= len) return;
 
   __shared__ alignas(16) E Kt[2][KT * D], Vt[2][KT * D];
 
-  const int wq0 = q0 + 32 * wave, wq1 = min(wq0 + 31, len - 1);
+  const int wq0 = q0 + 16 * CT * wave, wq1 = min(wq0 + 16 * CT - 1, len - 1);
   u32x4_t qf[CT][NS], df[CT][NS];
   float lse2[CT], delta[CT];
 #pragma unroll
@@ -73,7 +74,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   }
   const E* const kb = static_cast<const E*>(p.k) + bos * p.k_stride + hk * D;
   const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
-  const int win = max(0, q0 - p.W + 1) / KT * KT, last = min(q0 + kSwaQueries, len) - 1;
+  const int win = max(0, q0 - p.W + 1) / KT * KT, last = min(q0 + QB, len) - 1;
   const int nfirst = (min(p.S, win) + KT - 1) / KT, tiles = nfirst + (last - win) / KT + 1;
   auto start = [&](int t) { return t < nfirst ? t * KT : win + (t - nfirst) * KT; };
 
@@ -189,14 +190,19 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 
 // ---------------------------------------------------------------------------- dk, dv
 
-// FAR: the first tokens' sums over the queries of a run whose window has left them behind;
-// the waves hold the same 32 keys and take a step's queries of a tile each (32, fp32 16).  Else 32 keys a wave
-// and the queries whose window holds them.
-template <typename Op, int D, bool FAR>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dkv_kernel(SwaParams p, int items, int blocks) {
+// What a workgroup's waves hold.
+enum Form {
+  kKeys,    // 32 keys each, of the queries whose window holds them
+  kShared,  // the same 32 keys, and parted queries: where the blocks of 128 keys leave CUs without work
+  kFar      // the same 16 first tokens, and parted queries of a run whose window has left them behind
+};
+
+template <typename Op, int D, Form FORM>
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || FORM == kKeys) ? 2 : 1) void swa_dkv_kernel(SwaParams p, int items, int blocks) {
   using E = typename Op::elem;
-  constexpr int CT = 2, KB = Op::kBlocks, NS = D / Op::kCols, ND = D / 16;
-  constexpr int QT = FAR ? 64 * KB : 32, KT = FAR ? 32 : kSwaKeys;
+  constexpr bool FAR = FORM == kFar, PART = FORM != kKeys;  // PART: each wave takes a step of a tile's queries
+  constexpr int CT = FAR ? 1 : 2, KW = 16 * CT, KT = PART ? KW : 4 * KW;  // keys of a wave, of the workgroup
+  constexpr int KB = Op::kBlocks, NS = D / Op::kCols, ND = D / 16, QT = PART ? 64 * KB : 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int item = xcd_item(blockIdx.x, items);
@@ -205,7 +211,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   int64_t bos, len64;
   chunk::seq_range(p.seq, blockIdx.y, bos, len64);
   const int len = static_cast<int>(len64);
-  const int k0 = FAR ? 32 * blockIdx.z : block * kSwaKeys, wk0 = FAR ? k0 : k0 + 32 * wave;
+  const int k0 = FAR ? KT * blockIdx.z : block * KT, wk0 = PART ? k0 : k0 + KW * wave;
   if (k0 >= len || (FAR && len <= p.W)) return;
   // queries i0 .. i1
   int i0, i1;
@@ -215,12 +221,12 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     if (i1 < k0 + p.W) return;  // none of them is so far behind
   } else {
     i0 = k0;
-    i1 = min(static_cast<int64_t>(len), static_cast<int64_t>(k0) + kSwaKeys - 1 + p.W) - 1;
+    i1 = min(static_cast<int64_t>(len), static_cast<int64_t>(k0) + KT - 1 + p.W) - 1;
   }
 
   // the keys stay in LDS, the values in registers: both in registers would leave a SIMD one wave
   __shared__ alignas(16) E Ks[KT * D];
-  __shared__ alignas(16) E Qt[2][QT * D], Dt[2][QT * D];
+  __shared__ alignas(16) E raw[2][2][QT * D];  // two tiles of queries and of do
   __shared__ alignas(16) float lt[2][QT], dt[2][QT];
 
   Stage<E, D, KT>::load(Ks, static_cast<const E*>(p.k) + (bos + k0) * p.k_stride + hk * D, p.k_stride, len - k0);
@@ -243,8 +249,8 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   float rl = 0.f, rd = 0.f;
   auto fetch = [&](int step) {
     const int h = hk * group + step / tiles, row = i0 + (step % tiles) * QT;
-    Stage<E, D, QT>::load(Qt[step & 1], static_cast<const E*>(p.q) + (bos + row) * p.q_stride + h * D, p.q_stride, len - row);
-    Stage<E, D, QT>::load(Dt[step & 1], static_cast<const E*>(p.dout) + ((bos + row) * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, len - row);
+    Stage<E, D, QT>::load(raw[step & 1][0], static_cast<const E*>(p.q) + (bos + row) * p.q_stride + h * D, p.q_stride, len - row);
+    Stage<E, D, QT>::load(raw[step & 1][1], static_cast<const E*>(p.dout) + ((bos + row) * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, len - row);
     if (threadIdx.x < QT) {
       const int64_t at = (bos + min(row + static_cast<int>(threadIdx.x), len - 1)) * p.Hq + h;
       rl = p.lse[at] * kLog2e;
@@ -254,8 +260,8 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   fetch(0);
   for (int step = 0; step < steps; ++step) {
     const int r0 = i0 + (step % tiles) * QT;
-    const E* const Qs = Qt[step & 1];
-    const E* const Ds = Dt[step & 1];
+    const E* const Qs = raw[step & 1][0];
+    const E* const Ds = raw[step & 1][1];
     const float* const ls = lt[step & 1];
     const float* const dl = dt[step & 1];
     landed();
@@ -266,12 +272,12 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     __syncthreads();  // and the other buffer is read
     if (step + 1 < steps) fetch(step + 1);
 #pragma unroll
-    for (int b1 = 0; b1 < (FAR ? KB : QT / 16); b1 += KB) {
-      const int b0 = FAR ? KB * wave : b1;
+    for (int b1 = 0; b1 < (PART ? KB : QT / 16); b1 += KB) {
+      const int b0 = PART ? KB * wave : b1;
       const int first = r0 + 16 * b0, end = first + 16 * KB - 1;
       // no query here sees a key of this wave's
-      if (wk0 >= len || first >= len || (FAR ? end < wk0 + p.W : end < wk0 || first - (wk0 + 31) >= p.W)) continue;
-      const bool whole = !FAR && first >= wk0 + 31 && end - wk0 < p.W && end < len && wk0 + 31 < len;
+      if (wk0 >= len || first >= len || (FAR ? end < wk0 + p.W : end < wk0 || first - (wk0 + KW - 1) >= p.W)) continue;
+      const bool whole = !FAR && first >= wk0 + KW - 1 && end - wk0 < p.W && end < len && wk0 + KW - 1 < len;
       f32x4_t s[KB][CT], dp[KB][CT];
 #pragma unroll
       for (int b = 0; b < KB; ++b)
@@ -340,6 +346,32 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
       }
     }
   }
+  if constexpr (PART) {
+    // the waves' sums, added in order in LDS and taken over by the first; a lane's values
+    // side by side, 16 bytes a lane
+    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(&raw[0][0][0]) + lane;
+    static_assert(sizeof(raw) >= 2 * ND * CT * 64 * sizeof(f32x4_t), "room for a wave's sums");
+    for (int w = 3; w >= 0; --w) {
+      __syncthreads();
+      if (wave != w) continue;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          f32x4_t* const k4 = sums + (2 * (d * CT + u)) * 64;
+          f32x4_t* const v4 = k4 + 64;
+          if (w < 3) {
+            ak[d][u] += *k4;
+            av[d][u] += *v4;
+          }
+          if (w > 0) {
+            *k4 = ak[d][u];
+            *v4 = av[d][u];
+          }
+        }
+    }
+    if (wave) return;
+  }
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
     const int j = wk0 + 16 * u + c;
@@ -348,7 +380,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     if (FAR) {
       if (j >= p.S) continue;
       const int64_t slot = bos / kSwaFar + blockIdx.y + block;
-      part = p.first_far + (((slot * 4 + wave) * p.Hk + hk) * p.S + j) * 2 * D;
+      part = p.first_far + ((slot * p.Hk + hk) * p.S + j) * 2 * D;
     } else if (j < p.S && len > p.W) {
       part = p.first_win + ((static_cast<int64_t>(blockIdx.y) * p.Hk + hk) * p.S + j) * 2 * D;
     }
@@ -379,12 +411,9 @@ __global__ __launch_bounds__(2 * D) void swa_first_kernel(SwaParams p) {
   if (len <= p.W || j >= len) return;
   float sum = p.first_win[((static_cast<int64_t>(n) * p.Hk + hk) * p.S + j) * 2 * D + x];
   const int64_t slot = bos / kSwaFar + n, runs = (len + kSwaFar - 1) / kSwaFar;
-  // as in the kernel above: the keys' block of 32 says which runs were formed
-  for (int64_t r = 0; r < runs; ++r) {
-    if (min((r + 1) * kSwaFar, len) - 1 < (j / 32 * 32) + p.W) continue;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) sum += p.first_far[((((slot + r) * 4 + w) * p.Hk + hk) * p.S + j) * 2 * D + x];
-  }
+  // as in the kernel above: the keys' block of 16 says which runs were formed
+  for (int64_t r = 0; r < runs; ++r)
+    if (min((r + 1) * kSwaFar, len) - 1 >= (j & ~15) + p.W) sum += p.first_far[(((slot + r) * p.Hk + hk) * p.S + j) * 2 * D + x];
   const int64_t at = ((bos + j) * p.Hk + hk) * D;
   if (x < D)
     IoT<E>::st(static_cast<E*>(p.dk) + at + x, sum * p.scale);
@@ -394,19 +423,25 @@ __global__ __launch_bounds__(2 * D) void swa_first_kernel(SwaParams p) {
 
 unsigned of8(int items) { return static_cast<unsigned>((items + 7) / 8 * 8); }
 
-template <typename Op, int D>
-hipError_t launch_t(const SwaParams& p, hipStream_t s) {
+template <typename Op, int D, int CT, Form FORM>
+hipError_t launch_c(const SwaParams& p, hipStream_t s) {
   const unsigned N = static_cast<unsigned>(p.N);
-  const int qblocks = (p.max_len + kSwaQueries - 1) / kSwaQueries, qitems = p.Hq * qblocks;
-  hipLaunchKernelGGL((swa_dq_kernel<Op, D>), dim3(of8(qitems), N), dim3(256), 0, s, p, qitems, qblocks);
-  const int kblocks = (p.max_len + kSwaKeys - 1) / kSwaKeys, kitems = p.Hk * kblocks;
-  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, false>), dim3(of8(kitems), N), dim3(256), 0, s, p, kitems, kblocks);
+  const int qblocks = (p.max_len + 64 * CT - 1) / (64 * CT), qitems = p.Hq * qblocks;
+  hipLaunchKernelGGL((swa_dq_kernel<Op, D, CT>), dim3(of8(qitems), N), dim3(256), 0, s, p, qitems, qblocks);
+  constexpr int keys = FORM == kKeys ? kSwaKeys : 32;
+  const int kblocks = (p.max_len + keys - 1) / keys, kitems = p.Hk * kblocks;
+  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, FORM>), dim3(of8(kitems), N), dim3(256), 0, s, p, kitems, kblocks);
   if (p.S > 0) {
     const int runs = (p.max_len + kSwaFar - 1) / kSwaFar, items = p.Hk * runs;
-    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, true>), dim3(of8(items), N, static_cast<unsigned>((p.S + 31) / 32)), dim3(256), 0, s, p, items, runs);
+    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, kFar>), dim3(of8(items), N, static_cast<unsigned>((p.S + 15) / 16)), dim3(256), 0, s, p, items, runs);
     hipLaunchKernelGGL((swa_first_kernel<typename Op::elem, D>), dim3(static_cast<unsigned>(p.S * p.Hk), N), dim3(2 * D), 0, s, p);
   }
   return hipGetLastError();
+}
+template <typename Op, int D>
+hipError_t launch_t(const SwaParams& p, hipStream_t s) {
+  if (p.few) return launch_c<Op, D, 1, kShared>(p, s);  // keys are fewer still
+  return p.few_keys ? launch_c<Op, D, 2, kShared>(p, s) : launch_c<Op, D, 2, kKeys>(p, s);
 }
 
 }  // namespace

@@ -114,7 +114,7 @@ template <typename E, int D, int ROWS>
 struct Stage {
   using T = Tile<E, D>;
   static constexpr int kRows = 64 / T::kPieces;      // rows of a wave's load
-  static constexpr int kN = ROWS / (4 * kRows);      // loads of a wave
+  static constexpr int kN = (ROWS + 4 * kRows - 1) / (4 * kRows);  // loads of a wave
   // `rows` rows (any number; those of the tile count) from `base` on, `stride` values apart
   static __device__ __forceinline__ void load(E* tile, const E* base, int64_t stride, int rows) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -126,6 +126,7 @@ struct Stage {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int first = (4 * i + wave) * kRows, row = first + lane / T::kPieces;
+      if (ROWS % (4 * kRows) && first >= ROWS) break;  // fewer rows than four waves take
       const int off = row * step + ((lane % T::kPieces) ^ T::swizzle(row)) * 16;
       const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(tile + first * D)));
       // In assembly, since the compiler would wait for the next tile's loads before it reads this

@@ -2,7 +2,8 @@
 // gfx950:  o_i = sum_j p_ij v_j,  p_i = softmax over the visible j of scale q_i . k_j.
 //
 // One pass over the keys that a block of queries sees, with the running maximum and sum of
-// the softmax (in base 2, fp32).  A workgroup holds 128 queries of a head, 32 a wave; keys
+// the softmax (in base 2, fp32).  A workgroup holds 128 queries of a head, 32 a wave (half
+// as many where that leaves CUs without work); keys
 // and values come in tiles of 64 rows through LDS, loaded while the tile before is worked
 // on.  Scores are formed transposed (keys down the accumulator, a query a lane), so the
 // softmax runs inside lanes but for two exchanges of the maximum, and the probabilities are
@@ -17,10 +18,11 @@ namespace {
 
 using namespace swa;
 
-template <typename Op, int D>
+// CT: 16-query columns of a wave, two or, where that leaves CUs without work, one.
+template <typename Op, int D, int CT>
 __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int blocks) {
   using E = typename Op::elem;
-  constexpr int CT = 2, KT = 64, NS = D / Op::kCols, NR = 4 / Op::kBlocks, ND = D / 16;
+  constexpr int KT = 64, QB = 64 * CT, NS = D / Op::kCols, NR = 4 / Op::kBlocks, ND = D / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int item = xcd_item(blockIdx.x, items);
@@ -30,12 +32,12 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   const int block = rest / group, h = hk * group + rest - block * group;
   int64_t bos, len64;
   chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64), q0 = block * kSwaQueries;
+  const int len = static_cast<int>(len64), q0 = block * QB;
   if (q0 >= len) return;
 
   __shared__ alignas(16) E Kt[2][KT * D], Vt[2][KT * D];
 
-  const int wq0 = q0 + 32 * wave, wq1 = min(wq0 + 31, len - 1);  // this wave's queries; none if wq0 >= len
+  const int wq0 = q0 + 16 * CT * wave, wq1 = min(wq0 + 16 * CT - 1, len - 1);  // this wave's queries; none if wq0 >= len
   u32x4_t qf[CT][NS];
 #pragma unroll
   for (int t = 0; t < CT; ++t) {
@@ -52,7 +54,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
 
   // tiles: the first tokens' as far as they lie before the window's, then the window's
-  const int win = max(0, q0 - p.W + 1) / KT * KT, last = min(q0 + kSwaQueries, len) - 1;
+  const int win = max(0, q0 - p.W + 1) / KT * KT, last = min(q0 + QB, len) - 1;
   const int nfirst = (min(p.S, win) + KT - 1) / KT, tiles = nfirst + (last - win) / KT + 1;
   auto start = [&](int t) { return t < nfirst ? t * KT : win + (t - nfirst) * KT; };
 
@@ -172,12 +174,16 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   }
 }
 
-template <typename Op, int D>
-hipError_t launch_t(const SwaParams& p, hipStream_t s) {
-  const int blocks = (p.max_len + kSwaQueries - 1) / kSwaQueries, items = p.Hq * blocks;
-  hipLaunchKernelGGL((swa_fwd_kernel<Op, D>), dim3(static_cast<unsigned>((items + 7) / 8 * 8), static_cast<unsigned>(p.N)), dim3(256), 0, s, p,
+template <typename Op, int D, int CT>
+hipError_t launch_c(const SwaParams& p, hipStream_t s) {
+  const int blocks = (p.max_len + 64 * CT - 1) / (64 * CT), items = p.Hq * blocks;
+  hipLaunchKernelGGL((swa_fwd_kernel<Op, D, CT>), dim3(static_cast<unsigned>((items + 7) / 8 * 8), static_cast<unsigned>(p.N)), dim3(256), 0, s, p,
                      items, blocks);
   return hipGetLastError();
+}
+template <typename Op, int D>
+hipError_t launch_t(const SwaParams& p, hipStream_t s) {
+  return p.few ? launch_c<Op, D, 1>(p, s) : launch_c<Op, D, 2>(p, s);
 }
 
 }  // namespace

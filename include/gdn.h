@@ -686,7 +686,7 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
  * gdn_rope_problem (0: contiguous; up to 2^21); all else is contiguous.  16-byte aligned,
  * lse and lens 4-byte.  Supported: D in {64, 128}, Hq a multiple of Hk up to 4096, window >= 1 (as long as
  * wanted), sinks up to 1024, B T up to 2^30, up to 65535 sequences, and fewer than 2^24
- * workgroups in a launch (one for 128 tokens of the longest sequence, every query head and
+ * workgroups in a launch (counted as one for 32 tokens of the longest sequence, every query head and
  * every sequence), else GDN_ERR_UNSUPPORTED.
  * Scores, sums and statistics of the softmax are fp32; with bf16 io the probabilities and
  * the scores' gradients are rounded to bf16 as operands of the products that sum over them.
