@@ -4,13 +4,22 @@
 //   h <- a h + m sigmoid(i_t) x_t;  y_t = h  or  h silu(z_t)
 //
 // A linear recurrence composes: a run of tokens takes h to A h + B, with A the product of
-// its decays and B its end from zero.  A workgroup holds 32 channels (rows of 64 or 128
-// bytes) and walks over its tokens in tiles; a thread takes a run of eight tokens of two or
-// four channels, so the tile's runs are composed by lane shifts inside a
-// wave and through LDS between waves, and the run is gone through once more from its own
-// start.  Inputs are read once, while the tile before is worked on.  Where the channels
-// alone are too few workgroups, sequences are cut into segments whose (A, B) come from a
-// pass of their own, over the inputs once more.
+// its decays and B its end from zero.  A workgroup holds a segment of 64 channels (rows of
+// 128 or 256 bytes; at 64 bytes the same loads took a third longer) in registers, runs of eight tokens a
+// thread: it forms every run's (A, B), composes them by lane shifts inside a wave and through
+// LDS between waves, learns the state in front of the segment, and goes through the runs once
+// more.  So all is read once, and the segments of a sequence work at the same time.
+//
+// The state in front comes from the other segments.  Each gives out its (A, B) as soon as it
+// has them.  Sixteen segments are a group: a segment composes those of its group before it,
+// all loaded at once, onto the group's start, and the group's last one gives out the next
+// group's.  The order of every composition is fixed, whoever comes first, so results are
+// bit-identical from call to call.  The words that pass carry a mark beside the value and are
+// single 64-bit stores and loads of device scope, so a value cannot be taken before it is
+// there, and nothing else need be ordered.  Segments are counted off as workgroups start,
+// earlier ones of a sequence first, so a workgroup waits only for others that already run and
+// wait for none behind it: the first that has not ended never waits.  The wait is bounded all
+// the same (a state of NaN follows, for calls that share a workspace against the rules).
 //
 // Backward.  With K_t = dL/dh_t through the later tokens and ds_t = dL/dh_t through y_t,
 //   G_t = ds_t + K_t;  K_{t-1} = a_t G_t
@@ -44,8 +53,10 @@ struct Row {
   __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t byte) {
     if constexpr (kWords == 1)
       w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, byte, 0, 0);
-    else
+    else if constexpr (kWords == 2)
       w = __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b64(r, byte, 0, 0));
+    else
+      w = __builtin_bit_cast(vec_t, __builtin_amdgcn_raw_buffer_load_b128(r, byte, 0, 0));
   }
   static __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t byte, const float* f) {
     vec_t v;
@@ -53,8 +64,10 @@ struct Row {
     for (int i = 0; i < kWords; ++i) v[i] = sizeof(E) == 2 ? pack_bf16x2(f[2 * i], f[2 * i + 1]) : __float_as_uint(f[i]);
     if constexpr (kWords == 1)
       __builtin_amdgcn_raw_buffer_store_b32(v[0], r, byte, 0, 0);
-    else
+    else if constexpr (kWords == 2)
       __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(chunk::u32x2v_t, v), r, byte, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(chunk::u32x4v_t, v), r, byte, 0, 0);
   }
   __device__ __forceinline__ float get(int e) const {
     if constexpr (sizeof(E) == 2) {
@@ -106,34 +119,108 @@ __device__ __forceinline__ float one_minus_square(float la2, float a) {
 }
 __device__ __forceinline__ float root_(float x) { return __builtin_amdgcn_sqrtf(x); }
 
-// Tile of 8 XCDs in turn: workgroups x, x + 8, ... share one, so neighbouring channels,
-// which share cache lines, go to one L2.
-__device__ __forceinline__ int xcd_tile(int x, int tiles) { return (x & 7) * ((tiles + 7) / 8) + (x >> 3); }
+// A tile's rows of one tensor, as a resource that ends with the segment, which is `left` rows
+// off: at most 2^29 bytes (128 rows of 2^20 values).
+template <typename E, int ROWS>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_of(const void* base, int64_t row, int64_t left, int C) {
+  static_assert(ROWS <= 128, "2^29 bytes");
+  const int64_t rows = min(left, static_cast<int64_t>(ROWS));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(static_cast<const E*>(base) + row * C), 0,
+                                           static_cast<int>(static_cast<uint32_t>(rows) * C * sizeof(E)), 0x00020000);
+}
 
-// Where a workgroup's thread stands: lanes of a row, runs of a wave, its own run.
-template <int V, int NW>
+// What a workgroup works on, and where its threads stand in it.
+template <int V>
 struct Place {
-  static constexpr int kLanes = kGlrTile / V;       // lanes of a row
-  static constexpr int kRuns = 64 / kLanes;         // runs of a wave
-  static constexpr int kTokens = kRuns * kRun * NW; // tokens of a tile
-  int lane, wave, run, ch;                          // ch: first channel in the tile's 32
-  __device__ __forceinline__ Place() {
+  static constexpr int kLanes = kGlrTile / V;                  // lanes of a row
+  static constexpr int kRuns = 64 / kLanes;                    // runs of a wave
+  static constexpr int kTokens = kRuns * kRun * kGlrWaves;     // of a segment
+  int lane, wave, run, ch;  // ch: first channel in the tile's 64
+  int n, seg, segs;         // sequence, segment (from its start), its segments
+  int64_t bos, len, t0;     // t0: the segment's first token
+  int64_t slot;
+  int tile;
+  bool live;
+  __device__ __forceinline__ int token() const { return (wave * kRuns + run) * kRun; }
+  // `index` counts workgroups; `back`: later segments of a sequence come first
+  __device__ __forceinline__ Place(const GlrParams& p, int64_t index, int tiles, bool back) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     run = lane / kLanes;
     ch = (lane % kLanes) * V;
+    slot = index / tiles;
+    tile = static_cast<int>(index - slot * tiles);
+    if (back) slot = p.slots - 1 - slot;
+    // the sequence whose slots hold this one: the last that starts at or before it
+    int lo = 0, hi = p.N;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start(p, mid) <= slot)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    n = lo;
+    chunk::seq_range(p.seq, n, bos, len);
+    seg = static_cast<int>(slot - start(p, n));
+    segs = static_cast<int>(max((len + kTokens - 1) / kTokens, static_cast<int64_t>(1)));
+    t0 = static_cast<int64_t>(seg) * kTokens;
+    live = seg < segs;  // an empty sequence has one segment, of no tokens
   }
-  __device__ __forceinline__ int token() const { return (wave * kRuns + run) * kRun; }
+  static __device__ __forceinline__ int64_t start(const GlrParams& p, int n) {
+    const int64_t bos = p.seq.cu ? p.seq.cu[n] : static_cast<int64_t>(n) * p.seq.T;
+    return bos / kTokens + n;
+  }
 };
 
-// A tile's rows of one tensor, as a resource that ends with the segment, which is `left` rows
-// off: at most 2^30 bytes (512 rows of bf16 or 256 of fp32, of 2^20 values).
-template <typename E, int ROWS>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_of(const void* base, int64_t row, int64_t left, int C) {
-  static_assert(ROWS * sizeof(E) <= 1024, "2^30 bytes");
-  const int64_t rows = min(left, static_cast<int64_t>(ROWS));
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(static_cast<const E*>(base) + row * C), 0,
-                                           static_cast<int>(static_cast<uint32_t>(rows) * C * sizeof(E)), 0x00020000);
+// The workgroup's number: in the order in which they start where they wait for each other.
+__device__ __forceinline__ int64_t number(const GlrParams& p) {
+  if (!p.chained) return blockIdx.x;
+  __shared__ uint32_t mine;
+  if (threadIdx.x == 0)
+    mine = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(p.chain), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(mine);
+}
+
+// A value given out with its mark, V channels of them.
+template <int V>
+__device__ __forceinline__ void give(uint64_t* to, const float* f) {
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    __hip_atomic_store(to + e, (UINT64_C(1) << 32) | __float_as_uint(f[e]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Waits until all lanes of the wave have theirs; lanes without one (`want` false) keep f.
+template <int V, int COUNT>
+__device__ __forceinline__ void take(const uint64_t* const* from, bool want, float (*f)[V]) {
+  uint64_t w[COUNT][V];
+  for (int tries = 0;; ++tries) {
+    bool there = true;
+    if (want) {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          w[i][e] = __hip_atomic_load(from[i] + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          there &= (w[i][e] >> 32) != 0;
+        }
+    }
+    if (__all(there)) break;
+    if (tries >= 1 << 20) {  // about a second: whoever should give it shares its workspace with another call
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[i][e] = 0x7fc00000u;
+      break;
+    }
+    __builtin_amdgcn_s_sleep(2);
+  }
+  if (want) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[i][e] = __uint_as_float(static_cast<uint32_t>(w[i][e]));
+  }
 }
 
 // (A, B) of the runs before this lane's in the wave, (1, 0) in front of the first; `A`, `B`
@@ -182,427 +269,388 @@ __device__ __forceinline__ void scan_runs_back(float* A, float* B, float* eA, fl
   }
 }
 
+// (A, B) of a wave's runs by wave, in LDS; and of the segments before, by wave.
+struct Shared {
+  alignas(16) float wave[kGlrWaves][2][kGlrTile];
+  alignas(16) float before[kGlrWaves][2][kGlrTile];
+  alignas(16) float start[kGlrTile];
+};
+
+// The state in front of the segment, for this thread's channels: `carry` holds the sequence's
+// own (the first group's start), `a`, `b` the segment's (A, B).  `place` counts segments in the
+// direction of the walk.  Called by the whole workgroup.
+template <int V>
+__device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Place<V>& at, int place, int64_t first_slot, int dir,
+                                       int64_t group_slot, int d, bool chan, const float* a, const float* b, float* carry) {
+  using P = Place<V>;
+  const int group = place / kGlrGroup, index = place % kGlrGroup;
+  const bool lead = threadIdx.x < P::kLanes && chan;
+  if (place + 1 < at.segs && index + 1 < kGlrGroup && lead) {
+    uint64_t* const to = p.whole + (first_slot + dir * place) * 2 * p.C + d;
+    give<V>(to, a);
+    give<V>(to + p.C, b);
+  }
+  if (place == 0) return;
+  // The other segments of the group, one for every run of the workgroup's lanes; what is
+  // beyond those of the runs comes in turns.
+  constexpr int kAtOnce = P::kRuns * kGlrWaves;
+  float ca[V], cb[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    ca[e] = 1.f;
+    cb[e] = 0.f;
+  }
+  constexpr int kTurns = (kGlrGroup + kAtOnce - 1) / kAtOnce;
+  // consecutive segments a lane
+#pragma unroll
+  for (int turn = 0; turn < kTurns; ++turn) {
+    const int k = (at.wave * P::kRuns + at.run) * kTurns + turn;
+    float f[2][V];
+    const bool want = k < index;
+    const uint64_t* const from = p.whole + (first_slot + dir * (group * kGlrGroup + (want ? k : 0))) * 2 * p.C + d;
+    const uint64_t* const words[2] = {from, from + p.C};
+    take<V, 2>(words, want, f);
+    if (want) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        cb[e] = fmaf(f[0][e], cb[e], f[1][e]);
+        ca[e] *= f[0][e];
+      }
+    }
+  }
+  // the wave's, in order of its runs
+#pragma unroll
+  for (int off = P::kLanes; off < 64; off <<= 1) {
+    const bool later = at.lane & off;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float oa = __shfl_xor(ca[e], off, 64), ob = __shfl_xor(cb[e], off, 64);
+      cb[e] = later ? fmaf(ca[e], ob, cb[e]) : fmaf(oa, cb[e], ob);
+      ca[e] *= oa;
+    }
+  }
+  if (at.run == 0) {
+    Row<float, V>::store(&sh.before[at.wave][0][at.ch], ca);
+    Row<float, V>::store(&sh.before[at.wave][1][at.ch], cb);
+  }
+  if (group > 0 && at.wave == 0) {
+    float f[1][V];
+    const uint64_t* const words[1] = {p.end + (group_slot + group - 1) * p.C + d};
+    take<V, 1>(words, true, f);
+    if (at.run == 0) Row<float, V>::store(&sh.start[at.ch], f[0]);
+  }
+  __syncthreads();
+  if (group > 0) load_f32<V>(&sh.start[at.ch], true, carry);
+#pragma unroll
+  for (int w = 0; w < kGlrWaves; ++w) {
+    float wa[V], wb[V];
+    load_f32<V>(&sh.before[w][0][at.ch], true, wa);
+    load_f32<V>(&sh.before[w][1][at.ch], true, wb);
+#pragma unroll
+    for (int e = 0; e < V; ++e) carry[e] = fmaf(wa[e], carry[e], wb[e]);
+  }
+  if (index + 1 == kGlrGroup && place + 1 < at.segs && lead) {
+    float f[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = fmaf(a[e], carry[e], b[e]);
+    give<V>(p.end + (group_slot + group) * p.C + d, f);
+  }
+}
+
 // ---------------------------------------------------------------------------- forward
 
-// Z: there is a gate.  SUM: the segments' (A, B) alone.
-template <typename E, int V, int NW, bool Z, bool SUM>
-__global__ __launch_bounds__(64 * NW) void glr_fwd_kernel(GlrParams p, int tiles) {
-  using P = Place<V, NW>;
-  const P at;
-  const int tile = xcd_tile(blockIdx.x, tiles);
-  if (tile >= tiles) return;
-  const int n = blockIdx.y, s = blockIdx.z;
-  int64_t bos, len;
-  chunk::seq_range(p.seq, n, bos, len);
-  const int64_t t_begin = s * p.seg_len, t_end = min(len, t_begin + p.seg_len);
-  // a segment that starts behind its sequence has nothing to do (the first keeps an empty
-  // sequence's state), and nothing follows the last one that needs its (A, B)
-  if (s > 0 && t_begin >= len) return;
-  if (SUM && t_begin + p.seg_len >= len) return;
-  const bool chan = tile * kGlrTile + at.ch < p.C;  // whole vectors: C is a multiple of 8
-  const int d = chan ? tile * kGlrTile + at.ch : 0;
-  __shared__ alignas(16) float pair[2][NW][2][kGlrTile];
+// Z: there is a gate.
+template <typename E, int V, bool Z>
+__global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_fwd_kernel(GlrParams p, int tiles) {
+  using P = Place<V>;
+  const P at(p, number(p), tiles, false);
+  if (!at.live) return;
+  const bool chan = at.tile * kGlrTile + at.ch < p.C;  // whole vectors: C is a multiple of 8
+  const int d = chan ? at.tile * kGlrTile + at.ch : 0;
+  const int64_t row = at.bos + at.t0, left = at.len - at.t0;
+  const int have = static_cast<int>(min(left, static_cast<int64_t>(P::kTokens))) - at.token();  // tokens of the run and behind it
+  // offset of this thread's run; of channels behind the last, behind every tile's end
+  const uint32_t step = static_cast<uint32_t>(p.C) * sizeof(E);
+  const uint32_t first = chan ? static_cast<uint32_t>(at.token()) * step + static_cast<uint32_t>(d * sizeof(E)) : 0x7ffffff0u - kRun * step;
+  __shared__ Shared sh;
 
+  Row<E, V> rx[kRun], rr[kRun], ri[kRun], rz[kRun];
+  {
+    const __amdgpu_buffer_rsrc_t x = tile_of<E, P::kTokens>(p.x, row, left, p.C), r = tile_of<E, P::kTokens>(p.r, row, left, p.C),
+                                 gi = tile_of<E, P::kTokens>(p.i, row, left, p.C);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) rr[j].load(r, first + j * step);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) ri[j].load(gi, first + j * step);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) rx[j].load(x, first + j * step);
+    if constexpr (Z) {
+      const __amdgpu_buffer_rsrc_t z = tile_of<E, P::kTokens>(p.z, row, left, p.C);
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) rz[j].load(z, first + j * step);
+    }
+  }
   float rate[V], carry[V];
   load_f32<V>(p.lam + d, true, rate);
 #pragma unroll
   for (int e = 0; e < V; ++e) rate[e] = rate_(rate[e], p.c);
-  load_f32<V>(p.h0 + static_cast<int64_t>(n) * p.C + d, p.h0 != nullptr && !SUM, carry);
-  const int64_t slot = bos / p.seg_len + n;
-  float prod[V];  // SUM: the product of all decays so far
-#pragma unroll
-  for (int e = 0; e < V; ++e) prod[e] = 1.f;
-  if (!SUM) {
-    for (int j = 0; j < s; ++j) {
-      float a[V], b[V];
-      load_f32<V>(p.seg + (slot + j) * 2 * p.C + d, true, a);
-      load_f32<V>(p.seg + ((slot + j) * 2 + 1) * p.C + d, true, b);
-#pragma unroll
-      for (int e = 0; e < V; ++e) carry[e] = fmaf(a[e], carry[e], b[e]);
-    }
-  }
+  load_f32<V>(p.h0 + static_cast<int64_t>(at.n) * p.C + d, p.h0 != nullptr, carry);
 
-  // offset of this thread's run in a tile; of channels behind the last, behind every tile's end
-  const uint32_t step = static_cast<uint32_t>(p.C) * sizeof(E);
-  const uint32_t first = chan ? static_cast<uint32_t>(at.token()) * step + static_cast<uint32_t>(d * sizeof(E)) : 0x7ffffff0u - kRun * step;
-  Row<E, V> rx[kRun], rr[kRun], ri[kRun], rz[kRun];
-  auto fetch = [&](int64_t t0) {
-    const __amdgpu_buffer_rsrc_t x = tile_of<E, P::kTokens>(p.x, bos + t0, t_end - t0, p.C), r = tile_of<E, P::kTokens>(p.r, bos + t0, t_end - t0, p.C),
-                                 gi = tile_of<E, P::kTokens>(p.i, bos + t0, t_end - t0, p.C);
+  float a[kRun][V], b[kRun][V];
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      rr[j].load(r, first + j * step);
-      ri[j].load(gi, first + j * step);
-      rx[j].load(x, first + j * step);
-    }
-    if constexpr (Z) {
-      const __amdgpu_buffer_rsrc_t z = tile_of<E, P::kTokens>(p.z, bos + t0, t_end - t0, p.C);
-#pragma unroll
-      for (int j = 0; j < kRun; ++j) rz[j].load(z, first + j * step);
-    }
-  };
-  // The pass for the sums goes from the segment's end to its start, so that the cache that all
-  // XCDs share holds the first of what the next pass reads.
-  const int64_t count = (t_end - t_begin + P::kTokens - 1) / P::kTokens;
-  if (count > 0) fetch(SUM ? t_begin + (count - 1) * P::kTokens : t_begin);
-  int buf = 0;
-  for (int64_t k = 0; k < count; ++k, buf ^= 1) {
-    const int64_t t0 = t_begin + (SUM ? count - 1 - k : k) * P::kTokens;
-    const int have = static_cast<int>(min(t_end - t0, static_cast<int64_t>(512))) - at.token();  // tokens of the run and behind it
-    Row<E, V> cx[kRun], cr[kRun], ci[kRun], cz[kRun];
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      cx[j] = rx[j];
-      cr[j] = rr[j];
-      ci[j] = ri[j];
-      if constexpr (Z) cz[j] = rz[j];
-    }
-    if (k + 1 < count) fetch(SUM ? t0 - P::kTokens : t0 + P::kTokens);
-    float a[kRun][V], b[kRun][V];
-#pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float la2 = rate[e] * sigmoid_(cr[j].get(e));
-        const float decay = exp2_(la2);
-        a[j][e] = decay;
-        b[j][e] = root_(one_minus_square(la2, decay)) * sigmoid_(ci[j].get(e)) * cx[j].get(e);
-      }
-    }
-    if (t_end - t0 < P::kTokens) {  // behind the end a token changes nothing (b is zero, as x there)
-#pragma unroll
-      for (int j = 0; j < kRun; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) a[j][e] = j < have ? a[j][e] : 1.f;
-    }
-    float A[V], B[V], eA[V], eB[V];
+  for (int j = 0; j < kRun; ++j) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      A[e] = a[0][e];
-      B[e] = b[0][e];
-#pragma unroll
-      for (int j = 1; j < kRun; ++j) {
-        B[e] = fmaf(a[j][e], B[e], b[j][e]);
-        A[e] *= a[j][e];
-      }
-    }
-    scan_runs<V, P::kLanes>(A, B, eA, eB, at.lane);
-    float start[V], tile_a[V], tile_b[V];
-    if constexpr (NW > 1) {
-      if (at.run == P::kRuns - 1) {
-        Row<float, V>::store(&pair[buf][at.wave][0][at.ch], A);
-        Row<float, V>::store(&pair[buf][at.wave][1][at.ch], B);
-      }
-      __syncthreads();  // the other buffer is written behind the next one
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        if (w == at.wave) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) start[e] = carry[e];
-        }
-        float wa[V], wb[V];
-        load_f32<V>(&pair[buf][w][0][at.ch], true, wa);
-        load_f32<V>(&pair[buf][w][1][at.ch], true, wb);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (SUM) {
-            tile_b[e] = w == 0 ? wb[e] : fmaf(wa[e], tile_b[e], wb[e]);
-            tile_a[e] = w == 0 ? wa[e] : tile_a[e] * wa[e];
-          } else {
-            carry[e] = fmaf(wa[e], carry[e], wb[e]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        start[e] = carry[e];
-        const int last = (P::kRuns - 1) * P::kLanes + at.lane % P::kLanes;
-        const float wa = __shfl(A[e], last, 64), wb = __shfl(B[e], last, 64);
-        tile_a[e] = wa;
-        tile_b[e] = wb;
-        if (!SUM) carry[e] = fmaf(wa, carry[e], wb);
-      }
-    }
-    if (SUM) {  // in front of the tiles so far
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        carry[e] = fmaf(prod[e], tile_b[e], carry[e]);
-        prod[e] *= tile_a[e];
-      }
-    }
-    if constexpr (!SUM) {
-      float h[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) h[e] = fmaf(eA[e], start[e], eB[e]);
-      if (p.saved && chan && have > 0)
-        Row<float, V>::store(p.saved + (bos / kRun + n + (t0 + at.token()) / kRun) * p.C + d, h);
-      const __amdgpu_buffer_rsrc_t y = tile_of<E, P::kTokens>(p.y, bos + t0, t_end - t0, p.C);
-#pragma unroll
-      for (int j = 0; j < kRun; ++j) {
-        float out[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          h[e] = fmaf(a[j][e], h[e], b[j][e]);
-          out[e] = h[e];
-          if constexpr (Z) {
-            const float g = cz[j].get(e);
-            out[e] = h[e] * (g * sigmoid_(g));
-          }
-        }
-        Row<E, V>::store(y, first + j * step, out);
-      }
+      const float la2 = rate[e] * sigmoid_(rr[j].get(e));
+      const float decay = exp2_(la2);
+      a[j][e] = decay;
+      b[j][e] = root_(one_minus_square(la2, decay)) * sigmoid_(ri[j].get(e)) * rx[j].get(e);
     }
   }
-  if (threadIdx.x < P::kLanes && chan) {
-    if constexpr (SUM) {
-      Row<float, V>::store(p.seg + (slot + s) * 2 * p.C + d, prod);
-      Row<float, V>::store(p.seg + ((slot + s) * 2 + 1) * p.C + d, carry);
-    } else if (p.h_final && t_begin + p.seg_len >= len) {
-      Row<float, V>::store(p.h_final + static_cast<int64_t>(n) * p.C + d, carry);
+  if (left < P::kTokens) {  // behind the end a token changes nothing (b is zero, as x there)
+#pragma unroll
+    for (int j = 0; j < kRun; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[j][e] = j < have ? a[j][e] : 1.f;
+  }
+  float A[V], B[V], eA[V], eB[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    A[e] = a[0][e];
+    B[e] = b[0][e];
+#pragma unroll
+    for (int j = 1; j < kRun; ++j) {
+      B[e] = fmaf(a[j][e], B[e], b[j][e]);
+      A[e] *= a[j][e];
     }
+  }
+  scan_runs<V, P::kLanes>(A, B, eA, eB, at.lane);
+  if (at.run == P::kRuns - 1) {
+    Row<float, V>::store(&sh.wave[at.wave][0][at.ch], A);
+    Row<float, V>::store(&sh.wave[at.wave][1][at.ch], B);
+  }
+  __syncthreads();
+  float fa[V], fb[V];  // the segment's
+#pragma unroll
+  for (int w = 0; w < kGlrWaves; ++w) {
+    float wa[V], wb[V];
+    load_f32<V>(&sh.wave[w][0][at.ch], true, wa);
+    load_f32<V>(&sh.wave[w][1][at.ch], true, wb);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (w == at.wave) {  // the runs before this one, in the segment
+        const float sa = w ? fa[e] : 1.f, sb = w ? fb[e] : 0.f;
+        eB[e] = fmaf(eA[e], sb, eB[e]);
+        eA[e] *= sa;
+      }
+      fb[e] = w ? fmaf(wa[e], fb[e], wb[e]) : wb[e];
+      fa[e] = w ? fa[e] * wa[e] : wa[e];
+    }
+  }
+  arrive<V>(p, sh, at, at.seg, P::start(p, at.n), 1, at.bos / (P::kTokens * kGlrGroup) + at.n, d, chan, fa, fb, carry);
+
+  float h[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) h[e] = fmaf(eA[e], carry[e], eB[e]);
+  if (p.saved && chan && have > 0)
+    Row<float, V>::store(p.saved + (at.bos / kRun + at.n + (at.t0 + at.token()) / kRun) * p.C + d, h);
+  const __amdgpu_buffer_rsrc_t y = tile_of<E, P::kTokens>(p.y, row, left, p.C);
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+    float out[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      h[e] = fmaf(a[j][e], h[e], b[j][e]);
+      out[e] = h[e];
+      if constexpr (Z) {
+        const float g = rz[j].get(e);
+        out[e] = h[e] * (g * sigmoid_(g));
+      }
+    }
+    Row<E, V>::store(y, first + j * step, out);
+  }
+  if (threadIdx.x < P::kLanes && chan && p.h_final && at.seg + 1 == at.segs) {
+    float last[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) last[e] = fmaf(fa[e], carry[e], fb[e]);
+    Row<float, V>::store(p.h_final + static_cast<int64_t>(at.n) * p.C + d, last);
   }
 }
 
 // ---------------------------------------------------------------------------- backward
 
-// Z: there is a gate.  SUM: the segments' (A, B) of K alone.
-template <typename E, int V, int NW, bool Z, bool SUM>
-__global__ __launch_bounds__(64 * NW) void glr_bwd_kernel(GlrParams p, int tiles) {
-  using P = Place<V, NW>;
-  const P at;
-  const int tile = xcd_tile(blockIdx.x, tiles);
-  if (tile >= tiles) return;
-  const int n = blockIdx.y, s = blockIdx.z;
-  int64_t bos, len;
-  chunk::seq_range(p.seq, n, bos, len);
-  const int64_t t_begin = s * p.seg_len, t_end = min(len, t_begin + p.seg_len);
-  if (s > 0 && t_begin >= len) return;
-  if (SUM && s == 0) return;  // nothing comes before the first
-  const bool chan = tile * kGlrTile + at.ch < p.C;
-  const int d = chan ? tile * kGlrTile + at.ch : 0;
-  __shared__ alignas(16) float pair[2][NW][2][kGlrTile];
-
-  float rate[V], carry[V], total[V], prod[V];
-  load_f32<V>(p.lam + d, true, rate);
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    rate[e] = rate_(rate[e], p.c);
-    total[e] = 0.f;
-    prod[e] = 1.f;
-  }
-  load_f32<V>(p.dh_final + static_cast<int64_t>(n) * p.C + d, p.dh_final != nullptr && !SUM, carry);
-  const int64_t slot = bos / p.seg_len + n;
-  if (!SUM) {
-    const int last = len > 0 ? static_cast<int>((len - 1) / p.seg_len) : 0;
-    for (int j = last; j > s; --j) {
-      float a[V], b[V];
-      load_f32<V>(p.seg + (slot + j) * 2 * p.C + d, true, a);
-      load_f32<V>(p.seg + ((slot + j) * 2 + 1) * p.C + d, true, b);
-#pragma unroll
-      for (int e = 0; e < V; ++e) carry[e] = fmaf(a[e], carry[e], b[e]);
-    }
-  }
-
+template <typename E, int V, bool Z>
+__global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bwd_kernel(GlrParams p, int tiles) {
+  using P = Place<V>;
+  const P at(p, number(p), tiles, true);
+  if (!at.live) return;
+  const bool chan = at.tile * kGlrTile + at.ch < p.C;
+  const int d = chan ? at.tile * kGlrTile + at.ch : 0;
+  const int64_t row = at.bos + at.t0, left = at.len - at.t0;
+  const int have = static_cast<int>(min(left, static_cast<int64_t>(P::kTokens))) - at.token();
   const uint32_t step = static_cast<uint32_t>(p.C) * sizeof(E);
   const uint32_t first = chan ? static_cast<uint32_t>(at.token()) * step + static_cast<uint32_t>(d * sizeof(E)) : 0x7ffffff0u - kRun * step;
-  // fp32 leaves no registers for a tile ahead
-  constexpr bool kAhead = SUM || sizeof(E) == 2;
+  __shared__ Shared sh;
+
   Row<E, V> rx[kRun], rr[kRun], ri[kRun], rz[kRun], rd[kRun];
-  Row<float, V> rh;
-  auto fetch = [&](int64_t t0) {
-    const __amdgpu_buffer_rsrc_t r = tile_of<E, P::kTokens>(p.r, bos + t0, t_end - t0, p.C), dy = tile_of<E, P::kTokens>(p.dy, bos + t0, t_end - t0, p.C);
+  float h[V];
+  {
+    const __amdgpu_buffer_rsrc_t r = tile_of<E, P::kTokens>(p.r, row, left, p.C), dy = tile_of<E, P::kTokens>(p.dy, row, left, p.C),
+                                 x = tile_of<E, P::kTokens>(p.x, row, left, p.C), gi = tile_of<E, P::kTokens>(p.i, row, left, p.C);
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      rr[j].load(r, first + j * step);
-      rd[j].load(dy, first + j * step);
-    }
+    for (int j = 0; j < kRun; ++j) rr[j].load(r, first + j * step);
+#pragma unroll
+    for (int j = 0; j < kRun; ++j) rd[j].load(dy, first + j * step);
     if constexpr (Z) {
-      const __amdgpu_buffer_rsrc_t z = tile_of<E, P::kTokens>(p.z, bos + t0, t_end - t0, p.C);
+      const __amdgpu_buffer_rsrc_t z = tile_of<E, P::kTokens>(p.z, row, left, p.C);
 #pragma unroll
       for (int j = 0; j < kRun; ++j) rz[j].load(z, first + j * step);
     }
-    if constexpr (!SUM) {
-      const __amdgpu_buffer_rsrc_t x = tile_of<E, P::kTokens>(p.x, bos + t0, t_end - t0, p.C), gi = tile_of<E, P::kTokens>(p.i, bos + t0, t_end - t0, p.C);
 #pragma unroll
-      for (int j = 0; j < kRun; ++j) {
-        rx[j].load(x, first + j * step);
-        ri[j].load(gi, first + j * step);
-      }
-      rh.load(p.saved + (bos / kRun + n + min(t0 + at.token(), t_end - 1) / kRun) * p.C + d);
-    }
-  };
-  // The pass for the sums goes from the segment's start to its end, as the next does not.
-  const int64_t count = (t_end - t_begin + P::kTokens - 1) / P::kTokens;
-  if (kAhead && count > 0) fetch(SUM ? t_begin : t_begin + (count - 1) * P::kTokens);
-  int buf = 0;
-  for (int64_t k = 0; k < count; ++k, buf ^= 1) {
-    const int64_t t0 = t_begin + (SUM ? k : count - 1 - k) * P::kTokens;
-    const int have = static_cast<int>(min(t_end - t0, static_cast<int64_t>(512))) - at.token();
-    if (!kAhead) fetch(t0);
-    Row<E, V> cx[kRun], cr[kRun], ci[kRun], cz[kRun], cd[kRun];
-    float h[V];
+    for (int j = 0; j < kRun; ++j) ri[j].load(gi, first + j * step);
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-      cx[j] = rx[j];
-      cr[j] = rr[j];
-      ci[j] = ri[j];
-      if constexpr (Z) cz[j] = rz[j];
-      cd[j] = rd[j];
-    }
-    if constexpr (!SUM) {
+    for (int j = 0; j < kRun; ++j) rx[j].load(x, first + j * step);
+    load_f32<V>(p.saved + (at.bos / kRun + at.n + (at.t0 + at.token()) / kRun) * p.C + d, have > 0, h);
+  }
+  float rate[V], carry[V];
+  load_f32<V>(p.lam + d, true, rate);
 #pragma unroll
-      for (int e = 0; e < V; ++e) h[e] = rh.get(e);
-    }
-    if (kAhead && k + 1 < count) fetch(SUM ? t0 + P::kTokens : t0 - P::kTokens);
-    float a[kRun][V], before[kRun][V], ds[kRun][V];
-    float A[V], B[V], eA[V], eB[V];
+  for (int e = 0; e < V; ++e) rate[e] = rate_(rate[e], p.c);
+  load_f32<V>(p.dh_final + static_cast<int64_t>(at.n) * p.C + d, p.dh_final != nullptr, carry);
+
+  float a[kRun][V], ds[kRun][V];
 #pragma unroll
-    for (int j = 0; j < kRun; ++j) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float la2 = rate[e] * sigmoid_(cr[j].get(e));
-        const float decay = exp2_(la2);
-        a[j][e] = decay;
-        float g = cd[j].get(e);
-        if constexpr (Z) {
-          const float zz = cz[j].get(e);
-          g *= zz * sigmoid_(zz);
-        }
-        ds[j][e] = g;
-        if constexpr (!SUM) {
-          before[j][e] = h[e];
-          h[e] = fmaf(decay, h[e], root_(one_minus_square(la2, decay)) * sigmoid_(ci[j].get(e)) * cx[j].get(e));
-        }
-      }
-    }
-    if (t_end - t0 < P::kTokens) {  // behind the end a token changes nothing (ds is zero, as dy there)
-#pragma unroll
-      for (int j = 0; j < kRun; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) a[j][e] = j < have ? a[j][e] : 1.f;
-    }
+  for (int j = 0; j < kRun; ++j) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      A[e] = 1.f;
-      B[e] = 0.f;
-#pragma unroll
-      for (int j = kRun - 1; j >= 0; --j) {
-        B[e] = a[j][e] * (ds[j][e] + B[e]);
-        A[e] *= a[j][e];
+      a[j][e] = exp2_(rate[e] * sigmoid_(rr[j].get(e)));
+      float g = rd[j].get(e);
+      if constexpr (Z) {
+        const float zz = rz[j].get(e);
+        g *= zz * sigmoid_(zz);
       }
-    }
-    scan_runs_back<V, P::kLanes>(A, B, eA, eB, at.lane);
-    float start[V], tile_a[V], tile_b[V];
-    if constexpr (NW > 1) {
-      if (at.run == 0) {
-        Row<float, V>::store(&pair[buf][at.wave][0][at.ch], A);
-        Row<float, V>::store(&pair[buf][at.wave][1][at.ch], B);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int w = NW - 1; w >= 0; --w) {
-        if (w == at.wave) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) start[e] = carry[e];
-        }
-        float wa[V], wb[V];
-        load_f32<V>(&pair[buf][w][0][at.ch], true, wa);
-        load_f32<V>(&pair[buf][w][1][at.ch], true, wb);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (SUM) {
-            tile_b[e] = w == NW - 1 ? wb[e] : fmaf(wa[e], tile_b[e], wb[e]);
-            tile_a[e] = w == NW - 1 ? wa[e] : tile_a[e] * wa[e];
-          } else {
-            carry[e] = fmaf(wa[e], carry[e], wb[e]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        start[e] = carry[e];
-        const float wa = __shfl(A[e], at.lane % P::kLanes, 64), wb = __shfl(B[e], at.lane % P::kLanes, 64);
-        tile_a[e] = wa;
-        tile_b[e] = wb;
-        if (!SUM) carry[e] = fmaf(wa, carry[e], wb);
-      }
-    }
-    if (SUM) {  // behind the tiles so far
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        carry[e] = fmaf(prod[e], tile_b[e], carry[e]);
-        prod[e] *= tile_a[e];
-      }
-    }
-    if constexpr (!SUM) {
-      float K[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) K[e] = fmaf(eA[e], start[e], eB[e]);
-      const __amdgpu_buffer_rsrc_t bx = tile_of<E, P::kTokens>(p.dx, bos + t0, t_end - t0, p.C), br = tile_of<E, P::kTokens>(p.dr, bos + t0, t_end - t0, p.C),
-                                   bi = tile_of<E, P::kTokens>(p.di, bos + t0, t_end - t0, p.C);
-#pragma unroll
-      for (int j = kRun - 1; j >= 0; --j) {
-        cr[j].forget();
-        ci[j].forget();
-        cx[j].forget();
-        if constexpr (Z) {
-          cz[j].forget();
-          cd[j].forget();
-        }
-        float ox[V], orr[V], oi[V], oz[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float sr = sigmoid_(cr[j].get(e)), si = sigmoid_(ci[j].get(e)), xv = cx[j].get(e);
-          const float la2 = rate[e] * sr, la = la2 * kLn2;
-          const float decay = a[j][e], m = root_(one_minus_square(la2, decay));
-          const float G = ds[j][e] + K[e];
-          K[e] = decay * G;
-          const float six = si * xv, hp = before[j][e];
-          const float E1 = G * (decay * la * hp - decay * decay * (m > 0.f ? la * rcp_(m) : 0.f) * six);
-          ox[e] = G * m * si;
-          orr[e] = E1 * (1.f - sr);
-          oi[e] = G * m * six * (1.f - si);
-          if constexpr (Z) {
-            const float zz = cz[j].get(e), sz = sigmoid_(zz);
-            const float hn = fmaf(decay, hp, m * six);
-            oz[e] = cd[j].get(e) * hn * sz * (1.f + zz * (1.f - sz));
-          }
-          total[e] += j < have ? E1 : 0.f;
-        }
-        Row<E, V>::store(bx, first + j * step, ox);
-        Row<E, V>::store(br, first + j * step, orr);
-        Row<E, V>::store(bi, first + j * step, oi);
-        if (Z && p.dz) Row<E, V>::store(tile_of<E, P::kTokens>(p.dz, bos + t0, t_end - t0, p.C), first + j * step, oz);
-      }
+      ds[j][e] = g;
     }
   }
-  if constexpr (SUM) {
-    if (threadIdx.x < P::kLanes && chan) {
-      Row<float, V>::store(p.seg + (slot + s) * 2 * p.C + d, prod);
-      Row<float, V>::store(p.seg + ((slot + s) * 2 + 1) * p.C + d, carry);
+  if (left < P::kTokens) {  // behind the end a token changes nothing (ds is zero, as dy there)
+#pragma unroll
+    for (int j = 0; j < kRun; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[j][e] = j < have ? a[j][e] : 1.f;
+  }
+  float A[V], B[V], eA[V], eB[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    A[e] = 1.f;
+    B[e] = 0.f;
+#pragma unroll
+    for (int j = kRun - 1; j >= 0; --j) {
+      B[e] = a[j][e] * (ds[j][e] + B[e]);
+      A[e] *= a[j][e];
     }
-  } else {
-    if (threadIdx.x < P::kLanes && chan && s == 0 && p.dh0) Row<float, V>::store(p.dh0 + static_cast<int64_t>(n) * p.C + d, carry);
-    // the segment's sum of E, over the runs of a wave and then over the waves
+  }
+  scan_runs_back<V, P::kLanes>(A, B, eA, eB, at.lane);
+  if (at.run == 0) {
+    Row<float, V>::store(&sh.wave[at.wave][0][at.ch], A);
+    Row<float, V>::store(&sh.wave[at.wave][1][at.ch], B);
+  }
+  __syncthreads();
+  float fa[V], fb[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e)
+  for (int w = kGlrWaves - 1; w >= 0; --w) {
+    const bool none = w == kGlrWaves - 1;
+    float wa[V], wb[V];
+    load_f32<V>(&sh.wave[w][0][at.ch], true, wa);
+    load_f32<V>(&sh.wave[w][1][at.ch], true, wb);
 #pragma unroll
-      for (int off = P::kLanes; off < 64; off <<= 1) total[e] += __shfl_xor(total[e], off, 64);
-    __syncthreads();
-    if (at.run == 0) Row<float, V>::store(&pair[0][at.wave][0][at.ch], total);
-    __syncthreads();
-    if (threadIdx.x < P::kLanes && chan) {
-      float sum[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) sum[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w)
-#pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] += pair[0][w][0][at.ch + e];
-      Row<float, V>::store(p.part_lam + (slot + s) * p.C + d, sum);
+    for (int e = 0; e < V; ++e) {
+      if (w == at.wave) {  // the runs behind this one, in the segment
+        const float sa = none ? 1.f : fa[e], sb = none ? 0.f : fb[e];
+        eB[e] = fmaf(eA[e], sb, eB[e]);
+        eA[e] *= sa;
+      }
+      fb[e] = none ? wb[e] : fmaf(wa[e], fb[e], wb[e]);
+      fa[e] = none ? wa[e] : fa[e] * wa[e];
     }
+  }
+  arrive<V>(p, sh, at, at.segs - 1 - at.seg, P::start(p, at.n) + at.segs - 1, -1, at.bos / (P::kTokens * kGlrGroup) + at.n, d, chan, fa,
+            fb, carry);
+
+  float before[kRun][V];
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      before[j][e] = h[e];
+      const float la2 = rate[e] * sigmoid_(rr[j].get(e));
+      h[e] = fmaf(a[j][e], h[e], root_(one_minus_square(la2, a[j][e])) * sigmoid_(ri[j].get(e)) * rx[j].get(e));
+    }
+  }
+  float K[V], total[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    K[e] = fmaf(eA[e], carry[e], eB[e]);
+    total[e] = 0.f;
+  }
+  const __amdgpu_buffer_rsrc_t bx = tile_of<E, P::kTokens>(p.dx, row, left, p.C), br = tile_of<E, P::kTokens>(p.dr, row, left, p.C),
+                               bi = tile_of<E, P::kTokens>(p.di, row, left, p.C);
+#pragma unroll
+  for (int j = kRun - 1; j >= 0; --j) {
+    rr[j].forget();
+    ri[j].forget();
+    rx[j].forget();
+    if constexpr (Z) {
+      rz[j].forget();
+      rd[j].forget();
+    }
+    float ox[V], orr[V], oi[V], oz[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float sr = sigmoid_(rr[j].get(e)), si = sigmoid_(ri[j].get(e)), xv = rx[j].get(e);
+      const float la2 = rate[e] * sr, la = la2 * kLn2;
+      const float decay = a[j][e], m = root_(one_minus_square(la2, decay));
+      const float G = ds[j][e] + K[e];
+      K[e] = decay * G;
+      const float six = si * xv, hp = before[j][e];
+      const float E1 = G * (decay * la * hp - decay * decay * (m > 0.f ? la * rcp_(m) : 0.f) * six);
+      ox[e] = G * m * si;
+      orr[e] = E1 * (1.f - sr);
+      oi[e] = G * m * six * (1.f - si);
+      if constexpr (Z) {
+        const float zz = rz[j].get(e), sz = sigmoid_(zz);
+        const float hn = fmaf(decay, hp, m * six);
+        oz[e] = rd[j].get(e) * hn * sz * (1.f + zz * (1.f - sz));
+      }
+      total[e] += j < have ? E1 : 0.f;
+    }
+    Row<E, V>::store(bx, first + j * step, ox);
+    Row<E, V>::store(br, first + j * step, orr);
+    Row<E, V>::store(bi, first + j * step, oi);
+    if (Z && p.dz) Row<E, V>::store(tile_of<E, P::kTokens>(p.dz, row, left, p.C), first + j * step, oz);
+  }
+  if (threadIdx.x < P::kLanes && chan && at.seg == 0 && p.dh0) {
+    float last[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) last[e] = fmaf(fa[e], carry[e], fb[e]);
+    Row<float, V>::store(p.dh0 + static_cast<int64_t>(at.n) * p.C + d, last);
+  }
+  // the segment's sum of E, over the runs of a wave and then over the waves
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+#pragma unroll
+    for (int off = P::kLanes; off < 64; off <<= 1) total[e] += __shfl_xor(total[e], off, 64);
+  __syncthreads();  // the waves' (A, B) are read
+  if (at.run == 0) Row<float, V>::store(&sh.wave[at.wave][0][at.ch], total);
+  __syncthreads();
+  if (threadIdx.x < P::kLanes && chan) {
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kGlrWaves; ++w)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum[e] += sh.wave[w][0][at.ch + e];
+    Row<float, V>::store(p.part_lam + at.slot * p.C + d, sum);
   }
 }
 
@@ -616,7 +664,8 @@ __global__ __launch_bounds__(256) void glr_lam_kernel(GlrParams p) {
     for (int n = wave; n < p.N; n += 4) {
       int64_t bos, len;
       chunk::seq_range(p.seq, n, bos, len);
-      const int64_t slot = bos / p.seg_len + n, count = (len + p.seg_len - 1) / p.seg_len;
+      constexpr int kSeg = glr_seg(true);
+      const int64_t slot = bos / kSeg + n, count = (len + kSeg - 1) / kSeg;
       for (int64_t j = 0; j < count; ++j) sum += p.part_lam[(slot + j) * p.C + d];
     }
   }
@@ -660,53 +709,48 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrParams p) {
   Row<E, V>::store(static_cast<E*>(p.y) + at, out);
 }
 
-dim3 grid_of(const GlrParams& p, int tiles) {
-  return dim3(static_cast<unsigned>((tiles + 7) / 8 * 8), static_cast<unsigned>(p.N), static_cast<unsigned>(p.segs));
-}
-
-template <typename E, int NW, bool Z>
-void fwd(const GlrParams& p, hipStream_t s) {
-  constexpr int V = glr_vec(false, sizeof(E) == 2);
-  const int tiles = glr_tiles(p.C);
-  if (p.segs > 1) hipLaunchKernelGGL((glr_fwd_kernel<E, V, NW, false, true>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-  hipLaunchKernelGGL((glr_fwd_kernel<E, V, NW, Z, false>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-}
-
-template <typename E, int NW, bool Z>
-void bwd(const GlrParams& p, hipStream_t s) {
-  constexpr int V = glr_vec(true, sizeof(E) == 2);
-  const int tiles = glr_tiles(p.C);
-  if (p.segs > 1) hipLaunchKernelGGL((glr_bwd_kernel<E, V, NW, Z, true>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-  if (p.N > 0) hipLaunchKernelGGL((glr_bwd_kernel<E, V, NW, Z, false>), grid_of(p, tiles), dim3(64 * NW), 0, s, p, tiles);
-  hipLaunchKernelGGL(glr_lam_kernel, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(256), 0, s, p);
-}
-
-template <typename E, int NW, bool BWD>
-hipError_t launch(const GlrParams& p, hipStream_t s) {
-  if constexpr (BWD)
-    p.z ? bwd<E, NW, true>(p, s) : bwd<E, NW, false>(p, s);
-  else
-    p.z ? fwd<E, NW, true>(p, s) : fwd<E, NW, false>(p, s);
-  return hipGetLastError();
+// The counter and the words' marks cleared, in 16 bytes a thread.
+__global__ __launch_bounds__(256) void glr_clear_kernel(uint64_t* chain, int64_t pairs) {
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (at < pairs) reinterpret_cast<u32x4_t*>(chain)[at] = u32x4_t(0u);
 }
 
 template <typename E, bool BWD>
-hipError_t launch_waves(const GlrParams& p, hipStream_t s) {
-  switch (p.waves) {
-    case 1: return launch<E, 1, BWD>(p, s);
-    case 4: return launch<E, 4, BWD>(p, s);
-    default: return launch<E, 8, BWD>(p, s);
+hipError_t launch(const GlrParams& p, hipStream_t s) {
+  constexpr int V = glr_vec(BWD);
+  static_assert(Place<V>::kTokens == glr_seg(BWD), "segments as the workspace counts them");
+  const int tiles = glr_tiles(p.C);
+  if (p.chained) {
+    const int64_t groups = glr_slots(p.rows, p.N, glr_seg(BWD) * kGlrGroup);
+    const int64_t pairs = 16 + p.slots * p.C + (groups * p.C + 1) / 2;
+    hipLaunchKernelGGL(glr_clear_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, s, p.chain, pairs);
   }
+  const dim3 grid(static_cast<unsigned>(p.slots * tiles)), block(64 * kGlrWaves);
+  if constexpr (BWD) {
+    if (p.N > 0) {
+      if (p.z)
+        hipLaunchKernelGGL((glr_bwd_kernel<E, V, true>), grid, block, 0, s, p, tiles);
+      else
+        hipLaunchKernelGGL((glr_bwd_kernel<E, V, false>), grid, block, 0, s, p, tiles);
+    }
+    hipLaunchKernelGGL(glr_lam_kernel, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(256), 0, s, p);
+  } else {
+    if (p.z)
+      hipLaunchKernelGGL((glr_fwd_kernel<E, V, true>), grid, block, 0, s, p, tiles);
+    else
+      hipLaunchKernelGGL((glr_fwd_kernel<E, V, false>), grid, block, 0, s, p, tiles);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_glr_fwd(const GlrParams& p, bool bf16, hipStream_t s) {
-  return bf16 ? launch_waves<uint16_t, false>(p, s) : launch_waves<float, false>(p, s);
+  return bf16 ? launch<uint16_t, false>(p, s) : launch<float, false>(p, s);
 }
 
 hipError_t launch_glr_bwd(const GlrParams& p, bool bf16, hipStream_t s) {
-  return bf16 ? launch_waves<uint16_t, true>(p, s) : launch_waves<float, true>(p, s);
+  return bf16 ? launch<uint16_t, true>(p, s) : launch<float, true>(p, s);
 }
 
 hipError_t launch_glr_step(const GlrParams& p, bool bf16, hipStream_t s) {

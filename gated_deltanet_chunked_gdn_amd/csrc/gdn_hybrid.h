@@ -23,35 +23,39 @@ struct GlrParams {
   void* y;
   float* h_final;      // [N][C] or nullptr; the step's state, updated in place
   float* saved;        // [run slot][C] states before every run of kGlrRun tokens, or nullptr
-  float* seg;          // [part][2][C] decay product and end state of every segment
   const void* dy;
   const float* dh_final;  // or nullptr
   void* dx;
   void* dr;
   void* di;
   void* dz;            // or nullptr
-  float* part_lam;     // [part][C] sums of a segment
+  float* part_lam;     // [segment slot][C] sums of a segment
   float* dlam;
   float* dh0;          // or nullptr
+  // What the segments of a sequence tell each other (chained): a counter, then words of a
+  // value and a mark that it is there.
+  uint64_t* chain;     // cleared before the launch: [32] whose first counts workgroups, then
+  uint64_t* whole;     // [segment slot][2][C] decay product and end from zero of a segment
+  uint64_t* end;       // [group slot][C] state behind (backward: gradient in front of) a group
   SeqInfo seq;
   int64_t rows;        // B * T
+  int64_t slots;       // segment slots
   int32_t N, C;
-  int32_t segs;        // segments of the longest sequence, of seg_len tokens
-  int32_t waves;       // waves of a workgroup (1, 2, 4 or 8)
-  int64_t seg_len;
+  int32_t chained;     // some sequence has several segments
   float c;
 };
 
-constexpr int kGlrRun = 8;    // tokens that a thread takes one after another
-constexpr int kGlrTile = 32;  // channels of a workgroup
-// Channels of a lane: 8 bytes, in the backward 4 (bf16) or 8.
-constexpr int glr_vec(bool bwd, bool bf16) { return bf16 && !bwd ? 4 : 2; }
-// Tokens of a wave: its 64 lanes over those of a row, a run each.
-constexpr int glr_wave_tokens(bool bwd, bool bf16) { return 64 / (kGlrTile / glr_vec(bwd, bf16)) * kGlrRun; }
+constexpr int kGlrRun = 8;     // tokens that a thread takes one after another
+constexpr int kGlrTile = 64;   // channels of a workgroup: rows of 128 bytes (bf16)
+constexpr int kGlrWaves = 4;
+constexpr int kGlrGroup = 16;  // segments of a group
+// Channels of a lane.
+constexpr int glr_vec(bool bwd) { return bwd ? 2 : 4; }
+// Tokens of a segment: the runs of a workgroup's lanes.
+constexpr int glr_seg(bool bwd) { return kGlrWaves * 64 / (kGlrTile / glr_vec(bwd)) * kGlrRun; }
 inline int glr_tiles(int C) { return (C + kGlrTile - 1) / kGlrTile; }
-// Run c of a sequence that starts at row bos uses slot bos / run + n + c (distinct).
-inline int64_t glr_slots(int64_t rows, int64_t n) { return rows / kGlrRun + n + 1; }
-inline int64_t glr_parts(int64_t rows, int64_t n, int64_t seg_len) { return rows / seg_len + n; }
+// Part c (of `len` tokens) of a sequence that starts at row bos uses slot bos / len + n + c (distinct).
+inline int64_t glr_slots(int64_t rows, int64_t n, int64_t len) { return rows / len + n; }
 hipError_t launch_glr_fwd(const GlrParams& p, bool bf16, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrParams& p, bool bf16, hipStream_t s);
 hipError_t launch_glr_step(const GlrParams& p, bool bf16, hipStream_t s);

@@ -21,9 +21,12 @@ namespace {
 // ---------------------------------------------------------------------------- recurrence
 
 struct GlrSize {
-  size_t io = 0, values = 0, chan = 0, state = 0, saved = 0, seg = 0, part = 0;
-  int64_t rows = 0, seg_len = 1;
-  int32_t segs = 1, waves = 1;
+  size_t io = 0, values = 0, chan = 0, state = 0, saved = 0;
+  size_t whole = 0, end = 0, part = 0;  // words of the segments and groups, partial sums
+  int64_t rows = 0, slots = 0;
+  int32_t chained = 0;
+  // the counter, then the words: what is cleared before a launch
+  size_t chain() const { return chained ? 256 + whole + end : 0; }
 };
 
 gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
@@ -40,32 +43,34 @@ gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
   c->values = static_cast<size_t>(c->rows) * p->C * c->io;
   c->chan = static_cast<size_t>(p->C) * 4;
   c->state = static_cast<size_t>(p->num_seqs) * c->chan;
-  c->saved = static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs)) * c->chan;
-  // A tile as long as the longest sequence needs, up to eight waves.
-  const int64_t wave = gdn::glr_wave_tokens(bwd, c->io == 2);
-  c->waves = max_len <= wave ? 1 : max_len <= 4 * wave ? 4 : 8;
-  // Segments where the channels leave CUs idle, of two tiles at least.
-  const int64_t tile = wave * c->waves, tiles = gdn::glr_tiles(p->C);
-  const int64_t groups = std::max<int64_t>(1, (c->rows + std::max<int64_t>(max_len, 1) - 1) / std::max<int64_t>(max_len, 1)) * tiles;
-  const int64_t segs = std::max<int64_t>(1, std::min<int64_t>((256 + groups - 1) / groups, max_len / (2 * tile)));
-  c->seg_len = std::max<int64_t>(((max_len + segs - 1) / segs + tile - 1) / tile * tile, tile);
-  c->segs = static_cast<int32_t>(std::max<int64_t>(1, (max_len + c->seg_len - 1) / c->seg_len));
-  const size_t parts = static_cast<size_t>(gdn::glr_parts(c->rows, p->num_seqs, c->seg_len));
-  c->seg = c->segs > 1 ? up256(parts * 2 * c->chan) : 0;
-  c->part = bwd ? parts * c->chan : 0;
-  // a launch counts its threads in 32 bits; the step has fewer than any other
-  if (static_cast<int64_t>((tiles + 7) / 8 * 8) * p->num_seqs * c->segs * 64 * c->waves >= INT64_C(1) << 32) return GDN_ERR_UNSUPPORTED;
+  c->saved = static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs, gdn::kGlrRun)) * c->chan;
+  const int64_t seg = gdn::glr_seg(bwd);
+  c->slots = gdn::glr_slots(c->rows, p->num_seqs, seg);
+  c->chained = max_len > seg;
+  c->whole = static_cast<size_t>(c->slots) * 4 * c->chan;
+  c->end = up256(static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs, seg * gdn::kGlrGroup)) * 2 * c->chan);
+  c->part = bwd ? static_cast<size_t>(c->slots) * c->chan : 0;
+  // workgroups of 256 threads, counted in 32 bits: segments of the longer of the two
+  // directions' segments or shorter, so that what the forward takes the backward takes too
+  const int64_t most = gdn::glr_slots(c->rows, p->num_seqs, gdn::glr_seg(true));
+  if (most * gdn::glr_tiles(p->C) >= 1 << 24) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 
 gdn::GlrParams glr_params(const gdn_glr_problem* p, const GlrSize& c, const void* x, const void* r, const void* i,
-                          const float* lam, const void* z) {
+                          const float* lam, const void* z, void* ws) {
   gdn::GlrParams gp{};
   gp.x = x; gp.r = r; gp.i = i; gp.lam = lam; gp.z = z;
   gp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
   gp.rows = c.rows; gp.N = p->num_seqs; gp.C = p->C;
-  gp.segs = c.segs; gp.seg_len = c.seg_len; gp.waves = c.waves;
+  gp.slots = c.slots; gp.chained = c.chained;
   gp.c = p->c;
+  if (c.chained) {
+    char* const at = static_cast<char*>(ws);
+    gp.chain = reinterpret_cast<uint64_t*>(at);
+    gp.whole = reinterpret_cast<uint64_t*>(at + 256);
+    gp.end = reinterpret_cast<uint64_t*>(at + 256 + c.whole);
+  }
   return gp;
 }
 
@@ -80,13 +85,12 @@ gdn_status glr_fwd(const gdn_glr_problem* p, const void* x, const void* r, const
                      {{y, c.values, 16, true}, {h_final, c.state, 16, false}, {saved, saved_bytes, 16, false},
                       {ws, ws_bytes, 16, false}});
   if (st != GDN_OK) return st;
-  if (c.seg && (!ws || ws_bytes < c.seg)) return GDN_ERR_WORKSPACE;
-  if (save && (!saved || saved_bytes < c.saved)) return GDN_ERR_WORKSPACE;
+  if (c.chained && (!ws || ws_bytes < c.chain())) return GDN_ERR_WORKSPACE;
+  if (save && c.saved && (!saved || saved_bytes < c.saved)) return GDN_ERR_WORKSPACE;
   if (p->num_seqs == 0) return GDN_OK;
-  gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z);
+  gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z, ws);
   gp.h0 = h0; gp.y = y; gp.h_final = h_final;
   gp.saved = save ? static_cast<float*>(saved) : nullptr;
-  gp.seg = static_cast<float*>(ws);
   return hip_status(gdn::launch_glr_fwd(gp, c.io == 2, static_cast<hipStream_t>(stream)));
 }
 
@@ -244,7 +248,7 @@ gdn_status gdn_glr_workspace_size(const gdn_glr_problem* p, int32_t pass, size_t
   GlrSize c;
   const gdn_status st = check_glr(p, pass == GDN_GLR_BWD, &c);
   if (st != GDN_OK) return st;
-  *bytes = pass == GDN_GLR_SAVED ? c.saved : c.seg + c.part;
+  *bytes = pass == GDN_GLR_SAVED ? c.saved : c.chain() + c.part;
   return GDN_OK;
 }
 
@@ -273,14 +277,14 @@ gdn_status gdn_glr_bwd_saved(const gdn_glr_problem* p, const void* x, const void
                      {{dx, c.values, 16, true}, {dr, c.values, 16, true}, {di, c.values, 16, true}, {dlam, c.chan, 16, true},
                       {dz, c.values, 16, false}, {dh0, c.state, 16, false}, {ws, ws_bytes, 16, false}});
   if (st != GDN_OK) return st;
-  if (c.seg + c.part && (!ws || ws_bytes < c.seg + c.part)) return GDN_ERR_WORKSPACE;
-  if (!saved || saved_bytes < c.saved) return GDN_ERR_WORKSPACE;
-  gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z);
+  const size_t need = c.chain() + c.part;
+  if (need && (!ws || ws_bytes < need)) return GDN_ERR_WORKSPACE;
+  if (c.saved && (!saved || saved_bytes < c.saved)) return GDN_ERR_WORKSPACE;
+  gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z, ws);
   gp.saved = const_cast<float*>(static_cast<const float*>(saved));
   gp.dy = dy; gp.dh_final = dh_final;
   gp.dx = dx; gp.dr = dr; gp.di = di; gp.dlam = dlam; gp.dz = dz; gp.dh0 = dh0;
-  gp.seg = static_cast<float*>(ws);
-  gp.part_lam = reinterpret_cast<float*>(static_cast<char*>(ws) + c.seg);
+  gp.part_lam = reinterpret_cast<float*>(static_cast<char*>(ws) + c.chain());
   return hip_status(gdn::launch_glr_bwd(gp, c.io == 2, static_cast<hipStream_t>(stream)));
 }
 
@@ -294,7 +298,7 @@ gdn_status gdn_glr_step(const gdn_glr_problem* p, const void* x, const void* r, 
                       {z, c.values, 16, false}},
                      {{h, c.state, 16, true}, {y, c.values, 16, true}});
   if (st != GDN_OK || p->B == 0) return st;
-  gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z);
+  gdn::GlrParams gp = glr_params(p, c, x, r, i, lam, z, nullptr);
   gp.h_final = h; gp.y = y;
   return hip_status(gdn::launch_glr_step(gp, c.io == 2, static_cast<hipStream_t>(stream)));
 }

@@ -135,7 +135,7 @@ def glr_bwd_saved(x, r, i, lam, dy, saved, z=None, dh_final=None, c: float = 8.0
     ins = _glr_inputs(x, r, i, lam, z, dev)
     shape = (prob.num_seqs, prob.C)
     dyp, dhp = _want(dy, x.shape, x.dtype, dev, "dy"), _may(dh_final, shape, _F32, dev, "dh_final")
-    if saved is None:
+    if saved is None and _glr_size(prob, nat.GDN_GLR_SAVED):
         raise ValueError("saved must be the buffer glr_fwd_save filled")
     _, sv, nsv = _buffer(saved, 0, dev, "saved")
     buf, ws, nws = _buffer(workspace, _glr_size(prob, nat.GDN_GLR_BWD), dev, "workspace")

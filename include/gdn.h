@@ -564,11 +564,8 @@ gdn_status gdn_scan_step(const gdn_scan_problem* problem, const void* u, const v
  *     y_t = h   or, with z,   h z_t sigmoid(z_t)
  * Tensors: x, r, i, z, y and their gradients [B,T,C] (io dtype); lam, dlam [C], h0,
  * h_final, dh_final, dh0, h [num_seqs,C] fp32.  All of them 16-byte aligned.  Supported: C a
- * multiple of 8 up to 2^20, B T < 2^31, up to 65535 sequences, c >= 0, and fewer than 2^32
- * threads in a launch, else GDN_ERR_UNSUPPORTED.  A launch has 64 threads for 1, 4 or 8 (the
- * fewest that hold the longest sequence at 64 tokens, in the backward 32; else 8), for every
- * 32 channels (rounded up to 256), every sequence and every segment of the longest one (one
- * segment wherever sequences and channels alone are 256 workgroups).  Finite lam is documented,
+ * multiple of 8 up to 2^20, B T < 2^31, up to 65535 sequences, c >= 0, and
+ * (B T / 64 + sequences) ceil(C / 64) < 2^24, else GDN_ERR_UNSUPPORTED.  Finite lam is documented,
  * not checked.  All arithmetic is fp32; io outputs are rounded once.  NaN and Inf reach what
  * the definition makes of them and nothing that it leaves finite; where it gives an infinity
  * NaN may stand instead (a state that is infinite while the decays over several tokens
@@ -595,8 +592,9 @@ gdn_status gdn_glr_workspace_size(const gdn_glr_problem* problem, int32_t pass, 
 
 /* Forward.  in: x, r, i, lam; z, h0 (each may be NULL: no gate, zero); out: y, h_final
  * (NULL: not wanted; a sequence of no tokens keeps h0).  The time axis is composed of runs
- * and, where the channels are few, of segments: results are those of the serial order up to
- * fp32 rounding, bit-identical from call to call. */
+ * and segments: results are those of the serial order up to fp32 rounding, bit-identical from
+ * call to call.  The segments of a call pass their states on in the workspace: calls that may
+ * overlap in time and share one may end late (a second or so) and give NaN. */
 gdn_status gdn_glr_fwd(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
                        const float* lam, const void* z, const float* h0, void* y, float* h_final,
                        void* workspace, size_t workspace_bytes, void* stream);
