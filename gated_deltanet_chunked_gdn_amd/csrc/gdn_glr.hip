@@ -11,7 +11,7 @@
 // more.  So all is read once, and the segments of a sequence work at the same time.
 //
 // The state in front comes from the other segments.  Each gives out its (A, B) as soon as it
-// has them.  Sixteen segments are a group: a segment composes those of its group before it,
+// has them.  Some segments are a group: a segment composes those of its group before it,
 // all loaded at once, onto the group's start, and the group's last one gives out the next
 // group's.  The order of every composition is fixed, whoever comes first, so results are
 // bit-identical from call to call.  The words that pass carry a mark beside the value and are
@@ -161,15 +161,15 @@ struct Place {
         hi = mid;
     }
     n = lo;
-    chunk::seq_range(p.seq, n, bos, len);
     seg = static_cast<int>(slot - start(p, n));
+    chunk::seq_range(p.seq, n, bos, len);
     segs = static_cast<int>(max((len + kTokens - 1) / kTokens, static_cast<int64_t>(1)));
     t0 = static_cast<int64_t>(seg) * kTokens;
     live = seg < segs;  // an empty sequence has one segment, of no tokens
   }
+  // A sequence's first slot.  Dense ones have the slots that their segments need and no more.
   static __device__ __forceinline__ int64_t start(const GlrParams& p, int n) {
-    const int64_t bos = p.seq.cu ? p.seq.cu[n] : static_cast<int64_t>(n) * p.seq.T;
-    return bos / kTokens + n;
+    return p.seq.cu ? p.seq.cu[n] / kTokens + n : static_cast<int64_t>(n) * (p.slots / p.N);
   }
 };
 
@@ -183,43 +183,59 @@ __device__ __forceinline__ int64_t number(const GlrParams& p) {
   return __builtin_amdgcn_readfirstlane(mine);
 }
 
-// A value given out with its mark, V channels of them.
+// Words that workgroups pass to each other; zero: not there yet.  A state stands beside a one;
+// of a segment's (A, B), A is positive or zero (or NaN), so its sign is the mark.
+// Two words go in one access of 16 bytes, each of them whole, of a scope past the caches of an
+// XCD (sc1), which the compiler neither merges nor moves (volatile).
+constexpr int kDevice = 1 << 4, kVolatile = 1 << 31;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));  // value, mark
 template <int V>
-__device__ __forceinline__ void give(uint64_t* to, const float* f) {
+__device__ __forceinline__ void give_(uint64_t* to, uint32_t off, const u32x2_t* w) {
+  const __amdgpu_buffer_rsrc_t r = chunk::buffer_rsrc(to, 0x7fffffff);
 #pragma unroll
-  for (int e = 0; e < V; ++e)
-    __hip_atomic_store(to + e, (UINT64_C(1) << 32) | __float_as_uint(f[e]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int e = 0; e < V; e += 2) {
+    const chunk::u32x4v_t v = {w[e][0], w[e][1], w[e + 1][0], w[e + 1][1]};
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, off + 8 * e, 0, kDevice);
+  }
 }
-// Waits until all lanes of the wave have theirs; lanes without one (`want` false) keep f.
+// Waits until all words of all lanes of the wave are there: V at each place, `off` bytes from
+// `from`; lanes that want none of a place say so.
 template <int V, int COUNT>
-__device__ __forceinline__ void take(const uint64_t* const* from, bool want, float (*f)[V]) {
-  uint64_t w[COUNT][V];
+__device__ __forceinline__ void take_(const uint64_t* from, const uint32_t* off, const bool* want, u32x2_t (*w)[V]) {
+  const __amdgpu_buffer_rsrc_t r = chunk::buffer_rsrc(from, 0x7fffffff);
+  bool missing[COUNT];
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) missing[i] = want[i];
   for (int tries = 0;; ++tries) {
-    bool there = true;
-    if (want) {
 #pragma unroll
-      for (int i = 0; i < COUNT; ++i)
+    for (int i = 0; i < COUNT; ++i)
+      if (missing[i]) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          w[i][e] = __hip_atomic_load(from[i] + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          there &= (w[i][e] >> 32) != 0;
+        for (int e = 0; e < V; e += 2) {
+          const chunk::u32x4v_t v = __builtin_amdgcn_raw_buffer_load_b128(r, off[i] + 8 * e, 0, kDevice | kVolatile);
+          w[i][e] = u32x2_t{v[0], v[1]};
+          w[i][e + 1] = u32x2_t{v[2], v[3]};
         }
+      }
+    bool there = true;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      if (missing[i]) {
+        missing[i] = false;
+#pragma unroll
+        for (int e = 0; e < V; ++e) missing[i] |= w[i][e][1] == 0;
+      }
+      there &= !missing[i];
     }
-    if (__all(there)) break;
+    if (__all(there)) return;
     if (tries >= 1 << 20) {  // about a second: whoever should give it shares its workspace with another call
 #pragma unroll
       for (int i = 0; i < COUNT; ++i)
 #pragma unroll
-        for (int e = 0; e < V; ++e) w[i][e] = 0x7fc00000u;
-      break;
+        for (int e = 0; e < V; ++e) w[i][e] = u32x2_t{0x7fc00000u, 0x7fc00000u};
+      return;
     }
     __builtin_amdgcn_s_sleep(2);
-  }
-  if (want) {
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[i][e] = __uint_as_float(static_cast<uint32_t>(w[i][e]));
   }
 }
 
@@ -281,42 +297,51 @@ struct Shared {
 // direction of the walk.  Called by the whole workgroup.
 template <int V>
 __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Place<V>& at, int place, int64_t first_slot, int dir,
-                                       int64_t group_slot, int d, bool chan, const float* a, const float* b, float* carry) {
+                                       int d, bool chan, const float* a, const float* b, float* carry) {
   using P = Place<V>;
   const int group = place / kGlrGroup, index = place % kGlrGroup;
+  const int64_t group_slot = at.bos / (P::kTokens * kGlrGroup) + at.n;
   const bool lead = threadIdx.x < P::kLanes && chan;
+  const uint32_t lane_off = static_cast<uint32_t>(d) * 8;
   if (place + 1 < at.segs && index + 1 < kGlrGroup && lead) {
-    uint64_t* const to = p.whole + (first_slot + dir * place) * 2 * p.C + d;
-    give<V>(to, a);
-    give<V>(to + p.C, b);
+    u32x2_t w[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = u32x2_t{__float_as_uint(b[e]), __float_as_uint(a[e]) | 0x80000000u};
+    give_<V>(p.whole + (first_slot + dir * place) * p.C, lane_off, w);
   }
   if (place == 0) return;
-  // The other segments of the group, one for every run of the workgroup's lanes; what is
-  // beyond those of the runs comes in turns.
-  constexpr int kAtOnce = P::kRuns * kGlrWaves;
+  // The segments of the group before this one, a few consecutive ones for every run of the
+  // workgroup's lanes, all loaded at once.
+  constexpr int kPlaces = P::kRuns * kGlrWaves, kEach = kGlrGroup > kPlaces ? kGlrGroup / kPlaces : 1;
   float ca[V], cb[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     ca[e] = 1.f;
     cb[e] = 0.f;
   }
-  constexpr int kTurns = (kGlrGroup + kAtOnce - 1) / kAtOnce;
-  // consecutive segments a lane
+  {
+    u32x2_t w[kEach][V];
+    uint32_t off[kEach];
+    bool want[kEach];
+    // the lowest slot of them: walked backwards, the nearest
+    const int64_t lowest = first_slot + dir * (dir > 0 ? group * kGlrGroup : place - 1);
 #pragma unroll
-  for (int turn = 0; turn < kTurns; ++turn) {
-    const int k = (at.wave * P::kRuns + at.run) * kTurns + turn;
-    float f[2][V];
-    const bool want = k < index;
-    const uint64_t* const from = p.whole + (first_slot + dir * (group * kGlrGroup + (want ? k : 0))) * 2 * p.C + d;
-    const uint64_t* const words[2] = {from, from + p.C};
-    take<V, 2>(words, want, f);
-    if (want) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        cb[e] = fmaf(f[0][e], cb[e], f[1][e]);
-        ca[e] *= f[0][e];
-      }
+    for (int i = 0; i < kEach; ++i) {
+      const int k = (at.wave * P::kRuns + at.run) * kEach + i;
+      want[i] = k < index;
+      off[i] = lane_off + static_cast<uint32_t>(want[i] ? (dir > 0 ? k : index - 1 - k) : 0) * p.C * 8;
     }
+    take_<V, kEach>(p.whole + lowest * p.C, off, want, w);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (want[i]) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float sa = __uint_as_float(w[i][e][1] & 0x7fffffffu);
+          cb[e] = fmaf(sa, cb[e], __uint_as_float(w[i][e][0]));
+          ca[e] *= sa;
+        }
+      }
   }
   // the wave's, in order of its runs
 #pragma unroll
@@ -334,10 +359,15 @@ __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Pla
     Row<float, V>::store(&sh.before[at.wave][1][at.ch], cb);
   }
   if (group > 0 && at.wave == 0) {
-    float f[1][V];
-    const uint64_t* const words[1] = {p.end + (group_slot + group - 1) * p.C + d};
-    take<V, 1>(words, true, f);
-    if (at.run == 0) Row<float, V>::store(&sh.start[at.ch], f[0]);
+    u32x2_t w[1][V];
+    const bool want[1] = {at.run == 0};
+    take_<V, 1>(p.end + (group_slot + group - 1) * p.C, &lane_off, want, w);
+    if (at.run == 0) {
+      float f[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e] = __uint_as_float(w[0][e][0]);
+      Row<float, V>::store(&sh.start[at.ch], f);
+    }
   }
   __syncthreads();
   if (group > 0) load_f32<V>(&sh.start[at.ch], true, carry);
@@ -350,10 +380,10 @@ __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Pla
     for (int e = 0; e < V; ++e) carry[e] = fmaf(wa[e], carry[e], wb[e]);
   }
   if (index + 1 == kGlrGroup && place + 1 < at.segs && lead) {
-    float f[V];
+    u32x2_t w[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = fmaf(a[e], carry[e], b[e]);
-    give<V>(p.end + (group_slot + group) * p.C + d, f);
+    for (int e = 0; e < V; ++e) w[e] = u32x2_t{__float_as_uint(fmaf(a[e], carry[e], b[e])), 1u};
+    give_<V>(p.end + (group_slot + group) * p.C, lane_off, w);
   }
 }
 
@@ -447,7 +477,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_fw
       fa[e] = w ? fa[e] * wa[e] : wa[e];
     }
   }
-  arrive<V>(p, sh, at, at.seg, P::start(p, at.n), 1, at.bos / (P::kTokens * kGlrGroup) + at.n, d, chan, fa, fb, carry);
+  arrive<V>(p, sh, at, at.seg, P::start(p, at.n), 1, d, chan, fa, fb, carry);
 
   float h[V];
 #pragma unroll
@@ -483,8 +513,14 @@ template <typename E, int V, bool Z>
 __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bwd_kernel(GlrParams p, int tiles) {
   using P = Place<V>;
   const P at(p, number(p), tiles, true);
-  if (!at.live) return;
   const bool chan = at.tile * kGlrTile + at.ch < p.C;
+  if (!at.live) {  // a slot between two sequences'
+    if (threadIdx.x < P::kLanes && chan) {
+      const float none[V] = {};
+      Row<float, V>::store(p.part_lam + at.slot * p.C + at.tile * kGlrTile + at.ch, none);
+    }
+    return;
+  }
   const int d = chan ? at.tile * kGlrTile + at.ch : 0;
   const int64_t row = at.bos + at.t0, left = at.len - at.t0;
   const int have = static_cast<int>(min(left, static_cast<int64_t>(P::kTokens))) - at.token();
@@ -573,7 +609,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bw
       fa[e] = none ? wa[e] : fa[e] * wa[e];
     }
   }
-  arrive<V>(p, sh, at, at.segs - 1 - at.seg, P::start(p, at.n) + at.segs - 1, -1, at.bos / (P::kTokens * kGlrGroup) + at.n, d, chan, fa,
+  arrive<V>(p, sh, at, at.segs - 1 - at.seg, P::start(p, at.n) + at.segs - 1, -1, d, chan, fa,
             fb, carry);
 
   float before[kRun][V];
@@ -654,25 +690,22 @@ __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bw
   }
 }
 
-// dlam from the segments' sums, 64 channels a workgroup: each of four waves adds every
-// fourth sequence's in order, then the four are added.
-__global__ __launch_bounds__(256) void glr_lam_kernel(GlrParams p) {
+// dlam from the segments' sums, 64 channels a workgroup: each of 16 waves adds every
+// sixteenth slot's in order, then the sixteen are added.
+__global__ __launch_bounds__(1024) void glr_lam_kernel(GlrParams p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = blockIdx.x * 64 + lane;
-  __shared__ float part[4][64];
+  __shared__ float part[16][64];
   float sum = 0.f;
   if (d < p.C) {
-    for (int n = wave; n < p.N; n += 4) {
-      int64_t bos, len;
-      chunk::seq_range(p.seq, n, bos, len);
-      constexpr int kSeg = glr_seg(true);
-      const int64_t slot = bos / kSeg + n, count = (len + kSeg - 1) / kSeg;
-      for (int64_t j = 0; j < count; ++j) sum += p.part_lam[(slot + j) * p.C + d];
-    }
+#pragma unroll 8
+    for (int64_t slot = wave; slot < p.slots; slot += 16) sum += p.part_lam[slot * p.C + d];
   }
   part[wave][lane] = sum;
   __syncthreads();
   if (wave == 0 && d < p.C) {
-    sum = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) sum += part[w][lane];
     float sig;
     const float soft = softplus_(p.lam[d], sig);
     // both are exp(lam) where that underflows
@@ -722,7 +755,7 @@ hipError_t launch(const GlrParams& p, hipStream_t s) {
   const int tiles = glr_tiles(p.C);
   if (p.chained) {
     const int64_t groups = glr_slots(p.rows, p.N, glr_seg(BWD) * kGlrGroup);
-    const int64_t pairs = 16 + p.slots * p.C + (groups * p.C + 1) / 2;
+    const int64_t pairs = 16 + p.slots * p.C / 2 + groups * p.C / 2;  // C is even
     hipLaunchKernelGGL(glr_clear_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, s, p.chain, pairs);
   }
   const dim3 grid(static_cast<unsigned>(p.slots * tiles)), block(64 * kGlrWaves);
@@ -733,7 +766,7 @@ hipError_t launch(const GlrParams& p, hipStream_t s) {
       else
         hipLaunchKernelGGL((glr_bwd_kernel<E, V, false>), grid, block, 0, s, p, tiles);
     }
-    hipLaunchKernelGGL(glr_lam_kernel, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL(glr_lam_kernel, dim3(static_cast<unsigned>((p.C + 63) / 64)), dim3(1024), 0, s, p);
   } else {
     if (p.z)
       hipLaunchKernelGGL((glr_fwd_kernel<E, V, true>), grid, block, 0, s, p, tiles);

@@ -35,7 +35,7 @@ struct GlrParams {
   // What the segments of a sequence tell each other (chained): a counter, then words of a
   // value and a mark that it is there.
   uint64_t* chain;     // cleared before the launch: [32] whose first counts workgroups, then
-  uint64_t* whole;     // [segment slot][2][C] decay product and end from zero of a segment
+  uint64_t* whole;     // [segment slot][C] decay product and end from zero of a segment
   uint64_t* end;       // [group slot][C] state behind (backward: gradient in front of) a group
   SeqInfo seq;
   int64_t rows;        // B * T
@@ -48,7 +48,7 @@ struct GlrParams {
 constexpr int kGlrRun = 8;     // tokens that a thread takes one after another
 constexpr int kGlrTile = 64;   // channels of a workgroup: rows of 128 bytes (bf16)
 constexpr int kGlrWaves = 4;
-constexpr int kGlrGroup = 16;  // segments of a group
+constexpr int kGlrGroup = 8;   // segments of a group
 // Channels of a lane.
 constexpr int glr_vec(bool bwd) { return bwd ? 2 : 4; }
 // Tokens of a segment: the runs of a workgroup's lanes.

@@ -45,14 +45,18 @@ gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
   c->state = static_cast<size_t>(p->num_seqs) * c->chan;
   c->saved = static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs, gdn::kGlrRun)) * c->chan;
   const int64_t seg = gdn::glr_seg(bwd);
-  c->slots = gdn::glr_slots(c->rows, p->num_seqs, seg);
+  // dense sequences have the slots that their segments need (one, of no tokens, where T is 0)
+  const auto slots = [p, c](int64_t len) {
+    return p->cu_seqlens_host ? gdn::glr_slots(c->rows, p->num_seqs, len) : p->B * std::max<int64_t>(1, (p->T + len - 1) / len);
+  };
+  c->slots = slots(seg);
   c->chained = max_len > seg;
-  c->whole = static_cast<size_t>(c->slots) * 4 * c->chan;
+  c->whole = static_cast<size_t>(c->slots) * 2 * c->chan;
   c->end = up256(static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs, seg * gdn::kGlrGroup)) * 2 * c->chan);
   c->part = bwd ? static_cast<size_t>(c->slots) * c->chan : 0;
   // workgroups of 256 threads, counted in 32 bits: segments of the longer of the two
   // directions' segments or shorter, so that what the forward takes the backward takes too
-  const int64_t most = gdn::glr_slots(c->rows, p->num_seqs, gdn::glr_seg(true));
+  const int64_t most = slots(gdn::glr_seg(true));
   if (most * gdn::glr_tiles(p->C) >= 1 << 24) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
