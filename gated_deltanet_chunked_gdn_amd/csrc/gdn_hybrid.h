@@ -88,11 +88,12 @@ struct RopeParams {
 // Tokens of a workgroup at a time: four where that leaves every CU several workgroups.
 constexpr int kRopeMost = 4;
 inline int rope_tokens(int64_t tokens) { return tokens >= 1024 * kRopeMost ? kRopeMost : 1; }
-// The backward's workgroups go on to further tokens, so that few partial sums are left.
-constexpr int kRopeBwdGroups = 1024;
-inline int64_t rope_bwd_groups(int64_t tokens) {
+// Workgroups go on to further tokens, so that the weights are loaded once and, in the
+// backward, few partial sums are left.
+constexpr int kRopeGroups = 1024;
+inline int64_t rope_groups(int64_t tokens) {
   const int64_t n = (tokens + rope_tokens(tokens) - 1) / rope_tokens(tokens);
-  return n < kRopeBwdGroups ? n : kRopeBwdGroups;
+  return n < kRopeGroups ? n : kRopeGroups;
 }
 hipError_t launch_rope_fwd(const RopeParams& p, int D, bool bf16, bool interleaved, hipStream_t s);
 hipError_t launch_rope_bwd(const RopeParams& p, int D, bool bf16, bool interleaved, hipStream_t s);

@@ -128,8 +128,6 @@ gdn_status check_rope(const gdn_rope_problem* p, RopeSize* c) {
   c->io = p->io_dtype == GDN_BF16 ? 2 : 4;
   c->tokens = static_cast<int64_t>(p->B) * p->T;
   if (c->tokens > INT32_MAX || c->tokens * (p->Hq + p->Hk) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
-  // 256 threads for every four tokens and more (one below 4096), counted in 32 bits
-  if (c->tokens / gdn::kRopeMost >= INT64_C(1) << 24) return GDN_ERR_UNSUPPORTED;
   const int64_t qrow = static_cast<int64_t>(p->Hq) * p->D, krow = static_cast<int64_t>(p->Hk) * p->D;
   gdn_status st = check_stride(p->q_stride, qrow, c->io, &c->q_stride);
   if (st == GDN_OK) st = check_stride(p->k_stride, krow, c->io, &c->k_stride);
@@ -141,7 +139,7 @@ gdn_status check_rope(const gdn_rope_problem* p, RopeSize* c) {
   c->freq = static_cast<size_t>(p->R) / 2 * 4;
   c->pos = static_cast<size_t>(c->tokens) * 4;
   c->weight = static_cast<size_t>(p->D) * 4;
-  c->ws = static_cast<size_t>(gdn::rope_bwd_groups(c->tokens)) * 2 * c->weight;
+  c->ws = static_cast<size_t>(gdn::rope_groups(c->tokens)) * 2 * c->weight;
   return GDN_OK;
 }
 
@@ -319,7 +317,7 @@ gdn_status gdn_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k,
   if (st != GDN_OK || c.tokens == 0) return st;
   gdn::RopeParams rp = rope_params(p, c, q, k, inv_freq, positions, wq, wk);
   rp.q_out = q_out; rp.k_out = k_out;
-  rp.groups = static_cast<int32_t>((c.tokens + rp.per_group - 1) / rp.per_group);
+  rp.groups = static_cast<int32_t>(gdn::rope_groups(c.tokens));
   return hip_status(gdn::launch_rope_fwd(rp, p->D, c.io == 2, p->interleaved != 0, static_cast<hipStream_t>(stream)));
 }
 
@@ -349,7 +347,7 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k,
   gdn::RopeParams rp = rope_params(p, c, q, k, inv_freq, positions, wq, wk);
   rp.q_out = dq; rp.k_out = dk; rp.dq_out = dq_out; rp.dk_out = dk_out; rp.dwq = dwq; rp.dwk = dwk;
   rp.part = static_cast<float*>(ws);
-  rp.groups = static_cast<int32_t>(gdn::rope_bwd_groups(c.tokens));
+  rp.groups = static_cast<int32_t>(gdn::rope_groups(c.tokens));
   return hip_status(gdn::launch_rope_bwd(rp, p->D, c.io == 2, p->interleaved != 0, static_cast<hipStream_t>(stream)));
 }
 

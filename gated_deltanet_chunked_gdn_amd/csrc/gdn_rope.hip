@@ -85,9 +85,14 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeParams p) {
   for (int k = 0; k < 2; ++k) {
     const float* const ws = k ? p.wk : p.wq;
 #pragma unroll
-    for (int e = 0; e < EPV; ++e) {
-      w[k][e] = ws ? ws[c0 + e] : 1.f;
-      wp[k][e] = ws ? ws[cp + e] : 1.f;
+    for (int e = 0; e < EPV; e += 4) {
+      const f32x4_t one = {1.f, 1.f, 1.f, 1.f};
+      const f32x4_t a = ws ? *reinterpret_cast<const f32x4_t*>(ws + c0 + e) : one, b = ws ? *reinterpret_cast<const f32x4_t*>(ws + cp + e) : one;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[k][e + i] = a[i];
+        wp[k][e + i] = b[i];
+      }
     }
   }
   float dw[2][EPV];
@@ -196,6 +201,7 @@ __global__ __launch_bounds__(1024) void rope_weight_kernel(RopeParams p, int D) 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = blockIdx.x * 64 + lane;  // at: of 2 D
   __shared__ float part[16][64];
   float s = 0.f;
+#pragma unroll 8
   for (int g = wave; g < p.groups; g += 16) s += p.part[static_cast<int64_t>(g) * 2 * D + at];
   part[wave][lane] = s;
   __syncthreads();
