@@ -163,22 +163,29 @@ __global__ __launch_bounds__(256, 2) void swa_step_kernel(SwaParams p) {
   }
 }
 
-// The runs' sums joined in order, a head a workgroup.
+// The runs' sums joined in order, a head a workgroup: a lane takes a run's maximum and sum, 64
+// runs at a time, and a thread a column of the values, several runs' in flight.
 template <typename E, int D>
 __global__ __launch_bounds__(D) void swa_join_kernel(SwaParams p) {
-  const int n = blockIdx.y, x = threadIdx.x;
+  const int n = blockIdx.y, x = threadIdx.x, lane = x & 63;
   const int64_t out = static_cast<int64_t>(n) * p.Hq + blockIdx.x, all = static_cast<int64_t>(p.N) * p.Hq;
-  const float* const vals = p.part + 2 * all * p.splits;
+  const float* const vals = p.part + 2 * all * p.splits + out * D + x;
   const int before = p.lens[n];
   const int count = before < 0 ? 0 : min(before, p.slots - 1) + 1, runs = (count + p.run - 1) / p.run;
   float high = -INFINITY, total = 0.f, o = 0.f;
-  for (int s = 0; s < runs; ++s) high = fmaxf(high, p.part[2 * (s * all + out)]);
-  const float base = high == -INFINITY ? 0.f : high;
-  for (int s = 0; s < runs; ++s) {
-    const float2 t = *reinterpret_cast<const float2*>(p.part + 2 * (s * all + out));
+  for (int s0 = 0; s0 < runs; s0 += 64) {
+    const int many = min(runs - s0, 64);
+    const float2 t = lane < many ? *reinterpret_cast<const float2*>(p.part + 2 * ((s0 + lane) * all + out)) : float2{-INFINITY, 0.f};
+    float m = t.x;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+    const float now = fmaxf(high, m), base = now == -INFINITY ? 0.f : now, fade = exp2_(high - base);
+    high = now;
     const float f = exp2_(t.x - base);
-    total = fmaf(t.y, f, total);
-    o = fmaf(vals[(s * all + out) * D + x], f, o);
+    total = fmaf(total, fade, wave_sum(t.y * f));
+    o *= fade;
+#pragma unroll 8
+    for (int s = 0; s < many; ++s) o = fmaf(vals[(s0 + s) * all * D], __shfl(f, s, 64), o);
   }
   IoT<E>::st(static_cast<E*>(p.o) + out * D + x, before < 0 ? 0.f : o / total);
 }

@@ -46,6 +46,10 @@ def _problem(kind, sizes, *rest):
     return kind(*sizes, *rest)
 
 
+def _like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 # a problem of dense tensors: the same sizes give the same (never written) structure
 _dense = functools.lru_cache(maxsize=256)(_problem)
 
@@ -222,7 +226,7 @@ def rope_fwd(q, k, inv_freq, positions=None, norm="rms", eps: float = 1e-6, wq=N
     ins = _rope_inputs(prob, inv_freq, positions, wq, wk, dev)
     outs = []
     for out, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        out = torch.empty(like.shape, dtype=like.dtype, device=dev) if out is None else out
+        out = _like(like) if out is None else out
         outs.append((out, _want(out, like.shape, like.dtype, dev, name)))
     _call(dev, "gdn_rope_fwd", prob, qp, kp, *ins, outs[0][1], outs[1][1])
     return outs[0][0], outs[1][0]
@@ -237,8 +241,7 @@ def rope_bwd(q, k, inv_freq, dq_out, dk_out, positions=None, norm="rms", eps: fl
     grads = (_want(dq_out, q.shape, q.dtype, dev, "dq_out"), _want(dk_out, k.shape, q.dtype, dev, "dk_out"))
     need = _size("gdn_rope_workspace_size", prob) if wq is not None or wk is not None else 0
     buf, ws, nws = _buffer(workspace, need, dev, "workspace")
-    fresh = lambda t: torch.empty(t.shape, dtype=t.dtype, device=dev) if t is not None else None  # noqa: E731
-    out = {"dq": fresh(q), "dk": fresh(k), "dwq": fresh(wq), "dwk": fresh(wk)}
+    out = {name: _like(t) if t is not None else None for name, t in (("dq", q), ("dk", k), ("dwq", wq), ("dwk", wk))}
     _call(dev, "gdn_rope_bwd", prob, qp, kp, *ins, *grads, *(t.data_ptr() if t is not None else None for t in out.values()),
           ws, nws)
     return out
@@ -269,7 +272,7 @@ def swa_fwd(q, k, v, window: int, sinks: int = 0, scale: float = 1.0, cu_seqlens
     D 64 or 128.  A query sees the last ``window`` tokens, itself among them, and the first
     ``sinks`` of its sequence.  Returns o, or (o, lse) with lse (B, T, Hq) fp32."""
     dev, seqs, prob, ptrs = _swa_problem(q, k, v, window, sinks, scale, cu_seqlens)  # seqs: keeps the offsets alive
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+    o = _like(q) if out is None else out
     optr = _want(o, q.shape, q.dtype, dev, "out")
     lse = torch.empty(q.shape[:3], dtype=_F32, device=dev) if return_lse else None
     _call(dev, "gdn_swa_fwd", prob, *ptrs, optr, lse.data_ptr() if return_lse else None)
@@ -281,7 +284,7 @@ def swa_bwd(q, k, v, o, lse, do, window: int, sinks: int = 0, scale: float = 1.0
     dev, seqs, prob, ptrs = _swa_problem(q, k, v, window, sinks, scale, cu_seqlens)  # seqs: keeps the offsets alive
     ins = (_want(o, q.shape, q.dtype, dev, "o"), _want(lse, q.shape[:3], _F32, dev, "lse"), _want(do, q.shape, q.dtype, dev, "do"))
     buf, ws, nws = _buffer(workspace, _size("gdn_swa_workspace_size", prob, nat.GDN_SWA_BWD), dev, "workspace")
-    out = {name: torch.empty(t.shape, dtype=t.dtype, device=dev) for name, t in (("dq", q), ("dk", k), ("dv", v))}
+    out = {name: _like(t) for name, t in (("dq", q), ("dk", k), ("dv", v))}
     _call(dev, "gdn_swa_bwd", prob, *ptrs, *ins, *(t.data_ptr() for t in out.values()), ws, nws)
     return out
 
@@ -314,7 +317,7 @@ def swa_step(q, k, v, kcache, vcache, lens, sinks: int = 0, scale: float = 1.0, 
     shape = (prob.B, slots, prob.Hk, prob.D)
     caches = (_want(kcache, shape, q.dtype, dev, "kcache"), _want(vcache, shape, q.dtype, dev, "vcache"))
     lp = _want(lens, (prob.B,), _I32, dev, "lens")
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+    o = _like(q) if out is None else out
     optr = _want(o, q.shape, q.dtype, dev, "out")
     need = _step_size(prob.B, prob.Hq, prob.Hk, prob.D, prob.window, prob.sinks, prob.io_dtype)
     buf, ws, nws = _buffer(workspace, need, dev, "workspace")
