@@ -92,10 +92,11 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   float own[CT];
 #pragma unroll
   for (int u = 0; u < CT; ++u) own[u] = 0.f;
+  const Stage<E, D, KT> stage_k(p.k_stride), stage_v(p.v_stride);
   auto fetch = [&](int t) {
     const int j0 = start(t >= tiles ? t - tiles : t);
-    Stage<E, D, KT>::load(Kt[t & 1], kb + j0 * p.k_stride, p.k_stride, len - j0);
-    Stage<E, D, KT>::load(Vt[t & 1], vb + j0 * p.v_stride, p.v_stride, len - j0);
+    stage_k.load(Kt[t & 1], kb + j0 * p.k_stride, len - j0);
+    stage_v.load(Vt[t & 1], vb + j0 * p.v_stride, len - j0);
   };
   fetch(0);
   for (int t = 0; t < steps; ++t) {
@@ -113,10 +114,13 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
         delta[u] += __shfl_xor(delta[u], 32, 64);
       }
     }
-    if (wq0 >= len || j0 > wq1 || (j0 + KT - 1 <= wq0 - p.W && j0 >= p.S)) continue;
-    const bool whole = j0 + KT - 1 <= wq0 && j0 > wq1 - p.W;
-#pragma unroll
+    if (wq0 >= len) continue;
+    // a step of the second product at a time: none seen, all seen, or a mask
+#pragma unroll 1
     for (int b0 = 0; b0 < 4; b0 += KB) {
+      const int jb = j0 + 16 * b0, je = jb + 16 * KB - 1;
+      if (jb > wq1 || (je <= wq0 - p.W && jb >= p.S)) continue;
+      const bool whole = je <= wq0 && jb > wq1 - p.W;
       f32x4_t s[KB][CT], dp[KB][CT];
 #pragma unroll
       for (int b = 0; b < KB; ++b) {
@@ -149,7 +153,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
           for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              s[b][u][r] = sees(wq0 + 16 * u + c, j0 + 16 * (b0 + b) + 4 * g + r, p.W, p.S) ? s[b][u][r] : 0.f;
+              s[b][u][r] = sees(wq0 + 16 * u + c, jb + 16 * b + 4 * g + r, p.W, p.S) ? s[b][u][r] : 0.f;
       }
       if (sums) {
 #pragma unroll
@@ -229,7 +233,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
   __shared__ alignas(16) E raw[2][2][QT * D];  // two tiles of queries and of do
   __shared__ alignas(16) float lt[2][QT], dt[2][QT];
 
-  Stage<E, D, KT>::load(Ks, static_cast<const E*>(p.k) + (bos + k0) * p.k_stride + hk * D, p.k_stride, len - k0);
+  Stage<E, D, KT>(p.k_stride).load(Ks, static_cast<const E*>(p.k) + (bos + k0) * p.k_stride + hk * D, len - k0);
   u32x4_t vf[CT][NS];
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
@@ -246,11 +250,13 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
 
   const int tiles = (i1 - i0) / QT + 1, steps = group * tiles;
   const float scale2 = p.scale * kLog2e;
+  const int64_t d_stride = static_cast<int64_t>(p.Hq) * D;
+  const Stage<E, D, QT> stage_q(p.q_stride), stage_d(d_stride);
   float rl = 0.f, rd = 0.f;
   auto fetch = [&](int step) {
     const int h = hk * group + step / tiles, row = i0 + (step % tiles) * QT;
-    Stage<E, D, QT>::load(raw[step & 1][0], static_cast<const E*>(p.q) + (bos + row) * p.q_stride + h * D, p.q_stride, len - row);
-    Stage<E, D, QT>::load(raw[step & 1][1], static_cast<const E*>(p.dout) + ((bos + row) * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, len - row);
+    stage_q.load(raw[step & 1][0], static_cast<const E*>(p.q) + (bos + row) * p.q_stride + h * D, len - row);
+    stage_d.load(raw[step & 1][1], static_cast<const E*>(p.dout) + (bos + row) * d_stride + h * D, len - row);
     if (threadIdx.x < QT) {
       const int64_t at = (bos + min(row + static_cast<int>(threadIdx.x), len - 1)) * p.Hq + h;
       rl = p.lse[at] * kLog2e;

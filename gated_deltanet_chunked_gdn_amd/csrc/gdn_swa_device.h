@@ -113,27 +113,39 @@ __device__ __forceinline__ u32x4_t load_row(const typename Op::elem* row, int s,
 template <typename E, int D, int ROWS>
 struct Stage {
   using T = Tile<E, D>;
-  static constexpr int kRows = 64 / T::kPieces;      // rows of a wave's load
+  static constexpr int kRows = 64 / T::kPieces;                    // rows of a wave's load
   static constexpr int kN = (ROWS + 4 * kRows - 1) / (4 * kRows);  // loads of a wave
-  // `rows` rows (any number; those of the tile count) from `base` on, `stride` values apart
-  static __device__ __forceinline__ void load(E* tile, const E* base, int64_t stride, int rows) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = min(rows, ROWS), step = static_cast<int>(stride) * static_cast<int>(sizeof(E));
+  static constexpr int kKinds = 4 * kRows % 16 && T::kPieces > 8 ? 2 : 1;  // swizzles of a lane's rows
+  uint32_t off[kKinds];  // of this lane's piece in the first loads
+  uint32_t step, wave;   // bytes from row to row
+  // `stride` values from row to row
+  __device__ __forceinline__ explicit Stage(int64_t stride) {
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    step = static_cast<uint32_t>(stride) * sizeof(E);
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < kKinds; ++i) {
+      const int row = (4 * i + wave) * kRows + lane / T::kPieces;
+      off[i] = row * step + ((lane % T::kPieces) ^ T::swizzle(row)) * 16;
+    }
+  }
+  // `rows` rows (any number; those of the tile count) from `base` on
+  __device__ __forceinline__ void load(E* tile, const E* base, int rows) const {
+    const int n = min(rows, ROWS);
     // as chunk::buffer_rsrc
     const uint64_t at = reinterpret_cast<uint64_t>(base);
     const u32x4_t r = {static_cast<uint32_t>(at), static_cast<uint32_t>(at >> 32) & 0xffffu,
-                       static_cast<uint32_t>(n > 0 ? (n - 1) * step + D * static_cast<int>(sizeof(E)) : 0), 0x00020000u};
+                       n > 0 ? (n - 1) * step + D * static_cast<uint32_t>(sizeof(E)) : 0u, 0x00020000u};
+    const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)tile)) + wave * 1024;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int first = (4 * i + wave) * kRows, row = first + lane / T::kPieces;
-      if (ROWS % (4 * kRows) && first >= ROWS) break;  // fewer rows than four waves take
-      const int off = row * step + ((lane % T::kPieces) ^ T::swizzle(row)) * 16;
-      const uint32_t to = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(tile + first * D)));
+      if (ROWS % (4 * kRows) && (4 * i + wave) * kRows >= ROWS) break;  // fewer rows than four waves take
+      const uint32_t from = off[i % kKinds] + i / kKinds * kKinds * 4 * kRows * step;
       // In assembly, since the compiler would wait for the next tile's loads before it reads this
       // one: it cannot tell the two buffers apart.  Nothing is written to a register; M0 names
       // the place in LDS (a wait state between its write and the load).  The compiler keeps
       // nothing in M0 from one instruction to another; the kernels here have no other use of it.
-      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(r) : "memory");
+      asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to + i * 4096), "v"(from), "s"(r) : "memory");
     }
   }
 };

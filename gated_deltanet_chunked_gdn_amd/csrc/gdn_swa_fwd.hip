@@ -58,6 +58,39 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   const int nfirst = (min(p.S, win) + KT - 1) / KT, tiles = nfirst + (last - win) / KT + 1;
   auto start = [&](int t) { return t < nfirst ? t * KT : win + (t - nfirst) * KT; };
 
+  // What the queries do not see of a tile to minus infinity.  Tiles of first tokens lie before
+  // every window; of tiles behind the first tokens the window is all.
+  auto mask = [&](bool first, int j0, f32x4_t (*to)[CT]) {
+    if (first) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool ok = j0 + 16 * b + 4 * g + r < p.S;
+#pragma unroll
+          for (int u = 0; u < CT; ++u) to[b][u][r] = ok ? to[b][u][r] : -INFINITY;
+        }
+    } else if (j0 >= p.S) {
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        const int back = wq0 + 16 * u + c - j0 - 4 * g;  // from the lane's first key to the query
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            to[b][u][r] = static_cast<uint32_t>(back - 16 * b - r) < static_cast<uint32_t>(p.W) ? to[b][u][r] : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < CT; ++u)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            to[b][u][r] = sees(wq0 + 16 * u + c, j0 + 16 * b + 4 * g + r, p.W, p.S) ? to[b][u][r] : -INFINITY;
+    }
+  };
+
   f32x4_t acc[ND][CT];
   float top[CT], sum[CT];  // the exponents' base, in base 2, and the sum of this lane's keys
 #pragma unroll
@@ -68,69 +101,34 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     for (int d = 0; d < ND; ++d) acc[d][t] = zero4();
   }
   const float scale2 = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);  // not zero: -inf stays what is masked
-  auto fetch = [&](int t) {
-    const int j0 = start(t);
-    Stage<E, D, KT>::load(Kt[t & 1], kb + j0 * p.k_stride, p.k_stride, len - j0);
-    Stage<E, D, KT>::load(Vt[t & 1], vb + j0 * p.v_stride, p.v_stride, len - j0);
+  const Stage<E, D, KT> stage_k(p.k_stride), stage_v(p.v_stride);
+  auto fetch_k = [&](int t) {
+    if (t < tiles) stage_k.load(Kt[t & 1], kb + start(t) * p.k_stride, len - start(t));
   };
-  fetch(0);
-  for (int t = 0; t < tiles; ++t) {
+  auto fetch_v = [&](int t) {
+    if (t < tiles) stage_v.load(Vt[t & 1], vb + start(t) * p.v_stride, len - start(t));
+  };
+  // some query of this wave's sees a key of the tile
+  auto some = [&](int t) {
     const int j0 = start(t);
+    return t < tiles && wq0 < len && j0 <= wq1 && (j0 + KT - 1 > wq0 - p.W || j0 < p.S);
+  };
+  f32x4_t s[4][CT], next[4][CT];
+  auto scores = [&](int t, f32x4_t (*to)[CT]) {
     const E* const Ks = Kt[t & 1];
-    const E* const Vs = Vt[t & 1];
-    landed();
-    __syncthreads();  // and the other buffer is read
-    if (t + 1 < tiles) fetch(t + 1);
-    if (wq0 >= len || j0 > wq1 || (j0 + KT - 1 <= wq0 - p.W && j0 >= p.S)) continue;
-    f32x4_t s[4][CT];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
 #pragma unroll
-      for (int u = 0; u < CT; ++u) s[b][u] = zero4();
+      for (int u = 0; u < CT; ++u) to[b][u] = zero4();
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
         const u32x4_t a = read_row<Op, D>(Ks, 16 * b, n, lane);
 #pragma unroll
-        for (int u = 0; u < CT; ++u) s[b][u] = Op::mma(a, qf[u][n], s[b][u]);
+        for (int u = 0; u < CT; ++u) to[b][u] = Op::mma(a, qf[u][n], to[b][u]);
       }
     }
-    if (!(j0 + KT - 1 <= wq0 && j0 > wq1 - p.W)) {
-      seldom();
-#pragma unroll
-      for (int u = 0; u < CT; ++u)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            s[b][u][r] = sees(wq0 + 16 * u + c, j0 + 16 * b + 4 * g + r, p.W, p.S) ? s[b][u][r] : -INFINITY;
-    }
-    float high[CT];
-    bool rise = false;
-#pragma unroll
-    for (int u = 0; u < CT; ++u) {
-      high[u] = -INFINITY;
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) high[u] = fmaxf(high[u], s[b][u][r]);
-      // a score may pass the base by 2^8 before all that has been summed is brought to a new
-      // one: powers of two change no rounding, and after a few tiles no base moves
-      rise |= high[u] * scale2 > top[u] + 8.f;
-    }
-    if (__any(rise)) {
-#pragma unroll
-      for (int u = 0; u < CT; ++u) {
-        float m = fmaxf(high[u], __shfl_xor(high[u], 16, 64));
-        m = fmaxf(m, __shfl_xor(m, 32, 64));
-        const float now = fmaxf(top[u], m * scale2);
-        const float fade = now == -INFINITY ? 1.f : exp2_(top[u] - now);
-        top[u] = now;
-        sum[u] *= fade;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d][u] *= fade;
-      }
-    }
-    u32x4_t pf[NR][CT];
+  };
+  auto exponentials = [&]() {
 #pragma unroll
     for (int u = 0; u < CT; ++u) {
       const float base = top[u] == -INFINITY ? 0.f : top[u];  // nothing seen yet
@@ -142,21 +140,80 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
           sum[u] += s[b][u][r];
         }
     }
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
+  };
+  // The scores are formed a tile ahead, so that their products run beside the exponentials of
+  // the tile before; keys are loaded a tile ahead of the values for that.
+  fetch_k(0);
+  landed();
+  __syncthreads();
+  fetch_v(0);
+  fetch_k(1);
+  bool now = some(0);
+  if (now) scores(0, s);
+  for (int t = 0; t < tiles; ++t) {
+    const int j0 = start(t);
+    landed();
+    __syncthreads();  // values of this tile and keys of the next are there, those of the last two read
+    fetch_v(t + 1);
+    fetch_k(t + 2);
+    const bool then = some(t + 1);
+    if (now) {
+      if (!(j0 + KT - 1 <= wq0 && j0 > wq1 - p.W)) {
+        seldom();
+        mask(t < nfirst, j0, s);
+      }
+      float high[CT];
+      bool rise = false;
 #pragma unroll
       for (int u = 0; u < CT; ++u) {
-        const f32x4_t two[2] = {s[n * Op::kBlocks][u], s[n * Op::kBlocks + Op::kBlocks - 1][u]};
-        pf[n][u] = Op::operand(two);
+        high[u] = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) high[u] = fmaxf(high[u], s[b][u][r]);
+        // a score may pass the base by 2^8 before all that has been summed is brought to a new
+        // one: powers of two change no rounding, and after a few tiles no base moves
+        rise |= high[u] * scale2 > top[u] + 8.f;
       }
+      if (__any(rise)) {
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
+        for (int u = 0; u < CT; ++u) {
+          float m = fmaxf(high[u], __shfl_xor(high[u], 16, 64));
+          m = fmaxf(m, __shfl_xor(m, 32, 64));
+          const float base = fmaxf(top[u], m * scale2);
+          const float fade = base == -INFINITY ? 1.f : exp2_(top[u] - base);
+          top[u] = base;
+          sum[u] *= fade;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const u32x4_t a = Op::template read_tr<D>(Vs, n * 16 * Op::kBlocks, 16 * d, lane);
-#pragma unroll
-        for (int u = 0; u < CT; ++u) acc[d][u] = Op::mma(a, pf[n][u], acc[d][u]);
+          for (int d = 0; d < ND; ++d) acc[d][u] *= fade;
+        }
       }
+      scores(t + 1, next);  // whether there is one or not: no branch between these and the exponentials
+      exponentials();
+      const E* const Vs = Vt[t & 1];
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        u32x4_t pf[CT];
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          const f32x4_t two[2] = {s[n * Op::kBlocks][u], s[n * Op::kBlocks + Op::kBlocks - 1][u]};
+          pf[u] = Op::operand(two);
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const u32x4_t a = Op::template read_tr<D>(Vs, n * 16 * Op::kBlocks, 16 * d, lane);
+#pragma unroll
+          for (int u = 0; u < CT; ++u) acc[d][u] = Op::mma(a, pf[u], acc[d][u]);
+        }
+      }
+    } else if (then) {
+      scores(t + 1, next);
+    }
+    now = then;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int u = 0; u < CT; ++u) s[b][u] = next[b][u];
   }
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
