@@ -23,24 +23,16 @@ using namespace swa;
 
 // ---------------------------------------------------------------------------- dq
 
-// CT: 16-query columns of a wave, as in the forward.
-template <typename Op, int D, int CT>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
+// dq and delta of a block of queries, as the forward's attend.
+template <typename Op, int D, int CT, bool CAREFUL>
+__device__ __forceinline__ bool dq_block(const SwaParams& p, int64_t bos, int len, int q0, int h, int hk,
+                                         typename Op::elem (*Kt)[64 * D], typename Op::elem (*Vt)[64 * D]) {
   using E = typename Op::elem;
   constexpr int KT = 64, QB = 64 * CT, NS = D / Op::kCols, ND = D / 16, KB = Op::kBlocks;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int thread = threadIdx.x;
+  if (CAREFUL) asm volatile("" : "+v"(thread), "+s"(q0), "+s"(h), "+s"(hk));  // no register holds anything for the second time
+  const int lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int item = xcd_item(blockIdx.x, items);
-  if (item >= items) return;
-  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
-  const int block = rest / group, h = hk * group + rest - block * group;
-  int64_t bos, len64;
-  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64), q0 = block * QB;
-  if (q0 >= len) return;
-
-  __shared__ alignas(16) E Kt[2][KT * D], Vt[2][KT * D];
-
   const int wq0 = q0 + 16 * CT * wave, wq1 = min(wq0 + 16 * CT - 1, len - 1);
   u32x4_t qf[CT][NS], df[CT][NS];
   float lse2[CT], delta[CT];
@@ -70,7 +62,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     dot += __shfl_xor(dot, 16, 64);
     dot += __shfl_xor(dot, 32, 64);
     delta[t] = dot;
-    lse2[t] = p.lse[at] * kLog2e;
+    lse2[t] = odd_(p.lse[at]) ? __uint_as_float(0x7fc00000u) : p.lse[at] * kLog2e;  // no probability of an infinite sum
   }
   const E* const kb = static_cast<const E*>(p.k) + bos * p.k_stride + hk * D;
   const E* const vb = static_cast<const E*>(p.v) + bos * p.v_stride + hk * D;
@@ -92,7 +84,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   float own[CT];
 #pragma unroll
   for (int u = 0; u < CT; ++u) own[u] = 0.f;
-  const Stage<E, D, KT> stage_k(p.k_stride), stage_v(p.v_stride);
+  const Stage<E, D, KT> stage_k(p.k_stride, thread), stage_v(p.v_stride, thread);
   auto fetch = [&](int t) {
     const int j0 = start(t >= tiles ? t - tiles : t);
     stage_k.load(Kt[t & 1], kb + j0 * p.k_stride, len - j0);
@@ -172,7 +164,10 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
       }
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        const u32x4_t a = Op::template read_tr<D>(Ks, 16 * b0, 16 * d, lane);
+        if (CAREFUL) __builtin_amdgcn_sched_barrier(0);  // few registers: one operand after the other
+        u32x4_t a = Op::template read_tr<D>(Ks, 16 * b0, 16 * d, lane);
+        // who sees such a key has NaN for its probability, unless that is zero
+        if (CAREFUL && !whole) a = clean_<E>(a);
 #pragma unroll
         for (int u = 0; u < CT; ++u) acc[d][u] = Op::mma(a, sf[u], acc[d][u]);
       }
@@ -181,15 +176,39 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 #pragma unroll
   for (int u = 0; u < CT; ++u)
     if (g == 0 && wq0 + 16 * u + c < len) p.delta[(bos + wq0 + 16 * u + c) * p.Hq + h] = delta[u];
+  float rest = 0.f;  // NaN, if some sum is not finite
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
     const int i = wq0 + 16 * u + c;
     if (i >= len) continue;
     E* const row = static_cast<E*>(p.dq) + ((bos + i) * p.Hq + h) * D;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rest = fmaf(acc[d][u][r], 0.f, rest);
       chunk::store4<E>(row + 16 * d + 4 * g, acc[d][u][0] * p.scale, acc[d][u][1] * p.scale, acc[d][u][2] * p.scale, acc[d][u][3] * p.scale);
+    }
   }
+  return rest != 0.f;
+}
+
+template <typename Op, int D, int CT>
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
+  const int item = xcd_item(blockIdx.x, items);
+  if (item >= items) return;
+  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
+  const int block = rest / group, h = hk * group + rest - block * group;
+  int64_t bos, len64;
+  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
+  const int len = static_cast<int>(len64), q0 = block * 64 * CT;
+  if (q0 >= len) return;
+
+  __shared__ alignas(16) typename Op::elem Kt[2][64 * D], Vt[2][64 * D];
+  __shared__ int found;
+  if (threadIdx.x == 0) found = 0;
+  if (dq_block<Op, D, CT, false>(p, bos, len, q0, h, hk, Kt, Vt)) found = 1;
+  __syncthreads();
+  if (found) dq_block<Op, D, CT, true>(p, bos, len, q0, h, hk, Kt, Vt);
 }
 
 // ---------------------------------------------------------------------------- dk, dv
@@ -259,15 +278,15 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
     stage_d.load(raw[step & 1][1], static_cast<const E*>(p.dout) + (bos + row) * d_stride + h * D, len - row);
     if (threadIdx.x < QT) {
       const int64_t at = (bos + min(row + static_cast<int>(threadIdx.x), len - 1)) * p.Hq + h;
-      rl = p.lse[at] * kLog2e;
+      rl = odd_(p.lse[at]) ? __uint_as_float(0x7fc00000u) : p.lse[at] * kLog2e;
       rd = p.delta[at];
     }
   };
   fetch(0);
   for (int step = 0; step < steps; ++step) {
     const int r0 = i0 + (step % tiles) * QT;
-    const E* const Qs = raw[step & 1][0];
-    const E* const Ds = raw[step & 1][1];
+    E* const Qs = raw[step & 1][0];
+    E* const Ds = raw[step & 1][1];
     const float* const ls = lt[step & 1];
     const float* const dl = dt[step & 1];
     landed();
@@ -277,6 +296,20 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
     }
     __syncthreads();  // and the other buffer is read
     if (step + 1 < steps) fetch(step + 1);
+    // Queries, or rows of do, that are not finite, where some key is not seen by them: their
+    // lse, or their delta, is not finite either.  Those keys that they see get NaN from it.
+    bool strange = false;
+    if (FAR || r0 < k0 + KT - 1 || r0 + QT - k0 > p.W) {
+      seldom();
+#pragma unroll
+      for (int i = 0; i < QT; i += 64) strange |= odd_(ls[i + lane % QT]) || odd_(dl[i + lane % QT]);
+      strange = __any(strange);  // the same in all waves
+      if (strange) {
+        clean_part<E, QT * D>(Qs);
+        clean_part<E, QT * D>(Ds);
+        __syncthreads();
+      }
+    }
 #pragma unroll
     for (int b1 = 0; b1 < (PART ? KB : QT / 16); b1 += KB) {
       const int b0 = PART ? KB * wave : b1;
@@ -349,6 +382,18 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
           av[d][u] = Op::mma(da, pf[u], av[d][u]);
           ak[d][u] = Op::mma(qa, sf[u], ak[d][u]);
         }
+      }
+    }
+    if (strange) {
+#pragma unroll 1
+      for (int i = r0; i < min(r0 + QT, len); ++i) {
+        bool in[CT];
+#pragma unroll
+        for (int u = 0; u < CT; ++u) {
+          const int j = wk0 + 16 * u + c;
+          in[u] = j < len && (FAR ? j < p.S && i - j >= p.W : j <= i && i - j < p.W);
+        }
+        spoil<E, ND, CT>(av, static_cast<const E*>(p.dout) + (bos + i) * d_stride + (hk * group + step / tiles) * D, in, lane);
       }
     }
   }

@@ -119,10 +119,10 @@ struct Stage {
   uint32_t off[kKinds];  // of this lane's piece in the first loads
   uint32_t step, wave;   // bytes from row to row
   // `stride` values from row to row
-  __device__ __forceinline__ explicit Stage(int64_t stride) {
-    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __device__ __forceinline__ explicit Stage(int64_t stride, int thread = threadIdx.x) {
+    wave = __builtin_amdgcn_readfirstlane(thread >> 6);
     step = static_cast<uint32_t>(stride) * sizeof(E);
-    const int lane = threadIdx.x & 63;
+    const int lane = thread & 63;
 #pragma unroll
     for (int i = 0; i < kKinds; ++i) {
       const int row = (4 * i + wave) * kRows + lane / T::kPieces;
@@ -161,6 +161,53 @@ __device__ __forceinline__ void seldom() { __builtin_amdgcn_wave_barrier(); }
 // Query i sees key j: no later one, and of the earlier ones the last W (itself among them)
 // and the first S.
 __device__ __forceinline__ bool sees(int i, int j, int W, int S) { return j <= i && (j > i - W || j < S); }
+
+// Infinities and NaN.  A row that some columns of a product do not see stands there with
+// zeros, and zero times what is not finite would be NaN.  So where a tile is not seen whole,
+// such values are taken out of it (clean), and whoever has seen one becomes NaN (spoil).
+__device__ __forceinline__ bool odd_(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+// The values of a register that are not finite to zero.
+template <typename E>
+__device__ __forceinline__ uint32_t clean_(uint32_t w) {
+  if constexpr (sizeof(E) == 4) return (w & 0x7f800000u) == 0x7f800000u ? 0u : w;
+  return w & (((w & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u));
+}
+template <typename E>
+__device__ __forceinline__ u32x4_t clean_(u32x4_t v) {
+  return u32x4_t{clean_<E>(v[0]), clean_<E>(v[1]), clean_<E>(v[2]), clean_<E>(v[3])};
+}
+// By all 256 threads: whether this thread's part of a tile holds such values.
+template <typename E, int SIZE>
+__device__ __forceinline__ bool odd_part(const E* tile) {
+  bool mine = false;
+#pragma unroll
+  for (int i = 0; i < SIZE * static_cast<int>(sizeof(E)) / 4096; ++i) {
+    const u32x4_t v = reinterpret_cast<const u32x4_t*>(tile)[256 * i + threadIdx.x], w = clean_<E>(v);
+    mine |= w[0] != v[0] || w[1] != v[1] || w[2] != v[2] || w[3] != v[3];
+  }
+  return mine;
+}
+template <typename E, int SIZE>
+__device__ __forceinline__ void clean_part(E* tile) {
+#pragma unroll 1
+  for (int i = 0; i < SIZE * static_cast<int>(sizeof(E)) / 4096; ++i) {
+    u32x4_t* const v = reinterpret_cast<u32x4_t*>(tile) + 256 * i + threadIdx.x;
+    *v = clean_<E>(*v);
+  }
+}
+// The sums of those columns that see row `row`, where its value is not finite.  `values`: the
+// row, whole; column u of this lane sees it if sees[u].
+template <typename E, int ND, int CT>
+__device__ __forceinline__ void spoil(f32x4_t (*acc)[CT], const E* values, const bool* sees, int lane) {
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const bool bad = odd_(IoT<E>::ld(values + 16 * d + 4 * (lane >> 4) + r));
+#pragma unroll
+      for (int u = 0; u < CT; ++u) acc[d][u][r] = bad && sees[u] ? __uint_as_float(0x7fc00000u) : acc[d][u][r];
+    }
+}
 
 // Workgroups x, x + 8, ... share an XCD and its L2: items in order, an eighth of them each.
 __device__ __forceinline__ int xcd_item(int x, int items) { return (x & 7) * ((items + 7) / 8) + (x >> 3); }

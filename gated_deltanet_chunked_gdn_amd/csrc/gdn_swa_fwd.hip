@@ -18,25 +18,16 @@ namespace {
 
 using namespace swa;
 
-// CT: 16-query columns of a wave, two or, where that leaves CUs without work, one.
-template <typename Op, int D, int CT>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int blocks) {
+// The outputs of a block of queries q0 .. (CT 16-query columns of a wave: two or, where that
+// leaves CUs without work, one); whether this lane's sums are not all finite.  CAREFUL: values
+// that are not finite reach the queries that see them alone.
+template <typename Op, int D, int CT, bool CAREFUL>
+__device__ __forceinline__ bool attend(const SwaParams& p, int64_t bos, int len, int q0, int h, int hk,
+                                       typename Op::elem (*Kt)[64 * D], typename Op::elem (*Vt)[64 * D], int* odd) {
   using E = typename Op::elem;
   constexpr int KT = 64, QB = 64 * CT, NS = D / Op::kCols, NR = 4 / Op::kBlocks, ND = D / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int item = xcd_item(blockIdx.x, items);
-  if (item >= items) return;
-  // a key head's query heads next to each other, then its blocks of queries
-  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
-  const int block = rest / group, h = hk * group + rest - block * group;
-  int64_t bos, len64;
-  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64), q0 = block * QB;
-  if (q0 >= len) return;
-
-  __shared__ alignas(16) E Kt[2][KT * D], Vt[2][KT * D];
-
   const int wq0 = q0 + 16 * CT * wave, wq1 = min(wq0 + 16 * CT - 1, len - 1);  // this wave's queries; none if wq0 >= len
   u32x4_t qf[CT][NS];
 #pragma unroll
@@ -143,6 +134,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
   };
   // The scores are formed a tile ahead, so that their products run beside the exponentials of
   // the tile before; keys are loaded a tile ahead of the values for that.
+  if (CAREFUL && threadIdx.x == 0) odd[0] = 0;
   fetch_k(0);
   landed();
   __syncthreads();
@@ -157,6 +149,19 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     fetch_v(t + 1);
     fetch_k(t + 2);
     const bool then = some(t + 1);
+    bool strange = false;
+    if constexpr (CAREFUL) {
+      if (threadIdx.x == 0) odd[(t + 1) & 1] = 0;
+      if (j0 + KT - 1 > q0 || j0 <= last - p.W) {  // some query does not see all of it
+        if (odd_part<E, KT * D>(Vt[t & 1])) odd[t & 1] = 1;
+        __syncthreads();
+        strange = odd[t & 1] != 0;
+        if (strange) {
+          clean_part<E, KT * D>(Vt[t & 1]);
+          __syncthreads();
+        }
+      }
+    }
     if (now) {
       if (!(j0 + KT - 1 <= wq0 && j0 > wq1 - p.W)) {
         seldom();
@@ -206,6 +211,15 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
           for (int u = 0; u < CT; ++u) acc[d][u] = Op::mma(a, pf[u], acc[d][u]);
         }
       }
+      if (CAREFUL && strange) {
+#pragma unroll 1
+        for (int j = j0; j < min(j0 + KT, len); ++j) {
+          bool in[CT];
+#pragma unroll
+          for (int u = 0; u < CT; ++u) in[u] = sees(wq0 + 16 * u + c, j, p.W, p.S);
+          spoil<E, ND, CT>(acc, vb + j * p.v_stride, in, lane);
+        }
+      }
     } else if (then) {
       scores(t + 1, next);
     }
@@ -215,6 +229,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 #pragma unroll
       for (int u = 0; u < CT; ++u) s[b][u] = next[b][u];
   }
+  float rest = 0.f;  // NaN, if some sum is not finite
 #pragma unroll
   for (int u = 0; u < CT; ++u) {
     const int i = wq0 + 16 * u + c;
@@ -225,10 +240,37 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
     const float inv = 1.f / total;
     E* const row = static_cast<E*>(p.o) + ((bos + i) * p.Hq + h) * D;
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) rest = fmaf(acc[d][u][r], 0.f, rest);
       chunk::store4<E>(row + 16 * d + 4 * g, acc[d][u][0] * inv, acc[d][u][1] * inv, acc[d][u][2] * inv, acc[d][u][3] * inv);
+    }
     if (p.lse && g == 0) p.lse[(bos + i) * p.Hq + h] = kLn2 * (top[u] + __builtin_amdgcn_logf(total));
   }
+  return rest != 0.f;
+}
+
+template <typename Op, int D, int CT>
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int blocks) {
+  const int item = xcd_item(blockIdx.x, items);
+  if (item >= items) return;
+  // a key head's query heads next to each other, then its blocks of queries
+  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
+  const int block = rest / group, h = hk * group + rest - block * group;
+  int64_t bos, len64;
+  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
+  const int len = static_cast<int>(len64), q0 = block * 64 * CT;
+  if (q0 >= len) return;
+
+  __shared__ alignas(16) typename Op::elem Kt[2][64 * D], Vt[2][64 * D];
+  __shared__ int odd[2], found;
+  if (threadIdx.x == 0) found = 0;
+  // sums that are not finite: once more, with care for those that should be
+  if (attend<Op, D, CT, false>(p, bos, len, q0, h, hk, Kt, Vt, odd)) found = 1;
+  __syncthreads();
+  int again = q0;
+  asm volatile("" : "+s"(again));  // nothing of the first time is kept in registers for it
+  if (found) attend<Op, D, CT, true>(p, bos, len, again, h, hk, Kt, Vt, odd);
 }
 
 template <typename Op, int D, int CT>

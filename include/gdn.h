@@ -688,7 +688,10 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
  * every sequence), else GDN_ERR_UNSUPPORTED.
  * Scores, sums and statistics of the softmax are fp32; with bf16 io the probabilities and
  * the scores' gradients are rounded to bf16 as operands of the products that sum over them.
- * Outputs are rounded once.  Sums run in a fixed order (bit-identical from call to call). */
+ * Outputs are rounded once.  Sums run in a fixed order (bit-identical from call to call).
+ * NaN and Inf reach what sees them and nothing else, in a result as the definition makes of
+ * them or, where it gives an infinity, NaN; a key whose probability is zero because its score
+ * is minus infinity may give its queries' dq NaN or nothing. */
 typedef struct gdn_swa_problem {
   int32_t B, T, Hq, Hk, D;
   int32_t window, sinks;

@@ -133,3 +133,67 @@ def test_infinite_scores_are_nan_in_their_row_alone():
     o = gdn.swa_fwd(q, k, v, 30)
     assert (~torch.isfinite(o)).any(-1).nonzero()[:, 1].unique().tolist() == [40]
     assert torch.equal(o[:, :40], clean[:, :40]) and torch.equal(o[:, 41:], clean[:, 41:])
+
+
+MANY = [(64, 150, 8, 8, 64, 40, 3), (64, 150, 8, 1, 128, 60, 0), (16, 530, 16, 2, 64, 100, 20), (8, 300, 64, 64, 128, 140, 2)]
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,W,S", MANY)
+def test_many_sequences_and_heads(B, T, Hq, Hk, D, W, S, io):
+    """More blocks than the CUs take at once, of queries and of keys: the wider tiles."""
+    q, k, v, do = inputs(B, T, Hq, Hk, D, io, seed=7)
+    compare(q, k, v, do, W, S, D ** -0.5, None)
+
+
+def _seen(B, T, W, S, cu):
+    """[rows, rows]: which query sees which key, over the flattened tokens."""
+    m = torch.zeros(B * T, B * T, dtype=torch.bool, device=DEV)
+    for a, b in ref.spans(B, T, cu):
+        m[a:b, a:b] = ref.seen(b - a, W, S).to(DEV)
+    return m
+
+
+ODD = [  # B, T, Hq, Hk, D, W, S, cu
+    (1, 300, 2, 1, 64, 100, 3, None),
+    (1, 420, 2, 2, 128, 33, 20, None),
+    (1, 333, 4, 2, 64, 40, 3, [0, 0, 1, 65, 193, 193, 332, 333, 333]),
+    (16, 130, 32, 32, 64, 48, 2, None),
+]
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,W,S,cu", ODD)
+def test_values_that_are_not_finite_stay_where_they_are_seen(B, T, Hq, Hk, D, W, S, cu, bad, io):
+    """In one row of q, k, v or do, at several places: who does not see it keeps its result
+    (within the bounds of the finite problem), and who sees a NaN has NaN."""
+    q, k, v, do = inputs(B, T, Hq, Hk, D, io, seed=8)
+    how = dict(sinks=S, scale=D ** -0.5, cu_seqlens=cu)
+    want, err = ref.swa(q, k, v, W, S, D ** -0.5, cu, do)
+    see, group, rows = _seen(B, T, W, S, cu), Hq // Hk, B * T
+    for name in "qkvd":
+        for at in (0, 1, 40, rows // 2, rows - 1):
+            t = {n: x.clone() for n, x in zip("qkvd", (q, k, v, do))}
+            h, d = (Hq if name in "qd" else Hk) - 1, 5
+            t[name].view(rows, -1, D)[at, h, d] = bad
+            heads = slice(Hq - 1, Hq) if name in "qd" else slice(Hq - group, Hq)
+            queries = torch.zeros(rows, Hq, dtype=torch.bool, device=DEV)  # whose probabilities or delta it reaches
+            queries[:, heads] = (torch.arange(rows, device=DEV) == at if name in "qd" else see[:, at])[:, None]
+            keys = torch.stack([(see & queries[:, i * group:(i + 1) * group].any(1)[:, None]).any(0) for i in range(Hk)], 1)
+            one = torch.arange(D, device=DEV) == d
+            every = torch.ones_like(one)
+            reach = {"o": queries[..., None] & {"q": every, "k": every, "v": one, "d": ~every}[name],
+                     "lse": queries if name in "qk" else torch.zeros_like(queries),
+                     "dq": queries[..., None] & every, "dk": keys[..., None] & every,
+                     "dv": keys[..., None] & {"q": every, "k": every, "v": ~every, "d": one}[name]}
+            o, lse = gdn.swa_fwd(t["q"], t["k"], t["v"], W, return_lse=True, **how)
+            got = gdn.swa_bwd(t["q"], t["k"], t["v"], o, lse, t["d"], W, **how)
+            got.update(o=o, lse=lse)
+            torch.cuda.synchronize()
+            for key, r in reach.items():
+                x, r = got[key], r.view(got[key].shape)
+                if math.isnan(bad):
+                    assert bool(torch.isnan(x[r]).all()), (name, at, key)
+                ref.check(f"{name}[{at}] {key}", torch.where(r, torch.zeros_like(x), x),
+                          want[key].masked_fill(r.cpu(), 0), err[key])
