@@ -241,7 +241,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
   if (FAR) {
     i0 = block * kSwaFar;
     i1 = min(i0 + kSwaFar, len) - 1;
-    if (i1 < k0 + p.W) return;  // none of them is so far behind
+    if (i0 >= len || i1 < k0 + p.W) return;  // a shorter sequence; none of them is so far behind
   } else {
     i0 = k0;
     i1 = min(static_cast<int64_t>(len), static_cast<int64_t>(k0) + KT - 1 + p.W) - 1;

@@ -73,6 +73,27 @@ def test_first_tokens_of_long_sequences(T, W, S, D, cu, io):
     compare(q, k, v, do, W, S, D ** -0.5, cu)
 
 
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("cu", [[0, 900, 930, 1700, 1710, 1730, 2000], [0, 1300, 1331, 1362], [0, 40, 300, 340, 1700, 1740]])
+def test_first_tokens_of_short_sequences_beside_long_ones(cu, io):
+    """Sequences of a run of queries or less beside others of several: each has its own sums, and
+    nothing is written behind the workspace."""
+    T, W, S = cu[-1], 20, 5
+    q, k, v, do = inputs(1, T, 2, 1, 64, io, seed=9)
+    compare(q, k, v, do, W, S, 0.125, cu)
+    o, lse = gdn.swa_fwd(q, k, v, W, sinks=S, scale=0.125, cu_seqlens=cu, return_lse=True)
+    n = len(cu) - 1
+    size = -(-T * 2 * 4 // 256) * 256 + -(-n * S * 2 * 64 * 4 // 256) * 256 + (T // 256 + n) * S * 2 * 64 * 4
+    room = torch.full((size + 65536,), 0x5a, dtype=torch.uint8, device=DEV)
+    got = gdn.swa_bwd(q, k, v, o, lse, do, W, sinks=S, scale=0.125, cu_seqlens=cu, workspace=room[:size])
+    with pytest.raises(gdn.GdnError):
+        gdn.swa_bwd(q, k, v, o, lse, do, W, sinks=S, scale=0.125, cu_seqlens=cu, workspace=room[:size - 1])
+    assert bool((room[size:] == 0x5a).all())
+    want, err = ref.swa(q, k, v, W, S, 0.125, cu, do)
+    for key in ("dq", "dk", "dv"):
+        ref.check(key, got[key], want[key], err[key])
+
+
 @pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, 4.0])
 def test_scales(scale):
     """Scores of up to a hundred and more, rising where the maximum moves, and none at all."""
