@@ -193,11 +193,15 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   const size_t first = static_cast<size_t>(p->Hk) * c->S * 2 * p->D * 4;
   c->win = up256(p->num_seqs * first);
   c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs)) * first;
-  // Blocks of half as many queries, or of a quarter as many keys, where whole ones are fewer
-  // than two a CU (packed sequences of other lengths count as so many of the rows).
+  // Blocks of half as many queries, or of a quarter as many keys, where whole ones leave CUs
+  // without work (packed sequences of other lengths count as so many of the rows).  bf16 training
+  // steps over one sequence, a window of 512, D = 128, us, halves | whole: 256 blocks of queries
+  // 111 | 118, 384 blocks 178 | 171, 512 blocks 215 | 131; quarters | whole: 128 blocks of keys
+  // 320 | 410, 256 blocks 333 | 279.  D = 64: 256 blocks 161 | 184, 320
+  // blocks 76 | 75.
   const int64_t whole = c->rows / gdn::kSwaQueries;
-  c->few = whole * p->Hq < 512;
-  c->few_keys = whole * p->Hk < 512;
+  c->few = whole * p->Hq < 384;
+  c->few_keys = whole * p->Hk < (p->D == 64 ? 320 : 256);
   // Workgroups of 256 threads, counted in 32 bits: blocks of queries of every query head (the
   // backward's blocks of keys are as long), rounded up to eight.
   const int64_t blocks = (max_len + 31) / 32;
@@ -220,8 +224,11 @@ gdn_status check_cache(const gdn_swa_problem* p, SwaSize* c) {
   c->cache = static_cast<size_t>(p->num_seqs) * slots * row * c->io;
   c->lens = static_cast<size_t>(p->num_seqs) * 4;
   const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(p->num_seqs) * p->Hk * ((p->Hq / p->Hk + 15) / 16));
-  // runs of at least 128 slots (32 a wave), as many as make 1024 workgroups
-  const int64_t splits = std::max<int64_t>(1, std::min<int64_t>((1024 + groups - 1) / groups, (slots + 127) / 128));
+  // Whole where there is a workgroup a CU, else runs of at least 128 slots (32 a wave) that make
+  // some 512 workgroups.  64 sequences of 4 key heads and 4100 slots, us: whole 97, two runs 104,
+  // four 107; 48 sequences: two runs 90, three 82, six 80; one of 30000 slots: 64 runs 21, 118 runs
+  // 24, 235 runs 31; eight: eight runs 77, 16 runs 72, 32 runs 67.
+  const int64_t splits = groups >= 256 ? 1 : std::min<int64_t>((512 + groups - 1) / groups, (slots + 127) / 128);
   c->run = static_cast<int32_t>(((slots + splits - 1) / splits + 127) / 128 * 128);
   c->splits = static_cast<int32_t>((slots + c->run - 1) / c->run);
   if (groups * c->splits >= 1 << 24) return GDN_ERR_UNSUPPORTED;

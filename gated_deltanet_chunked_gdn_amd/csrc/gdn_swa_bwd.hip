@@ -491,7 +491,7 @@ hipError_t launch_c(const SwaParams& p, hipStream_t s) {
 }
 template <typename Op, int D>
 hipError_t launch_t(const SwaParams& p, hipStream_t s) {
-  if (p.few) return launch_c<Op, D, 1, kShared>(p, s);  // keys are fewer still
+  if (p.few) return p.few_keys ? launch_c<Op, D, 1, kShared>(p, s) : launch_c<Op, D, 1, kKeys>(p, s);
   return p.few_keys ? launch_c<Op, D, 2, kShared>(p, s) : launch_c<Op, D, 2, kKeys>(p, s);
 }
 
