@@ -74,12 +74,13 @@ def event_times(call, n_calls, warmup, stream):
 
 
 # the operators around the delta rule, timed with --extra only
-LAYER_EXTRAS = ("step", "conv", "scan")
+LAYER_EXTRAS = ("step", "conv", "scan", "glr", "rope", "swa")
 EXTRAS = ("bwd", "segment_split", "prologue", "epilogue", "kda", "kda_bwd", "kda_segment_split", "policy")
 
 
 def layer_measurements(gdn, dev, steps, warmup, which):
-    """The single-token delta rule step, the short convolution and the selective scan at
+    """The single-token delta rule step, the short convolution, the selective scan, the gated
+    linear recurrence, the norm and rotation of queries and keys, and the window attention at
     a decoding, a prompt and a training shape each: milliseconds a call (HIP events) and
     the bytes that a call cannot do without.  Every call has the same inputs, much of which
     stays in the caches between calls."""
@@ -112,6 +113,38 @@ def layer_measurements(gdn, dev, steps, warmup, which):
         out["fwd_B4_T4096_C2048_bf16"] = timed(lambda: gdn.conv_fwd(x, w, bias=b), 2 * x.numel() * 2)
         out["bwd_B4_T4096_C2048_bf16"] = timed(lambda: gdn.conv_bwd(x, w, dy, bias=b), 3 * x.numel() * 2)
         out["step_B256_C2048_bf16"] = timed(lambda: gdn.conv_step(xs, w, state, bias=b), 2 * W * xs.numel() * 2)
+    elif which == "glr":
+        B, T, C = 4, 4096, 2048
+        x, r, i, z, dy = (rand(B, T, C) for _ in range(5))
+        lam = rand(C, dtype=f32) - 5
+        _, _, saved = gdn.glr_fwd_save(x, r, i, lam, z=z)
+        kept = saved.numel()
+        out["fwd_B4_T4096_C2048_bf16"] = timed(lambda: gdn.glr_fwd(x, r, i, lam, z=z), 5 * x.numel() * 2)
+        out["fwd_save"] = timed(lambda: gdn.glr_fwd_save(x, r, i, lam, z=z, saved=saved), 5 * x.numel() * 2 + kept)
+        out["bwd_saved"] = timed(lambda: gdn.glr_bwd_saved(x, r, i, lam, dy, saved, z=z), 9 * x.numel() * 2 + kept)
+        xs, h = rand(256, 1, C), rand(256, C, dtype=f32)
+        out["step_B256_C2048_bf16"] = timed(lambda: gdn.glr_step(xs, xs, xs, lam, h), 4 * xs.numel() * 2 + 2 * h.numel() * 4)
+    elif which == "rope":
+        B, T, Hq, Hk, D = 4, 4096, 16, 8, 128
+        q, k, dq, dk = rand(B, T, Hq, D), rand(B, T, Hk, D), rand(B, T, Hq, D), rand(B, T, Hk, D)
+        freq = 10000.0 ** (-torch.arange(D // 2, device=dev, dtype=f32) / (D // 2))
+        w, qs, ks = torch.ones(D, device=dev), q[:1, :64].transpose(0, 1).contiguous(), k[:1, :64].transpose(0, 1).contiguous()
+        both = (q.numel() + k.numel()) * 2
+        out["fwd_B4_T4096_16+8x128_bf16"] = timed(lambda: gdn.rope_fwd(q, k, freq, wq=w, wk=w), 2 * both)
+        out["bwd"] = timed(lambda: gdn.rope_bwd(q, k, freq, dq, dk, wq=w, wk=w), 3 * both)
+        out["step_B64"] = timed(lambda: gdn.rope_fwd(qs, ks, freq, wq=w, wk=w), 2 * both * 64 // (B * T))
+    elif which == "swa":
+        B, T, Hq, Hk, D, W, S = 4, 4096, 16, 8, 128, 512, 4
+        q, k, v, do = rand(B, T, Hq, D), rand(B, T, Hk, D), rand(B, T, Hk, D), rand(B, T, Hq, D)
+        how = dict(sinks=S, scale=D ** -0.5)
+        o, lse = gdn.swa_fwd(q, k, v, W, return_lse=True, **how)
+        ins = (q.numel() + k.numel() + v.numel()) * 2
+        out["fwd_B4_T4096_16+8x128_W512_bf16"] = timed(lambda: gdn.swa_fwd(q, k, v, W, **how), ins + q.numel() * 2)
+        out["bwd"] = timed(lambda: gdn.swa_bwd(q, k, v, o, lse, do, W, **how), 2 * ins + 2 * q.numel() * 2 + lse.numel() * 4)
+        N = 64
+        kc, vc, lens = rand(N, S + 4096, 4, D), rand(N, S + 4096, 4, D), torch.full((N,), 10000, dtype=torch.int32, device=dev)
+        qs, ks = rand(N, 1, Hq, D), rand(N, 1, 4, D)
+        out["step_B64_16+4x128_W4096"] = timed(lambda: gdn.swa_step(qs, ks, ks, kc, vc, lens, **how), 2 * kc.numel() * 2)
     else:
         B, T, D, N = 4, 2048, 2048, 16
         u, dt, z, dy = rand(B, T, D), rand(B, T, D), rand(B, T, D), rand(B, T, D)
