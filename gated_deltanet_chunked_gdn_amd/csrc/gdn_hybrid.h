@@ -120,6 +120,7 @@ struct SwaParams {
   int32_t max_len;
   int32_t few;         // blocks of 128 queries are too few workgroups
   int32_t few_keys;    // blocks of 128 keys are
+  int32_t far;         // queries of a run for the first tokens' gradients
   float scale;
   // cache
   void* kc;            // [N][slots][Hk][D]
@@ -132,9 +133,8 @@ struct SwaParams {
 };
 constexpr int kSwaQueries = 128;  // queries of a workgroup
 constexpr int kSwaKeys = 128;     // keys of a workgroup of the backward
-constexpr int kSwaFar = 256;      // queries of a run for the first tokens' gradients
-// Run c of a sequence that starts at row bos uses slot bos / kSwaFar + n + c (distinct).
-inline int64_t swa_far_slots(int64_t rows, int64_t n) { return rows / kSwaFar + n; }
+// Run c (of `far` queries) of a sequence that starts at row bos uses slot bos / far + n + c (distinct).
+inline int64_t swa_far_slots(int64_t rows, int64_t n, int64_t far) { return rows / far + n; }
 hipError_t launch_swa_fwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
 hipError_t launch_swa_bwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
 hipError_t launch_swa_fill(const SwaParams& p, int D, bool bf16, hipStream_t s);

@@ -159,7 +159,7 @@ struct SwaSize {
   size_t io = 0, qin = 0, kin = 0, vin = 0, q = 0, k = 0, lse = 0, cache = 0, lens = 0;
   size_t delta = 0, win = 0, far = 0, step = 0;
   int64_t rows = 0, q_stride = 0, k_stride = 0, v_stride = 0;
-  int32_t W = 0, S = 0, max_len = 0, few = 0, few_keys = 0, splits = 1, run = 0;
+  int32_t W = 0, S = 0, max_len = 0, few = 0, few_keys = 0, run_far = 256, splits = 1, run = 0;
 };
 
 gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
@@ -192,7 +192,13 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   c->delta = up256(c->lse);
   const size_t first = static_cast<size_t>(p->Hk) * c->S * 2 * p->D * 4;
   c->win = up256(p->num_seqs * first);
-  c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs)) * first;
+  // Runs of 256 queries for the first tokens' sums, or of a tile of them where those leave most
+  // CUs without work: 10 runs (five sequences, 1501 tokens, fp32, D = 64) 117 us the step with 256
+  // queries each, 101 with 64; 64 (4096 tokens, bf16, D = 128) 205, with 128 201; 512 of them
+  // (16384 tokens) 499, with 128 509.
+  const int64_t far = c->rows / 256 * p->Hk * ((c->S + 15) / 16);
+  c->run_far = far >= 128 ? 256 : c->io == 2 ? 128 : 64;
+  c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs, c->run_far)) * first;
   // Blocks of half as many queries, or of a quarter as many keys, where whole ones leave CUs
   // without work (packed sequences of other lengths count as so many of the rows).  bf16 training
   // steps over one sequence, a window of 512, D = 128, us, halves | whole: 256 blocks of queries
@@ -206,7 +212,7 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   // backward's blocks of keys are as long), rounded up to eight.
   const int64_t blocks = (max_len + 31) / 32;
   if ((blocks * p->Hq + 7) / 8 * 8 * p->num_seqs >= 1 << 24) return GDN_ERR_UNSUPPORTED;
-  const int64_t runs = (max_len + gdn::kSwaFar - 1) / gdn::kSwaFar;
+  const int64_t runs = (max_len + c->run_far - 1) / c->run_far;
   if ((runs * p->Hk + 7) / 8 * 8 * p->num_seqs * ((c->S + 15) / 16) >= 1 << 24 || static_cast<int64_t>(c->S) * p->Hk * p->num_seqs >= 1 << 24)
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
@@ -242,7 +248,7 @@ gdn::SwaParams swa_params(const gdn_swa_problem* p, const SwaSize& c, const void
   sp.q_stride = c.q_stride; sp.k_stride = c.k_stride; sp.v_stride = c.v_stride;
   sp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
   sp.N = p->num_seqs; sp.Hq = p->Hq; sp.Hk = p->Hk; sp.W = c.W; sp.S = c.S; sp.max_len = c.max_len;
-  sp.few = c.few; sp.few_keys = c.few_keys;
+  sp.few = c.few; sp.few_keys = c.few_keys; sp.far = c.run_far;
   sp.scale = p->scale;
   return sp;
 }

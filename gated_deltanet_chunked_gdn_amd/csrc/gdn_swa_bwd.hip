@@ -239,8 +239,8 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
   // queries i0 .. i1
   int i0, i1;
   if (FAR) {
-    i0 = block * kSwaFar;
-    i1 = min(i0 + kSwaFar, len) - 1;
+    i0 = block * p.far;
+    i1 = min(i0 + p.far, len) - 1;
     if (i0 >= len || i1 < k0 + p.W) return;  // a shorter sequence; none of them is so far behind
   } else {
     i0 = k0;
@@ -430,7 +430,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
     float* part = nullptr;  // of the first tokens
     if (FAR) {
       if (j >= p.S) continue;
-      const int64_t slot = bos / kSwaFar + blockIdx.y + block;
+      const int64_t slot = bos / p.far + blockIdx.y + block;
       part = p.first_far + ((slot * p.Hk + hk) * p.S + j) * 2 * D;
     } else if (j < p.S && len > p.W) {
       part = p.first_win + ((static_cast<int64_t>(blockIdx.y) * p.Hk + hk) * p.S + j) * 2 * D;
@@ -461,10 +461,10 @@ __global__ __launch_bounds__(2 * D) void swa_first_kernel(SwaParams p) {
   chunk::seq_range(p.seq, n, bos, len);
   if (len <= p.W || j >= len) return;
   float sum = p.first_win[((static_cast<int64_t>(n) * p.Hk + hk) * p.S + j) * 2 * D + x];
-  const int64_t slot = bos / kSwaFar + n, runs = (len + kSwaFar - 1) / kSwaFar;
+  const int64_t slot = bos / p.far + n, runs = (len + p.far - 1) / p.far;
   // as in the kernel above: the keys' block of 16 says which runs were formed
   for (int64_t r = 0; r < runs; ++r)
-    if (min((r + 1) * kSwaFar, len) - 1 >= (j & ~15) + p.W) sum += p.first_far[(((slot + r) * p.Hk + hk) * p.S + j) * 2 * D + x];
+    if (min((r + 1) * p.far, len) - 1 >= (j & ~15) + p.W) sum += p.first_far[(((slot + r) * p.Hk + hk) * p.S + j) * 2 * D + x];
   const int64_t at = ((bos + j) * p.Hk + hk) * D;
   if (x < D)
     IoT<E>::st(static_cast<E*>(p.dk) + at + x, sum * p.scale);
@@ -483,7 +483,7 @@ hipError_t launch_c(const SwaParams& p, hipStream_t s) {
   const int kblocks = (p.max_len + keys - 1) / keys, kitems = p.Hk * kblocks;
   hipLaunchKernelGGL((swa_dkv_kernel<Op, D, FORM>), dim3(of8(kitems), N), dim3(256), 0, s, p, kitems, kblocks);
   if (p.S > 0) {
-    const int runs = (p.max_len + kSwaFar - 1) / kSwaFar, items = p.Hk * runs;
+    const int runs = (p.max_len + p.far - 1) / p.far, items = p.Hk * runs;
     hipLaunchKernelGGL((swa_dkv_kernel<Op, D, kFar>), dim3(of8(items), N, static_cast<unsigned>((p.S + 15) / 16)), dim3(256), 0, s, p, items, runs);
     hipLaunchKernelGGL((swa_first_kernel<typename Op::elem, D>), dim3(static_cast<unsigned>(p.S * p.Hk), N), dim3(2 * D), 0, s, p);
   }

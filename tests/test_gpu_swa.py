@@ -1,11 +1,14 @@
 """Window attention on the GPU against its float64 definition: forward and backward over
 dense and packed sequences (marked gpu).  The bounds are counted in _hybrid_oracle.swa."""
+import ctypes
 import math
 
+import numpy as np
 import pytest
 import torch
 
 import gated_deltanet_chunked_gdn_amd as gdn
+from gated_deltanet_chunked_gdn_amd import _native as nat
 import _hybrid_oracle as ref
 
 pytestmark = pytest.mark.gpu
@@ -82,8 +85,10 @@ def test_first_tokens_of_short_sequences_beside_long_ones(cu, io):
     q, k, v, do = inputs(1, T, 2, 1, 64, io, seed=9)
     compare(q, k, v, do, W, S, 0.125, cu)
     o, lse = gdn.swa_fwd(q, k, v, W, sinks=S, scale=0.125, cu_seqlens=cu, return_lse=True)
-    n = len(cu) - 1
-    size = -(-T * 2 * 4 // 256) * 256 + -(-n * S * 2 * 64 * 4 // 256) * 256 + (T // 256 + n) * S * 2 * 64 * 4
+    offsets = np.asarray(cu, dtype=np.int32)
+    prob, size = nat.SwaProblem(1, T, 2, 1, 64, W, S, len(cu) - 1, offsets.ctypes.data, 4096, int(io is BF), 0.125, 0, 0, 0), ctypes.c_size_t()
+    assert nat.load().gdn_swa_workspace_size(prob, nat.GDN_SWA_BWD, size) == nat.GDN_OK
+    size = size.value
     room = torch.full((size + 65536,), 0x5a, dtype=torch.uint8, device=DEV)
     got = gdn.swa_bwd(q, k, v, o, lse, do, W, sinks=S, scale=0.125, cu_seqlens=cu, workspace=room[:size])
     with pytest.raises(gdn.GdnError):
