@@ -12,6 +12,10 @@
 // The first tokens are seen by all later queries too: a few keys with long sums.  Their
 // part from behind the window is summed by runs of queries (the same kernel, its four waves
 // sharing the keys and parting the queries) and joined in order by a last kernel.
+//
+// Bound by the matrix units and what runs beside them.  4 x 4096 tokens, 16 query heads and 8 key
+// heads of 128, window 512, bf16: dq 183 us (109 GFLOP with the edges' tiles whole, 600
+// TFLOP/s), dk and dv 217 (137, 630), the first tokens 35 and 7.
 #include <hip/hip_runtime.h>
 
 #include "gdn_swa_device.h"

@@ -9,6 +9,10 @@
 // softmax runs inside lanes but for two exchanges of the maximum, and the probabilities are
 // the operand of the second product as they stand.  Tiles that all of a wave's queries see
 // whole take no mask, those that none sees no product.
+//
+// Bound by the matrix units and what runs beside them.  2 x 4096 tokens, 16 heads of 128, window
+// 1024, bf16: 96 us, 60 GFLOP (70 with the edges' tiles whole) at 630 (730) TFLOP/s (a large
+// product: 1320), matrix units busy 40 % of the cycles; taking away the loads, the reads from LDS or the exponentials gains 3 to 10 % each.
 #include <hip/hip_runtime.h>
 
 #include "gdn_swa_device.h"

