@@ -54,10 +54,24 @@ struct MmaBf16 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   }
   // Rounding to bf16: the operands of the second products are probabilities and the scores'
-  // gradients, off by at most 2^-8 of each, as the inputs they are multiplied with are.
+  // gradients, off by at most 2^-8 of each, as the inputs they are multiplied with are.  With `rest`
+  // as a second product the error of a prompt's o against 64 bits is 1.6e-3 for 2.1e-3, and the
+  // forward of 2 x 4096 tokens, 16 heads of 128, window 1024, takes 131 us for 98: the prompt and
+  // the backward do without it, the step, which waits for memory, does not.
   static __device__ __forceinline__ u32x4_t operand(const f32x4_t* acc) {
     return u32x4_t{pack_bf16x2(acc[0][0], acc[0][1]), pack_bf16x2(acc[0][2], acc[0][3]), pack_bf16x2(acc[1][0], acc[1][1]),
                    pack_bf16x2(acc[1][2], acc[1][3])};
+  }
+  // What that rounding leaves (exact in fp32), rounded in turn: as the operand of a second product
+  // it leaves 2^-16 of each value.
+  static __device__ __forceinline__ u32x4_t rest(const f32x4_t* acc, u32x4_t op) {
+    f32x4_t left[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      left[i >> 1][2 * (i & 1)] = acc[i >> 1][2 * (i & 1)] - __uint_as_float(op[i] << 16);
+      left[i >> 1][2 * (i & 1) + 1] = acc[i >> 1][2 * (i & 1) + 1] - __uint_as_float(op[i] & 0xffff0000u);
+    }
+    return operand(left);
   }
   // Columns d0 .. d0 + 15 of the 32 rows from row0 on, as the operand whose lane (c, g) holds
   // column d0 + c of rows 4 g + 0..3 of both blocks.  ds_read_b64_tr_b16: within 16 lanes, lane s names

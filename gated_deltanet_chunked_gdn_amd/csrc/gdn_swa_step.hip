@@ -6,8 +6,8 @@
 // have been written hold exactly the keys that the next query sees, so the step attends to
 // all of them and takes no mask but their count.
 //
-// Bound by the cache's bytes: 64 sequences of 4100 slots, 4 key heads of 128, bf16: 504 MB in 94 to
-// 96 us, 5.3 TB/s, above a copy.  The query heads of a key head (up to 16) are the columns of
+// Bound by the cache's bytes: 64 sequences of 4100 slots, 4 key heads of 128, bf16: 504 MB in 98 to
+// 101 us, 5.1 TB/s, as a copy (4 us of it the product that keeps the probabilities' lower bits).  The query heads of a key head (up to 16) are the columns of
 // one 16x16 product, so every key and value is read once for all of them; keys go from
 // memory into the operand, values through a tile in LDS of the wave's own, so the waves of a
 // workgroup meet only at the end.  Where the sequences and key heads are few, the slots are parted
@@ -110,8 +110,14 @@ __global__ __launch_bounds__(256, 2) void swa_step_kernel(SwaParams p) {
     for (int b = 0; b < NB; b += KB) {
       const f32x4_t two[2] = {s[b], s[b + KB - 1]};
       const u32x4_t pf = Op::operand(two);
+      u32x4_t rest;  // the matrix units wait for the cache: a second product keeps 16 bits of each probability
+      if constexpr (sizeof(E) == 2) rest = Op::rest(two, pf);
 #pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] = Op::mma(Op::template read_tr<D>(Vs, 16 * b, 16 * d, lane), pf, acc[d]);
+      for (int d = 0; d < ND; ++d) {
+        const u32x4_t vt = Op::template read_tr<D>(Vs, 16 * b, 16 * d, lane);
+        acc[d] = Op::mma(vt, pf, acc[d]);
+        if constexpr (sizeof(E) == 2) acc[d] = Op::mma(vt, rest, acc[d]);
+      }
     }
   }
   sum += __shfl_xor(sum, 16, 64);

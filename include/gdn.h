@@ -687,7 +687,8 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
  * workgroups in a launch (counted as one for 32 tokens of the longest sequence, every query head and
  * every sequence), else GDN_ERR_UNSUPPORTED.
  * Scores, sums and statistics of the softmax are fp32; with bf16 io the probabilities and
- * the scores' gradients are rounded to bf16 as operands of the products that sum over them.
+ * the scores' gradients are rounded to bf16 as operands of the products that sum over them
+ * (gdn_swa_step keeps the probabilities' next 8 bits in a second product).
  * Outputs are rounded once.  Sums run in a fixed order (bit-identical from call to call).
  * NaN and Inf reach what sees them and nothing else, in a result as the definition makes of
  * them or, where it gives an infinity, NaN; a key whose probability is zero because its score

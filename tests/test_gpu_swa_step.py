@@ -106,3 +106,20 @@ def test_runs_are_joined_and_workspaces_taken():
         ref.check(f"o {before}", o, want, err)
         space = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
         assert torch.equal(gdn.swa_step(q, k, v, kc, vc, lens, sinks=4, scale=0.09, workspace=space), o)
+
+
+@pytest.mark.parametrize("Hq,Hk,D,W,S", [(4, 1, 64, 300, 5), (16, 4, 128, 130, 0), (4, 1, 128, 1500, 4)])
+def test_probabilities_keep_sixteen_bits(Hq, Hk, D, W, S):
+    """In bf16 a probability enters its product as its rounding and the rounding of what that leaves:
+    2^-8 of 2^-8, so 2^-16 of each term beside the fp32 bounds and the result's own rounding."""
+    lens = [1, W // 2, S + W, S + 3 * W + 1]
+    g = _gen(W)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF)  # noqa: E731
+    B = len(lens)
+    q, k, v, kc, vc = r(B, 1, Hq, D), r(B, 1, Hk, D), r(B, 1, Hk, D), r(B, S + W, Hk, D), r(B, S + W, Hk, D)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    wide = [t.float() for t in (q, k, v, kc, vc)]
+    want, err, _, _ = ref.swa_step(*wide, at, S, D ** -0.5)
+    terms, _, _, _ = ref.swa_step(wide[0], wide[1], wide[2].abs(), wide[3], wide[4].abs(), at, S, D ** -0.5)
+    o = gdn.swa_step(q, k, v, kc, vc, at, sinks=S, scale=D ** -0.5)
+    ref.check("o", o, want, err + 2.0 ** -16 * terms)
