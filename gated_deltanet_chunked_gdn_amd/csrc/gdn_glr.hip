@@ -153,9 +153,8 @@ struct Place {
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     run = lane / kLanes;
     ch = (lane % kLanes) * V;
-    slot = index / tiles;
-    tile = static_cast<int>(index - slot * tiles);
-    if (back) slot = p.slots - 1 - slot;
+    slot = glr_slot(index, tiles, p.slots, back);
+    tile = static_cast<int>(index % tiles);
     // the sequence whose slots hold this one: the last that starts at or before it
     int lo = 0, hi = p.N;
     while (hi - lo > 1) {
@@ -170,7 +169,7 @@ struct Place {
     chunk::seq_range(p.seq, n, bos, len);
     segs = static_cast<int>(max((len + kTokens - 1) / kTokens, static_cast<int64_t>(1)));
     t0 = static_cast<int64_t>(seg) * kTokens;
-    live = seg < segs;  // an empty sequence has one segment, of no tokens
+    live = slot >= 0 && seg < segs;  // an empty sequence has one segment, of no tokens
   }
   // A sequence's first slot.  Dense ones have the slots that their segments need and no more.
   static __device__ __forceinline__ int64_t start(const GlrParams& p, int n) {
@@ -185,7 +184,7 @@ __device__ __forceinline__ int64_t number(const GlrParams& p) {
   if (threadIdx.x == 0)
     mine = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(p.chain), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(mine);
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(mine));
 }
 
 // Words that workgroups pass to each other; zero: not there yet.  A state stands beside a one;
@@ -518,6 +517,7 @@ template <typename E, int V, bool Z>
 __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bwd_kernel(GlrParams p, int tiles) {
   using P = Place<V>;
   const P at(p, number(p), tiles, true);
+  if (at.slot < 0) return;
   const bool chan = at.tile * kGlrTile + at.ch < p.C;
   if (!at.live) {  // a slot between two sequences'
     if (threadIdx.x < P::kLanes && chan) {

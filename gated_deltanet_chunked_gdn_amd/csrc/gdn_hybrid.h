@@ -56,6 +56,14 @@ constexpr int glr_seg(bool bwd) { return kGlrWaves * 64 / (kGlrTile / glr_vec(bw
 inline int glr_tiles(int C) { return (C + kGlrTile - 1) / kGlrTile; }
 // Part c (of `len` tokens) of a sequence that starts at row bos uses slot bos / len + n + c (distinct).
 inline int64_t glr_slots(int64_t rows, int64_t n, int64_t len) { return rows / len + n; }
+// The segment slot of workgroup `index` of a launch over `slots` slots of `tiles` channel tiles
+// (`back`: the last slot first), or -1 behind the last one: workgroups are numbered by a counter
+// in the workspace, and calls that overlap and share one, against the rules, count on past their end.
+__host__ __device__ inline int64_t glr_slot(int64_t index, int tiles, int64_t slots, bool back) {
+  const int64_t slot = index / tiles;
+  if (slot >= slots) return -1;
+  return back ? slots - 1 - slot : slot;
+}
 hipError_t launch_glr_fwd(const GlrParams& p, bool bf16, hipStream_t s);
 hipError_t launch_glr_bwd(const GlrParams& p, bool bf16, hipStream_t s);
 hipError_t launch_glr_step(const GlrParams& p, bool bf16, hipStream_t s);

@@ -594,7 +594,10 @@ gdn_status gdn_glr_workspace_size(const gdn_glr_problem* problem, int32_t pass, 
  * (NULL: not wanted; a sequence of no tokens keeps h0).  The time axis is composed of runs
  * and segments: results are those of the serial order up to fp32 rounding, bit-identical from
  * call to call.  The segments of a call pass their states on in the workspace: calls that may
- * overlap in time and share one may end late (a second or so) and give NaN. */
+ * overlap in time must not share one.  If they do, their outputs are wrong (NaN, a mixture, or
+ * left as they were) and they end late, since every wait for a word is bounded (by a second or
+ * so) but may run out once for each segment; nothing outside their outputs and workspace is
+ * written. */
 gdn_status gdn_glr_fwd(const gdn_glr_problem* problem, const void* x, const void* r, const void* i,
                        const float* lam, const void* z, const float* h0, void* y, float* h_final,
                        void* workspace, size_t workspace_bytes, void* stream);
