@@ -49,8 +49,8 @@ __device__ __forceinline__ void scale_(int norm, float eps, float ss, float& inv
     share = 1.f / D;
   } else if (norm == GDN_ROPE_L2) {
     const float n = sqrtf(ss);
-    inv = 1.f / fmaxf(n, 1e-30f);
-    share = n > 1e-30f ? 1.f : 0.f;
+    inv = 1.f / (n < 1e-30f ? 1e-30f : n);  // a NaN stays one
+    share = n <= 1e-30f ? 0.f : 1.f;
   }
 }
 

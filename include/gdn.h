@@ -648,8 +648,9 @@ typedef enum gdn_rope_norm {
  * (GDN_ERR_ALIGN), at least Hq D and Hk D (GDN_ERR_SHAPE), up to 2^21.  Supported: D in {64, 128, 256},
  * R a multiple of 16 up to D, Hq and Hk up to 4096, B T (Hq + Hk) < 2^31, else
  * GDN_ERR_UNSUPPORTED.  Angles are reduced in fp64 (2^-52 of the angle); all else is fp32,
- * squares included, and outputs are rounded once.  eps >= 0 and finite frequencies are
- * documented, not checked. */
+ * squares included, and outputs are rounded once.  A NaN in a row makes the row NaN (with
+ * GDN_ROPE_NONE its pair) and no other.  eps >= 0 and finite frequencies are documented, not
+ * checked. */
 typedef struct gdn_rope_problem {
   int32_t B, T, Hq, Hk, D, R;
   int32_t norm;             /* gdn_rope_norm; another value: GDN_ERR_UNSUPPORTED */

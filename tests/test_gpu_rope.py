@@ -120,3 +120,19 @@ def test_empty():
     yq, yk = gdn.rope_fwd(q, k, freq, positions=pos, wq=w[0], wk=w[1])
     got = gdn.rope_bwd(q, k, freq, dq, dk, positions=pos, wq=w[0], wk=w[1])
     assert yq.shape == q.shape and float(got["dwq"].abs().max()) == 0.0 and float(got["dwk"].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("io", [BF, F32])
+def test_nan_makes_its_row_nan(io, norm):
+    """The norm of a row that holds a NaN is NaN, and so is all of the row and of its gradient."""
+    q, k, freq, pos, _, dq, dk = inputs(1, 8, 2, 2, 64, 32, io, norm=norm, views=False)
+    clean = gdn.rope_fwd(q, k, freq, positions=pos, norm=norm), gdn.rope_bwd(q, k, freq, dq, dk, positions=pos, norm=norm)
+    q[0, 3, 1, 2] = math.nan
+    k[0, 5, 0, 40] = math.nan
+    y, got = gdn.rope_fwd(q, k, freq, positions=pos, norm=norm), gdn.rope_bwd(q, k, freq, dq, dk, positions=pos, norm=norm)
+    for t, was, at in ((y[0], clean[0][0], (3, 1)), (y[1], clean[0][1], (5, 0)), (got["dq"], clean[1]["dq"], (3, 1)), (got["dk"], clean[1]["dk"], (5, 0))):
+        assert bool(torch.isnan(t[0, at[0], at[1]]).all())
+        rest = torch.ones(t.shape[:3], dtype=torch.bool, device=DEV)
+        rest[0, at[0], at[1]] = False
+        assert torch.equal(t[rest], was[rest])
