@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "gdn_abi_check.h"
@@ -33,7 +34,7 @@ gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
   if (!p) return GDN_ERR_NULL;
   if (p->io_dtype != GDN_FP32 && p->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (p->B < 0 || p->T < 0 || p->C <= 0 || p->num_seqs < 0) return GDN_ERR_SHAPE;
-  if (p->C % 8 != 0 || p->C > 1 << 20 || !(p->c >= 0.f)) return GDN_ERR_UNSUPPORTED;
+  if (p->C % 8 != 0 || p->C > 1 << 20 || !(p->c >= 0.f) || !std::isfinite(p->c)) return GDN_ERR_UNSUPPORTED;
   int64_t max_len = 0;
   const gdn_status st = check_seqs(p, &max_len);
   if (st != GDN_OK) return st;
@@ -167,7 +168,7 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   if (p->io_dtype != GDN_FP32 && p->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
   if (p->B < 0 || p->T < 0 || p->Hq <= 0 || p->Hk <= 0 || p->D <= 0 || p->num_seqs < 0 || p->Hq % p->Hk != 0 || p->window <= 0 || p->sinks < 0)
     return GDN_ERR_SHAPE;
-  if ((p->D != 64 && p->D != 128) || p->Hq > 4096 || p->sinks > 1024) return GDN_ERR_UNSUPPORTED;
+  if ((p->D != 64 && p->D != 128) || p->Hq > 4096 || p->sinks > 1024 || !std::isfinite(p->scale)) return GDN_ERR_UNSUPPORTED;
   int64_t max_len = 0;
   gdn_status st = check_seqs(p, &max_len);
   if (st != GDN_OK) return st;

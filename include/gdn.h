@@ -564,7 +564,7 @@ gdn_status gdn_scan_step(const gdn_scan_problem* problem, const void* u, const v
  *     y_t = h   or, with z,   h z_t sigmoid(z_t)
  * Tensors: x, r, i, z, y and their gradients [B,T,C] (io dtype); lam, dlam [C], h0,
  * h_final, dh_final, dh0, h [num_seqs,C] fp32.  All of them 16-byte aligned.  Supported: C a
- * multiple of 8 up to 2^20, B T < 2^31, up to 65535 sequences, c >= 0, and
+ * multiple of 8 up to 2^20, B T < 2^31, up to 65535 sequences, c >= 0 and finite, and
  * (B T / 64 + sequences) ceil(C / 64) < 2^24, else GDN_ERR_UNSUPPORTED.  Finite lam is documented,
  * not checked.  All arithmetic is fp32; io outputs are rounded once.  NaN and Inf reach what
  * the definition makes of them and nothing that it leaves finite; where it gives an infinity
@@ -687,7 +687,7 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
  * q, k and v may have their tokens q_stride, k_stride, v_stride values apart as in
  * gdn_rope_problem (0: contiguous; up to 2^21); all else is contiguous.  16-byte aligned,
  * lse and lens 4-byte.  Supported: D in {64, 128}, Hq a multiple of Hk up to 4096, window >= 1 (as long as
- * wanted), sinks up to 1024, B T up to 2^30, up to 65535 sequences, and fewer than 2^24
+ * wanted), sinks up to 1024, a finite scale, B T up to 2^30, up to 65535 sequences, and fewer than 2^24
  * workgroups in a launch (counted as one for 32 tokens of the longest sequence, every query head and
  * every sequence), else GDN_ERR_UNSUPPORTED.
  * Scores, sums and statistics of the softmax are fp32; with bf16 io the probabilities and

@@ -259,3 +259,18 @@ def test_rows(T):
         if not bad.is_contiguous():
             with pytest.raises(ValueError, match="contiguous"):
                 hybrid._rows(bad, bad.shape, torch.float32, 0, "q")
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_factors_that_are_not_finite(lib, bad):
+    """An infinite c has no gradient (a la is zero times infinity), and the running maximum has no
+    base with a scale that is not finite."""
+    n = ctypes.c_size_t(7)
+    for call in kinds("gdn_glr"):
+        assert call(lib, call.make(c=bad)) == UNSUP, call.name
+    for call in kinds("gdn_swa"):
+        assert call(lib, call.make(scale=bad)) == UNSUP, call.name
+    for pass_ in range(3):
+        assert lib.gdn_glr_workspace_size(glr(c=bad), pass_, n) == UNSUP and n.value == 7
+    for pass_ in range(2):
+        assert lib.gdn_swa_workspace_size(swa(scale=bad), pass_, n) == UNSUP and n.value == 7
