@@ -123,9 +123,9 @@ struct SwaParams {
   float* first_far;    // backward: [slot][Hk][S][2][D] those from queries further on, by runs of them
   int64_t q_stride, k_stride, v_stride;
   SeqInfo seq;
+  int64_t rows;        // B * T
   int32_t N, Hq, Hk;
   int32_t W, S;        // W at most the longest sequence; S 0 where no window leaves a token behind
-  int32_t max_len;
   int32_t few;         // blocks of 128 queries are too few workgroups
   int32_t few_keys;    // blocks of 128 keys are
   int32_t far;         // queries of a run for the first tokens' gradients
@@ -143,6 +143,28 @@ constexpr int kSwaQueries = 128;  // queries of a workgroup
 constexpr int kSwaKeys = 128;     // keys of a workgroup of the backward
 // Run c (of `far` queries) of a sequence that starts at row bos uses slot bos / far + n + c (distinct).
 inline int64_t swa_far_slots(int64_t rows, int64_t n, int64_t far) { return rows / far + n; }
+// Blocks of `each` rows that a launch counts: a dense sequence's as many as it needs, those of
+// packed sequence n from cu[n] / each + n on (distinct; some are no sequence's).
+inline int64_t swa_slots(const SwaParams& p, int64_t rows, int64_t each) {
+  return p.seq.cu ? rows / each + p.N : p.N * ((p.seq.T + each - 1) / each);
+}
+// A launch over `items` (key heads, slots and, of queries, a key head's query heads, the last
+// the fastest), `stripe` of them after each other on an XCD.
+struct SwaGrid {
+  dim3 grid;
+  int slots, items, stripe;
+};
+inline SwaGrid swa_grid(const SwaParams& p, int64_t each, int heads, int z = 1) {
+  const int64_t slots = swa_slots(p, p.rows, each), items = slots * p.Hk * heads;
+  // Dense: an eighth each.  Packed sequences may be long and short ones in a row, and their
+  // blocks of unlike work: stripes of 16 blocks, or of as many fewer as leaves the XCDs even.
+  const int64_t rounds = p.seq.cu ? (items + 128 * heads - 1) / (128 * heads) : 1;
+  const int64_t stripe = (items + 8 * rounds - 1) / (8 * rounds), total = 8 * rounds * stripe;
+  // a grid's axis has up to 2^32 threads
+  const int64_t y = (total + (1 << 22) - 1) >> 22, x = ((total + y - 1) / y + 7) / 8 * 8;
+  return SwaGrid{dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z)), static_cast<int>(slots),
+                 static_cast<int>(items), static_cast<int>(stripe)};
+}
 hipError_t launch_swa_fwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
 hipError_t launch_swa_bwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
 hipError_t launch_swa_fill(const SwaParams& p, int D, bool bf16, hipStream_t s);

@@ -160,7 +160,7 @@ struct SwaSize {
   size_t io = 0, qin = 0, kin = 0, vin = 0, q = 0, k = 0, lse = 0, cache = 0, lens = 0;
   size_t delta = 0, win = 0, far = 0, step = 0;
   int64_t rows = 0, q_stride = 0, k_stride = 0, v_stride = 0;
-  int32_t W = 0, S = 0, max_len = 0, few = 0, few_keys = 0, run_far = 256, splits = 1, run = 0;
+  int32_t W = 0, S = 0, few = 0, few_keys = 0, run_far = 256, splits = 1, run = 0;
 };
 
 gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
@@ -180,7 +180,6 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   if (st == GDN_OK) st = check_stride(p->k_stride, krow, c->io, &c->k_stride);
   if (st == GDN_OK) st = check_stride(p->v_stride, krow, c->io, &c->v_stride);
   if (st != GDN_OK) return st;
-  c->max_len = static_cast<int32_t>(max_len);
   // a window as long as every sequence leaves nothing behind it
   c->W = static_cast<int32_t>(std::min<int64_t>(p->window, std::max<int64_t>(max_len, 1)));
   c->S = c->W >= max_len ? 0 : static_cast<int32_t>(std::min<int64_t>(p->sinks, max_len));
@@ -209,14 +208,24 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   const int64_t whole = c->rows / gdn::kSwaQueries;
   c->few = whole * p->Hq < 384;
   c->few_keys = whole * p->Hk < (p->D == 64 ? 320 : 256);
-  // Workgroups of 256 threads, counted in 32 bits: blocks of queries of every query head (the
-  // backward's blocks of keys are as long), rounded up to eight.
-  const int64_t blocks = (max_len + 31) / 32;
-  if ((blocks * p->Hq + 7) / 8 * 8 * p->num_seqs >= 1 << 24) return GDN_ERR_UNSUPPORTED;
-  const int64_t runs = (max_len + c->run_far - 1) / c->run_far;
-  if ((runs * p->Hk + 7) / 8 * 8 * p->num_seqs * ((c->S + 15) / 16) >= 1 << 24 || static_cast<int64_t>(c->S) * p->Hk * p->num_seqs >= 1 << 24)
-    return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
+}
+
+// The limit on the attention's workgroups, whose numbers are 32-bit: blocks of 32 rows (the launches'
+// are as long or longer) of every sequence and query head, and what the first tokens add.
+gdn_status check_swa_grid(const gdn_swa_problem* p, const SwaSize& c) {
+  if (c.rows == 0) return GDN_OK;
+  const auto blocks = [p](int64_t each) {
+    const int32_t* const cu = p->cu_seqlens_host;
+    if (!cu) return p->num_seqs * ((p->T + each - 1) / each);
+    int64_t sum = 0;
+    for (int32_t n = 0; n < p->num_seqs; ++n) sum += std::max<int64_t>(1, (cu[n + 1] - cu[n] + each - 1) / each);
+    return sum;
+  };
+  const int64_t most = (1 << 24) - 1;
+  const bool fits = blocks(32) * p->Hq <= most && blocks(c.run_far) * p->Hk * ((c.S + 15) / 16) <= most &&
+                    static_cast<int64_t>(c.S) * p->Hk * p->num_seqs <= most;
+  return fits ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 
 // What the cache adds: its slots, and the step's runs of them.
@@ -248,7 +257,7 @@ gdn::SwaParams swa_params(const gdn_swa_problem* p, const SwaSize& c, const void
   sp.q = q; sp.k = k; sp.v = v;
   sp.q_stride = c.q_stride; sp.k_stride = c.k_stride; sp.v_stride = c.v_stride;
   sp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
-  sp.N = p->num_seqs; sp.Hq = p->Hq; sp.Hk = p->Hk; sp.W = c.W; sp.S = c.S; sp.max_len = c.max_len;
+  sp.rows = c.rows; sp.N = p->num_seqs; sp.Hq = p->Hq; sp.Hk = p->Hk; sp.W = c.W; sp.S = c.S;
   sp.few = c.few; sp.few_keys = c.few_keys; sp.far = c.run_far;
   sp.scale = p->scale;
   return sp;
@@ -369,7 +378,8 @@ gdn_status gdn_swa_workspace_size(const gdn_swa_problem* p, int32_t pass, size_t
   if (!bytes) return GDN_ERR_NULL;
   if (pass != GDN_SWA_BWD && pass != GDN_SWA_STEP) return GDN_ERR_UNSUPPORTED;
   SwaSize c;
-  const gdn_status st = pass == GDN_SWA_BWD ? check_swa(p, &c) : check_cache(p, &c);
+  gdn_status st = pass == GDN_SWA_BWD ? check_swa(p, &c) : check_cache(p, &c);
+  if (st == GDN_OK) st = check_swa_grid(p, c);
   if (st != GDN_OK) return st;
   *bytes = pass == GDN_SWA_BWD ? c.delta + c.win + c.far : c.step;
   return GDN_OK;
@@ -378,6 +388,7 @@ gdn_status gdn_swa_workspace_size(const gdn_swa_problem* p, int32_t pass, size_t
 gdn_status gdn_swa_fwd(const gdn_swa_problem* p, const void* q, const void* k, const void* v, void* o, float* lse, void* stream) {
   SwaSize c;
   gdn_status st = check_swa(p, &c);
+  if (st == GDN_OK) st = check_swa_grid(p, c);
   if (st != GDN_OK) return st;
   st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {v, c.vin, 16, true}}, {{o, c.q, 16, true}, {lse, c.lse, 4, false}});
   if (st != GDN_OK || c.rows == 0) return st;
@@ -390,6 +401,7 @@ gdn_status gdn_swa_bwd(const gdn_swa_problem* p, const void* q, const void* k, c
                        const void* dout, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
   SwaSize c;
   gdn_status st = check_swa(p, &c);
+  if (st == GDN_OK) st = check_swa_grid(p, c);
   if (st != GDN_OK) return st;
   st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {v, c.vin, 16, true}, {o, c.q, 16, true}, {lse, c.lse, 4, true},
                       {dout, c.q, 16, true}},
@@ -421,6 +433,7 @@ gdn_status gdn_swa_step(const gdn_swa_problem* p, const void* q, const void* k, 
                         const int32_t* lens, void* o, void* ws, size_t ws_bytes, void* stream) {
   SwaSize c;
   gdn_status st = check_cache(p, &c);
+  if (st == GDN_OK) st = check_swa_grid(p, c);
   if (st != GDN_OK) return st;
   if (p->T != 1 || p->cu_seqlens_host) return GDN_ERR_SHAPE;
   st = check_tensors({{q, c.qin, 16, true}, {k, c.kin, 16, true}, {v, c.vin, 16, true}, {lens, c.lens, 4, true}},

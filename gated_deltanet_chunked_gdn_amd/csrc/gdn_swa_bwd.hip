@@ -197,14 +197,14 @@ __device__ __forceinline__ bool dq_block(const SwaParams& p, int64_t bos, int le
 }
 
 template <typename Op, int D, int CT>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int blocks) {
-  const int item = xcd_item(blockIdx.x, items);
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int slots, int stripe) {
+  const int item = xcd_item(stripe);
   if (item >= items) return;
-  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
-  const int block = rest / group, h = hk * group + rest - block * group;
-  int64_t bos, len64;
-  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64), q0 = block * 64 * CT;
+  const int group = p.Hq / p.Hk, hk = item / (group * slots), rest = item - hk * group * slots;
+  const int slot = rest / group, h = hk * group + rest - slot * group;
+  const Spot at = spot(p, slot, 64 * CT);
+  const int64_t bos = at.bos;
+  const int len = at.len, q0 = at.block * 64 * CT;
   if (q0 >= len) return;
 
   __shared__ alignas(16) typename Op::elem Kt[2][64 * D], Vt[2][64 * D];
@@ -225,19 +225,19 @@ enum Form {
 };
 
 template <typename Op, int D, Form FORM>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || FORM == kKeys) ? 2 : 1) void swa_dkv_kernel(SwaParams p, int items, int blocks) {
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || FORM == kKeys) ? 2 : 1) void swa_dkv_kernel(SwaParams p, int items, int slots, int stripe) {
   using E = typename Op::elem;
   constexpr bool FAR = FORM == kFar, PART = FORM != kKeys;  // PART: each wave takes a step of a tile's queries
   constexpr int CT = FAR ? 1 : 2, KW = 16 * CT, KT = PART ? KW : 4 * KW;  // keys of a wave, of the workgroup
   constexpr int KB = Op::kBlocks, NS = D / Op::kCols, ND = D / 16, QT = PART ? 64 * KB : 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int item = xcd_item(blockIdx.x, items);
+  const int item = xcd_item(stripe);
   if (item >= items) return;
-  const int group = p.Hq / p.Hk, hk = item / blocks, block = item - hk * blocks;
-  int64_t bos, len64;
-  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64);
+  const int group = p.Hq / p.Hk, hk = item / slots;
+  const Spot place = spot(p, item - hk * slots, FAR ? p.far : KT);
+  const int64_t bos = place.bos;
+  const int len = place.len, block = place.block;
   const int k0 = FAR ? KT * blockIdx.z : block * KT, wk0 = PART ? k0 : k0 + KW * wave;
   if (k0 >= len || (FAR && len <= p.W)) return;
   // queries i0 .. i1
@@ -434,10 +434,10 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || 
     float* part = nullptr;  // of the first tokens
     if (FAR) {
       if (j >= p.S) continue;
-      const int64_t slot = bos / p.far + blockIdx.y + block;
+      const int64_t slot = bos / p.far + place.n + block;
       part = p.first_far + ((slot * p.Hk + hk) * p.S + j) * 2 * D;
     } else if (j < p.S && len > p.W) {
-      part = p.first_win + ((static_cast<int64_t>(blockIdx.y) * p.Hk + hk) * p.S + j) * 2 * D;
+      part = p.first_win + ((static_cast<int64_t>(place.n) * p.Hk + hk) * p.S + j) * 2 * D;
     }
     if (part) {
 #pragma unroll
@@ -476,20 +476,17 @@ __global__ __launch_bounds__(2 * D) void swa_first_kernel(SwaParams p) {
     IoT<E>::st(static_cast<E*>(p.dv) + at + x - D, sum);
 }
 
-unsigned of8(int items) { return static_cast<unsigned>((items + 7) / 8 * 8); }
-
 template <typename Op, int D, int CT, Form FORM>
 hipError_t launch_c(const SwaParams& p, hipStream_t s) {
-  const unsigned N = static_cast<unsigned>(p.N);
-  const int qblocks = (p.max_len + 64 * CT - 1) / (64 * CT), qitems = p.Hq * qblocks;
-  hipLaunchKernelGGL((swa_dq_kernel<Op, D, CT>), dim3(of8(qitems), N), dim3(256), 0, s, p, qitems, qblocks);
-  constexpr int keys = FORM == kKeys ? kSwaKeys : 32;
-  const int kblocks = (p.max_len + keys - 1) / keys, kitems = p.Hk * kblocks;
-  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, FORM>), dim3(of8(kitems), N), dim3(256), 0, s, p, kitems, kblocks);
+  SwaGrid g = swa_grid(p, 64 * CT, p.Hq / p.Hk);
+  hipLaunchKernelGGL((swa_dq_kernel<Op, D, CT>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
+  g = swa_grid(p, FORM == kKeys ? kSwaKeys : 32, 1);
+  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, FORM>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
   if (p.S > 0) {
-    const int runs = (p.max_len + p.far - 1) / p.far, items = p.Hk * runs;
-    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, kFar>), dim3(of8(items), N, static_cast<unsigned>((p.S + 15) / 16)), dim3(256), 0, s, p, items, runs);
-    hipLaunchKernelGGL((swa_first_kernel<typename Op::elem, D>), dim3(static_cast<unsigned>(p.S * p.Hk), N), dim3(2 * D), 0, s, p);
+    g = swa_grid(p, p.far, 1, (p.S + 15) / 16);
+    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, kFar>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
+    hipLaunchKernelGGL((swa_first_kernel<typename Op::elem, D>), dim3(static_cast<unsigned>(p.S * p.Hk), static_cast<unsigned>(p.N)), dim3(2 * D), 0,
+                       s, p);
   }
   return hipGetLastError();
 }

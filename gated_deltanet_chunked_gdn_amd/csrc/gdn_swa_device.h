@@ -223,8 +223,43 @@ __device__ __forceinline__ void spoil(f32x4_t (*acc)[CT], const E* values, const
     }
 }
 
-// Workgroups x, x + 8, ... share an XCD and its L2: items in order, an eighth of them each.
-__device__ __forceinline__ int xcd_item(int x, int items) { return (x & 7) * ((items + 7) / 8) + (x >> 3); }
+// The workgroup's item: workgroups x, x + 8, ... share an XCD and its L2, which takes stripes of
+// items in order.
+__device__ __forceinline__ int xcd_item(int stripe) {
+  const int x = blockIdx.y * gridDim.x + blockIdx.x, k = x >> 3, round = k / stripe;
+  return (8 * round + (x & 7)) * stripe + k - round * stripe;
+}
+
+// The sequence of a slot (swa_slots) and its block there.
+struct Spot {
+  int n, block, len;
+  int64_t bos;
+};
+__device__ __forceinline__ Spot spot(const SwaParams& p, int slot, int each) {
+  Spot s;
+  int64_t len;
+  if (p.seq.cu) {
+    // The last sequence whose slots begin at or before this one, by a whole wave: 64 places at a time.
+    int lo = 0, hi = p.N;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 63) >> 6, mid = lo + (threadIdx.x & 63) * step;
+      const bool in = mid < hi && p.seq.cu[mid] / each + mid <= slot;  // the first is in
+      const int at = lo + (63 - __builtin_clzll(__ballot(in))) * step;
+      hi = min(hi, at + step);
+      lo = at;
+    }
+    s.n = lo;
+    chunk::seq_range(p.seq, lo, s.bos, len);
+    s.block = slot - static_cast<int>(s.bos / each) - lo;
+  } else {
+    const int blocks = (p.seq.T + each - 1) / each;
+    s.n = slot / blocks;
+    s.block = slot - s.n * blocks;
+    chunk::seq_range(p.seq, s.n, s.bos, len);
+  }
+  s.len = static_cast<int>(len);
+  return s;
+}
 
 }  // namespace swa
 }  // namespace gdn

@@ -255,15 +255,15 @@ __device__ __forceinline__ bool attend(const SwaParams& p, int64_t bos, int len,
 }
 
 template <typename Op, int D, int CT>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int blocks) {
-  const int item = xcd_item(blockIdx.x, items);
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int slots, int stripe) {
+  const int item = xcd_item(stripe);
   if (item >= items) return;
   // a key head's query heads next to each other, then its blocks of queries
-  const int group = p.Hq / p.Hk, hk = item / (group * blocks), rest = item - hk * group * blocks;
-  const int block = rest / group, h = hk * group + rest - block * group;
-  int64_t bos, len64;
-  chunk::seq_range(p.seq, blockIdx.y, bos, len64);
-  const int len = static_cast<int>(len64), q0 = block * 64 * CT;
+  const int group = p.Hq / p.Hk, hk = item / (group * slots), rest = item - hk * group * slots;
+  const int slot = rest / group, h = hk * group + rest - slot * group;
+  const Spot at = spot(p, slot, 64 * CT);
+  const int64_t bos = at.bos;
+  const int len = at.len, q0 = at.block * 64 * CT;
   if (q0 >= len) return;
 
   __shared__ alignas(16) typename Op::elem Kt[2][64 * D], Vt[2][64 * D];
@@ -279,9 +279,8 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 
 template <typename Op, int D, int CT>
 hipError_t launch_c(const SwaParams& p, hipStream_t s) {
-  const int blocks = (p.max_len + 64 * CT - 1) / (64 * CT), items = p.Hq * blocks;
-  hipLaunchKernelGGL((swa_fwd_kernel<Op, D, CT>), dim3(static_cast<unsigned>((items + 7) / 8 * 8), static_cast<unsigned>(p.N)), dim3(256), 0, s, p,
-                     items, blocks);
+  const SwaGrid g = swa_grid(p, 64 * CT, p.Hq / p.Hk);
+  hipLaunchKernelGGL((swa_fwd_kernel<Op, D, CT>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
   return hipGetLastError();
 }
 template <typename Op, int D>

@@ -687,9 +687,11 @@ gdn_status gdn_rope_bwd(const gdn_rope_problem* problem, const void* q, const vo
  * q, k and v may have their tokens q_stride, k_stride, v_stride values apart as in
  * gdn_rope_problem (0: contiguous; up to 2^21); all else is contiguous.  16-byte aligned,
  * lse and lens 4-byte.  Supported: D in {64, 128}, Hq a multiple of Hk up to 4096, window >= 1 (as long as
- * wanted), sinks up to 1024, a finite scale, B T up to 2^30, up to 65535 sequences, and fewer than 2^24
- * workgroups in a launch (counted as one for 32 tokens of the longest sequence, every query head and
- * every sequence), else GDN_ERR_UNSUPPORTED.
+ * wanted), sinks up to 1024, a finite scale, B T up to 2^30, up to 65535 sequences, and (but for
+ * gdn_swa_fill) fewer than 2^24 workgroups in a launch, else GDN_ERR_UNSUPPORTED: counted as one for every
+ * query head and every 32 tokens of a sequence, or part of them; and, where windows leave first tokens
+ * behind, one for every sequence, key head and first token, and one for every key head, 16 first
+ * tokens and 64 tokens of a sequence, or part of them.
  * Scores, sums and statistics of the softmax are fp32; with bf16 io the probabilities and
  * the scores' gradients are rounded to bf16 as operands of the products that sum over them
  * (gdn_swa_step keeps the probabilities' next 8 bits in a second product).

@@ -223,3 +223,36 @@ def test_values_that_are_not_finite_stay_where_they_are_seen(B, T, Hq, Hk, D, W,
                     assert bool(torch.isnan(x[r]).all()), (name, at, key)
                 ref.check(f"{name}[{at}] {key}", torch.where(r, torch.zeros_like(x), x),
                           want[key].masked_fill(r.cpu(), 0), err[key])
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+def test_one_long_sequence_beside_many_short_ones(io):
+    """Two thousand sequences of a token or none around one of four thousand tokens: heads that
+    share nothing, of which two are looked at."""
+    before, long, behind, W, S = 1500, 4096, 600, 100, 3
+    lens = [i % 2 for i in range(before)] + [long] + [1] * behind
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    q, k, v, do = inputs(1, cu[-1], 64, 64, 64, io, seed=10)
+    seqs, how = gdn.SeqLens(cu, torch.device(DEV)), dict(sinks=S, scale=0.125)
+    o, lse = gdn.swa_fwd(q, k, v, W, cu_seqlens=seqs, return_lse=True, **how)
+    got = dict(gdn.swa_bwd(q, k, v, o, lse, do, W, cu_seqlens=seqs, **how), o=o, lse=lse)
+    caches = [torch.full((len(lens), S + W, 64, 64), 7.0, device=DEV, dtype=io) for _ in range(2)]
+    gdn.swa_fill(k, v, *caches, sinks=S, cu_seqlens=seqs)
+    assert torch.equal(caches[0][before, :S], k[0, cu[before]:cu[before] + S]) and torch.equal(caches[1][-1, 0], v[0, -1])
+    for h in (0, 63):
+        want, err = ref.swa(*(t[:, :, h:h + 1] for t in (q, k, v)), W, S, 0.125, cu, do[:, :, h:h + 1])
+        for key in got:
+            ref.check(f"{key} of head {h}", got[key][:, :, h:h + 1], want[key], err[key])
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("N", [63, 64, 65, 4095, 4097, 5000])
+def test_thousands_of_sequences(N, io):
+    """Every number of sequences finds its blocks, empty sequences among them."""
+    lens = torch.randint(0, 3, (N,), generator=torch.Generator().manual_seed(N))
+    lens[::501] = 70
+    cu = [0] + lens.cumsum(0).tolist()
+    q, k, v, do = inputs(1, cu[-1], 2, 1, 64, io, seed=11)
+    compare(q, k, v, do, 9, 2, 0.125, cu)

@@ -274,3 +274,21 @@ def test_factors_that_are_not_finite(lib, bad):
         assert lib.gdn_glr_workspace_size(glr(c=bad), pass_, n) == UNSUP and n.value == 7
     for pass_ in range(2):
         assert lib.gdn_swa_workspace_size(swa(scale=bad), pass_, n) == UNSUP and n.value == 7
+
+
+def test_one_long_sequence_beside_many_short_ones(lib):
+    """Blocks are counted by what the sequences hold, not by the longest one's length."""
+    n = ctypes.c_size_t(7)
+    for long, many, each in ((32768, 1100, 8), (16384, 2100, 16), (4096, 60000, 1), (128, 65000, 0)):
+        cu = np.concatenate([[0], long + each * np.arange(many + 1)])
+        p = swa(B=1, T=int(cu[-1]), Hq=16, Hk=4, D=128, window=1024, sinks=4, num_seqs=len(cu) - 1, cu_seqlens_host=offsets(cu), cu_seqlens_dev=P)
+        assert lib.gdn_swa_workspace_size(p, nat.GDN_SWA_BWD, n) == OK and n.value > 0
+        if not torch.cuda.is_available():  # they reach the launch
+            for name in ("gdn_swa_fwd", "gdn_swa_bwd", "gdn_swa_fill"):
+                assert CALLS[name](lib, p) == nat.GDN_ERR_HIP, name
+    # too many blocks for the attention, which filling the cache has none of
+    cu = np.arange(0, 33 * 65535 + 1, 33)
+    p = swa(B=1, T=int(cu[-1]), Hq=132, Hk=1, num_seqs=65535, cu_seqlens_host=offsets(cu), cu_seqlens_dev=P)
+    assert CALLS["gdn_swa_fwd"](lib, p) == UNSUP and lib.gdn_swa_workspace_size(p, nat.GDN_SWA_BWD, n) == UNSUP
+    if not torch.cuda.is_available():
+        assert CALLS["gdn_swa_fill"](lib, p) == nat.GDN_ERR_HIP
