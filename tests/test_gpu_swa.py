@@ -256,3 +256,46 @@ def test_thousands_of_sequences(N, io):
     cu = [0] + lens.cumsum(0).tolist()
     q, k, v, do = inputs(1, cu[-1], 2, 1, 64, io, seed=11)
     compare(q, k, v, do, 9, 2, 0.125, cu)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+@pytest.mark.parametrize("B,T,Hq,Hk,D,W,S,cu", ODD)
+def test_infinities_reach_those_that_see_them(B, T, Hq, Hk, D, W, S, cu, bad, io):
+    """Where the definition leaves no finite result, there is none: an infinite v gives its column of
+    o, an infinite q or a score of plus infinity the row of o and lse, an infinite do its column of dv;
+    delta is not finite then, and with it dq, and dk of all keys that are seen.  (Left out: scores of
+    minus infinity, whose probability is zero.)"""
+    q, k, v, do = inputs(B, T, Hq, Hk, D, io, seed=8)
+    how = dict(sinks=S, scale=D ** -0.5, cu_seqlens=cu)
+    see, group, rows, d = _seen(B, T, W, S, cu), Hq // Hk, B * T, 5
+    for name in "qkvd":
+        for at in (0, 1, 40, rows // 2, rows - 1):
+            t = {n: x.clone() for n, x in zip("qkvd", (q, k, v, do))}
+            h = (Hq if name in "qd" else Hk) - 1
+            t[name].view(rows, -1, D)[at, h, d] = bad
+            heads = slice(Hq - 1, Hq) if name in "qd" else slice(Hq - group, Hq)
+            hit = torch.zeros(rows, Hq, dtype=torch.bool, device=DEV)  # queries whose result is not finite
+            hit[:, heads] = (torch.arange(rows, device=DEV) == at if name in "qd" else see[:, at])[:, None]
+            if name == "k":
+                hit &= q.view(rows, Hq, D)[..., d].float() * bad > 0
+            keys = torch.stack([(see & hit[:, i * group:(i + 1) * group].any(1)[:, None]).any(0) for i in range(Hk)], 1)
+            o, lse = gdn.swa_fwd(t["q"], t["k"], t["v"], W, return_lse=True, **how)
+            got = gdn.swa_bwd(t["q"], t["k"], t["v"], o, lse, t["d"], W, **how)
+            fine = {key: torch.isfinite(x.view(rows, *x.shape[2:])) for key, x in dict(got, o=o, lse=lse).items()}
+            torch.cuda.synchronize()
+            if name in "qk":
+                assert not bool(fine["o"][hit].any()) and not bool(fine["lse"][hit].any()), (name, at)
+            elif name == "v":
+                assert not bool(fine["o"][..., d][hit].any()), (name, at)
+            else:
+                assert not bool(fine["dv"][..., d][keys].any()), (name, at)
+            assert not bool(fine["dq"][hit].any()) and not bool(fine["dk"][keys].any()), (name, at)
+
+
+@pytest.mark.parametrize("io,D", [(BF, 64), (BF, 128), (F32, 128)])
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3, -4.0])
+def test_scales_of_both_signs(scale, D, io):
+    """In both types and widths; a negative scale turns the forward's queries."""
+    q, k, v, do = inputs(1, 150, 2, 1, D, io, seed=2)
+    compare(q, k, v, do, 50, 2, scale, None)

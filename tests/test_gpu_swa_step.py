@@ -123,3 +123,18 @@ def test_probabilities_keep_sixteen_bits(Hq, Hk, D, W, S):
     terms, _, _, _ = ref.swa_step(wide[0], wide[1], wide[2].abs(), wide[3], wide[4].abs(), at, S, D ** -0.5)
     o = gdn.swa_step(q, k, v, kc, vc, at, sinks=S, scale=D ** -0.5)
     ref.check("o", o, want, err + 2.0 ** -16 * terms)
+
+
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("scale", [0.0, -0.1, -2.0])
+@pytest.mark.parametrize("W", [40, 1500])
+def test_scales_of_both_signs(W, scale, io):
+    """None, and negative ones, in one run of slots and in several."""
+    Hq, Hk, D, S, lens = 4, 1, 128, 3, [0, 20, W + 2, 5 * W]
+    g = _gen(W)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(io)  # noqa: E731
+    B = len(lens)
+    q, k, v, kc, vc = r(B, 1, Hq, D), r(B, 1, Hk, D), r(B, 1, Hk, D), r(B, S + W, Hk, D), r(B, S + W, Hk, D)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want, err, _, _ = ref.swa_step(q, k, v, kc, vc, at, S, scale)
+    ref.check("o", gdn.swa_step(q, k, v, kc, vc, at, sinks=S, scale=scale), want, err)
