@@ -189,24 +189,21 @@ __device__ __forceinline__ int64_t number(const GlrParams& p) {
 
 // Words that workgroups pass to each other; zero: not there yet.  A state stands beside a one;
 // of a segment's (A, B), A is positive or zero (or NaN), so its sign is the mark.
-// Two words go in one access of 16 bytes, each of them whole, of a scope past the caches of an
-// XCD (sc1), which the compiler neither merges nor moves (volatile).
-constexpr int kDevice = 1 << 4, kVolatile = 1 << 31;
+// A word is one atomic access of 64 bits, the widest that there are, of device scope: past the
+// caches of an XCD (sc1), neither merged nor moved.  Word e of lane l of a tile's row of channels
+// stands at e kLanes + l, so that an access of the lanes is one piece of memory (channels in
+// order: 178 us for 172, 65536 x 1024).
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));  // value, mark
-template <int V>
+template <int V, int LANES>
 __device__ __forceinline__ void give_(uint64_t* to, uint32_t off, const u32x2_t* w) {
-  const __amdgpu_buffer_rsrc_t r = chunk::buffer_rsrc(to, 0x7fffffff);
+  uint64_t* const p = reinterpret_cast<uint64_t*>(reinterpret_cast<char*>(to) + off);
 #pragma unroll
-  for (int e = 0; e < V; e += 2) {
-    const chunk::u32x4v_t v = {w[e][0], w[e][1], w[e + 1][0], w[e + 1][1]};
-    __builtin_amdgcn_raw_buffer_store_b128(v, r, off + 8 * e, 0, kDevice);
-  }
+  for (int e = 0; e < V; ++e) __hip_atomic_store(p + e * LANES, __builtin_bit_cast(uint64_t, w[e]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Waits until all words of all lanes of the wave are there: V at each place, `off` bytes from
 // `from`; lanes that want none of a place say so.
-template <int V, int COUNT>
+template <int V, int LANES, int COUNT>
 __device__ __forceinline__ void take_(const uint64_t* from, const uint32_t* off, const bool* want, u32x2_t (*w)[V]) {
-  const __amdgpu_buffer_rsrc_t r = chunk::buffer_rsrc(from, 0x7fffffff);
   bool missing[COUNT];
 #pragma unroll
   for (int i = 0; i < COUNT; ++i) missing[i] = want[i];
@@ -215,11 +212,9 @@ __device__ __forceinline__ void take_(const uint64_t* from, const uint32_t* off,
     for (int i = 0; i < COUNT; ++i)
       if (missing[i]) {
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          const chunk::u32x4v_t v = __builtin_amdgcn_raw_buffer_load_b128(r, off[i] + 8 * e, 0, kDevice | kVolatile);
-          w[i][e] = u32x2_t{v[0], v[1]};
-          w[i][e + 1] = u32x2_t{v[2], v[3]};
-        }
+        for (int e = 0; e < V; ++e)
+          w[i][e] = __builtin_bit_cast(u32x2_t, __hip_atomic_load(reinterpret_cast<const uint64_t*>(reinterpret_cast<const char*>(from) + off[i]) + e * LANES,
+                                                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
       }
     bool there = true;
 #pragma unroll
@@ -301,17 +296,18 @@ struct Shared {
 // direction of the walk.  Called by the whole workgroup.
 template <int V>
 __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Place<V>& at, int place, int64_t first_slot, int dir,
-                                       int d, bool chan, const float* a, const float* b, float* carry) {
+                                       bool chan, const float* a, const float* b, float* carry) {
   using P = Place<V>;
   const int group = place / kGlrGroup, index = place % kGlrGroup;
   const int64_t group_slot = at.bos / (P::kTokens * kGlrGroup) + at.n;
   const bool lead = threadIdx.x < P::kLanes && chan;
-  const uint32_t lane_off = static_cast<uint32_t>(d) * 8;
+  // of channels behind the last: words that are given all the same
+  const uint32_t lane_off = chan ? static_cast<uint32_t>(at.tile * kGlrTile + at.ch / V) * 8 : 0;
   if (place + 1 < at.segs && index + 1 < kGlrGroup && lead) {
     u32x2_t w[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) w[e] = u32x2_t{__float_as_uint(b[e]), __float_as_uint(a[e]) | 0x80000000u};
-    give_<V>(p.whole + (first_slot + dir * place) * p.C, lane_off, w);
+    give_<V, P::kLanes>(p.whole + (first_slot + dir * place) * p.words, lane_off, w);
   }
   if (place == 0) return;
   // The segments of the group before this one, a few consecutive ones for every run of the
@@ -333,9 +329,9 @@ __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Pla
     for (int i = 0; i < kEach; ++i) {
       const int k = (at.wave * P::kRuns + at.run) * kEach + i;
       want[i] = k < index;
-      off[i] = lane_off + static_cast<uint32_t>(want[i] ? (dir > 0 ? k : index - 1 - k) : 0) * p.C * 8;
+      off[i] = lane_off + static_cast<uint32_t>(want[i] ? (dir > 0 ? k : index - 1 - k) : 0) * p.words * 8;
     }
-    take_<V, kEach>(p.whole + lowest * p.C, off, want, w);
+    take_<V, P::kLanes, kEach>(p.whole + lowest * p.words, off, want, w);
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
       if (want[i]) {
@@ -365,7 +361,7 @@ __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Pla
   if (group > 0 && at.wave == 0) {
     u32x2_t w[1][V];
     const bool want[1] = {at.run == 0};
-    take_<V, 1>(p.end + (group_slot + group - 1) * p.C, &lane_off, want, w);
+    take_<V, P::kLanes, 1>(p.end + (group_slot + group - 1) * p.words, &lane_off, want, w);
     if (at.run == 0) {
       float f[V];
 #pragma unroll
@@ -387,7 +383,7 @@ __device__ __forceinline__ void arrive(const GlrParams& p, Shared& sh, const Pla
     u32x2_t w[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) w[e] = u32x2_t{__float_as_uint(fmaf(a[e], carry[e], b[e])), 1u};
-    give_<V>(p.end + (group_slot + group) * p.C, lane_off, w);
+    give_<V, P::kLanes>(p.end + (group_slot + group) * p.words, lane_off, w);
   }
 }
 
@@ -481,7 +477,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_fw
       fa[e] = w ? fa[e] * wa[e] : wa[e];
     }
   }
-  arrive<V>(p, sh, at, at.seg, P::start(p, at.n), 1, d, chan, fa, fb, carry);
+  arrive<V>(p, sh, at, at.seg, P::start(p, at.n), 1, chan, fa, fb, carry);
 
   float h[V];
 #pragma unroll
@@ -513,8 +509,9 @@ __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_fw
 
 // ---------------------------------------------------------------------------- backward
 
+// Without a gate four waves a SIMD: 4 x 4096 x 2048 both ways 220 us, with three (two registers more) 225.
 template <typename E, int V, bool Z>
-__global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bwd_kernel(GlrParams p, int tiles) {
+__global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? (Z ? 3 : 4) : 2) void glr_bwd_kernel(GlrParams p, int tiles) {
   using P = Place<V>;
   const P at(p, number(p), tiles, true);
   if (at.slot < 0) return;
@@ -614,7 +611,7 @@ __global__ __launch_bounds__(64 * kGlrWaves, sizeof(E) == 2 ? 3 : 2) void glr_bw
       fa[e] = none ? wa[e] : fa[e] * wa[e];
     }
   }
-  arrive<V>(p, sh, at, at.segs - 1 - at.seg, P::start(p, at.n) + at.segs - 1, -1, d, chan, fa,
+  arrive<V>(p, sh, at, at.segs - 1 - at.seg, P::start(p, at.n) + at.segs - 1, -1, chan, fa,
             fb, carry);
 
   float before[kRun][V];
@@ -760,7 +757,7 @@ hipError_t launch(const GlrParams& p, hipStream_t s) {
   const int tiles = glr_tiles(p.C);
   if (p.chained) {
     const int64_t groups = glr_slots(p.rows, p.N, glr_seg(BWD) * kGlrGroup);
-    const int64_t pairs = 16 + p.slots * p.C / 2 + groups * p.C / 2;  // C is even
+    const int64_t pairs = 16 + (p.slots + groups) * p.words / 2;
     hipLaunchKernelGGL(glr_clear_kernel, dim3(static_cast<unsigned>((pairs + 255) / 256)), dim3(256), 0, s, p.chain, pairs);
   }
   const dim3 grid(static_cast<unsigned>(p.slots * tiles)), block(64 * kGlrWaves);

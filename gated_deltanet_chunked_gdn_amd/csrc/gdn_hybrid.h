@@ -35,12 +35,13 @@ struct GlrParams {
   // What the segments of a sequence tell each other (chained): a counter, then words of a
   // value and a mark that it is there.
   uint64_t* chain;     // cleared before the launch: [32] whose first counts workgroups, then
-  uint64_t* whole;     // [segment slot][C] decay product and end from zero of a segment
-  uint64_t* end;       // [group slot][C] state behind (backward: gradient in front of) a group
+  uint64_t* whole;     // [segment slot][words] decay product and end from zero of a segment
+  uint64_t* end;       // [group slot][words] state behind (backward: gradient in front of) a group
   SeqInfo seq;
   int64_t rows;        // B * T
   int64_t slots;       // segment slots
   int32_t N, C;
+  int32_t words;       // C up to whole tiles
   int32_t chained;     // some sequence has several segments
   float c;
 };

@@ -52,8 +52,9 @@ gdn_status check_glr(const gdn_glr_problem* p, bool bwd, GlrSize* c) {
   };
   c->slots = slots(seg);
   c->chained = max_len > seg;
-  c->whole = static_cast<size_t>(c->slots) * 2 * c->chan;
-  c->end = up256(static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs, seg * gdn::kGlrGroup)) * 2 * c->chan);
+  const size_t words = static_cast<size_t>(gdn::glr_tiles(p->C)) * gdn::kGlrTile * 8;
+  c->whole = static_cast<size_t>(c->slots) * words;
+  c->end = static_cast<size_t>(gdn::glr_slots(c->rows, p->num_seqs, seg * gdn::kGlrGroup)) * words;
   c->part = bwd ? static_cast<size_t>(c->slots) * c->chan : 0;
   // workgroups of 256 threads, counted in 32 bits: segments of the longer of the two
   // directions' segments or shorter, so that what the forward takes the backward takes too
@@ -68,6 +69,7 @@ gdn::GlrParams glr_params(const gdn_glr_problem* p, const GlrSize& c, const void
   gp.x = x; gp.r = r; gp.i = i; gp.lam = lam; gp.z = z;
   gp.seq = gdn::SeqInfo{p->cu_seqlens_dev, p->T};
   gp.rows = c.rows; gp.N = p->num_seqs; gp.C = p->C;
+  gp.words = gdn::glr_tiles(p->C) * gdn::kGlrTile;
   gp.slots = c.slots; gp.chained = c.chained;
   gp.c = p->c;
   if (c.chained) {
