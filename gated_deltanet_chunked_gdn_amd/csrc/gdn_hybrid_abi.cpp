@@ -117,7 +117,9 @@ size_t extent(int64_t rows, int64_t stride, int64_t row, size_t io) {
 gdn_status check_stride(int64_t given, int64_t row, size_t io, int64_t* stride) {
   *stride = given ? given : row;
   if (*stride < row) return GDN_ERR_SHAPE;
-  // the kernels address up to 128 rows from one of them in 32 bits
+  // The attention's kernels address up to 128 rows from one of them in 32 bits.  The rotation and
+  // the cache's calls go by 64 bits; they have the same limit, so that what one of the calls takes
+  // the others take.
   if (*stride > INT64_C(1) << 21) return GDN_ERR_UNSUPPORTED;
   return *stride * static_cast<int64_t>(io) % 16 ? GDN_ERR_ALIGN : GDN_OK;
 }
@@ -195,18 +197,30 @@ gdn_status check_swa(const gdn_swa_problem* p, SwaSize* c) {
   const size_t first = static_cast<size_t>(p->Hk) * c->S * 2 * p->D * 4;
   c->win = up256(p->num_seqs * first);
   // Runs of 256 queries for the first tokens' sums, or of a tile of them where those leave most
-  // CUs without work: 10 runs (five sequences, 1501 tokens, fp32, D = 64) 117 us the step with 256
-  // queries each, 101 with 64; 64 (4096 tokens, bf16, D = 128) 205, with 128 201; 512 of them
-  // (16384 tokens) 499, with 128 509.
+  // CUs without work.  Training steps, us, by runs of 64, 128 and 256 queries: 10 runs of 256 (five
+  // sequences, 1501 tokens, 2 key heads, fp32, D = 64) 85, 90, 104; 64 (4096 tokens, 4 key heads of
+  // 128) bf16 211, 202, 206, fp32 989, 991, 1015; 512 (16384 tokens, 8 key heads of 128) bf16 598,
+  // 544, 521, fp32 3927, 3884, 3869.
   const int64_t far = c->rows / 256 * p->Hk * ((c->S + 15) / 16);
   c->run_far = far >= 128 ? 256 : c->io == 2 ? 128 : 64;
   c->far = static_cast<size_t>(gdn::swa_far_slots(c->rows, p->num_seqs, c->run_far)) * first;
   // Blocks of half as many queries, or of a quarter as many keys, where whole ones leave CUs
-  // without work (packed sequences of other lengths count as so many of the rows).  bf16 training
-  // steps over one sequence, a window of 512, D = 128, us, halves | whole: 256 blocks of queries
-  // 111 | 118, 384 blocks 178 | 171, 512 blocks 215 | 131; quarters | whole: 128 blocks of keys
-  // 320 | 410, 256 blocks 333 | 279.  D = 64: 256 blocks 161 | 184, 320
-  // blocks 76 | 75.
+  // without work (packed sequences of other lengths count as so many of the rows).  Training steps
+  // over one sequence, window 512, us, halves | whole, by tokens and heads of queries / of keys:
+  //   blocks of queries            bf16, D = 128   fp32, D = 128   bf16, D = 64   fp32, D = 64
+  //   256  (2048, 16 / 4)              98 | 104       472 | 461        69 | 75       231 | 244
+  //   384  (4096, 12 / 4)             151 | 150       712 | 815        74 | 82       308 | 365
+  //   512  (4096, 16 / 4)             184 | 174       941 | 915        91 | 93       396 | 407
+  //   1024 (8192, 16 / 8)             262 | 234      1892 | 1834      148 | 149      783 | 807
+  // and quarters | whole:
+  //   blocks of keys               bf16, D = 128   fp32, D = 128   bf16, D = 64   fp32, D = 64
+  //   128  (4096, 16 / 4)             174 | 216       915 | 1286       93 | 156      407 | 628
+  //   256  (4096, 16 / 8)             179 | 144       923 | 919        94 | 101      411 | 435
+  //   320  (4096, 20 / 10)            249 | 203      1285 | 1557      131 | 137      625 | 716
+  //   512  (4096, 16 / 16)            209 | 135       950 | 936       102 | 85       422 | 417
+  // (256 blocks fill the CUs once, 320 take a second turn.)  The bounds are those of bf16, for queries
+  // of D = 128: fp32 at 384 blocks of queries or 320 of keys, and D = 64 from 384 blocks of queries
+  // on, stand on the side that the table shows to be the slower one.
   const int64_t whole = c->rows / gdn::kSwaQueries;
   c->few = whole * p->Hq < 384;
   c->few_keys = whole * p->Hk < (p->D == 64 ? 320 : 256);
@@ -243,9 +257,9 @@ gdn_status check_cache(const gdn_swa_problem* p, SwaSize* c) {
   c->lens = static_cast<size_t>(p->num_seqs) * 4;
   const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(p->num_seqs) * p->Hk * ((p->Hq / p->Hk + 15) / 16));
   // Whole where there is a workgroup a CU, else runs of at least 128 slots (32 a wave) that make
-  // some 512 workgroups.  64 sequences of 4 key heads and 4100 slots, us: whole 97, two runs 104,
-  // four 107; 48 sequences: two runs 90, three 82, six 80; one of 30000 slots: 64 runs 21, 118 runs
-  // 24, 235 runs 31; eight: eight runs 77, 16 runs 72, 32 runs 67.
+  // some 512 workgroups.  Aims of 256, 512 and 1024, us, 16 / 4 heads of 128: bf16, one sequence of
+  // 30000 slots 21, 24, 32; eight 83, 74, 67; 16 of 4100 slots 35, 32, 30; 48 90, 82, 80; fp32 38,
+  // 37, 46; 170, 131, 135; 63, 56, 62; 159, 172, 157.  64 of 4100 whole 97, as two runs 104.
   const int64_t splits = groups >= 256 ? 1 : std::min<int64_t>((512 + groups - 1) / groups, (slots + 127) / 128);
   c->run = static_cast<int32_t>(((slots + splits - 1) / splits + 127) / 128 * 128);
   c->splits = static_cast<int32_t>((slots + c->run - 1) / c->run);

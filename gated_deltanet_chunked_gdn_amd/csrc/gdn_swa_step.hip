@@ -172,7 +172,7 @@ __global__ __launch_bounds__(256, 2) void swa_step_kernel(SwaParams p) {
 
 // The runs' sums joined in order, a head a workgroup: four parts of them side by side, then
 // those.  A lane takes a run's maximum and sum, 64 runs at a time, and a thread a column of the
-// values, several runs' in flight.  (One part took 7 us longer over 118 runs.)
+// values, one run after another.  (One part took 7 us longer over 118 runs.)
 constexpr int kJoin = 4;
 template <typename E, int D>
 __global__ __launch_bounds__(kJoin * D) void swa_join_kernel(SwaParams p) {
@@ -195,7 +195,6 @@ __global__ __launch_bounds__(kJoin * D) void swa_join_kernel(SwaParams p) {
     const float f = exp2_(t.x - base);
     total = fmaf(total, fade, wave_sum(t.y * f));
     o *= fade;
-#pragma unroll 8
     for (int s = 0; s < many; ++s) o = fmaf(vals[(s0 + s) * all * D], __shfl(f, s, 64), o);
   }
   if (x == 0) {

@@ -18,7 +18,10 @@ HIP kernels.
     o        = swa_step(q, k, v, kcache, vcache, lens, sinks=0)  # one token, cache updated in place
 
 Tensors are contiguous; q, k and v of the last two operators may also be columns of
-contiguous rows, as a projection leaves them side by side.  Activations are bf16 or fp32 (one dtype a call), parameters and recurrent states fp32.
+contiguous rows, as a projection leaves them side by side, with up to 2^21 values from
+token to token (for single tokens: from sequence to sequence; a slice of one token out of
+longer sequences lies further apart and has to be made contiguous).  Activations are bf16
+or fp32 (one dtype a call), parameters and recurrent states fp32.
 Packed sequences: B == 1 and ``cu_seqlens`` the N + 1 offsets, best built once as a
 ``SeqLens``.  Outputs and gradients that were not asked for are None.  A ``workspace``
 holds nothing between calls, but calls that may overlap (on two streams, in graphs

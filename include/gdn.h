@@ -644,7 +644,8 @@ typedef enum gdn_rope_norm {
  *        positions [B,T] int32 (NULL: 0 .. T - 1 in every row); wq, wk [D] fp32 (each NULL:
  *        ones; only with GDN_ROPE_RMS, else GDN_ERR_UNSUPPORTED)
  *   out: q_out, k_out, contiguous
- * 16-byte aligned but for inv_freq and positions (4 bytes); strides of whole 16 bytes
+ * 16-byte aligned but for inv_freq and positions (4 bytes); strides (with T == 1 those from
+ * sequence to sequence) of whole 16 bytes
  * (GDN_ERR_ALIGN), at least Hq D and Hk D (GDN_ERR_SHAPE), up to 2^21.  Supported: D in {64, 128, 256},
  * R a multiple of 16 up to D, Hq and Hk up to 4096, B T (Hq + Hk) < 2^31, else
  * GDN_ERR_UNSUPPORTED.  Angles are reduced in fp64 (2^-52 of the angle); all else is fp32,
