@@ -31,7 +31,7 @@
 //   dx = G m sigmoid(i);  di = G m x sigmoid(i) (1 - sigmoid(i));  dz = dy h silu'(z)
 //
 // HBM-bound.  Forward of 65536 x 1024 with a gate, bf16: 170 us, 3.95 TB/s of the 671 MB it reads
-// and writes (a large copy: 5.1); 4 x 4096 x 2048: 97 us.  Backward of the latter: 172 us, 3.6 TB/s of
+// and writes (a large copy: 5.1); 4 x 4096 x 2048: 98 us.  Backward of the latter: 172 to 177 us, 3.5 TB/s of
 // its 621 MB, and 5 each for the clearing of the words and for dlam.  With two passes over the
 // inputs instead of words that pass on, 252 us and, training, 332 against 263.
 #include <hip/hip_runtime.h>

@@ -16,6 +16,7 @@
 // Bound by the matrix units and what runs beside them.  4 x 4096 tokens, 16 query heads and 8 key
 // heads of 128, window 512, bf16: dq 183 us (109 GFLOP with the edges' tiles whole, 600
 // TFLOP/s), dk and dv 217 (137, 630), the first tokens 35 and 7.
+// Two waves a SIMD leave 256 registers: dq keeps 48 bytes a lane in scratch there, dk and dv 8.
 #include <hip/hip_runtime.h>
 
 #include "gdn_swa_device.h"
