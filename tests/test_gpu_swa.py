@@ -299,3 +299,17 @@ def test_scales_of_both_signs(scale, D, io):
     """In both types and widths; a negative scale turns the forward's queries."""
     q, k, v, do = inputs(1, 150, 2, 1, D, io, seed=2)
     compare(q, k, v, do, 50, 2, scale, None)
+
+
+def test_more_workgroups_than_an_axis_of_the_grid():
+    """65535 sequences of one token and 70 heads, 4.6 million blocks: a token that sees itself alone
+    has its value for a result, and do for dv, exactly."""
+    N, H, D = 65535, 70, 64
+    q, k, v, do = inputs(1, N, H, H, D, BF, seed=12)
+    seqs = gdn.SeqLens(list(range(N + 1)), torch.device(DEV))
+    o, lse = gdn.swa_fwd(q, k, v, 5, sinks=2, scale=0.125, cu_seqlens=seqs, return_lse=True)
+    got = gdn.swa_bwd(q, k, v, o, lse, do, 5, sinks=2, scale=0.125, cu_seqlens=seqs)
+    assert torch.equal(o, v) and torch.equal(got["dv"], do)
+    # D products of absolute terms up to 6^2 and their sum; both sides' roundings
+    assert float((lse - (q.float() * k.float()).sum(-1) * 0.125).abs().max()) <= 2 * 64 * 67 * 36 * 0.125 * 2.0 ** -24
+    assert bool(torch.isfinite(got["dq"]).all()) and bool(torch.isfinite(got["dk"]).all())
