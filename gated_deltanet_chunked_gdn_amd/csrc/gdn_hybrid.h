@@ -149,22 +149,30 @@ inline int64_t swa_far_slots(int64_t rows, int64_t n, int64_t far) { return rows
 inline int64_t swa_slots(const SwaParams& p, int64_t rows, int64_t each) {
   return p.seq.cu ? rows / each + p.N : p.N * ((p.seq.T + each - 1) / each);
 }
-// A launch over `items` (key heads, slots and, of queries, a key head's query heads, the last
-// the fastest), `stripe` of them after each other on an XCD.
+// The workgroups of a launch: chunks of slots after each other, each chunk's key heads, slots and
+// (of queries) a key head's query heads, the last the fastest, an eighth on each XCD.  Dense
+// sequences are one chunk.  Packed ones, whose blocks of unlike work lie in rows, come in chunks of
+// 16 slots or fewer, so that every XCD has some of each.  Forward, 16 / 4 heads of 128, window 1024, bf16, us, by
+// chunks of 4, 8, 16, 32 and 64: 2048 tokens in two sequences 34, 34, 34, 40, 37; 10240 in six 101, 102,
+// 105, 106, 100; 4096 in nine 48, 45, 44, 46, 50; training, 8 / 1 heads of 64, fp32, 8192 tokens in
+// six 454, 477, 458, 521, 524.
+struct SwaWork {
+  int32_t slots, chunk;  // slots of a chunk
+  int32_t heads;         // query heads of a key head, or 1
+  int32_t share;         // workgroups of an XCD in a chunk
+};
 struct SwaGrid {
   dim3 grid;
-  int slots, items, stripe;
+  SwaWork work;
 };
 inline SwaGrid swa_grid(const SwaParams& p, int64_t each, int heads, int z = 1) {
-  const int64_t slots = swa_slots(p, p.rows, each), items = slots * p.Hk * heads;
-  // Dense: an eighth each.  Packed sequences may be long and short ones in a row, and their
-  // blocks of unlike work: stripes of 16 blocks, or of as many fewer as leaves the XCDs even.
-  const int64_t rounds = p.seq.cu ? (items + 128 * heads - 1) / (128 * heads) : 1;
-  const int64_t stripe = (items + 8 * rounds - 1) / (8 * rounds), total = 8 * rounds * stripe;
+  const int64_t slots = swa_slots(p, p.rows, each);
+  const int64_t chunks = p.seq.cu ? (slots + 15) / 16 : 1, chunk = (slots + chunks - 1) / chunks;
+  const int64_t share = (chunk * p.Hk * heads + 7) / 8, total = 8 * chunks * share;
   // a grid's axis has up to 2^32 threads
   const int64_t y = (total + (1 << 22) - 1) >> 22, x = ((total + y - 1) / y + 7) / 8 * 8;
-  return SwaGrid{dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z)), static_cast<int>(slots),
-                 static_cast<int>(items), static_cast<int>(stripe)};
+  return SwaGrid{dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z)),
+                 SwaWork{static_cast<int32_t>(slots), static_cast<int32_t>(chunk), heads, static_cast<int32_t>(share)}};
 }
 hipError_t launch_swa_fwd(const SwaParams& p, int D, bool bf16, hipStream_t s);
 hipError_t launch_swa_bwd(const SwaParams& p, int D, bool bf16, hipStream_t s);

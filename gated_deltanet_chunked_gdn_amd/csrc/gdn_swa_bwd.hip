@@ -198,12 +198,11 @@ __device__ __forceinline__ bool dq_block(const SwaParams& p, int64_t bos, int le
 }
 
 template <typename Op, int D, int CT>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, int items, int slots, int stripe) {
-  const int item = xcd_item(stripe);
-  if (item >= items) return;
-  const int group = p.Hq / p.Hk, hk = item / (group * slots), rest = item - hk * group * slots;
-  const int slot = rest / group, h = hk * group + rest - slot * group;
-  const Spot at = spot(p, slot, 64 * CT);
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_dq_kernel(SwaParams p, SwaWork w) {
+  const Item item = item_of(p, w);
+  if (item.slot < 0) return;
+  const int hk = item.hk, h = hk * w.heads + item.head;
+  const Spot at = spot(p, item.slot, 64 * CT);
   const int64_t bos = at.bos;
   const int len = at.len, q0 = at.block * 64 * CT;
   if (q0 >= len) return;
@@ -226,17 +225,17 @@ enum Form {
 };
 
 template <typename Op, int D, Form FORM>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || FORM == kKeys) ? 2 : 1) void swa_dkv_kernel(SwaParams p, int items, int slots, int stripe) {
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 && (D == 64 || FORM == kKeys) ? 2 : 1) void swa_dkv_kernel(SwaParams p, SwaWork w) {
   using E = typename Op::elem;
   constexpr bool FAR = FORM == kFar, PART = FORM != kKeys;  // PART: each wave takes a step of a tile's queries
   constexpr int CT = FAR ? 1 : 2, KW = 16 * CT, KT = PART ? KW : 4 * KW;  // keys of a wave, of the workgroup
   constexpr int KB = Op::kBlocks, NS = D / Op::kCols, ND = D / 16, QT = PART ? 64 * KB : 32;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int item = xcd_item(stripe);
-  if (item >= items) return;
-  const int group = p.Hq / p.Hk, hk = item / slots;
-  const Spot place = spot(p, item - hk * slots, FAR ? p.far : KT);
+  const Item item = item_of(p, w);
+  if (item.slot < 0) return;
+  const int group = p.Hq / p.Hk, hk = item.hk;
+  const Spot place = spot(p, item.slot, FAR ? p.far : KT);
   const int64_t bos = place.bos;
   const int len = place.len, block = place.block;
   const int k0 = FAR ? KT * blockIdx.z : block * KT, wk0 = PART ? k0 : k0 + KW * wave;
@@ -480,12 +479,12 @@ __global__ __launch_bounds__(2 * D) void swa_first_kernel(SwaParams p) {
 template <typename Op, int D, int CT, Form FORM>
 hipError_t launch_c(const SwaParams& p, hipStream_t s) {
   SwaGrid g = swa_grid(p, 64 * CT, p.Hq / p.Hk);
-  hipLaunchKernelGGL((swa_dq_kernel<Op, D, CT>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
+  hipLaunchKernelGGL((swa_dq_kernel<Op, D, CT>), g.grid, dim3(256), 0, s, p, g.work);
   g = swa_grid(p, FORM == kKeys ? kSwaKeys : 32, 1);
-  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, FORM>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
+  hipLaunchKernelGGL((swa_dkv_kernel<Op, D, FORM>), g.grid, dim3(256), 0, s, p, g.work);
   if (p.S > 0) {
     g = swa_grid(p, p.far, 1, (p.S + 15) / 16);
-    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, kFar>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
+    hipLaunchKernelGGL((swa_dkv_kernel<Op, D, kFar>), g.grid, dim3(256), 0, s, p, g.work);
     hipLaunchKernelGGL((swa_first_kernel<typename Op::elem, D>), dim3(static_cast<unsigned>(p.S * p.Hk), static_cast<unsigned>(p.N)), dim3(2 * D), 0,
                        s, p);
   }

@@ -223,11 +223,15 @@ __device__ __forceinline__ void spoil(f32x4_t (*acc)[CT], const E* values, const
     }
 }
 
-// The workgroup's item: workgroups x, x + 8, ... share an XCD and its L2, which takes stripes of
-// items in order.
-__device__ __forceinline__ int xcd_item(int stripe) {
-  const int x = blockIdx.y * gridDim.x + blockIdx.x, k = x >> 3, round = k / stripe;
-  return (8 * round + (x & 7)) * stripe + k - round * stripe;
+// What the workgroup works on: workgroups x, x + 8, ... share an XCD and its L2.
+struct Item {
+  int hk, slot, head;  // head: of the key head's; slot: -1 for no work
+};
+__device__ __forceinline__ Item item_of(const SwaParams& p, const SwaWork& w) {
+  const int x = blockIdx.y * gridDim.x + blockIdx.x, k = x >> 3, chunk = k / w.share;
+  const int at = (x & 7) * w.share + k - chunk * w.share, hk = at / (w.heads * w.chunk), rest = at - hk * w.heads * w.chunk;
+  const int in = rest / w.heads, slot = chunk * w.chunk + in;
+  return Item{hk, hk < p.Hk && slot < w.slots ? slot : -1, rest - in * w.heads};
 }
 
 // The sequence of a slot (swa_slots) and its block there.

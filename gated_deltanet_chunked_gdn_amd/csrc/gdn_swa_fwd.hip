@@ -255,13 +255,11 @@ __device__ __forceinline__ bool attend(const SwaParams& p, int64_t bos, int len,
 }
 
 template <typename Op, int D, int CT>
-__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, int items, int slots, int stripe) {
-  const int item = xcd_item(stripe);
-  if (item >= items) return;
-  // a key head's query heads next to each other, then its blocks of queries
-  const int group = p.Hq / p.Hk, hk = item / (group * slots), rest = item - hk * group * slots;
-  const int slot = rest / group, h = hk * group + rest - slot * group;
-  const Spot at = spot(p, slot, 64 * CT);
+__global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void swa_fwd_kernel(SwaParams p, SwaWork w) {
+  const Item item = item_of(p, w);
+  if (item.slot < 0) return;
+  const int hk = item.hk, h = hk * w.heads + item.head;
+  const Spot at = spot(p, item.slot, 64 * CT);
   const int64_t bos = at.bos;
   const int len = at.len, q0 = at.block * 64 * CT;
   if (q0 >= len) return;
@@ -280,7 +278,7 @@ __global__ __launch_bounds__(256, sizeof(typename Op::elem) == 2 ? 2 : 1) void s
 template <typename Op, int D, int CT>
 hipError_t launch_c(const SwaParams& p, hipStream_t s) {
   const SwaGrid g = swa_grid(p, 64 * CT, p.Hq / p.Hk);
-  hipLaunchKernelGGL((swa_fwd_kernel<Op, D, CT>), g.grid, dim3(256), 0, s, p, g.items, g.slots, g.stripe);
+  hipLaunchKernelGGL((swa_fwd_kernel<Op, D, CT>), g.grid, dim3(256), 0, s, p, g.work);
   return hipGetLastError();
 }
 template <typename Op, int D>
